@@ -288,12 +288,140 @@ int32_t kda_chunk_prefill_static_scratch(const kda_params* p,
                                          void* out,
                                          kda_stream_t stream);
 
+/* ==================================================================================================
+ * Softmax-attention layers: a paged key/value cache and the attention that reads it.
+ *
+ * A hybrid model interleaves KDA layers with softmax-attention layers ("linear_attention", three
+ * KDA layers to one).  These entry points serve the latter: append the new tokens' keys and values to the
+ * cache (rotated by their positions on the way), then attend over the cache, fully causal or through
+ * a sliding window with a few first tokens that stay visible.  The pages describe the layers' place
+ * in the model but no cache format; formats and formulas below are this library's own.
+ *
+ * Cache.  num_pages pages of page_size tokens, for keys and for values alike:
+ *   KDA_CACHE_BF16  k_cache, v_cache  bf16  [num_pages][num_kv_heads][page_size][head_dim]
+ *   KDA_CACHE_FP4   k_cache, v_cache  uint8 [num_pages][num_kv_heads][page_size][head_dim / 2], two
+ *                   e2m1 codes a byte (even channel in the low half; magnitudes 0, .5, 1, 1.5, 2, 3,
+ *                   4, 6), and k_scale, v_scale uint8 [num_pages][num_kv_heads][page_size]
+ *                   [head_dim / 16]: one e4m3 scale per 16 channels.  A value is code * scale.
+ *   k_scale and v_scale are ignored for KDA_CACHE_BF16 and may be NULL.
+ * Batch.  Request b owns rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of the packed [total_tokens][..]
+ * inputs, its new tokens.  kv_lens[b] is its number of tokens in the cache INCLUDING the new ones:
+ * new token i of n sits at position kv_lens[b] - n + i.  Position j of request b is row j % page_size
+ * of page block_table[b * max_pages + j / page_size].
+ *   cu_seqlens   device int32 [num_seqs + 1] as in kda_chunk_prefill, or NULL: one new token per
+ *                request (decode), total_tokens = num_seqs.
+ *   kv_lens      device int32 [num_seqs]; an entry <= 0 marks a padding row: nothing is appended and
+ *                its outputs are zeros.  A new token at a negative position is padding too.
+ *   block_table  device int32 [num_seqs][max_pages].  Entries that no visible token needs are never
+ *                read (pages that fell out of every window may be reused or hold -1).
+ * Bad tables never cause an access out of range; they are recorded as device errors, and the tokens
+ * concerned are not appended (attention: not visible, or visible with unspecified values):
+ *   code 2  cu_seqlens not non-decreasing within [0, total_tokens] (as far as the tokens' own entries
+ *           show it)
+ *   code 6  a page index outside [0, num_pages)
+ *   code 7  a position outside the rotation table
+ *   code 8  kv_lens[b] > max_pages * page_size, or > max_kv_len (attention)
+ * The rows of q, k and v may be strided: *_stride is the distance between tokens in elements (the
+ * heads of a token are contiguous), a multiple of 8.  Tensor pointers are 16-byte aligned.
+ * Limits (KDA_ERR_UNSUPPORTED beyond them): total_tokens < 2^22, num_pages * num_kv_heads * page_size
+ * < 2^31, max_pages * page_size < 2^31 - 256, num_q_heads <= 65535.
+ * ================================================================================================== */
+typedef enum kda_cache_dtype { KDA_CACHE_BF16 = 0, KDA_CACHE_FP4 = 1 } kda_cache_dtype;
+
+typedef struct kda_kv_params {
+    int32_t num_q_heads;        /* a multiple of num_kv_heads; query head h reads kv head
+                                   h / (num_q_heads / num_kv_heads); at most 128 per kv head */
+    int32_t num_kv_heads;
+    int32_t head_dim;           /* 64 or 128 */
+    int32_t page_size;          /* 16, 32, 64 or 128 tokens */
+    int32_t cache_dtype;        /* kda_cache_dtype; q, k, v and the outputs are bf16 */
+    int32_t rot_dim;            /* rotated channels per head: 0 (none) or a multiple of 32 up to head_dim */
+    int32_t rope_interleaved;   /* 0: channel i pairs with i + rot_dim / 2;  1: 2i with 2i + 1 */
+    int32_t window;             /* 0: every token up to a query's own is visible;
+                                   w > 0: token j is visible to position p if p - w < j <= p ... */
+    int32_t num_sinks;          /* ... or j < num_sinks (and j <= p) */
+    float softmax_scale;        /* <= 0 selects head_dim^{-1/2} */
+} kda_kv_params;
+
+/* Fill `p`: bf16 cache, rot_dim = head_dim in half style, no window, no sinks, default scale. */
+void kda_kv_params_init(kda_kv_params* p, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                        int32_t page_size);
+
+/*
+ * Append the new tokens' keys and values to the cache, with the position rotation applied on the way.
+ * With cos_i, sin_i = rope[position][i], rope[position][rot_dim / 2 + i], a rotated pair (x, y) becomes
+ * (x cos_i - y sin_i, y cos_i + x sin_i), rounded to bf16 (what a key in 4 bits is quantised from).
+ *   4 bits: s = e4m3(min(max|x| / 6, 448)) per 16 channels, code = e2m1(x / s), both to nearest, ties
+ *   to even, saturating; s = 0 gives zeros.  Non-finite values saturate.
+ *   q, q_out   [total_tokens][num_q_heads][head_dim]: the queries, rotated like the keys into q_out
+ *              (contiguous; may be q itself when q is contiguous).  Both NULL: keys and values only.
+ *   rope       device fp32 [rope_rows][rot_dim], cosines then sines; may be NULL when rot_dim = 0.
+ *              Entries of at most 16 significant bits make every product with a bf16 value exact.
+ *   positions  device int32 [total_tokens]: rotate by these instead of the positions in the cache;
+ *              or NULL.
+ * Slots of distinct requests must be distinct.  Padding tokens write nothing to the cache and zeros to
+ * q_out.  total_tokens = 0 or num_seqs = 0 is a no-op.
+ */
+int32_t kda_kv_append(const kda_kv_params* p,
+                      const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const void* v, int64_t v_stride,
+                      const float* rope, int64_t rope_rows, const int32_t* positions,
+                      const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table,
+                      int32_t num_seqs, int32_t max_pages, int64_t total_tokens,
+                      void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                      int64_t num_pages, void* q_out, kda_stream_t stream);
+
+/*
+ * Read tokens back from the cache as bf16 (exact for both cache types): k_out, v_out
+ * [total_tokens][num_kv_heads][head_dim] receive the last tokens of each request, as many as
+ * cu_seqlens gives it (with cu_seqlens = the cumulated kv_lens: everything it holds).  Padding rows and
+ * rows of bad pages are zeros.
+ */
+int32_t kda_kv_read(const kda_kv_params* p,
+                    const void* k_cache, const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                    int64_t num_pages,
+                    const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table,
+                    int32_t num_seqs, int32_t max_pages, int64_t total_tokens,
+                    void* k_out, void* v_out, kda_stream_t stream);
+
+/*
+ * Attention of the new tokens over the cache (the new tokens' own keys and values appended before):
+ *     s_j = softmax_scale * q . k_j over the visible tokens j,   o = sum_j softmax(s)_j v_j
+ *   out  [total_tokens][num_q_heads][head_dim] bf16
+ *   lse  [total_tokens][num_q_heads] fp32, log(sum_j exp(s_j)), for merging with attention over other
+ *        tokens; or NULL
+ * A query that sees no token (padding) gets zeros and lse = -infinity.  What masked and unwritten cache
+ * slots hold, NaN included, does not matter, with one exception: a non-finite VALUE that some query of a
+ * call may see can make the outputs of other queries of its request in that call non-finite.
+ *   max_new_tokens  host bound on the new tokens of any one request (1 when cu_seqlens is NULL)
+ *   max_kv_len      host bound on kv_lens; at most max_pages * page_size.  A tight bound means less
+ *                   workspace and better-sized work.
+ *   workspace       kda_paged_attention_workspace_size(...) bytes, 256-byte aligned, contents garbage
+ *                   before and after; may be NULL when that size is 0.  It must not be shared with a
+ *                   call that overlaps in time.
+ * Scores, softmax statistics and outputs are accumulated in fp32; the weights exp(s_j - max) enter the
+ * product with the values rounded to bf16 (4-bit cache: fp16).  Results do not depend on timing: the
+ * same call gives the same bits.
+ */
+size_t kda_paged_attention_workspace_size(const kda_kv_params* p, int32_t num_seqs, int64_t total_tokens,
+                                          int32_t max_new_tokens, int32_t max_kv_len);
+
+int32_t kda_paged_attention(const kda_kv_params* p,
+                            const void* q, int64_t q_stride,
+                            const void* k_cache, const void* v_cache,
+                            const uint8_t* k_scale, const uint8_t* v_scale, int64_t num_pages,
+                            const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table,
+                            int32_t num_seqs, int32_t max_pages, int64_t total_tokens,
+                            int32_t max_new_tokens, int32_t max_kv_len,
+                            void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
 /*
  * Synchronise `stream`, then read and clear the device error word that the kernels set when
  * they meet an out-of-range state_idx (code 1), a malformed cu_seqlens or a snapshot table too
  * small for it (code 2), a bounded wait inside a kernel that gave up (code 3; that call's
- * results are invalid), an accept_len outside [0, t_draft] (code 4) or a replay write_pos
- * outside [0, ring_len) (code 5).  *code receives
+ * results are invalid), an accept_len outside [0, t_draft] (code 4), a replay write_pos
+ * outside [0, ring_len) (code 5) or a bad table of the paged cache (codes 6 to 8, above).  *code receives
  * the first recorded code (0 when none) for the current device.  Returns KDA_OK when no error was
  * recorded, KDA_ERR_DEVICE_CHECK when one was, KDA_ERR_CUDA when the synchronisation failed.
  */

@@ -7,8 +7,10 @@ C ABI.  PyTorch supplies device memory and the current stream.  There is no fall
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -16,6 +18,7 @@ from . import build as _build
 
 KDA_OK = 0
 KDA_F32, KDA_BF16 = 0, 1
+CACHE_BF16, CACHE_FP4 = 0, 1
 GATE_PER_CHANNEL, GATE_PER_HEAD = 0, 1
 
 _STATUS = {
@@ -44,6 +47,22 @@ class Params(ctypes.Structure):
         ("scale", ctypes.c_float),
         ("l2_eps", ctypes.c_float),
         ("softplus_threshold", ctypes.c_float),
+    ]
+
+
+class KvParams(ctypes.Structure):
+    """Mirror of ``kda_kv_params``."""
+    _fields_ = [
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("cache_dtype", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("rope_interleaved", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("num_sinks", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
     ]
 
 
@@ -97,6 +116,18 @@ def lib() -> ctypes.CDLL:
         L.kda_check_device_errors.argtypes = [_P, ctypes.POINTER(ctypes.c_int32)]
         L.kda_selftest_wait_timeout.restype = ctypes.c_int32
         L.kda_selftest_wait_timeout.argtypes = [ctypes.c_uint32, _P, _P]
+        i32, i64 = ctypes.c_int32, ctypes.c_int64
+        KP, cache, batch = ctypes.POINTER(KvParams), [_P, _P, _P, _P], [_P, _P, _P, i32, i32, i64]
+        L.kda_kv_params_init.restype = None
+        L.kda_kv_params_init.argtypes = [KP, i32, i32, i32, i32]
+        L.kda_kv_append.restype = i32
+        L.kda_kv_append.argtypes = [KP, _P, i64, _P, i64, _P, i64, _P, i64, _P, *batch, *cache, i64, _P, _P]
+        L.kda_kv_read.restype = i32
+        L.kda_kv_read.argtypes = [KP, *cache, i64, *batch, _P, _P, _P]
+        L.kda_paged_attention_workspace_size.restype = ctypes.c_size_t
+        L.kda_paged_attention_workspace_size.argtypes = [KP, i32, i64, i32, i32]
+        L.kda_paged_attention.restype = i32
+        L.kda_paged_attention.argtypes = [KP, _P, i64, *cache, i64, *batch, i32, i32, _P, _P, _P, ctypes.c_size_t, _P]
         _lib = L
         return L
 
@@ -324,6 +355,231 @@ def commit_verified_states(inter, accept_len, state_pool, state_idx, *, params: 
                                           _ptr(state_pool), state_pool.shape[0], _ptr(state_idx), _stream(stream))
     _check(rc, "kda_commit_verified_states")
     return state_pool
+
+
+# ---- the paged key/value cache and its attention ------------------------------------------------------
+
+class KVCache(NamedTuple):
+    """A paged cache: ``k`` and ``v`` [pages, kv heads, page size, head_dim] bf16, or uint8 with two
+    4-bit channels a byte (last dimension head_dim / 2) and e4m3 scales [.., head_dim / 16].  Wherever
+    a cache is taken, a plain (k, v, k_scale, v_scale) tuple will do."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+
+def kv_cache(num_pages, num_kv_heads, page_size, head_dim, dtype="bf16", device="cuda") -> KVCache:
+    """Allocate a zeroed cache; ``dtype`` "bf16" or "fp4"."""
+    shape = (int(num_pages), int(num_kv_heads), int(page_size))
+    if dtype == "bf16":
+        k = torch.zeros(*shape, int(head_dim), dtype=torch.bfloat16, device=device)
+        return KVCache(k, torch.zeros_like(k))
+    if dtype != "fp4":
+        raise ValueError(f"dtype must be 'bf16' or 'fp4', got {dtype!r}")
+    k = torch.zeros(*shape, head_dim // 2, dtype=torch.uint8, device=device)
+    s = torch.zeros(*shape, head_dim // 16, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+    return KVCache(k, torch.zeros_like(k), s, s.clone())
+
+
+def rope_table(num_positions, rot_dim, theta=10000.0, device="cuda") -> torch.Tensor:
+    """Rotation table [num_positions, rot_dim] fp32 for :func:`kv_append`: cos(p f_i), then sin(p f_i),
+    f_i = theta^(-2i / rot_dim).  The angles are taken in fp64 and the entries kept to 16 significant
+    bits (off by at most 2^-16 relative, far below the 2^-8 of the bf16 result), so that a product with a
+    bf16 value is exact in fp32."""
+    f = float(theta) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(num_positions, dtype=torch.float64, device=device)[:, None] * f
+    m, e = torch.frexp(torch.cat([a.cos(), a.sin()], 1))
+    return torch.ldexp(torch.round(m * 65536.0), e - 16).float().contiguous()
+
+
+@functools.lru_cache(maxsize=256)
+def _kv_params(Hq, Hkv, D, page, fp4, rot=0, interleaved=False, window=0, sinks=0, scale=None):
+    p = KvParams(Hq, Hkv, D, page, CACHE_FP4 if fp4 else CACHE_BF16, rot, 1 if interleaved else 0, window, sinks,
+                 0.0 if scale is None else scale)
+    return ctypes.byref(p)
+
+
+def _kv_cache_args(cache):
+    """(kv heads, page size, head_dim, 4-bit?, k, v, k_scale and v_scale pointers, pages)."""
+    k, v, ks, vs = cache
+    _dev(k, "cache.k")
+    fp4 = k.dtype == torch.uint8
+    if not fp4 and k.dtype != torch.bfloat16:
+        raise TypeError(f"cache.k must be torch.bfloat16 or torch.uint8 (4 bits), got {k.dtype}")
+    _dev(v, "cache.v", k.dtype)
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError("cache.k and cache.v must be [pages, kv heads, page size, channels], of one shape")
+    pages, Hkv, page, D = k.shape
+    if not fp4:
+        return Hkv, page, D, False, k.data_ptr(), v.data_ptr(), None, None, pages
+    for name, t in (("cache.k_scale", ks), ("cache.v_scale", vs)):
+        if t is None:
+            raise ValueError(f"{name} is missing")
+        _dev(t, name)
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"{name} must be torch.float8_e4m3fn, got {t.dtype}")
+        if t.shape != (pages, Hkv, page, D // 8):
+            raise ValueError(f"{name} must be [pages, kv heads, page size, head_dim / 16]")
+    return Hkv, page, 2 * D, True, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages
+
+
+def _kv_batch(cu_seqlens, kv_lens, block_table, T):
+    """(cu_seqlens, kv_lens, block_table pointers, requests, pages per request, tokens)."""
+    _dev(kv_lens, "kv_lens", torch.int32)
+    _dev(block_table, "block_table", torch.int32)
+    n = kv_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table must be [requests, pages per request]")
+    if cu_seqlens is None:
+        if T != n:
+            raise ValueError("without cu_seqlens there is one token per request")
+        return None, kv_lens.data_ptr(), block_table.data_ptr(), n, block_table.shape[1], T
+    _dev(cu_seqlens, "cu_seqlens", torch.int32)
+    if cu_seqlens.shape[0] != n + 1:
+        raise ValueError("cu_seqlens must have one entry more than kv_lens")
+    return cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, block_table.shape[1], T
+
+
+def _rows(t, name, heads, D):
+    """Pointer and token stride of a bf16 [T, heads, D] tensor whose heads are contiguous (a slice of a
+    fused projection will do)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[1] * D
+    s = t.stride()
+    if s[2] != 1 or (s[1] != D and t.shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), s[0]
+
+
+def _raw_stream(stream, t):
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, *, q=None, q_out=None, rope=None,
+              interleaved=False, positions=None, stream=None):
+    """kda_kv_append: write the new tokens' keys and values ([T, kv heads, D] bf16) into the cache, the
+    keys rotated by the table ``rope`` ([positions, rot_dim], see :func:`rope_table`; None: no rotation).
+    With ``q`` ([T, q heads, D]) returns it rotated (into ``q_out``, which may be ``q``)."""
+    Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
+    kp, k_stride = _rows(k, "k", Hkv, D)
+    vp, v_stride = _rows(v, "v", Hkv, D)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same number of tokens")
+    batch = _kv_batch(cu_seqlens, kv_lens, block_table, T)
+    rot, rows, rp = 0, 0, None
+    if rope is not None:
+        _dev(rope, "rope", torch.float32)
+        if rope.dim() != 2:
+            raise ValueError("rope must be [positions, rot_dim]")
+        rows, rot = rope.shape
+        rp = rope.data_ptr()
+    if positions is not None:
+        _dev(positions, "positions", torch.int32)
+        if positions.shape != (T,):
+            raise ValueError("positions must hold one entry per token")
+        positions = positions.data_ptr()
+    Hq, qp, q_stride, qo = Hkv, None, 0, None
+    if q is not None:
+        qp, q_stride = _rows(q, "q", None, D)
+        Hq = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError("q and k must have the same number of tokens")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        else:
+            _dev(q_out, "q_out", torch.bfloat16)
+        qo = q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    p = _kv_params(Hq, Hkv, D, page, fp4, rot, interleaved)
+    _check(lib().kda_kv_append(p, qp, q_stride, kp, k_stride, vp, v_stride, rp, rows, positions, *batch, pk, pv, pks,
+                               pvs, pages, qo, _raw_stream(stream, k)), "kda_kv_append")
+    return q_out
+
+
+def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, out=None, stream=None):
+    """kda_kv_read: the last tokens of each request, as many as ``cu_seqlens`` gives it (None: one each),
+    as bf16 (k, v) [T, kv heads, D].  ``num_tokens`` = cu_seqlens[-1] is needed with ``cu_seqlens``."""
+    Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
+    T = kv_lens.shape[0] if cu_seqlens is None else num_tokens
+    if T is None:
+        raise ValueError("num_tokens is needed with cu_seqlens")
+    batch = _kv_batch(cu_seqlens, kv_lens, block_table, int(T))
+    if out is None:
+        out = tuple(torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=cache[0].device) for _ in range(2))
+    for name, t in (("out[0]", out[0]), ("out[1]", out[1])):
+        _dev(t, name, torch.bfloat16)
+        if t.shape != (T, Hkv, D):
+            raise ValueError(f"{name} must be [{T}, {Hkv}, {D}]")
+    p = _kv_params(Hkv, Hkv, D, page, fp4)
+    _check(lib().kda_kv_read(p, pk, pv, pks, pvs, pages, *batch, out[0].data_ptr(), out[1].data_ptr(),
+                             _raw_stream(stream, cache[0])), "kda_kv_read")
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(p, n, T, max_new, max_len):
+    return int(lib().kda_paged_attention_workspace_size(p, n, T, max_new, max_len))
+
+
+def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0, sinks=0, scale=None,
+                    max_new=None, max_len=None, out=None, lse=None, return_lse=False, workspace=None, stream=None):
+    """kda_paged_attention: ``q`` [T, q heads, D] bf16 over the cache; returns ``out`` (or ``(out, lse)``).
+
+    ``window`` 0: all tokens up to a query's own; w: the last w of them and the first ``sinks``.
+    ``max_new`` bounds the new tokens of a request (default: all T; 1 without ``cu_seqlens``), ``max_len``
+    bounds kv_lens (default: what block_table can hold): host numbers, the tighter the better."""
+    Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
+    qp, q_stride = _rows(q, "q", None, D)
+    T, Hq, _ = q.shape
+    batch = _kv_batch(cu_seqlens, kv_lens, block_table, T)
+    if max_new is None or cu_seqlens is None:
+        max_new = 1 if cu_seqlens is None else max(T, 1)
+    if max_len is None:
+        max_len = batch[4] * page
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _dev(out, "out", torch.bfloat16)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    if lse is not None:
+        _dev(lse, "lse", torch.float32)
+        if lse.shape != (T, Hq):
+            raise ValueError("lse must be [tokens, q heads]")
+    elif return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    p = _kv_params(Hq, Hkv, D, page, fp4, 0, False, int(window), int(sinks), scale)
+    need = _attention_workspace(p, batch[3], T, max_new, max_len)
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+    _check(lib().kda_paged_attention(p, qp, q_stride, pk, pv, pks, pvs, pages, *batch, max_new, max_len, out.data_ptr(),
+                                     None if lse is None else lse.data_ptr(),
+                                     None if workspace is None else workspace.data_ptr(),
+                                     0 if workspace is None else workspace.numel(), _raw_stream(stream, q)),
+           "kda_paged_attention")
+    return out if lse is None else (out, lse)
+
+
+def attention_workspace_size(num_q_heads, num_kv_heads, head_dim, page_size, num_seqs, num_tokens, max_new, max_len, *,
+                             dtype="bf16", window=0, sinks=0) -> int:
+    """Bytes of ``workspace`` that :func:`paged_attention` needs for these sizes (it allocates them itself
+    when none is given)."""
+    p = _kv_params(num_q_heads, num_kv_heads, head_dim, page_size, dtype == "fp4", 0, False, window, sinks)
+    return _attention_workspace(p, num_seqs, num_tokens, max_new, max_len)
 
 
 def selftest_wait_timeout(polls: int, result=None, stream=None) -> None:

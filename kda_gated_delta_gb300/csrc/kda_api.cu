@@ -7,6 +7,7 @@
 
 #include "kda.h"
 #include "kda_internal.cuh"
+#include "kda_kv.cuh"
 
 namespace {
 
@@ -98,7 +99,7 @@ const char* kda_status_string(int32_t status)
     case KDA_ERR_MISALIGNED: return "tensor pointer not 16-byte aligned";
     case KDA_ERR_WORKSPACE: return "workspace missing, too small or misaligned";
     case KDA_ERR_CUDA: return "CUDA runtime error";
-    case KDA_ERR_DEVICE_CHECK: return "a kernel recorded an error (bad state_idx, cu_seqlens, accept_len or write_pos, or a bounded wait that gave up)";
+    case KDA_ERR_DEVICE_CHECK: return "a kernel recorded an error (bad state_idx, cu_seqlens, accept_len, write_pos, page table or length, or a bounded wait that gave up)";
     case KDA_ERR_SCRATCH_LIMIT: return "problem needs more scratch than the library's fixed scratch array holds";
     default: return "unknown status";
     }
@@ -250,11 +251,13 @@ int32_t kda_check_device_errors(kda_stream_t stream, int32_t* code)
     if (!code) return KDA_ERR_INVALID_ARG;
     *code = 0;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return KDA_ERR_CUDA;
-    int32_t c1 = 0, c2 = 0, c3 = 0;
+    int32_t c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0;
     if (kda::recurrent_read_and_clear_error(&c1) != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::prefill_read_and_clear_error(&c2) != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::selftest_read_and_clear_error(&c3) != cudaSuccess) return KDA_ERR_CUDA;
-    *code = c1 ? c1 : (c2 ? c2 : c3);
+    if (kda::cache_read_and_clear_error(&c4) != cudaSuccess) return KDA_ERR_CUDA;
+    if (kda::attn_read_and_clear_error(&c5) != cudaSuccess) return KDA_ERR_CUDA;
+    *code = c1 ? c1 : c2 ? c2 : c3 ? c3 : c4 ? c4 : c5;
     return *code ? KDA_ERR_DEVICE_CHECK : KDA_OK;
 }
 
