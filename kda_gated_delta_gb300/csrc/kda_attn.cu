@@ -1,18 +1,544 @@
-// kda_attn.cu -- attention of new tokens over the paged cache (kda_paged_attention).
+// kda_attn.cu -- attention of new tokens over the paged cache (kda_paged_attention): the form for few
+// query rows (decode and short verifies), the joining of parts, and the dispatch.
 //
-// One warp per (token, query head): the lanes share the channels, the visible tokens are taken one at
-// a time with a running maximum and sum.
+// Few rows.  A kv head serves R = new tokens * G query rows.  For R <= 16 the cache's bytes are all that
+// counts (at 128 channels in bf16 a token's 512 bytes meet 4 * 128 * R flops), so the keys and values go
+// from global memory straight into the registers in which mma.sync m16n8k16 wants them, read once, and
+// nothing is staged in shared memory:
+//
+//   S^T = K Q^T     A = 16 tokens x 16 channels, B = Q^T with the query rows as the 8 columns
+//   O^T = V^T P^T   A = 16 channels x 16 tokens
+//
+// With the queries as the N = 8 side a tile computes 8 rows, not 16 of which most are padding, and the
+// accumulator of 128 channels takes 32 registers.  The order of the channels of a contraction and of the
+// rows of an output tile is free, so each lane's fragment is made of whole 16-byte loads (4-bit caches: 16
+// and 8) from the rows as they lie in the cache:
+//   K: lane (r, c) = (lane / 4, lane % 4) holds tokens r and r + 8, the c-th 16 bytes of each 64;
+//   V: it holds tokens 2c, 2c + 1, 2c + 8, 2c + 9, the r-th 16 bytes of each 128; two byte permutes make
+//      a register of one channel's two tokens.
+// P^T is made from S^T by movmatrix (a transposition of 8 x 8 across the warp).
+//
+// The softmax runs along the lanes' own tokens; a new maximum is taken over the warp only when some score
+// exceeds the current one by 8 in log2 (one vote), so that the common tile has no shuffles and no
+// rescaling.  The weights, at most 2^8 then, lose nothing by that in a floating-point format.
+//
+// A warp takes every fourth tile of its CTA's part, with the next tile's keys requested as soon as the
+// present ones are used and likewise the values.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kda_attn.cuh"
 #include "kda_internal.cuh"
-#include "kda_kv.cuh"
 
 namespace kda {
 namespace {
 
 __device__ int32_t g_attn_error = 0;
+
+using attn::Parts;
+using attn::Span;
+
+constexpr int kWarps = 4;
+constexpr float kSlack = 8.0f;      // growth of a maximum, in log2, that is let pass
+
+__device__ __forceinline__ uint4 ld16(const void* p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld8(const void* p)
+{
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld4(const void* p)
+{
+    uint32_t v;
+    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld2(const void* p)
+{
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld1(const void* p)
+{
+    uint32_t v;
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// D += A B, 16 x 8 x 16, fp32 accumulators; bf16 or fp16 operands.
+template <bool FP16>
+__device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if constexpr (FP16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t y;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+// Eight codes (one word) as four fp16 pairs.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* o)
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+}
+
+// One warp's keys or values of TB x 16 tokens, as loaded.
+template <int D, bool FP4, int TB>
+struct KeyTile {
+    static constexpr int kWords = FP4 ? D / 32 : D / 8;     // of one token, per lane
+    uint32_t w[TB][2][kWords];
+    uint32_t s[TB][2];                                        // 4 bits: the lane's scales
+
+    // row: cache row of token 0 of the 16; the lane reads tokens r and r + 8
+    __device__ __forceinline__ void load(int tb, const uint8_t* k, const uint8_t* ks, int64_t row, int r, int c)
+    {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int64_t t = row + r + 8 * e;
+            if constexpr (!FP4) {
+                const uint8_t* p = k + t * (2 * D) + c * 16;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 x = ld16(p + 64 * i);
+                    w[tb][e][4 * i] = x.x, w[tb][e][4 * i + 1] = x.y, w[tb][e][4 * i + 2] = x.z, w[tb][e][4 * i + 3] = x.w;
+                }
+            } else if constexpr (D == 128) {
+                const uint4 x = ld16(k + t * 64 + c * 16);
+                w[tb][e][0] = x.x, w[tb][e][1] = x.y, w[tb][e][2] = x.z, w[tb][e][3] = x.w;
+                s[tb][e] = ld2(ks + t * 8 + 2 * c);
+            } else {
+                const uint2 x = ld8(k + t * 32 + c * 8);
+                w[tb][e][0] = x.x, w[tb][e][1] = x.y;
+                s[tb][e] = ld1(ks + t * 4 + c);
+            }
+        }
+    }
+};
+
+template <int D, bool FP4, int TB>
+struct ValueTile {
+    static constexpr int kWords = FP4 ? D / 64 : D / 16;
+    uint32_t w[TB][4][kWords];
+    uint32_t s[TB][4];
+
+    // the lane reads tokens 2c, 2c + 1, 2c + 8, 2c + 9; those not in [lo, hi) or [0, sink_end) become zeros
+    __device__ __forceinline__ void load(int tb, const uint8_t* v, const uint8_t* vs, int64_t row, int base, const Span& sp, int r, int c)
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int o = 2 * c + (e & 1) + 8 * (e >> 1);
+            const int64_t t = row + o;
+            const int j = base + o;
+            const bool on = row >= 0 && j < sp.hi && (j >= sp.lo || j < sp.sink_end);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[tb][e][i] = 0;
+            s[tb][e] = 0;
+            if (!on) continue;
+            if constexpr (!FP4) {
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const uint4 x = ld16(v + t * (2 * D) + r * 16 + 128 * i);
+                    w[tb][e][4 * i] = x.x, w[tb][e][4 * i + 1] = x.y, w[tb][e][4 * i + 2] = x.z, w[tb][e][4 * i + 3] = x.w;
+                }
+            } else if constexpr (D == 128) {
+                const uint2 x = ld8(v + t * 64 + r * 8);
+                w[tb][e][0] = x.x, w[tb][e][1] = x.y;
+                s[tb][e] = ld1(vs + t * 8 + r);
+            } else {
+                w[tb][e][0] = ld4(v + t * 32 + r * 4);
+                s[tb][e] = ld1(vs + t * 4 + r / 2);
+            }
+        }
+    }
+};
+
+// First row of the page of a token's 16-token block, -1 where the table holds none (recorded).
+__device__ __forceinline__ int64_t block_row(const AttnCall& a, int b, int base, int h)
+{
+    const int64_t slot = kv::token_slot(a.c, b, base);
+    return slot < 0 ? -1 : slot + ((int64_t)h << a.c.page_shift);
+}
+
+template <int D, bool FP4, int NT, int TB>
+__global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts parts)
+{
+    a.c.err = &g_attn_error;
+    constexpr int kTile = 16 * TB;
+    constexpr int KS = D / 16;                                  // contraction steps over the channels
+    constexpr int MT = D / 16;                                  // 16-channel output tiles
+    const int h = blockIdx.x % a.c.Hkv, b = blockIdx.x / a.c.Hkv, part = blockIdx.y;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+    const int G = a.c.G;
+
+    int64_t t0, t1;
+    kv::request_rows(a.c, b, t0, t1);
+    const int len = a.c.lens[b];
+    const int fresh = (int)(t1 - t0);
+    const int rows = min(fresh * G, 8 * NT);                     // rows past the caller's bound are left out
+    if (rows == 0) return;
+    const int64_t room = a.max_len;
+    if (threadIdx.x == 0 && part == 0 && h == 0 && (len > room || fresh > a.max_new)) kv::record(a.c, kv::kErrLength);
+    const int first = len > 0 ? len - fresh : -1 - fresh;          // position of the first new token; a padding request has none
+    const Span sp = attn::make_span<kTile>(max(first, 0), len > 0 ? len - 1 : -1, room, a.window, a.sinks);
+    const int parts_here = parts.o ? max(1, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part) : 1;
+    if (part >= parts_here) return;
+    const int tile_lo = parts_here > 1 ? part * parts.tiles_per_part : 0;
+    const int tile_hi = parts_here > 1 ? min(sp.tiles, tile_lo + parts.tiles_per_part) : sp.tiles;
+
+    // ---- queries: B fragments in the channel order of the key loads -------------------------------------
+    uint32_t q[NT][KS][2];
+    float unit[NT][2];                                              // scores to log2, per column
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int row = nt * 8 + r;
+        uint32_t w[D / 8];                                        // the lane's D / 4 channels of its row
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = 0;
+        if (row < rows) {
+            const uint8_t* p = reinterpret_cast<const uint8_t*>(a.q) + ((t0 + row / G) * a.q_stride + (int64_t)(h * G + row % G) * D) * 2;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4*>(p + (FP4 ? c * (D / 2) + 16 * i : c * 16 + 64 * i));
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            }
+        }
+        unit[nt][0] = unit[nt][1] = a.scale * attn::kLog2e;
+        if constexpr (FP4) {
+            // fp16 operands: the row is divided by a power of two near its largest magnitude, which keeps
+            // every element's bf16 bits down to 2^-14 of the largest; the power goes back into the scores
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+            top = max(top, __shfl_xor_sync(~0u, top, 1));
+            top = max(top, __shfl_xor_sync(~0u, top, 2));
+            const int e = min(max((int)(top >> 7), 1), 253);          // biased exponent
+            const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const float2 f = kv::bf16x2_to_f32(w[i]);
+                w[i] = kv::f32_to_f16x2(f.x * down, f.y * down);
+            }
+            unit[nt][0] *= __shfl_sync(~0u, up, 8 * c);
+            unit[nt][1] *= __shfl_sync(~0u, up, 8 * c + 4);
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s) q[nt][s][0] = w[2 * s], q[nt][s][1] = w[2 * s + 1];
+    }
+    int pos[NT][2];                                                 // positions of the lane's two columns
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) pos[nt][i] = first + (nt * 8 + 2 * c + i) / G;
+    const int last = len - 1;
+
+    float o[NT][MT][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.f;
+    }
+
+    KeyTile<D, FP4, TB> kt;
+    ValueTile<D, FP4, TB> vt;
+    int64_t row_of[TB], next_row[TB];
+    int i = tile_lo + warp;
+    const auto rows_of = [&](int tile, int64_t* out) {
+        const int base = attn::tile_base<kTile>(sp, tile);
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+            const int j = base + 16 * tb;                             // only pages that hold a visible token are looked up
+            const bool needed = j < sp.hi && (j + 16 > sp.lo || j < sp.sink_end);
+            out[tb] = needed ? block_row(a, b, j, h) : -1;
+        }
+    };
+    const auto load_keys = [&](const int64_t* at) {
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb)
+            if (at[tb] >= 0) kt.load(tb, a.c.k, a.c.ks, at[tb], r, c);
+    };
+    const auto load_values = [&](int tile, const int64_t* at) {
+        const int base = attn::tile_base<kTile>(sp, tile);
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) vt.load(tb, a.c.v, a.c.vs, at[tb], base + 16 * tb, sp, r, c);
+    };
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            kt.s[tb][e] = 0;
+#pragma unroll
+            for (int x = 0; x < KeyTile<D, FP4, TB>::kWords; ++x) kt.w[tb][e][x] = 0;
+        }
+    if (i < tile_hi) {
+        rows_of(i, row_of);
+        load_keys(row_of);
+        load_values(i, row_of);
+        if (i + kWarps < tile_hi) rows_of(i + kWarps, next_row);
+    }
+    for (; i < tile_hi; i += kWarps) {
+        const int base = attn::tile_base<kTile>(sp, i);
+        const bool more = i + kWarps < tile_hi;
+        // ---- S^T ---------------------------------------------------------------------------------------
+        float s[NT][TB][4];
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[nt][tb][0] = s[nt][tb][1] = s[nt][tb][2] = s[nt][tb][3] = 0.f;
+            if constexpr (!FP4) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma<false>(s[nt][tb], kt.w[tb][0][2 * k], kt.w[tb][1][2 * k], kt.w[tb][0][2 * k + 1], kt.w[tb][1][2 * k + 1],
+                                   q[nt][k][0], q[nt][k][1]);
+            } else {
+                const uint32_t s0 = kv::e4m3x2_to_f16x2(kt.s[tb][0]), s1 = kv::e4m3x2_to_f16x2(kt.s[tb][1]);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    const uint32_t pick = (D == 128 && j >= 2) ? 0x3232u : 0x1010u;
+                    const uint32_t f0 = __byte_perm(s0, 0, pick), f1 = __byte_perm(s1, 0, pick);
+                    uint32_t x[4], y[4];
+                    e2m1x8_to_f16(kt.w[tb][0][j], x);
+                    e2m1x8_to_f16(kt.w[tb][1][j], y);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) x[z] = mul_f16x2(x[z], f0), y[z] = mul_f16x2(y[z], f1);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma<true>(s[nt][tb], x[2 * z], y[2 * z], x[2 * z + 1], y[2 * z + 1], q[nt][2 * j + z][0], q[nt][2 * j + z][1]);
+                }
+            }
+        }
+        bool whole = base + kTile - 1 <= first && (a.window == 0 || base > last - a.window || base + kTile <= a.sinks);
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) whole = whole && row_of[tb] >= 0;
+        uint32_t dead = 0;                                           // blocks of bad pages
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) dead |= row_of[tb] < 0 ? 1u << tb : 0u;
+        if (more) {
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) row_of[tb] = next_row[tb];
+            load_keys(row_of);
+            if (i + 2 * kWarps < tile_hi) rows_of(i + 2 * kWarps, next_row);
+        }
+        // ---- softmax -------------------------------------------------------------------------------------
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[nt][tb][e] *= unit[nt][e & 1];
+        if (!whole) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = base + 16 * tb + r + 8 * (e >> 1), p = pos[nt][e & 1];
+                        const bool on = j <= p && j < sp.hi && (a.window == 0 || j > p - a.window || j < a.sinks) && !(dead >> tb & 1u);
+                        if (!on) s[nt][tb][e] = -INFINITY;
+                    }
+        }
+        float top[NT][2];
+        bool grown = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = fmaxf(s[nt][0][e], s[nt][0][e + 2]);
+#pragma unroll
+                for (int tb = 1; tb < TB; ++tb) x = fmaxf(x, fmaxf(s[nt][tb][e], s[nt][tb][e + 2]));
+                top[nt][e] = x;
+                grown = grown || x > m[nt][e] + kSlack;
+            }
+        if (__any_sync(~0u, grown)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = fmaxf(top[nt][e], m[nt][e]);
+                    x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                    const float f = m[nt][e] == -INFINITY ? 0.f : attn::ex2(m[nt][e] - x);
+                    m[nt][e] = x;
+                    l[nt][e] *= f;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) o[nt][mt][e] *= f, o[nt][mt][e + 2] *= f;
+                }
+        }
+        // ---- P^T, O^T += V^T P^T -----------------------------------------------------------------------------
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                const float e0 = attn::ex2(s[nt][tb][0] - m0), e1 = attn::ex2(s[nt][tb][1] - m1);
+                const float e2 = attn::ex2(s[nt][tb][2] - m0), e3 = attn::ex2(s[nt][tb][3] - m1);
+                l[nt][0] += e0 + e2;
+                l[nt][1] += e1 + e3;
+                p[nt][0] = transpose8x8(FP4 ? kv::f32_to_f16x2(e0, e1) : kv::f32_to_bf16x2(e0, e1));
+                p[nt][1] = transpose8x8(FP4 ? kv::f32_to_f16x2(e2, e3) : kv::f32_to_bf16x2(e2, e3));
+            }
+            if constexpr (!FP4) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const uint32_t a0 = __byte_perm(vt.w[tb][0][mt], vt.w[tb][1][mt], 0x5410), a1 = __byte_perm(vt.w[tb][0][mt], vt.w[tb][1][mt], 0x7632);
+                    const uint32_t a2 = __byte_perm(vt.w[tb][2][mt], vt.w[tb][3][mt], 0x5410), a3 = __byte_perm(vt.w[tb][2][mt], vt.w[tb][3][mt], 0x7632);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt][mt], a0, a1, a2, a3, p[nt][0], p[nt][1]);
+                }
+            } else {
+                // the scales of the lane's token pairs, as the two halves of a register
+                uint32_t s01 = kv::e4m3x2_to_f16x2(vt.s[tb][0] | vt.s[tb][1] << 8), s23 = kv::e4m3x2_to_f16x2(vt.s[tb][2] | vt.s[tb][3] << 8);
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                    uint32_t x[4][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) e2m1x8_to_f16(vt.w[tb][e][j], x[e]);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint32_t a0 = mul_f16x2(__byte_perm(x[0][z], x[1][z], 0x5410), s01), a1 = mul_f16x2(__byte_perm(x[0][z], x[1][z], 0x7632), s01);
+                        const uint32_t a2 = mul_f16x2(__byte_perm(x[2][z], x[3][z], 0x5410), s23), a3 = mul_f16x2(__byte_perm(x[2][z], x[3][z], 0x7632), s23);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma<true>(o[nt][4 * j + z], a0, a1, a2, a3, p[nt][0], p[nt][1]);
+                    }
+                }
+            }
+        }
+        if (more) load_values(i + kWarps, row_of);
+    }
+
+    // ---- join the four warps ------------------------------------------------------------------------------
+    constexpr int N = 8 * NT, kPad = D + 4;
+    __shared__ float sm_m[kWarps][N], sm_l[kWarps][N];
+    extern __shared__ float sm_o[];                                   // [warps][rows][kPad]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x = l[nt][e];
+            x += __shfl_xor_sync(~0u, x, 4);
+            x += __shfl_xor_sync(~0u, x, 8);
+            x += __shfl_xor_sync(~0u, x, 16);
+            const int row = nt * 8 + 2 * c + e;
+            if (r == 0) sm_m[warp][row] = m[nt][e], sm_l[warp][row] = x;
+            if (row < rows) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    // channel of (tile, half) in the order of the value loads
+                    const int d = FP4 ? r * (D / 8) + 2 * mt : r * 8 + 64 * (mt / 4) + 2 * (mt % 4);
+                    *reinterpret_cast<float2*>(&sm_o[(warp * N + row) * kPad + d]) = make_float2(o[nt][mt][e], o[nt][mt][e + 2]);
+                }
+            }
+        }
+    __syncthreads();
+    for (int x = threadIdx.x; x < rows * (D / 4); x += kWarps * 32) {
+        const int row = x / (D / 4), d = x % (D / 4) * 4;
+        float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][row]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = sm_m[w][row] == -INFINITY ? 0.f : attn::ex2(sm_m[w][row] - mx);
+            sum += f * sm_l[w][row];
+            const float4 y = *reinterpret_cast<const float4*>(&sm_o[(w * N + row) * kPad + d]);
+            acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
+        }
+        // a warp that saw nothing, or nothing but NaN, has no maximum; NaN reaches the sum through l
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            if (sm_l[w][row] != sm_l[w][row]) sum = acc.x = acc.y = acc.z = acc.w = sm_l[w][row];
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t out_row = (t0 + row / G) * a.c.Hq + h * G + row % G;
+        const float lse2 = sum == 0.f ? -INFINITY : mx + attn::lg2(sum);
+        if (parts_here > 1) {
+            const int64_t at = out_row * parts.max_parts + part;
+            *reinterpret_cast<float4*>(parts.o + at * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (d == 0) parts.lse2[at] = lse2;
+        } else {
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + out_row * D + d) =
+                make_uint2(kv::f32_to_bf16x2(acc.x * inv, acc.y * inv), kv::f32_to_bf16x2(acc.z * inv, acc.w * inv));
+            if (a.lse && d == 0) a.lse[out_row] = lse2 * attn::kLn2;
+        }
+    }
+}
+
+// Joins the parts of each row that has several: a warp per row, D / 32 channels a lane.
+template <int D, int kTile>
+__global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts)
+{
+    a.c.err = &g_attn_error;
+    constexpr int N = D / 32;
+    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (row >= a.c.T * a.c.Hq) return;
+    int b;
+    int64_t pos;
+    const int64_t t = row / a.c.Hq;
+    if (!kv::token_place(a.c, t, b, pos)) return;                     // padding: written by the first part
+    int64_t t0, t1;
+    kv::request_rows(a.c, b, t0, t1);
+    const int len = a.c.lens[b];
+    const int64_t first = len - (t1 - t0);
+    const Span sp = attn::make_span<kTile>(first > 0 ? first : 0, len - 1, a.max_len, a.window, a.sinks);
+    const int n = (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part;
+    if (n <= 1) return;
+    const float* lse = parts.lse2 + row * parts.max_parts;
+    const float* src = parts.o + row * parts.max_parts * D + lane * N;
+    float mx = -INFINITY, sum = 0.f, o[N] = {};
+    for (int i = lane; i < n; i += 32) mx = fmaxf(mx, lse[i]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+    if (mx == -INFINITY) mx = 0.f;                                    // nothing seen, or NaN (which the weights carry on)
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float w = attn::ex2(lse[i] - mx);
+        sum += w;
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] += w * src[(int64_t)i * D + j];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + row * D + lane * N;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = kv::f32_to_bf16x2(o[j] * inv, o[j + 1] * inv);
+    if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + attn::lg2(sum)) * attn::kLn2;
+}
 
 template <int D, bool FP4>
 __device__ __forceinline__ void load_row(const uint8_t* base, const uint8_t* scales, int64_t row, int lane, float* x)
@@ -87,20 +613,98 @@ __global__ void __launch_bounds__(128) attention_kernel(AttnCall a)
 
 }  // namespace
 
-size_t attention_workspace_bytes(const kda_kv_params&, int32_t, int64_t, int32_t, int32_t) { return 0; }
+namespace {
 
-cudaError_t launch_attention(const kda_kv_params& p, const AttnCall& a, void*, cudaStream_t stream)
+constexpr int kFewRows = 16;
+
+// How a call of the few-rows form is cut along the cache.  An uncut call has one CTA per (request, kv
+// head).  The cut aims at kCtas CTAs for the longest histories the caller's bound allows, in parts of at
+// least kMinPart tokens.
+constexpr int kFewTile(bool fp4) { return fp4 ? 32 : 16; }
+constexpr int64_t kCtas = 2048;
+constexpr int kMinPart = 256;
+
+struct Cut {
+    int32_t parts, tiles_per_part;
+};
+
+Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t max_len)
 {
-    const int64_t blocks = (a.c.T * a.c.Hq + 3) / 4;
-    const bool fp4 = p.cache_dtype == KDA_CACHE_FP4;
-    if (p.head_dim == 128) {
-        if (fp4) attention_kernel<128, true><<<(unsigned)blocks, 128, 0, stream>>>(a);
-        else attention_kernel<128, false><<<(unsigned)blocks, 128, 0, stream>>>(a);
-    } else {
-        if (fp4) attention_kernel<64, true><<<(unsigned)blocks, 128, 0, stream>>>(a);
-        else attention_kernel<64, false><<<(unsigned)blocks, 128, 0, stream>>>(a);
+    const int tile = kFewTile(p.cache_dtype == KDA_CACHE_FP4);
+    int64_t tokens = max_len;
+    if (p.window) {
+        const int64_t seen = (int64_t)p.window + max_new + p.num_sinks + 3 * tile;   // both runs, rounded out to tiles
+        if (seen < tokens) tokens = seen;
     }
+    const int64_t tiles = (tokens + tile - 1) / tile;
+    const int64_t ctas = (int64_t)n * p.num_kv_heads;
+    int64_t parts = (kCtas + ctas - 1) / ctas;
+    const int64_t most = tokens / kMinPart;
+    if (parts > most) parts = most;
+    if (parts > 256) parts = 256;
+    if (parts < 1) parts = 1;
+    Cut c;
+    c.tiles_per_part = (int32_t)((tiles + parts - 1) / parts);
+    c.parts = (int32_t)((tiles + c.tiles_per_part - 1) / c.tiles_per_part);
+    return c;
+}
+
+size_t parts_bytes(const kda_kv_params& p, int64_t T, int32_t parts)
+{
+    return (size_t)T * p.num_q_heads * parts * (p.head_dim + 1) * 4 + 256;
+}
+
+Parts make_parts(const kda_kv_params& p, int64_t T, const Cut& c, void* workspace)
+{
+    Parts x;
+    x.max_parts = c.parts;
+    x.tiles_per_part = c.tiles_per_part;
+    x.o = c.parts > 1 ? (float*)workspace : nullptr;
+    x.lse2 = c.parts > 1 ? (float*)workspace + (size_t)T * p.num_q_heads * c.parts * p.head_dim : nullptr;
+    return x;
+}
+
+template <int D, bool FP4, int NT>
+cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const Cut& cut, void* workspace, cudaStream_t stream)
+{
+    constexpr int TB = kFewTile(FP4) / 16;
+    const Parts parts = make_parts(p, a.c.T, cut, workspace);
+    const size_t smem = (size_t)kWarps * 8 * NT * (D + 4) * 4;
+    few_rows_kernel<D, FP4, NT, TB><<<dim3((unsigned)(a.c.n * a.c.Hkv), (unsigned)cut.parts), kWarps * 32, smem, stream>>>(a, parts);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || cut.parts == 1) return e;
+    join_kernel<D, 16 * TB><<<(unsigned)((a.c.T * a.c.Hq + 3) / 4), 128, 0, stream>>>(a, parts);
     return cudaGetLastError();
+}
+
+template <int D, bool FP4>
+cudaError_t launch_typed(const kda_kv_params& p, const AttnCall& a, void* workspace, cudaStream_t stream)
+{
+    const int rows = a.max_new * a.c.G;
+    if (rows <= kFewRows) {
+        const Cut cut = cut_few(p, a.c.n, a.max_new, a.max_len);
+        return rows <= 8 ? launch_few<D, FP4, 1>(p, a, cut, workspace, stream) : launch_few<D, FP4, 2>(p, a, cut, workspace, stream);
+    }
+    attention_kernel<D, FP4><<<(unsigned)((a.c.T * a.c.Hq + 3) / 4), 128, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attention_workspace_bytes(const kda_kv_params& p, int32_t num_seqs, int64_t total_tokens, int32_t max_new,
+                                 int32_t max_len)
+{
+    const int64_t rows = (int64_t)max_new * (p.num_q_heads / p.num_kv_heads);
+    if (rows > kFewRows) return 0;
+    const Cut cut = cut_few(p, num_seqs, max_new, max_len);
+    return cut.parts > 1 ? parts_bytes(p, total_tokens, cut.parts) : 0;
+}
+
+cudaError_t launch_attention(const kda_kv_params& p, const AttnCall& a, void* workspace, cudaStream_t stream)
+{
+    const bool fp4 = p.cache_dtype == KDA_CACHE_FP4;
+    if (p.head_dim == 128) return fp4 ? launch_typed<128, true>(p, a, workspace, stream) : launch_typed<128, false>(p, a, workspace, stream);
+    return fp4 ? launch_typed<64, true>(p, a, workspace, stream) : launch_typed<64, false>(p, a, workspace, stream);
 }
 
 cudaError_t attn_read_and_clear_error(int32_t* code)

@@ -143,6 +143,13 @@ __device__ __forceinline__ uint32_t f32_to_bf16x2(float lo, float hi)
     return r;
 }
 
+__device__ __forceinline__ uint32_t f32_to_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 }  // namespace kv
 
 // ---- launchers (kda_cache.cu, kda_attn.cu) --------------------------------------------------------------
