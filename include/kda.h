@@ -320,7 +320,8 @@ int32_t kda_chunk_prefill_static_scratch(const kda_params* p,
  *           show it)
  *   code 6  a page index outside [0, num_pages)
  *   code 7  a position outside the rotation table
- *   code 8  kv_lens[b] > max_pages * page_size, or > max_kv_len (attention)
+ *   code 8  kv_lens[b] > max_pages * page_size; attention: kv_lens[b] > max_kv_len, or more new tokens than
+ *           max_new_tokens (whose outputs are then unspecified)
  * The rows of q, k and v may be strided: *_stride is the distance between tokens in elements (the
  * heads of a token are contiguous), a multiple of 8.  Tensor pointers are 16-byte aligned.
  * Limits (KDA_ERR_UNSUPPORTED beyond them): total_tokens < 2^22, num_pages * num_kv_heads * page_size
@@ -400,7 +401,7 @@ int32_t kda_kv_read(const kda_kv_params* p,
  *                   before and after; may be NULL when that size is 0.  It must not be shared with a
  *                   call that overlaps in time.
  * Scores, softmax statistics and outputs are accumulated in fp32; the weights exp(s_j - max) enter the
- * product with the values rounded to bf16 (4-bit cache: fp16).  Results do not depend on timing: the
+ * product with the values rounded to bf16.  Results do not depend on timing: the
  * same call gives the same bits.
  */
 size_t kda_paged_attention_workspace_size(const kda_kv_params* p, int32_t num_seqs, int64_t total_tokens,

@@ -16,6 +16,8 @@
 //   K: lane (r, c) = (lane / 4, lane % 4) holds tokens r and r + 8, the c-th 16 bytes of each 64;
 //   V: it holds tokens 2c, 2c + 1, 2c + 8, 2c + 9, the r-th 16 bytes of each 128; two byte permutes make
 //      a register of one channel's two tokens.
+// 4-bit values go to bf16 instead, with the weights, which need its range: a weight far below the largest
+// still counts in a channel where the heavy tokens hold zeros.
 // P^T is made from S^T by movmatrix (a transposition of 8 x 8 across the warp).
 //
 // The softmax runs along the lanes' own tokens; a new maximum is taken over the warp only when some score
@@ -91,21 +93,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t y;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-    return y;
-}
-// Eight codes (one word) as four fp16 pairs.
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* o)
-{
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-        : "r"(w));
 }
 
 // One warp's keys or values of TB x 16 tokens, as loaded.
@@ -206,7 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     if (threadIdx.x == 0 && part == 0 && h == 0 && (len > room || fresh > a.max_new)) kv::record(a.c, kv::kErrLength);
     const int first = len > 0 ? len - fresh : -1 - fresh;          // position of the first new token; a padding request has none
     const Span sp = attn::make_span<kTile>(max(first, 0), len > 0 ? len - 1 : -1, room, a.window, a.sinks);
-    const int parts_here = parts.o ? max(1, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part) : 1;
+    const int parts_here = parts.o ? min(parts.max_parts, max(1, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part)) : 1;
     if (part >= parts_here) return;
     const int tile_lo = parts_here > 1 ? part * parts.tiles_per_part : 0;
     const int tile_hi = parts_here > 1 ? min(sp.tiles, tile_lo + parts.tiles_per_part) : sp.tiles;
@@ -230,8 +217,9 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
         }
         unit[nt][0] = unit[nt][1] = a.scale * attn::kLog2e;
         if constexpr (FP4) {
-            // fp16 operands: the row is divided by a power of two near its largest magnitude, which keeps
-            // every element's bf16 bits down to 2^-14 of the largest; the power goes back into the scores
+            // 4-bit keys meet the queries in fp16, where they convert in one instruction a pair: a query row
+            // is divided by a power of two near its largest magnitude, which keeps every element's bf16
+            // bits down to 2^-14 of the largest; the power goes back into the scores
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
@@ -329,10 +317,10 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
                     const uint32_t pick = (D == 128 && j >= 2) ? 0x3232u : 0x1010u;
                     const uint32_t f0 = __byte_perm(s0, 0, pick), f1 = __byte_perm(s1, 0, pick);
                     uint32_t x[4], y[4];
-                    e2m1x8_to_f16(kt.w[tb][0][j], x);
-                    e2m1x8_to_f16(kt.w[tb][1][j], y);
+                    kv::e2m1x8_to_f16(kt.w[tb][0][j], x);
+                    kv::e2m1x8_to_f16(kt.w[tb][1][j], y);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) x[z] = mul_f16x2(x[z], f0), y[z] = mul_f16x2(y[z], f1);
+                    for (int z = 0; z < 4; ++z) x[z] = kv::mul_f16x2(x[z], f0), y[z] = kv::mul_f16x2(y[z], f1);
 #pragma unroll
                     for (int z = 0; z < 2; ++z)
 #pragma unroll
@@ -411,8 +399,8 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
                 const float e2 = attn::ex2(s[nt][tb][2] - m0), e3 = attn::ex2(s[nt][tb][3] - m1);
                 l[nt][0] += e0 + e2;
                 l[nt][1] += e1 + e3;
-                p[nt][0] = transpose8x8(FP4 ? kv::f32_to_f16x2(e0, e1) : kv::f32_to_bf16x2(e0, e1));
-                p[nt][1] = transpose8x8(FP4 ? kv::f32_to_f16x2(e2, e3) : kv::f32_to_bf16x2(e2, e3));
+                p[nt][0] = transpose8x8(kv::f32_to_bf16x2(e0, e1));
+                p[nt][1] = transpose8x8(kv::f32_to_bf16x2(e2, e3));
             }
             if constexpr (!FP4) {
 #pragma unroll
@@ -424,20 +412,26 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
                 }
             } else {
                 // the scales of the lane's token pairs, as the two halves of a register
-                uint32_t s01 = kv::e4m3x2_to_f16x2(vt.s[tb][0] | vt.s[tb][1] << 8), s23 = kv::e4m3x2_to_f16x2(vt.s[tb][2] | vt.s[tb][3] << 8);
+                const float2 f01 = kv::f16x2_to_f32(kv::e4m3x2_to_f16x2(vt.s[tb][0] | vt.s[tb][1] << 8));
+                const float2 f23 = kv::f16x2_to_f32(kv::e4m3x2_to_f16x2(vt.s[tb][2] | vt.s[tb][3] << 8));
+                const uint32_t s01 = kv::f32_to_bf16x2(f01.x * kv::kBf16Up, f01.y * kv::kBf16Up);
+                const uint32_t s23 = kv::f32_to_bf16x2(f23.x * kv::kBf16Up, f23.y * kv::kBf16Up);
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j) {
-                    uint32_t x[4][4];
+                for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) e2m1x8_to_f16(vt.w[tb][e][j], x[e]);
+                    for (int half = 0; half < 2; ++half) {             // channels 0..3 and 4..7 of the words
+                        const uint32_t pick = half ? 0x7632u : 0x5410u;
+                        uint32_t x[4], y[4];
+                        kv::e2m1_columns_to_bf16(__byte_perm(vt.w[tb][0][j], vt.w[tb][1][j], pick), x);
+                        kv::e2m1_columns_to_bf16(__byte_perm(vt.w[tb][2][j], vt.w[tb][3][j], pick), y);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const uint32_t a0 = mul_f16x2(__byte_perm(x[0][z], x[1][z], 0x5410), s01), a1 = mul_f16x2(__byte_perm(x[0][z], x[1][z], 0x7632), s01);
-                        const uint32_t a2 = mul_f16x2(__byte_perm(x[2][z], x[3][z], 0x5410), s23), a3 = mul_f16x2(__byte_perm(x[2][z], x[3][z], 0x7632), s23);
+                        for (int z = 0; z < 4; ++z) x[z] = kv::mul_bf16x2(x[z], s01), y[z] = kv::mul_bf16x2(y[z], s23);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma<true>(o[nt][4 * j + z], a0, a1, a2, a3, p[nt][0], p[nt][1]);
+                        for (int z = 0; z < 2; ++z)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma<false>(o[nt][4 * j + 2 * half + z], x[2 * z], x[2 * z + 1], y[2 * z], y[2 * z + 1], p[nt][0], p[nt][1]);
                     }
-                }
             }
         }
         if (more) load_values(i + kWarps, row_of);
@@ -484,7 +478,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             if (sm_l[w][row] != sm_l[w][row]) sum = acc.x = acc.y = acc.z = acc.w = sm_l[w][row];
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = sum == 0.f ? 0.f : (FP4 ? kv::kBf16Rest : 1.f) / sum;
         const int64_t out_row = (t0 + row / G) * a.c.Hq + h * G + row % G;
         const float lse2 = sum == 0.f ? -INFINITY : mx + attn::lg2(sum);
         if (parts_here > 1) {
@@ -499,12 +493,11 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     }
 }
 
-// Joins the parts of each row that has several: a warp per row, D / 32 channels a lane.
+// Joins the parts of each row that has several: a warp per row.
 template <int D, int kTile>
 __global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts)
 {
     a.c.err = &g_attn_error;
-    constexpr int N = D / 32;
     const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     if (row >= a.c.T * a.c.Hq) return;
@@ -517,98 +510,8 @@ __global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts)
     const int len = a.c.lens[b];
     const int64_t first = len - (t1 - t0);
     const Span sp = attn::make_span<kTile>(first > 0 ? first : 0, len - 1, a.max_len, a.window, a.sinks);
-    const int n = (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part;
-    if (n <= 1) return;
-    const float* lse = parts.lse2 + row * parts.max_parts;
-    const float* src = parts.o + row * parts.max_parts * D + lane * N;
-    float mx = -INFINITY, sum = 0.f, o[N] = {};
-    for (int i = lane; i < n; i += 32) mx = fmaxf(mx, lse[i]);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-    if (mx == -INFINITY) mx = 0.f;                                    // nothing seen, or NaN (which the weights carry on)
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float w = attn::ex2(lse[i] - mx);
-        sum += w;
-#pragma unroll
-        for (int j = 0; j < N; ++j) o[j] += w * src[(int64_t)i * D + j];
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + row * D + lane * N;
-#pragma unroll
-    for (int j = 0; j < N; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = kv::f32_to_bf16x2(o[j] * inv, o[j + 1] * inv);
-    if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + attn::lg2(sum)) * attn::kLn2;
-}
-
-template <int D, bool FP4>
-__device__ __forceinline__ void load_row(const uint8_t* base, const uint8_t* scales, int64_t row, int lane, float* x)
-{
-    constexpr int N = D / 32;
-    if constexpr (!FP4) {
-        const uint16_t* s = reinterpret_cast<const uint16_t*>(base) + row * D + lane * N;
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float2 f = kv::bf16x2_to_f32(*reinterpret_cast<const uint32_t*>(s + i));
-            x[i] = f.x, x[i + 1] = f.y;
-        }
-    } else {
-        const float s = kv::f16x2_to_f32(kv::e4m3x2_to_f16x2(scales[row * (D / 16) + lane * N / 16])).x;
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float2 f = kv::f16x2_to_f32(kv::e2m1x2_to_f16x2(base[row * (D / 2) + (lane * N + i) / 2]));
-            x[i] = f.x * s, x[i + 1] = f.y * s;
-        }
-    }
-}
-
-template <int D, bool FP4>
-__global__ void __launch_bounds__(128) attention_kernel(AttnCall a)
-{
-    a.c.err = &g_attn_error;
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-    const int64_t t = id / a.c.Hq;
-    const int hq = (int)(id - t * a.c.Hq), h = hq / a.c.G;
-    if (t >= a.c.T) return;
-    int b;
-    int64_t pos;
-    float o[N] = {}, q[N], m = -INFINITY, l = 0.f;
-    if (kv::token_place(a.c, t, b, pos)) {
-        const uint16_t* qs = reinterpret_cast<const uint16_t*>(a.q) + t * a.q_stride + (int64_t)hq * D + lane * N;
-#pragma unroll
-        for (int i = 0; i < N; ++i) q[i] = __uint_as_float((uint32_t)qs[i] << 16) * a.scale;
-        int64_t len = pos + 1;
-        const int64_t room = min((int64_t)a.max_len, (int64_t)a.c.max_pages << a.c.page_shift);
-        if (a.c.lens[b] > room) kv::record(a.c, kv::kErrLength);
-        if (len > room) len = room;
-        for (int64_t j = 0; j < len; ++j) {
-            if (a.window && j >= a.sinks && j <= pos - a.window) {
-                j = pos - a.window;
-                continue;
-            }
-            const int64_t slot = kv::token_slot(a.c, b, j);
-            if (slot < 0) continue;
-            const int64_t row = slot + ((int64_t)h << a.c.page_shift);
-            float x[N], s = 0.f;
-            load_row<D, FP4>(a.c.k, a.c.ks, row, lane, x);
-#pragma unroll
-            for (int i = 0; i < N; ++i) s += x[i] * q[i];
-#pragma unroll
-            for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-            load_row<D, FP4>(a.c.v, a.c.vs, row, lane, x);
-            const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : __expf(m - mn), e = __expf(s - mn);
-            l = l * f + e;
-#pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = o[i] * f + e * x[i];
-            m = mn;
-        }
-    }
-    const float r = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + (t * a.c.Hq + hq) * D + lane * N;
-#pragma unroll
-    for (int i = 0; i < N; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = kv::f32_to_bf16x2(o[i] * r, o[i + 1] * r);
-    if (a.lse && lane == 0) a.lse[t * a.c.Hq + hq] = l > 0.f ? m + logf(l) : -INFINITY;
+    const int n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
+    if (n > 1) attn::join_row<D>(a, parts, row, n, lane);
 }
 
 }  // namespace
@@ -624,11 +527,7 @@ constexpr int kFewTile(bool fp4) { return fp4 ? 32 : 16; }
 constexpr int64_t kCtas = 2048;
 constexpr int kMinPart = 256;
 
-struct Cut {
-    int32_t parts, tiles_per_part;
-};
-
-Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t max_len)
+attn::Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t max_len)
 {
     const int tile = kFewTile(p.cache_dtype == KDA_CACHE_FP4);
     int64_t tokens = max_len;
@@ -643,7 +542,7 @@ Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t max_len)
     if (parts > most) parts = most;
     if (parts > 256) parts = 256;
     if (parts < 1) parts = 1;
-    Cut c;
+    attn::Cut c;
     c.tiles_per_part = (int32_t)((tiles + parts - 1) / parts);
     c.parts = (int32_t)((tiles + c.tiles_per_part - 1) / c.tiles_per_part);
     return c;
@@ -654,7 +553,7 @@ size_t parts_bytes(const kda_kv_params& p, int64_t T, int32_t parts)
     return (size_t)T * p.num_q_heads * parts * (p.head_dim + 1) * 4 + 256;
 }
 
-Parts make_parts(const kda_kv_params& p, int64_t T, const Cut& c, void* workspace)
+Parts make_parts(const kda_kv_params& p, int64_t T, const attn::Cut& c, void* workspace)
 {
     Parts x;
     x.max_parts = c.parts;
@@ -665,7 +564,7 @@ Parts make_parts(const kda_kv_params& p, int64_t T, const Cut& c, void* workspac
 }
 
 template <int D, bool FP4, int NT>
-cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const Cut& cut, void* workspace, cudaStream_t stream)
+cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const attn::Cut& cut, void* workspace, cudaStream_t stream)
 {
     constexpr int TB = kFewTile(FP4) / 16;
     const Parts parts = make_parts(p, a.c.T, cut, workspace);
@@ -682,11 +581,11 @@ cudaError_t launch_typed(const kda_kv_params& p, const AttnCall& a, void* worksp
 {
     const int rows = a.max_new * a.c.G;
     if (rows <= kFewRows) {
-        const Cut cut = cut_few(p, a.c.n, a.max_new, a.max_len);
+        const attn::Cut cut = cut_few(p, a.c.n, a.max_new, a.max_len);
         return rows <= 8 ? launch_few<D, FP4, 1>(p, a, cut, workspace, stream) : launch_few<D, FP4, 2>(p, a, cut, workspace, stream);
     }
-    attention_kernel<D, FP4><<<(unsigned)((a.c.T * a.c.Hq + 3) / 4), 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    const attn::Cut cut = cut_many(p, a.c.n, a.c.T, a.max_new, a.max_len);
+    return launch_many<D, FP4>(p, a, make_parts(p, a.c.T, cut, workspace), stream);
 }
 
 }  // namespace
@@ -695,8 +594,7 @@ size_t attention_workspace_bytes(const kda_kv_params& p, int32_t num_seqs, int64
                                  int32_t max_len)
 {
     const int64_t rows = (int64_t)max_new * (p.num_q_heads / p.num_kv_heads);
-    if (rows > kFewRows) return 0;
-    const Cut cut = cut_few(p, num_seqs, max_new, max_len);
+    const attn::Cut cut = rows <= kFewRows ? cut_few(p, num_seqs, max_new, max_len) : cut_many(p, num_seqs, total_tokens, max_new, max_len);
     return cut.parts > 1 ? parts_bytes(p, total_tokens, cut.parts) : 0;
 }
 
@@ -709,10 +607,12 @@ cudaError_t launch_attention(const kda_kv_params& p, const AttnCall& a, void* wo
 
 cudaError_t attn_read_and_clear_error(int32_t* code)
 {
-    int32_t zero = 0;
+    int32_t zero = 0, many = 0;
     cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_error, sizeof(int32_t));
-    if (e != cudaSuccess) return e;
-    return cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(int32_t));
+    if (e == cudaSuccess) e = attn_tc_read_and_clear_error(&many);
+    if (*code == 0) *code = many;
+    return e;
 }
 
 }  // namespace kda

@@ -52,6 +52,11 @@ struct Parts {
     int32_t tiles_per_part;
 };
 
+// How the host cuts a call along the cache; parts = 1: not at all.
+struct Cut {
+    int32_t parts, tiles_per_part;
+};
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -65,5 +70,38 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
+// One row's n > 1 parts joined by a warp, D / 32 channels a lane.
+template <int D>
+__device__ __forceinline__ void join_row(const AttnCall& a, const Parts& parts, int64_t row, int n, int lane)
+{
+    constexpr int N = D / 32;
+    const float* lse = parts.lse2 + row * parts.max_parts;
+    const float* src = parts.o + row * parts.max_parts * D + lane * N;
+    float mx = -INFINITY, sum = 0.f, o[N] = {};
+    for (int i = lane; i < n; i += 32) mx = fmaxf(mx, lse[i]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+    if (mx == -INFINITY) mx = 0.f;                                    // nothing seen, or NaN (which the weights carry on)
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float w = ex2(lse[i] - mx);
+        sum += w;
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] += w * src[(int64_t)i * D + j];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + row * D + lane * N;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = kv::f32_to_bf16x2(o[j] * inv, o[j + 1] * inv);
+    if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + lg2(sum)) * kLn2;
+}
+
 }  // namespace attn
+
+// kda_attn_tc.cu: the form for many query rows
+attn::Cut cut_many(const kda_kv_params& p, int32_t n, int64_t T, int32_t max_new, int32_t max_len);
+template <int D, bool FP4>
+cudaError_t launch_many(const kda_kv_params& p, const AttnCall& a, const attn::Parts& parts, cudaStream_t stream);
+cudaError_t attn_tc_read_and_clear_error(int32_t* code);
+
 }  // namespace kda

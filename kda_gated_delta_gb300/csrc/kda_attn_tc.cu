@@ -1,0 +1,725 @@
+// kda_attn_tc.cu -- attention of new tokens over the paged cache for many query rows (prompts, wide
+// verifies): tcgen05 matrix products with the scores, the weights and the outputs in tensor memory.
+//
+// A kv head serves R = new tokens * G query rows, row = token * G + head of the group, so that the heads of
+// a group share every key and value tile.  A CTA takes 256 rows as two tiles of 128 and walks the cache
+// tokens that any of them may see in tiles of 128:
+//
+//   S_i = Q_i K_j^T      M 128 (rows) x N 128 (tokens) x K D, both operands K-major in shared memory
+//   P_i = exp2(S_i - m)  one thread per row: no shuffles; packed over S_i's own columns
+//   O_i += P_i V_j       A from tensor memory, V_j as it lies in the cache (MN-major)
+//
+// Tensor memory, all 512 columns: S_0, S_1 (128 each; P_i takes the first 64 of S_i's) and O_0, O_1 (D each).
+// Roles: warps 0-3 and 4-7 are the softmax of row tile 0 and 1, warp 8 issues the products, the warps after
+// it fill a ring of key and value tiles (128 tokens x D, 128-byte swizzle).  The products go
+// PV_0(j), S_0(j+1), PV_1(j), S_1(j+1), so that each softmax works while the other tile's products run.
+//   bf16 cache: one warp, a lane per page, two tensor-map copies (64 channels each) per page and tile;
+//   4-bit cache: three warps convert on the way into shared memory, exactly: keys to fp16 (one instruction a
+//   pair; the queries are fp16 then, each row divided by a power of two), values to bf16, whose range the
+//   weights need.
+// A rescaling of O happens only when a row's maximum grows by more than 2^8 since the last one; the S_i(j)
+// barrier implies that PV_i(j-1) is complete, so the softmax warps do it themselves.
+//
+// Value rows of tokens that no row of the CTA may see (the ends of the cache and of a window) are zeroed in
+// shared memory before their product: what lies there may be NaN, which a weight of zero does not stop.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <stdint.h>
+
+#include "kda_attn.cuh"
+#include "kda_internal.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace {
+
+__device__ int32_t g_attn_tc_error = 0;
+
+using attn::Parts;
+using attn::Span;
+
+constexpr int kRows = 256;            // query rows of a CTA
+constexpr int kTile = 128;            // cache tokens of a tile
+constexpr int kThreads = 384;         // three warpgroups: two of softmax, one of the other roles
+// Registers: 384 threads start with 168 each (64,512 of the SM's 65,536); the last warpgroup gives 72 x 128
+// back and the softmax ones take 32 x 256 of these: 200 hold a row of 128 scores without spilling.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
+constexpr uint32_t kPolls = 1u << 24;
+constexpr float kSlack = 8.0f;
+
+template <int D, bool FP4>
+struct Cfg {
+    static constexpr int kFillThreads = FP4 ? 96 : 32;
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kSlots = D == 128 ? 5 : 8;
+    static constexpr int kPanel = kTile * 128;               // 64 channels of 128 rows
+    static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024 /* alignment */ + 256 /* barriers */;
+};
+
+struct __align__(8) Bars {
+    uint64_t full[8], empty[8];
+    uint64_t q_full[2], s_full[2], p_ready[2], o_full[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t place[4];                 // request, first row of the CTA, found
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+// Matrix descriptor of a 128-byte-swizzled operand: 8 rows of 128 bytes make an atom, `sbo` the distance of
+// atoms along the strided dimension, `lbo` (MN-major only) that of 64-element panels.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+template <bool FP16>
+__host__ __device__ constexpr uint32_t idesc(uint32_t N, bool b_mn)
+{
+    return (1u << 4) | (FP16 ? 0u : 1u << 7 | 1u << 10) | (b_mn ? 1u << 16 : 0u) | (N >> 3) << 17 | (128u >> 4) << 24;
+}
+
+#define KDA_X8(p, i) p(r[i]), p(r[i + 1]), p(r[i + 2]), p(r[i + 3]), p(r[i + 4]), p(r[i + 5]), p(r[i + 6]), p(r[i + 7])
+#define KDA_OUT(x) "=r"(x)
+#define KDA_IN(x) "r"(x)
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : KDA_X8(KDA_OUT, 0), KDA_X8(KDA_OUT, 8), KDA_X8(KDA_OUT, 16), KDA_X8(KDA_OUT, 24)
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        KDA_X8(KDA_IN, 0), KDA_X8(KDA_IN, 8), KDA_X8(KDA_IN, 16), KDA_X8(KDA_IN, 24)
+        : "memory");
+}
+// Waits for the loads; the empty statements keep every use of their registers after the wait.
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+#define KDA_BOTH(x) "+r"(x)
+__device__ __forceinline__ void pin32(uint32_t* r)
+{
+    asm volatile("" : KDA_X8(KDA_BOTH, 0), KDA_X8(KDA_BOTH, 8), KDA_X8(KDA_BOTH, 16), KDA_X8(KDA_BOTH, 24)::"memory");
+}
+#undef KDA_X8
+#undef KDA_OUT
+#undef KDA_IN
+#undef KDA_BOTH
+// Request and first row of the CTA with index x among all row tiles; false past the last one.  One warp.
+__device__ __forceinline__ bool find_rows(const kv::Paged& c, int64_t x, int lane, int& b, int64_t& row0)
+{
+    for (int base = 0; base < c.n; base += 32) {
+        int64_t t0 = 0, t1 = 0;
+        if (base + lane < c.n) kv::request_rows(c, base + lane, t0, t1);
+        const int64_t tiles = ((t1 - t0) * c.G + kRows - 1) / kRows;
+        int64_t sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(~0u, sum, d);
+            if (lane >= d) sum += y;
+        }
+        const unsigned hit = __ballot_sync(~0u, x < sum);
+        if (hit) {
+            const int who = __ffs(hit) - 1;
+            const int64_t before = __shfl_sync(~0u, sum - tiles, who), mine = __shfl_sync(~0u, tiles, who);
+            b = base + who;
+            row0 = (mine - 1 - (x - before)) * kRows;            // a request's last rows, which see most, first
+            return true;
+        }
+        x -= __shfl_sync(~0u, sum, 31);
+    }
+    return false;
+}
+
+struct Work {
+    int b, h, nq, tile_lo, tile_hi;
+    int64_t t0;
+    int32_t R, row0;               // rows of (request, head), first row of this CTA
+    int first;                     // position of the request's first new token
+    Span sp;
+};
+
+// ---- filling the ring --------------------------------------------------------------------------------
+__device__ __forceinline__ bool seen_by_any(const Span& sp, int j) { return j < sp.hi && (j >= sp.lo || j < sp.sink_end); }
+__device__ __forceinline__ bool page_needed(const Span& sp, int j, int page) { return j < sp.hi && (j + page > sp.lo || j < sp.sink_end); }
+
+template <int D>
+__device__ bool fill_bf16(const AttnCall& a, const Work& w, const CUtensorMap* km, const CUtensorMap* vm, uint8_t* ring, Bars* bars, int lane)
+{
+    using C = Cfg<D, false>;
+    const int shift = a.c.page_shift, page = 1 << shift, per_tile = kTile >> shift;
+    bool ok = true;
+    int idx = 0;
+    for (int i = w.tile_lo; i < w.tile_hi; ++i) {
+        const int base = attn::tile_base<kTile>(w.sp, i), j = base + lane * page;
+        int64_t row = -1;
+        if (lane < per_tile && page_needed(w.sp, j, page)) {
+            row = kv::token_slot(a.c, w.b, j);
+            if (row >= 0) row += (int64_t)w.h << shift;
+        }
+        const uint32_t bytes = __popc(__ballot_sync(~0u, row >= 0)) * (uint32_t)(page * D * 2);
+#pragma unroll
+        for (int which = 0; which < 2; ++which, ++idx) {
+            const int slot = idx % C::kSlots;
+            uint8_t* dst = ring + slot * C::kTileBytes + lane * page * 128;
+            ok = tc::mbar_wait(&bars->empty[slot], ((idx / C::kSlots) & 1) ^ 1, kPolls);
+            if (!__all_sync(~0u, ok)) return false;
+            if (lane == 0) tc::mbar_arrive_expect_tx(&bars->full[slot], bytes);
+            __syncwarp();
+            if (row >= 0) {
+#pragma unroll
+                for (int p = 0; p < D / 64; ++p)
+                    tc::tma_load_2d(dst + p * C::kPanel, which ? vm : km, p * 64, (int32_t)row, &bars->full[slot]);
+            }
+        }
+    }
+    return true;
+}
+
+template <int D>
+__device__ bool fill_fp4(const AttnCall& a, const Work& w, uint8_t* ring, Bars* bars, int tid)
+{
+    using C = Cfg<D, true>;
+    constexpr int kUnits = D / 32, kAll = kTile * kUnits, kPer = (kAll + 95) / 96;   // 32-channel units of a row, a tile, a thread
+    const int shift = a.c.page_shift;
+    int idx = 0;
+    for (int i = w.tile_lo; i < w.tile_hi; ++i) {
+        const int base = attn::tile_base<kTile>(w.sp, i);
+#pragma unroll
+        for (int which = 0; which < 2; ++which, ++idx) {
+            const int slot = idx % C::kSlots;
+            uint8_t* dst = ring + slot * C::kTileBytes;
+            const uint8_t* src = which ? a.c.v : a.c.k;
+            const uint8_t* scl = which ? a.c.vs : a.c.ks;
+            uint4 x[kPer];
+            uint32_t s[kPer];
+#pragma unroll
+            for (int n = 0; n < kPer; ++n) {
+                const int at = tid + 96 * n, r = at / kUnits, u = at % kUnits;
+                x[n] = make_uint4(0, 0, 0, 0);
+                s[n] = 0;
+                if (at < kAll && seen_by_any(w.sp, base + r)) {
+                    const int64_t row = kv::token_slot(a.c, w.b, base + r);
+                    if (row >= 0) {
+                        const int64_t t = row + ((int64_t)w.h << shift);
+                        x[n] = __ldg(reinterpret_cast<const uint4*>(src + t * (D / 2) + u * 16));
+                        s[n] = __ldg(reinterpret_cast<const uint16_t*>(scl + t * (D / 16) + u * 2));
+                    }
+                }
+            }
+            if (!tc::mbar_wait(&bars->empty[slot], ((idx / C::kSlots) & 1) ^ 1, kPolls)) return false;
+#pragma unroll
+            for (int n = 0; n < kPer; ++n) {
+                const int at = tid + 96 * n, r = at / kUnits, u = at % kUnits;
+                if (at >= kAll) break;
+                const uint32_t f = kv::e4m3x2_to_f16x2(s[n]);
+                const uint32_t f0 = __byte_perm(f, 0, 0x1010), f1 = __byte_perm(f, 0, 0x3232);
+                const uint32_t wd[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t y[4];
+                    kv::e2m1x8_to_f16(wd[q], y);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        y[z] = kv::mul_f16x2(y[z], q < 2 ? f0 : f1);
+                        if (which) {                                    // at most 6 significant bits: exact in bf16 too
+                            const float2 f = kv::f16x2_to_f32(y[z]);
+                            y[z] = kv::f32_to_bf16x2(f.x, f.y);
+                        }
+                    }
+                    const int chunk = (u * 4 + q) & 7, panel = (u * 4 + q) >> 3;
+                    *reinterpret_cast<uint4*>(dst + panel * C::kPanel + r * 128 + ((chunk ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
+            tc::fence_proxy_async();
+            tc::mbar_arrive(&bars->full[slot]);
+        }
+    }
+    return true;
+}
+
+// ---- issuing the products --------------------------------------------------------------------------------
+template <int D, bool FP4>
+__device__ bool issue(const Work& w, const uint8_t* q, uint8_t* ring, Bars* bars, uint32_t tmem, int lane)
+{
+    using C = Cfg<D, FP4>;
+    constexpr uint32_t id_s = idesc<FP4>(kTile, false), id_o = idesc<false>(D, true);
+    const int n = w.tile_hi - w.tile_lo;
+    const uint32_t q0 = tc::smem_u32(q), r0 = tc::smem_u32(ring);
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, tc::mbar_wait(bar, parity, kPolls)); };
+    const auto full = [&](int idx) { return wait(&bars->full[idx % C::kSlots], (idx / C::kSlots) & 1); };
+    const auto scores = [&](int i, int j) {
+        if (lane == 0) {
+            const uint32_t kb = r0 + (2 * j % C::kSlots) * C::kTileBytes, qb = q0 + i * C::kTileBytes;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                const uint32_t off = (s / 4) * C::kPanel + (s % 4) * 32;
+                tc::mma_f16_ss(tmem + 128 * i, desc_sw128(qb + off, 16, 1024), desc_sw128(kb + off, 16, 1024), id_s, s > 0);
+            }
+            tc::mma_commit(&bars->s_full[i]);
+        }
+        __syncwarp();
+    };
+    if (!full(0)) return false;
+    for (int i = 0; i < w.nq; ++i) {
+        if (!wait(&bars->q_full[i], 0)) return false;
+        scores(i, 0);
+    }
+    if (lane == 0) tc::mma_commit(&bars->empty[0]);
+    for (int j = 0; j < n; ++j) {
+        const int vi = 2 * j + 1, slot = vi % C::kSlots;
+        uint8_t* vt = ring + slot * C::kTileBytes;
+        if (!full(vi)) return false;
+        if constexpr (!FP4) {
+            const int base = attn::tile_base<kTile>(w.sp, w.tile_lo + j);
+            if (base + kTile > w.sp.hi || (base < w.sp.lo && base + kTile > w.sp.sink_end)) {
+                for (int r = lane; r < kTile; r += 32) {
+                    if (seen_by_any(w.sp, base + r)) continue;
+#pragma unroll
+                    for (int p = 0; p < D / 64; ++p)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vt + p * C::kPanel + r * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async();
+                __syncwarp();
+            }
+        }
+        for (int i = 0; i < w.nq; ++i) {
+            if (!wait(&bars->p_ready[i], j & 1)) return false;
+            tc::tc_fence_after();
+            if (lane == 0) {
+                const uint32_t vb = tc::smem_u32(vt);
+#pragma unroll
+                for (int s = 0; s < kTile / 16; ++s)
+                    tc::mma_f16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * s, desc_sw128(vb + s * 2048, C::kPanel, 1024), id_o, j > 0 || s > 0);
+                if (j + 1 == n) tc::mma_commit(&bars->o_full[i]);
+            }
+            __syncwarp();
+            if (j + 1 < n) {
+                if (i == 0 && !full(vi + 1)) return false;
+                scores(i, j + 1);
+            }
+        }
+        if (lane == 0) {
+            tc::mma_commit(&bars->empty[slot]);
+            if (j + 1 < n) tc::mma_commit(&bars->empty[(vi + 1) % C::kSlots]);
+        }
+        __syncwarp();
+    }
+    return true;
+}
+
+// ---- one thread per query row ------------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+// Loads query row `row` of the tile into its swizzled place; returns the factor from scores to log2.
+template <int D, bool FP4>
+__device__ __forceinline__ float load_query(const AttnCall& a, const Work& w, uint8_t* q, int tile_row)
+{
+    using C = Cfg<D, FP4>;
+    const int row = w.row0 + tile_row, r = tile_row & 127;
+    uint8_t* dst = q + (tile_row >> 7) * C::kTileBytes + r * 128;
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (w.t0 + row / a.c.G) * a.q_stride + (int64_t)(w.h * a.c.G + row % a.c.G) * D;
+    uint4 x[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) x[i] = row < w.R ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+    float unit = a.scale * attn::kLog2e;
+    if constexpr (FP4) {
+        // fp16 operands: the row is divided by a power of two near its largest magnitude (see the few-rows form)
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) top = max(top, max(y[z] & 0x7fffu, (y[z] >> 16) & 0x7fffu));
+        }
+        const int e = min(max((int)(top >> 7), 1), 253);
+        const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+        unit *= __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const float2 f = kv::bf16x2_to_f32(y[z]);
+                y[z] = kv::f32_to_f16x2(f.x * down, f.y * down);
+            }
+            x[i] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(dst + (i >> 3) * C::kPanel + (((i & 7) ^ (r & 7)) << 4)) = x[i];
+    return unit;
+}
+
+template <int D, bool FP4>
+__device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, int parts_here, int part, uint8_t* q, Bars* bars, uint32_t tmem,
+                        int i, int tid)
+{
+    const int tile_row = 128 * i + tid, row = w.row0 + tile_row;
+    const float unit = load_query<D, FP4>(a, w, q, tile_row);
+    tc::fence_proxy_async();
+    tc::mbar_arrive(&bars->q_full[i]);
+
+    const uint32_t lanes = (uint32_t)(tid & 96) << 16;                  // the warp's 32 tensor-memory lanes
+    const uint32_t ts = tmem + 128 * i + lanes, to = tmem + 256 + D * i + lanes;
+    const int p = w.first + row / a.c.G;
+    const int p_lo = w.first + (w.row0 + 128 * i) / a.c.G;                // of the tile's first and last row
+    const int p_hi = w.first + min(w.R - 1, w.row0 + 128 * i + 127) / a.c.G;
+    const int n = w.tile_hi - w.tile_lo;
+    float m = -INFINITY;
+    uint64_t l2 = pack2(0.f, 0.f);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+        const int base = attn::tile_base<kTile>(w.sp, w.tile_lo + j);
+        ok = __all_sync(~0u, tc::mbar_wait(&bars->s_full[i], j & 1, kPolls));
+        if (!ok) return false;
+        tc::tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s + 32 * x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) pin32(s + 32 * x);
+        const bool whole = base + kTile <= w.sp.hi && base + kTile - 1 <= p_lo && (a.window == 0 || base > p_hi - a.window || base + kTile <= a.sinks);
+        if (!whole) {
+            // visible columns: [from, to) and [0, sink)
+            const int end = min(p + 1, w.sp.hi) - base, from = a.window ? p - a.window + 1 - base : 0, sink = a.sinks - base;
+#pragma unroll
+            for (int x = 0; x < 128; ++x)
+                if (!(x < end && (x >= from || x < sink))) s[x] = 0xff800000u;
+        }
+        float top = -INFINITY;
+        {
+            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int x = 0; x < 128; x += 8)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) t4[z] = fmaxf(t4[z], fmaxf(__uint_as_float(s[x + 2 * z]), __uint_as_float(s[x + 2 * z + 1])));
+            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * unit;
+        }
+        if (__any_sync(~0u, top > m + kSlack)) {
+            const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.f : attn::ex2(m - mn);
+            m = mn;
+            const uint64_t f2 = pack2(f, f);
+            l2 = fma2(l2, f2, pack2(0.f, 0.f));
+            if (j > 0) {
+#pragma unroll
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(to + x, o);
+                    tmem_wait_ld();
+                    pin32(o);
+#pragma unroll
+                    for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+                    tmem_st32(to + x, o);
+                }
+            }
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        const uint64_t u2 = pack2(unit, unit), m2 = pack2(-mu, -mu);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+                const int e = 64 * half + 2 * x;
+                const float2 y = unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), u2, m2));
+                const float e0 = attn::ex2(y.x), e1 = attn::ex2(y.y);
+                l2 = add2(l2, pack2(e0, e1));
+                pk[x] = kv::f32_to_bf16x2(e0, e1);
+            }
+            tmem_st32(ts + 32 * half, pk);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        tc::mbar_arrive(&bars->p_ready[i]);
+    }
+
+    // ---- the row's output --------------------------------------------------------------------------------
+    const float2 lp = unpack2(l2);
+    const float l = lp.x + lp.y;
+    if (n > 0) {
+        ok = __all_sync(~0u, tc::mbar_wait(&bars->o_full[i], 0, kPolls));
+        if (!ok) return false;
+        tc::tc_fence_after();
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float lse2 = l == 0.f ? -INFINITY : m + attn::lg2(l);
+    const int64_t out_row = (w.t0 + row / a.c.G) * a.c.Hq + w.h * a.c.G + row % a.c.G;
+    const int64_t at = out_row * parts.max_parts + part;
+    const bool live = row < w.R;
+#pragma unroll
+    for (int x = 0; x < D; x += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+            tmem_ld32(to + x, o);
+            tmem_wait_ld();
+            pin32(o);
+        }
+        if (!live) continue;
+        // a row whose weights are all zero may stand beside non-finite products: its output is zero
+#pragma unroll
+        for (int z = 0; z < 32; ++z) o[z] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[z]) * inv);
+        if (parts_here > 1) {
+            uint4* dst = reinterpret_cast<uint4*>(parts.o + at * D + x);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) dst[z] = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+        } else {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + out_row * D + x);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                uint32_t y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = kv::f32_to_bf16x2(__uint_as_float(o[8 * z + 2 * k]), __uint_as_float(o[8 * z + 2 * k + 1]));
+                dst[z] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        }
+    }
+    if (live) {
+        if (parts_here > 1) parts.lse2[at] = lse2;
+        else if (a.lse) a.lse[out_row] = lse2 * attn::kLn2;
+    }
+    return true;
+}
+
+template <int D, bool FP4>
+__global__ void __launch_bounds__(kThreads, 1)
+    many_rows_kernel(AttnCall a, Parts parts, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm)
+{
+    a.c.err = &g_attn_tc_error;
+    using C = Cfg<D, FP4>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
+    uint8_t* q = smem;
+    uint8_t* ring = smem + 2 * C::kTileBytes;
+    Bars* bars = reinterpret_cast<Bars*>(ring + C::kSlots * C::kTileBytes);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (warp == 0) {
+        int b = 0;
+        int64_t row0 = 0;
+        const bool found = find_rows(a.c, blockIdx.x / a.c.Hkv, lane, b, row0);
+        if (lane == 0) bars->place[0] = found ? 1 : 0, bars->place[1] = b, bars->place[2] = (int32_t)row0;
+    } else if (warp == 1 && lane == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            tc::mbar_init(&bars->full[i], FP4 ? C::kFillThreads : 1);
+            tc::mbar_init(&bars->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bars->q_full[i], 128);
+            tc::mbar_init(&bars->s_full[i], 1);
+            tc::mbar_init(&bars->p_ready[i], 128);
+            tc::mbar_init(&bars->o_full[i], 1);
+        }
+        tc::mbar_init(&bars->drain, 1);
+        tc::fence_mbar_init();
+    } else if (warp == 8) {
+        tc::tmem_alloc(&bars->tmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+
+    Work w;
+    bool live = bars->place[0] != 0;
+    int parts_here = 1;
+    const int part = blockIdx.y;
+    if (live) {
+        w.b = bars->place[1];
+        w.h = blockIdx.x % a.c.Hkv;
+        w.row0 = bars->place[2];
+        int64_t t1;
+        kv::request_rows(a.c, w.b, w.t0, t1);
+        const int fresh = (int)(t1 - w.t0), len = a.c.lens[w.b];
+        w.R = fresh * a.c.G;
+        if (threadIdx.x == 0 && part == 0 && w.h == 0 && (len > a.max_len || fresh > a.max_new)) kv::record(a.c, kv::kErrLength);
+        w.first = len > 0 ? len - fresh : -1 - fresh;
+        const int lo = w.first + w.row0 / a.c.G, hi = w.first + min(w.R - 1, w.row0 + kRows - 1) / a.c.G;
+        w.sp = attn::make_span<kTile>(max(lo, 0), len > 0 ? hi : -1, a.max_len, a.window, a.sinks);
+        w.nq = w.R - w.row0 > 128 ? 2 : 1;
+        if (parts.o) parts_here = min(parts.max_parts, max(1, (w.sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part));
+        w.tile_lo = parts_here > 1 ? part * parts.tiles_per_part : 0;
+        w.tile_hi = parts_here > 1 ? min(w.sp.tiles, w.tile_lo + parts.tiles_per_part) : w.sp.tiles;
+        live = part < parts_here;
+    }
+    bool ok = true;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        if (live && warp / 4 < w.nq) ok = softmax<D, FP4>(a, parts, w, parts_here, part, q, bars, tmem, warp / 4, threadIdx.x % 128);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (live && w.tile_hi > w.tile_lo) {
+            if (warp == 8) {
+                ok = issue<D, FP4>(w, q, ring, bars, tmem, lane);
+                if (lane == 0) tc::mma_commit(&bars->drain);           // everything issued ends before the exit
+                __syncwarp();
+                ok = tc::mbar_wait(&bars->drain, 0, kPolls) && ok;
+            } else if constexpr (FP4) {
+                ok = fill_fp4<D>(a, w, ring, bars, threadIdx.x - 288);
+            } else if (warp == 9) {
+                ok = fill_bf16<D>(a, w, &km, &vm, ring, bars, lane);
+                if (!ok)                                               // and the copies in flight land
+                    for (int i = 0; i < C::kSlots; ++i) {
+                        tc::mbar_wait(&bars->full[i], 0, 1u << 16);
+                        tc::mbar_wait(&bars->full[i], 1, 1u << 16);
+                    }
+            }
+        }
+    }
+    if (!ok) kv::record(a.c, kDevErrTimeout);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of each row that has several: a warp per row, D / 32 channels a lane.
+template <int D>
+__global__ void __launch_bounds__(128) join_rows_kernel(AttnCall a, Parts parts)
+{
+    a.c.err = &g_attn_tc_error;
+    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (row >= a.c.T * a.c.Hq) return;
+    const int64_t t = row / a.c.Hq;
+    int b = 0;
+    int64_t pos;
+    const bool sees = kv::token_place(a.c, t, b, pos);
+    int64_t t0, t1;
+    kv::request_rows(a.c, b, t0, t1);
+    const int len = a.c.lens[b];
+    if ((!sees && (t < t0 || t >= t1)) || len <= 0) return;
+    const int fresh = (int)(t1 - t0), G = a.c.G, first = len - fresh;
+    const int64_t row0 = ((t - t0) * G + row % a.c.Hq % G) / kRows * kRows;
+    const int64_t last = min((int64_t)fresh * G - 1, row0 + kRows - 1);
+    const Span sp = attn::make_span<kTile>(max(first + row0 / G, (int64_t)0), first + last / G, a.max_len, a.window, a.sinks);
+    const int n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
+    if (n > 1) attn::join_row<D>(a, parts, row, n, lane);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess || r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+// The cache as rows of D channels, read in boxes of one page x 64 channels, 128-byte swizzle.
+cudaError_t encode_pages(CUtensorMap* m, const void* base, int64_t rows, int D, int page)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)page};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int64_t row_tiles(const kda_kv_params& p, int32_t n, int64_t T, int32_t max_new)
+{
+    const int G = p.num_q_heads / p.num_kv_heads;
+    const int64_t by_sum = T * G / kRows + n, by_most = (int64_t)n * (((int64_t)max_new * G + kRows - 1) / kRows);
+    return by_sum < by_most ? by_sum : by_most;
+}
+
+}  // namespace
+
+// How a call is cut along the cache when its row tiles do not fill the SMs: parts of at least kMinTiles
+// tiles, kWaves parts per SM.
+attn::Cut cut_many(const kda_kv_params& p, int32_t n, int64_t T, int32_t max_new, int32_t max_len)
+{
+    constexpr int64_t kSms = 152, kWaves = 2, kMinTiles = 4;
+    const int G = p.num_q_heads / p.num_kv_heads;
+    int64_t tokens = max_len;
+    if (p.window) {
+        const int64_t seen = (int64_t)p.window + kRows / G + 1 + p.num_sinks + 3 * kTile;
+        if (seen < tokens) tokens = seen;
+    }
+    const int64_t tiles = (tokens + kTile - 1) / kTile, ctas = row_tiles(p, n, T, max_new) * p.num_kv_heads;
+    int64_t parts = kSms * kWaves / ctas;
+    if (parts > tiles / kMinTiles) parts = tiles / kMinTiles;
+    if (parts > 256) parts = 256;
+    if (parts < 1) parts = 1;
+    attn::Cut c;
+    c.tiles_per_part = (int32_t)((tiles + parts - 1) / parts);
+    c.parts = (int32_t)((tiles + c.tiles_per_part - 1) / c.tiles_per_part);
+    return c;
+}
+
+template <int D, bool FP4>
+cudaError_t launch_many(const kda_kv_params& p, const AttnCall& a, const Parts& parts, cudaStream_t stream)
+{
+    using C = Cfg<D, FP4>;
+    CUtensorMap km = {}, vm = {};
+    if (!FP4) {
+        const int64_t rows = a.c.num_pages * a.c.Hkv << a.c.page_shift;
+        if (rows > 0) {
+            cudaError_t e = encode_pages(&km, a.c.k, rows, D, p.page_size);
+            if (e == cudaSuccess) e = encode_pages(&vm, a.c.v, rows, D, p.page_size);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    cudaError_t e = cudaFuncSetAttribute(many_rows_kernel<D, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = row_tiles(p, a.c.n, a.c.T, a.max_new);
+    many_rows_kernel<D, FP4><<<dim3((unsigned)(tiles * a.c.Hkv), (unsigned)parts.max_parts), kThreads, C::kSmem, stream>>>(a, parts, km, vm);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || parts.max_parts == 1) return e;
+    join_rows_kernel<D><<<(unsigned)((a.c.T * a.c.Hq + 3) / 4), 128, 0, stream>>>(a, parts);
+    return cudaGetLastError();
+}
+
+template cudaError_t launch_many<64, false>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
+template cudaError_t launch_many<64, true>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
+template cudaError_t launch_many<128, false>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
+template cudaError_t launch_many<128, true>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
+
+cudaError_t attn_tc_read_and_clear_error(int32_t* code)
+{
+    int32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_tc_error, sizeof(int32_t));
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyToSymbol(g_attn_tc_error, &zero, sizeof(int32_t));
+}
+
+}  // namespace kda
