@@ -10,8 +10,8 @@
 //   O_i += P_i V_j       A from tensor memory, V_j as it lies in the cache (MN-major)
 //
 // Tensor memory, all 512 columns: S_0, S_1 (128 each; P_i takes the first 64 of S_i's) and O_0, O_1 (D each).
-// Roles: warps 0-3 and 4-7 are the softmax of row tile 0 and 1, warp 8 issues the products, the warps after
-// it fill a ring of key and value tiles (128 tokens x D, 128-byte swizzle).  The products go
+// Roles: warps 0-3 and 4-7 are the softmax of row tile 0 and 1, a thread of warp 8 issues the products,
+// the warps after it fill a ring of key and value tiles (128 tokens x D, 128-byte swizzle).  The products go
 // PV_0(j), S_0(j+1), PV_1(j), S_1(j+1), so that each softmax works while the other tile's products run.
 //   bf16 cache: one warp, a lane per page, two tensor-map copies (64 channels each) per page and tile;
 //   4-bit cache: three warps convert on the way into shared memory, exactly: keys to fp16 (one instruction a
@@ -21,7 +21,8 @@
 // barrier implies that PV_i(j-1) is complete, so the softmax warps do it themselves.
 //
 // Value rows of tokens that no row of the CTA may see (the ends of the cache and of a window) are zeroed in
-// shared memory before their product: what lies there may be NaN, which a weight of zero does not stop.
+// shared memory before their product, by a warp of its own: what lies there may be NaN, which a weight of
+// zero does not stop.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,31 +43,31 @@ using attn::Span;
 
 constexpr int kRows = 256;            // query rows of a CTA
 constexpr int kTile = 128;            // cache tokens of a tile
-constexpr int kThreads = 384;         // three warpgroups: two of softmax, one of the other roles
-// Registers: 384 threads start with 168 each (64,512 of the SM's 65,536); the last warpgroup gives 72 x 128
-// back and the softmax ones take 32 x 256 of these: 200 hold a row of 128 scores without spilling.
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
 constexpr uint32_t kPolls = 1u << 24;
 constexpr float kSlack = 8.0f;
 
 template <int D, bool FP4>
 struct Cfg {
     static constexpr int kFillThreads = FP4 ? 96 : 32;
+    // Registers: the launch gives each of the 384 threads 168 (64,512 of the SM's 65,536); the last warpgroup
+    // gives back what it does not need, and 192 hold a row of 128 scores without spilling.
+    static constexpr int kThreads = 384, kSoftmaxRegs = 192, kOtherRegs = 112;
+    static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kSlots = D == 128 ? 5 : 8;
     static constexpr int kPanel = kTile * 128;               // 64 channels of 128 rows
-    static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024 /* alignment */ + 256 /* barriers */;
+    static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024 /* alignment */ + 320 /* barriers */;
 };
 
 struct __align__(8) Bars {
     uint64_t full[8], empty[8];
-    uint64_t q_full[2], s_full[2], p_ready[2], o_full[2];
+    uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2];
     uint64_t drain;
+    uint64_t patch[4];                // arrival of the value tiles that are mended before use
     uint32_t tmem;
     int32_t place[4];                 // request, first row of the CTA, found
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= 320, "barrier block");
 
 // Matrix descriptor of a 128-byte-swizzled operand: 8 rows of 128 bytes make an atom, `sbo` the distance of
 // atoms along the strided dimension, `lbo` (MN-major only) that of 64-element panels.
@@ -111,6 +112,29 @@ __device__ __forceinline__ void pin32(uint32_t* r)
 #undef KDA_OUT
 #undef KDA_IN
 #undef KDA_BOTH
+// Whether the phase with the given parity is complete, without waiting (try_wait may suspend the thread).
+__device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// A warp's wait with one lane polling: 32 lanes on one barrier are 32 accesses, and they slow every other
+// barrier operation of the SM down.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane)
+{
+    bool ok = true;
+    if (lane == 0) ok = tc::mbar_wait(bar, parity, kPolls);
+    return __all_sync(~0u, ok);
+}
+
 // Request and first row of the CTA with index x among all row tiles; false past the last one.  One warp.
 __device__ __forceinline__ bool find_rows(const kv::Paged& c, int64_t x, int lane, int& b, int64_t& row0)
 {
@@ -149,13 +173,19 @@ struct Work {
 __device__ __forceinline__ bool seen_by_any(const Span& sp, int j) { return j < sp.hi && (j >= sp.lo || j < sp.sink_end); }
 __device__ __forceinline__ bool page_needed(const Span& sp, int j, int page) { return j < sp.hi && (j + page > sp.lo || j < sp.sink_end); }
 
+// A value tile with rows that nobody may see: what lies there is not known, and a weight of zero does not
+// stop a NaN.  Such tiles are at the end of the sinks, the start of the window and the end of the cache.
+__device__ __forceinline__ bool needs_mending(const Span& sp, int base)
+{
+    return base + kTile > sp.hi || (base < sp.lo && base + kTile > sp.sink_end);
+}
+
 template <int D>
 __device__ bool fill_bf16(const AttnCall& a, const Work& w, const CUtensorMap* km, const CUtensorMap* vm, uint8_t* ring, Bars* bars, int lane)
 {
     using C = Cfg<D, false>;
     const int shift = a.c.page_shift, page = 1 << shift, per_tile = kTile >> shift;
-    bool ok = true;
-    int idx = 0;
+    int idx = 0, mended = 0;
     for (int i = w.tile_lo; i < w.tile_hi; ++i) {
         const int base = attn::tile_base<kTile>(w.sp, i), j = base + lane * page;
         int64_t row = -1;
@@ -168,149 +198,207 @@ __device__ bool fill_bf16(const AttnCall& a, const Work& w, const CUtensorMap* k
         for (int which = 0; which < 2; ++which, ++idx) {
             const int slot = idx % C::kSlots;
             uint8_t* dst = ring + slot * C::kTileBytes + lane * page * 128;
-            ok = tc::mbar_wait(&bars->empty[slot], ((idx / C::kSlots) & 1) ^ 1, kPolls);
-            if (!__all_sync(~0u, ok)) return false;
-            if (lane == 0) tc::mbar_arrive_expect_tx(&bars->full[slot], bytes);
+            if (!warp_wait(&bars->empty[slot], ((idx / C::kSlots) & 1) ^ 1, lane)) return false;
+            uint64_t* bar = which && needs_mending(w.sp, base) ? &bars->patch[mended++] : &bars->full[slot];
+            if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
             __syncwarp();
             if (row >= 0) {
 #pragma unroll
                 for (int p = 0; p < D / 64; ++p)
-                    tc::tma_load_2d(dst + p * C::kPanel, which ? vm : km, p * 64, (int32_t)row, &bars->full[slot]);
+                    tc::tma_load_2d(dst + p * C::kPanel, which ? vm : km, p * 64, (int32_t)row, bar);
             }
         }
     }
     return true;
 }
 
+// One warp beside fill_bf16: value tiles that need it get zeros in their unseen rows before they count as full.
+template <int D>
+__device__ bool mend_bf16(const Work& w, uint8_t* ring, Bars* bars, int lane)
+{
+    using C = Cfg<D, false>;
+    int mended = 0;
+    for (int i = w.tile_lo; i < w.tile_hi; ++i) {
+        const int base = attn::tile_base<kTile>(w.sp, i), slot = (2 * (i - w.tile_lo) + 1) % C::kSlots;
+        if (!needs_mending(w.sp, base)) continue;
+        if (!warp_wait(&bars->patch[mended++], 0, lane)) return false;
+        uint8_t* vt = ring + slot * C::kTileBytes;
+        for (int r = lane; r < kTile; r += 32) {
+            if (seen_by_any(w.sp, base + r)) continue;
+#pragma unroll
+            for (int p = 0; p < D / 64; ++p)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vt + p * C::kPanel + r * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->full[slot]);
+    }
+    return true;
+}
+
+// 4-bit pages: the loads of the next tile are in flight while one is converted.
 template <int D>
 __device__ bool fill_fp4(const AttnCall& a, const Work& w, uint8_t* ring, Bars* bars, int tid)
 {
     using C = Cfg<D, true>;
-    constexpr int kUnits = D / 32, kAll = kTile * kUnits, kPer = (kAll + 95) / 96;   // 32-channel units of a row, a tile, a thread
-    const int shift = a.c.page_shift;
-    int idx = 0;
-    for (int i = w.tile_lo; i < w.tile_hi; ++i) {
-        const int base = attn::tile_base<kTile>(w.sp, i);
+    constexpr int kUnits = D / 32, kAll = kTile * kUnits;                  // 32-channel units of a row, of a tile
+    constexpr int kPer = (kAll + C::kFillThreads - 1) / C::kFillThreads;
+    const int shift = a.c.page_shift, total = 2 * (w.tile_hi - w.tile_lo);
+    uint4 x[kPer], nx[kPer];
+    uint32_t s[kPer], ns[kPer];
+    const auto load = [&](int idx, uint4* data, uint32_t* scale) {
+        const int base = attn::tile_base<kTile>(w.sp, w.tile_lo + (idx >> 1));
+        const uint8_t* src = idx & 1 ? a.c.v : a.c.k;
+        const uint8_t* scl = idx & 1 ? a.c.vs : a.c.ks;
 #pragma unroll
-        for (int which = 0; which < 2; ++which, ++idx) {
-            const int slot = idx % C::kSlots;
-            uint8_t* dst = ring + slot * C::kTileBytes;
-            const uint8_t* src = which ? a.c.v : a.c.k;
-            const uint8_t* scl = which ? a.c.vs : a.c.ks;
-            uint4 x[kPer];
-            uint32_t s[kPer];
-#pragma unroll
-            for (int n = 0; n < kPer; ++n) {
-                const int at = tid + 96 * n, r = at / kUnits, u = at % kUnits;
-                x[n] = make_uint4(0, 0, 0, 0);
-                s[n] = 0;
-                if (at < kAll && seen_by_any(w.sp, base + r)) {
-                    const int64_t row = kv::token_slot(a.c, w.b, base + r);
-                    if (row >= 0) {
-                        const int64_t t = row + ((int64_t)w.h << shift);
-                        x[n] = __ldg(reinterpret_cast<const uint4*>(src + t * (D / 2) + u * 16));
-                        s[n] = __ldg(reinterpret_cast<const uint16_t*>(scl + t * (D / 16) + u * 2));
-                    }
-                }
-            }
-            if (!tc::mbar_wait(&bars->empty[slot], ((idx / C::kSlots) & 1) ^ 1, kPolls)) return false;
-#pragma unroll
-            for (int n = 0; n < kPer; ++n) {
-                const int at = tid + 96 * n, r = at / kUnits, u = at % kUnits;
-                if (at >= kAll) break;
-                const uint32_t f = kv::e4m3x2_to_f16x2(s[n]);
-                const uint32_t f0 = __byte_perm(f, 0, 0x1010), f1 = __byte_perm(f, 0, 0x3232);
-                const uint32_t wd[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t y[4];
-                    kv::e2m1x8_to_f16(wd[q], y);
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        y[z] = kv::mul_f16x2(y[z], q < 2 ? f0 : f1);
-                        if (which) {                                    // at most 6 significant bits: exact in bf16 too
-                            const float2 f = kv::f16x2_to_f32(y[z]);
-                            y[z] = kv::f32_to_bf16x2(f.x, f.y);
-                        }
-                    }
-                    const int chunk = (u * 4 + q) & 7, panel = (u * 4 + q) >> 3;
-                    *reinterpret_cast<uint4*>(dst + panel * C::kPanel + r * 128 + ((chunk ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                }
-            }
-            tc::fence_proxy_async();
-            tc::mbar_arrive(&bars->full[slot]);
+        for (int n = 0; n < kPer; ++n) {
+            const int at = tid + C::kFillThreads * n, r = at / kUnits, u = at % kUnits;
+            data[n] = make_uint4(0, 0, 0, 0);
+            scale[n] = 0;
+            if (at >= kAll || !seen_by_any(w.sp, base + r)) continue;       // zeros where nobody looks
+            const int64_t row = kv::token_slot(a.c, w.b, base + r);
+            if (row < 0) continue;
+            const int64_t t = row + ((int64_t)w.h << shift);
+            data[n] = __ldg(reinterpret_cast<const uint4*>(src + t * (D / 2) + u * 16));
+            scale[n] = __ldg(reinterpret_cast<const uint16_t*>(scl + t * (D / 16) + u * 2));
         }
+    };
+    load(0, x, s);
+    int slot = 0;
+    uint32_t parity = 1;
+    for (int idx = 0; idx < total; ++idx) {
+        if (idx + 1 < total) load(idx + 1, nx, ns);
+        uint8_t* dst = ring + slot * C::kTileBytes;
+        if (!warp_wait(&bars->empty[slot], parity, tid & 31)) return false;
+#pragma unroll
+        for (int n = 0; n < kPer; ++n) {
+            const int at = tid + C::kFillThreads * n, r = at / kUnits, u = at % kUnits;
+            if (at >= kAll) break;
+            const uint32_t f = kv::e4m3x2_to_f16x2(s[n]);
+            const uint32_t f0 = __byte_perm(f, 0, 0x1010), f1 = __byte_perm(f, 0, 0x3232);
+            const uint32_t wd[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t y[4];
+                kv::e2m1x8_to_f16(wd[q], y);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    y[z] = kv::mul_f16x2(y[z], q < 2 ? f0 : f1);
+                    if (idx & 1) {                                          // at most 6 significant bits: exact in bf16 too
+                        const float2 g = kv::f16x2_to_f32(y[z]);
+                        y[z] = kv::f32_to_bf16x2(g.x, g.y);
+                    }
+                }
+                const int chunk = (u * 4 + q) & 7, panel = (u * 4 + q) >> 3;
+                *reinterpret_cast<uint4*>(dst + panel * C::kPanel + r * 128 + ((chunk ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        }
+        tc::fence_proxy_async();
+        __syncwarp();
+        if ((tid & 31) == 0) tc::mbar_arrive(&bars->full[slot]);
+        if (++slot == C::kSlots) slot = 0, parity ^= 1;
+#pragma unroll
+        for (int n = 0; n < kPer; ++n) x[n] = nx[n], s[n] = ns[n];
     }
     return true;
 }
 
-// ---- issuing the products --------------------------------------------------------------------------------
-template <int D, bool FP4>
-__device__ bool issue(const Work& w, const uint8_t* q, uint8_t* ring, Bars* bars, uint32_t tmem, int lane)
+// ---- issuing the products: one thread ------------------------------------------------------------------------
+// The tensor cores' queue is a few products deep, a wait costs its thread some 190 cycles even when there is
+// nothing to wait for, and a commit 110.  So each barrier is first looked at (Peek) while products are still
+// being issued and waited for only if it was not complete then, and the only commits are those of the scores:
+// that a tile's scores are complete tells its softmax that the keys and the last values are free, and it says
+// so.  (One thread per row tile hides the same waits, but the tiles fall into step and the tensor cores idle
+// while both softmaxes run.)
+struct Peek {
+    uint64_t* bar;
+    uint32_t parity;
+    bool done;
+    __device__ __forceinline__ void look(uint64_t* b, uint32_t p) { bar = b, parity = p, done = bar_test(b, p); }
+    __device__ __forceinline__ bool wait() const { return __all_sync(~0u, done) || __all_sync(~0u, tc::mbar_wait(bar, parity, kPolls)); }
+};
+
+template <int D, bool FP4, int NQ>
+__device__ bool issue(const int n_, const uint8_t* q, uint8_t* ring, Bars* bars, const uint32_t tmem_, const bool leader)
 {
+    const int n = (int)__reduce_max_sync(~0u, (unsigned)n_);
+    const uint32_t tmem = __reduce_max_sync(~0u, tmem_);
     using C = Cfg<D, FP4>;
     constexpr uint32_t id_s = idesc<FP4>(kTile, false), id_o = idesc<false>(D, true);
-    const int n = w.tile_hi - w.tile_lo;
-    const uint32_t q0 = tc::smem_u32(q), r0 = tc::smem_u32(ring);
-    const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, tc::mbar_wait(bar, parity, kPolls)); };
-    const auto full = [&](int idx) { return wait(&bars->full[idx % C::kSlots], (idx / C::kSlots) & 1); };
-    const auto scores = [&](int i, int j) {
-        if (lane == 0) {
-            const uint32_t kb = r0 + (2 * j % C::kSlots) * C::kTileBytes, qb = q0 + i * C::kTileBytes;
+    constexpr uint32_t kStep = C::kTileBytes >> 4;                          // descriptors count in units of 16 bytes
+    const uint64_t dq = desc_sw128(tc::smem_u32(q), 16, 1024);
+    const uint64_t dk = desc_sw128(tc::smem_u32(ring), 16, 1024), dv = desc_sw128(tc::smem_u32(ring), C::kPanel, 1024);
+    Peek vals, keys, part;
+    int ks = 0, vs = 1;                                                     // slots of the keys and the values, and
+    uint32_t kp = 0, vp = 0;                                                // the parities of their filling
+    const auto next = [](int& slot, uint32_t& parity) {
+        slot += 2;
+        if (slot >= C::kSlots) slot -= C::kSlots, parity ^= 1;
+    };
+    // S_i from the keys in slot ks; the next weights to come are looked at before its end
+    const auto scores = [&](const int i, const int next_i, uint32_t next_parity) {
+        const uint64_t b = dk + (uint32_t)ks * kStep;
+        if (leader) {
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const uint32_t off = (s / 4) * C::kPanel + (s % 4) * 32;
-                tc::mma_f16_ss(tmem + 128 * i, desc_sw128(qb + off, 16, 1024), desc_sw128(kb + off, 16, 1024), id_s, s > 0);
+            for (int s = 0; s < D / 16 - 2; ++s) {
+                const uint32_t off = ((s / 4) * C::kPanel + (s % 4) * 32) >> 4;
+                tc::mma_f16_ss(tmem + 128 * i, dq + (i * kStep + off), b + off, id_s, s > 0);
+            }
+        }
+        part.look(&bars->p_ready[next_i][0], next_parity);
+        if (leader) {
+#pragma unroll
+            for (int s = D / 16 - 2; s < D / 16; ++s) {
+                const uint32_t off = ((s / 4) * C::kPanel + (s % 4) * 32) >> 4;
+                tc::mma_f16_ss(tmem + 128 * i, dq + (i * kStep + off), b + off, id_s, s > 0);
             }
             tc::mma_commit(&bars->s_full[i]);
         }
-        __syncwarp();
     };
-    if (!full(0)) return false;
-    for (int i = 0; i < w.nq; ++i) {
-        if (!wait(&bars->q_full[i], 0)) return false;
-        scores(i, 0);
+    if (!tc::mbar_wait(&bars->full[0], 0, kPolls)) return false;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        if (!tc::mbar_wait(&bars->q_full[i], 0, kPolls)) return false;
+        scores(i, 0, 0);
     }
-    if (lane == 0) tc::mma_commit(&bars->empty[0]);
+    next(ks, kp);
+    vals.look(&bars->full[vs], vp);
+    if (n > 1) keys.look(&bars->full[ks], kp);
     for (int j = 0; j < n; ++j) {
-        const int vi = 2 * j + 1, slot = vi % C::kSlots;
-        uint8_t* vt = ring + slot * C::kTileBytes;
-        if (!full(vi)) return false;
-        if constexpr (!FP4) {
-            const int base = attn::tile_base<kTile>(w.sp, w.tile_lo + j);
-            if (base + kTile > w.sp.hi || (base < w.sp.lo && base + kTile > w.sp.sink_end)) {
-                for (int r = lane; r < kTile; r += 32) {
-                    if (seen_by_any(w.sp, base + r)) continue;
+        const bool more = j + 1 < n;
+        const uint64_t b = dv + (uint32_t)vs * kStep;
+        if (!vals.wait()) return false;
 #pragma unroll
-                    for (int p = 0; p < D / 64; ++p)
+        for (int i = 0; i < NQ; ++i) {
+            constexpr int kLast = NQ - 1;
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vt + p * C::kPanel + r * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+            for (int half = 0; half < 2; ++half) {
+                if (!part.wait()) return false;
+                tc::tc_fence_after();
+                if (half == 0) part.look(&bars->p_ready[i][1], j & 1);
+                else if (i < kLast && !more) part.look(&bars->p_ready[kLast][0], j & 1);
+                if (leader) {
+#pragma unroll
+                for (int s = 4 * half; s < 4 * half + 4; ++s)
+                    tc::mma_f16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * s, b + (s * 2048 >> 4), id_o, s > 0 ? 1u : (uint32_t)j);
                 }
-                tc::fence_proxy_async();
-                __syncwarp();
+            }
+            if (more) {
+                if (i == 0 && !keys.wait()) return false;
+                if (i == kLast) {
+                    next(vs, vp);
+                    vals.look(&bars->full[vs], vp);
+                }
+                scores(i, i == kLast ? 0 : kLast, (i == kLast ? j + 1 : j) & 1);
+                if (i == kLast) {
+                    next(ks, kp);
+                    if (j + 2 < n) keys.look(&bars->full[ks], kp);
+                }
+            } else if (leader) {
+                tc::mma_commit(&bars->o_full[i]);
             }
         }
-        for (int i = 0; i < w.nq; ++i) {
-            if (!wait(&bars->p_ready[i], j & 1)) return false;
-            tc::tc_fence_after();
-            if (lane == 0) {
-                const uint32_t vb = tc::smem_u32(vt);
-#pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                    tc::mma_f16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * s, desc_sw128(vb + s * 2048, C::kPanel, 1024), id_o, j > 0 || s > 0);
-                if (j + 1 == n) tc::mma_commit(&bars->o_full[i]);
-            }
-            __syncwarp();
-            if (j + 1 < n) {
-                if (i == 0 && !full(vi + 1)) return false;
-                scores(i, j + 1);
-            }
-        }
-        if (lane == 0) {
-            tc::mma_commit(&bars->empty[slot]);
-            if (j + 1 < n) tc::mma_commit(&bars->empty[(vi + 1) % C::kSlots]);
-        }
-        __syncwarp();
     }
     return true;
 }
@@ -341,43 +429,61 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
     return r;
 }
 
-// Loads query row `row` of the tile into its swizzled place; returns the factor from scores to log2.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+// A warp loads its 32 query rows of tile i into their swizzled places, D / 8 lanes to a row; returns the
+// factor from scores to log2 of the lane's own row.
 template <int D, bool FP4>
-__device__ __forceinline__ float load_query(const AttnCall& a, const Work& w, uint8_t* q, int tile_row)
+__device__ __forceinline__ float load_queries(const AttnCall& a, const Work& w, uint8_t* q, int i, int tid)
 {
     using C = Cfg<D, FP4>;
-    const int row = w.row0 + tile_row, r = tile_row & 127;
-    uint8_t* dst = q + (tile_row >> 7) * C::kTileBytes + r * 128;
-    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (w.t0 + row / a.c.G) * a.q_stride + (int64_t)(w.h * a.c.G + row % a.c.G) * D;
-    uint4 x[D / 8];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) x[i] = row < w.R ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;                    // lanes of a row, rows of a load
+    const int lane = tid & 31, chunk = lane % kLanes, G = a.c.G;
     float unit = a.scale * attn::kLog2e;
-    if constexpr (FP4) {
-        // fp16 operands: the row is divided by a power of two near its largest magnitude (see the few-rows form)
-        uint32_t top = 0;
+    uint8_t* tile = q + i * C::kTileBytes;
+    constexpr int kBatch = 8;
+#pragma unroll 1
+    for (int x0 = 0; x0 < 32 / kAtOnce; x0 += kBatch) {
+        uint4 v[kBatch];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-            for (int z = 0; z < 4; ++z) top = max(top, max(y[z] & 0x7fffu, (y[z] >> 16) & 0x7fffu));
+        for (int b = 0; b < kBatch; ++b) {
+            const int row = w.row0 + 128 * i + (tid & 96) + (x0 + b) * kAtOnce + lane / kLanes, t = a.token_of(row);
+            v[b] = make_uint4(0, 0, 0, 0);
+            if (row < w.R)
+                v[b] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + (w.t0 + t) * a.q_stride +
+                                                       (int64_t)(w.h * G + row - t * G) * D + 8 * chunk);
         }
-        const int e = min(max((int)(top >> 7), 1), 253);
-        const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-        unit *= __uint_as_float((uint32_t)e << 23);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int b = 0; b < kBatch; ++b) {
+            const int r = (tid & 96) + (x0 + b) * kAtOnce + lane / kLanes;
+            if constexpr (FP4) {
+                // fp16 operands: the row is divided by a power of two near its largest magnitude (see the few-rows form)
+                uint32_t y[4] = {v[b].x, v[b].y, v[b].z, v[b].w}, top = 0;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const float2 f = kv::bf16x2_to_f32(y[z]);
-                y[z] = kv::f32_to_f16x2(f.x * down, f.y * down);
+                for (int z = 0; z < 4; ++z) top = max(top, max(y[z] & 0x7fffu, (y[z] >> 16) & 0x7fffu));
+#pragma unroll
+                for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+                const int e = min(max((int)(top >> 7), 1), 253);
+                const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float2 f = kv::bf16x2_to_f32(y[z]);
+                    y[z] = kv::f32_to_f16x2(f.x * down, f.y * down);
+                }
+                v[b] = make_uint4(y[0], y[1], y[2], y[3]);
+                // the lane whose row this is takes the factor
+                const float mine = __shfl_sync(~0u, up, lane % kAtOnce * kLanes);
+                if (lane / kAtOnce == x0 + b) unit *= mine;
             }
-            x[i] = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(tile + (chunk >> 3) * C::kPanel + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)) = v[b];
         }
     }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(dst + (i >> 3) * C::kPanel + (((i & 7) ^ (r & 7)) << 4)) = x[i];
     return unit;
 }
 
@@ -385,24 +491,26 @@ template <int D, bool FP4>
 __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, int parts_here, int part, uint8_t* q, Bars* bars, uint32_t tmem,
                         int i, int tid)
 {
+    using C = Cfg<D, FP4>;
     const int tile_row = 128 * i + tid, row = w.row0 + tile_row;
-    const float unit = load_query<D, FP4>(a, w, q, tile_row);
+    const float unit = load_queries<D, FP4>(a, w, q, i, tid);
+    const int lane = tid & 31;
     tc::fence_proxy_async();
-    tc::mbar_arrive(&bars->q_full[i]);
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bars->q_full[i]);
 
     const uint32_t lanes = (uint32_t)(tid & 96) << 16;                  // the warp's 32 tensor-memory lanes
     const uint32_t ts = tmem + 128 * i + lanes, to = tmem + 256 + D * i + lanes;
-    const int p = w.first + row / a.c.G;
-    const int p_lo = w.first + (w.row0 + 128 * i) / a.c.G;                // of the tile's first and last row
-    const int p_hi = w.first + min(w.R - 1, w.row0 + 128 * i + 127) / a.c.G;
+    const int p = w.first + a.token_of(row);
+    const int p_lo = w.first + a.token_of(w.row0 + 128 * i);                // of the tile's first and last row
+    const int p_hi = w.first + a.token_of(min(w.R - 1, w.row0 + 128 * i + 127));
     const int n = w.tile_hi - w.tile_lo;
     float m = -INFINITY;
-    uint64_t l2 = pack2(0.f, 0.f);
-    bool ok = true;
+    uint64_t l2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+    int key_slot = 0;
     for (int j = 0; j < n; ++j) {
         const int base = attn::tile_base<kTile>(w.sp, w.tile_lo + j);
-        ok = __all_sync(~0u, tc::mbar_wait(&bars->s_full[i], j & 1, kPolls));
-        if (!ok) return false;
+        if (!warp_wait(&bars->s_full[i], j & 1, lane)) return false;
         tc::tc_fence_after();
         uint32_t s[128];
 #pragma unroll
@@ -412,36 +520,38 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
         for (int x = 0; x < 4; ++x) pin32(s + 32 * x);
         const bool whole = base + kTile <= w.sp.hi && base + kTile - 1 <= p_lo && (a.window == 0 || base > p_hi - a.window || base + kTile <= a.sinks);
         if (!whole) {
-            // visible columns: [from, to) and [0, sink)
+            // visible columns: those below `end` that are from `from` on or below `sink`, 32 to a word
             const int end = min(p + 1, w.sp.hi) - base, from = a.window ? p - a.window + 1 - base : 0, sink = a.sinks - base;
 #pragma unroll
-            for (int x = 0; x < 128; ++x)
-                if (!(x < end && (x >= from || x < sink))) s[x] = 0xff800000u;
-        }
-        float top = -INFINITY;
-        {
-            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int x = 0; x < 128; x += 32) {
+                const uint32_t on = low_bits(end - x) & (~low_bits(from - x) | low_bits(sink - x));
 #pragma unroll
-            for (int x = 0; x < 128; x += 8)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) t4[z] = fmaxf(t4[z], fmaxf(__uint_as_float(s[x + 2 * z]), __uint_as_float(s[x + 2 * z + 1])));
-            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * unit;
+                for (int z = 0; z < 32; ++z)
+                    if (!(on & (1u << z))) s[x + z] = 0xff800000u;
+            }
         }
+        float t4[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) t4[z] = fmaxf(__uint_as_float(s[2 * z]), __uint_as_float(s[2 * z + 1]));
+#pragma unroll
+        for (int x = 8; x < 128; x += 8)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], __uint_as_float(s[x + 2 * z]), __uint_as_float(s[x + 2 * z + 1]));
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * unit;
         if (__any_sync(~0u, top > m + kSlack)) {
             const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.f : attn::ex2(m - mn);
             m = mn;
             const uint64_t f2 = pack2(f, f);
-            l2 = fma2(l2, f2, pack2(0.f, 0.f));
+            l2[0] = fma2(l2[0], f2, pack2(0.f, 0.f));
+            l2[1] = fma2(l2[1], f2, pack2(0.f, 0.f));
             if (j > 0) {
 #pragma unroll
-                for (int x = 0; x < D; x += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(to + x, o);
-                    tmem_wait_ld();
-                    pin32(o);
+                for (int x = 0; x < D; x += 16) {                      // 16 at a time: the scores stay in registers
+                    float o[16];
+                    tc::tmem_ld16(to + x, o);
 #pragma unroll
-                    for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
-                    tmem_st32(to + x, o);
+                    for (int z = 0; z < 16; ++z) o[z] *= f;
+                    tc::tmem_st16_nowait(to + x, o);
                 }
             }
         }
@@ -455,65 +565,106 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
                 const int e = 64 * half + 2 * x;
                 const float2 y = unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), u2, m2));
                 const float e0 = attn::ex2(y.x), e1 = attn::ex2(y.y);
-                l2 = add2(l2, pack2(e0, e1));
+                l2[x & 1] = add2(l2[x & 1], pack2(e0, e1));
                 pk[x] = kv::f32_to_bf16x2(e0, e1);
             }
             tmem_st32(ts + 32 * half, pk);
+            tc::tmem_wait_st();                                        // half of the product can start
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars->p_ready[i][half]);
         }
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        tc::mbar_arrive(&bars->p_ready[i]);
+        // these scores were complete, so the products before them are: their keys and the last values are free
+        // (a CTA of one row tile counts for both)
+        if (tid == 0) {
+            for (int x = w.nq; x < 3; ++x) {
+                tc::mbar_arrive(&bars->empty[key_slot]);
+                if (j > 0) tc::mbar_arrive(&bars->empty[key_slot == 0 ? C::kSlots - 1 : key_slot - 1]);
+            }
+            key_slot = key_slot + 2 < C::kSlots ? key_slot + 2 : key_slot + 2 - C::kSlots;
+        }
     }
 
     // ---- the row's output --------------------------------------------------------------------------------
-    const float2 lp = unpack2(l2);
+    const float2 lp = unpack2(add2(l2[0], l2[1]));
     const float l = lp.x + lp.y;
     if (n > 0) {
-        ok = __all_sync(~0u, tc::mbar_wait(&bars->o_full[i], 0, kPolls));
-        if (!ok) return false;
+        if (!warp_wait(&bars->o_full[i], 0, lane)) return false;
         tc::tc_fence_after();
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const float lse2 = l == 0.f ? -INFINITY : m + attn::lg2(l);
-    const int64_t out_row = (w.t0 + row / a.c.G) * a.c.Hq + w.h * a.c.G + row % a.c.G;
-    const int64_t at = out_row * parts.max_parts + part;
+    const int G = a.c.G;
+    const auto out_row = [&](int rw) {
+        const int t = a.token_of(rw);
+        return (w.t0 + t) * a.c.Hq + w.h * G + rw - t * G;
+    };
     const bool live = row < w.R;
-#pragma unroll
-    for (int x = 0; x < D; x += 32) {
-        uint32_t o[32];
+    // 128 bytes of a row at a time through the tile's place among the queries, which no product reads any
+    // more, so that eight neighbouring lanes write them.
+    uint8_t* stage = q + i * C::kTileBytes + (tid & 96) * (C::kTileBytes / 128);
+#pragma unroll 1
+    for (int x = 0; x < D; x += 64) {
+        uint32_t o[64];
         if (n > 0) {
             tmem_ld32(to + x, o);
+            tmem_ld32(to + x + 32, o + 32);
             tmem_wait_ld();
             pin32(o);
+            pin32(o + 32);
         }
-        if (!live) continue;
         // a row whose weights are all zero may stand beside non-finite products: its output is zero
 #pragma unroll
-        for (int z = 0; z < 32; ++z) o[z] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[z]) * inv);
+        for (int z = 0; z < 64; ++z) o[z] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[z]) * inv);
         if (parts_here > 1) {
-            uint4* dst = reinterpret_cast<uint4*>(parts.o + at * D + x);
+            // a warp's 32 rows x 32 channels of fp32 at a time: 4 KB
 #pragma unroll
-            for (int z = 0; z < 8; ++z) dst[z] = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((z ^ (lane & 7)) << 4)) =
+                        make_uint4(o[32 * half + 4 * z], o[32 * half + 4 * z + 1], o[32 * half + 4 * z + 2], o[32 * half + 4 * z + 3]);
+                __syncwarp();
+                uint4 v[8];
+#pragma unroll
+                for (int z = 0; z < 8; ++z) v[z] = *reinterpret_cast<const uint4*>(stage + (z * 4 + lane / 8) * 128 + ((lane % 8 ^ (z * 4 + lane / 8 & 7)) << 4));
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    const int rw = w.row0 + 128 * i + (tid & 96) + z * 4 + lane / 8;
+                    if (rw < w.R) *reinterpret_cast<uint4*>(parts.o + (out_row(rw) * parts.max_parts + part) * D + x + 32 * half + 4 * (lane % 8)) = v[z];
+                }
+                __syncwarp();
+            }
         } else {
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + out_row * D + x);
+            // 64 channels of bf16: 128 bytes a row
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
+            for (int z = 0; z < 8; ++z) {
                 uint32_t y[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[k] = kv::f32_to_bf16x2(__uint_as_float(o[8 * z + 2 * k]), __uint_as_float(o[8 * z + 2 * k + 1]));
-                dst[z] = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((z ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
             }
+            __syncwarp();
+            uint4 v[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) v[z] = *reinterpret_cast<const uint4*>(stage + (z * 4 + lane / 8) * 128 + ((lane % 8 ^ (z * 4 + lane / 8 & 7)) << 4));
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+                const int rw = w.row0 + 128 * i + (tid & 96) + z * 4 + lane / 8;
+                if (rw < w.R) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + out_row(rw) * D + x + 8 * (lane % 8)) = v[z];
+            }
+            __syncwarp();
         }
     }
     if (live) {
-        if (parts_here > 1) parts.lse2[at] = lse2;
-        else if (a.lse) a.lse[out_row] = lse2 * attn::kLn2;
+        if (parts_here > 1) parts.lse2[out_row(row) * parts.max_parts + part] = lse2;
+        else if (a.lse) a.lse[out_row(row)] = lse2 * attn::kLn2;
     }
     return true;
 }
 
 template <int D, bool FP4>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, FP4>::kThreads, 1)
     many_rows_kernel(AttnCall a, Parts parts, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm)
 {
     a.c.err = &g_attn_tc_error;
@@ -532,15 +683,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) bars->place[0] = found ? 1 : 0, bars->place[1] = b, bars->place[2] = (int32_t)row0;
     } else if (warp == 1 && lane == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            tc::mbar_init(&bars->full[i], FP4 ? C::kFillThreads : 1);
-            tc::mbar_init(&bars->empty[i], 1);
+            tc::mbar_init(&bars->full[i], FP4 ? C::kFillThreads / 32 : 1);
+            tc::mbar_init(&bars->empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bars->q_full[i], 128);
+            tc::mbar_init(&bars->q_full[i], 4);
             tc::mbar_init(&bars->s_full[i], 1);
-            tc::mbar_init(&bars->p_ready[i], 128);
+            tc::mbar_init(&bars->p_ready[i][0], 4);
+            tc::mbar_init(&bars->p_ready[i][1], 4);
             tc::mbar_init(&bars->o_full[i], 1);
         }
+        for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->patch[i], 1);
         tc::mbar_init(&bars->drain, 1);
         tc::fence_mbar_init();
     } else if (warp == 8) {
@@ -566,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.R = fresh * a.c.G;
         if (threadIdx.x == 0 && part == 0 && w.h == 0 && (len > a.max_len || fresh > a.max_new)) kv::record(a.c, kv::kErrLength);
         w.first = len > 0 ? len - fresh : -1 - fresh;
-        const int lo = w.first + w.row0 / a.c.G, hi = w.first + min(w.R - 1, w.row0 + kRows - 1) / a.c.G;
+        const int lo = w.first + a.token_of(w.row0), hi = w.first + a.token_of(min(w.R - 1, w.row0 + kRows - 1));
         w.sp = attn::make_span<kTile>(max(lo, 0), len > 0 ? hi : -1, a.max_len, a.window, a.sinks);
         w.nq = w.R - w.row0 > 128 ? 2 : 1;
         if (parts.o) parts_here = min(parts.max_parts, max(1, (w.sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part));
@@ -576,14 +729,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     bool ok = true;
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         if (live && warp / 4 < w.nq) ok = softmax<D, FP4>(a, parts, w, parts_here, part, q, bars, tmem, warp / 4, threadIdx.x % 128);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (live && w.tile_hi > w.tile_lo) {
             if (warp == 8) {
-                ok = issue<D, FP4>(w, q, ring, bars, tmem, lane);
-                if (lane == 0) tc::mma_commit(&bars->drain);           // everything issued ends before the exit
+                const int n = w.tile_hi - w.tile_lo;
+                uint32_t leader = 0;
+                asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+                ok = w.nq == 2 ? issue<D, FP4, 2>(n, q, ring, bars, tmem, leader) : issue<D, FP4, 1>(n, q, ring, bars, tmem, leader);
+                if (leader) tc::mma_commit(&bars->drain);              // everything issued ends before the exit
                 __syncwarp();
                 ok = tc::mbar_wait(&bars->drain, 0, kPolls) && ok;
             } else if constexpr (FP4) {
@@ -594,7 +750,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < C::kSlots; ++i) {
                         tc::mbar_wait(&bars->full[i], 0, 1u << 16);
                         tc::mbar_wait(&bars->full[i], 1, 1u << 16);
+                        if (i < 4) tc::mbar_wait(&bars->patch[i], 0, 1u << 16);
                     }
+            } else if (warp == 10) {
+                ok = mend_bf16<D>(w, ring, bars, lane);
             }
         }
     }
@@ -702,7 +861,7 @@ cudaError_t launch_many(const kda_kv_params& p, const AttnCall& a, const Parts& 
     cudaError_t e = cudaFuncSetAttribute(many_rows_kernel<D, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = row_tiles(p, a.c.n, a.c.T, a.max_new);
-    many_rows_kernel<D, FP4><<<dim3((unsigned)(tiles * a.c.Hkv), (unsigned)parts.max_parts), kThreads, C::kSmem, stream>>>(a, parts, km, vm);
+    many_rows_kernel<D, FP4><<<dim3((unsigned)(tiles * a.c.Hkv), (unsigned)parts.max_parts), C::kThreads, C::kSmem, stream>>>(a, parts, km, vm);
     e = cudaGetLastError();
     if (e != cudaSuccess || parts.max_parts == 1) return e;
     join_rows_kernel<D><<<(unsigned)((a.c.T * a.c.Hq + 3) / 4), 128, 0, stream>>>(a, parts);

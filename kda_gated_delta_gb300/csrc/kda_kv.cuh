@@ -203,6 +203,8 @@ struct AttnCall {
     float scale;
     void* out;
     float* lse;
+    uint64_t by_group;         // 2^36 / G rounded up: row / G for row < 2^22 G is (row * by_group) >> 36
+    __device__ __forceinline__ int token_of(int row) const { return (int)(((uint64_t)(uint32_t)row * by_group) >> 36); }
 };
 size_t attention_workspace_bytes(const kda_kv_params& p, int32_t num_seqs, int64_t total_tokens, int32_t max_new,
                                  int32_t max_len);

@@ -165,6 +165,7 @@ int32_t kda_paged_attention(const kda_kv_params* p, const void* q, int64_t q_str
     a.scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / sqrtf((float)p->head_dim);
     a.out = out;
     a.lse = lse;
+    a.by_group = (((uint64_t)1 << 36) + a.c.G - 1) / a.c.G;
     return from_cuda(kda::launch_attention(*p, a, workspace, (cudaStream_t)stream));
 }
 
