@@ -6,15 +6,15 @@
 // tokens that any of them may see in tiles of 128:
 //
 //   S_i = Q_i K_j^T      M 128 (rows) x N 128 (tokens) x K D, both operands K-major in shared memory
-//   P_i = exp2(S_i - m)  one thread per row: no shuffles; packed over S_i's own columns
+//   P_i = exp2(S_i - m)  one thread per row: no shuffles; packed over half of S_i's own columns
 //   O_i += P_i V_j       A from tensor memory, V_j as it lies in the cache (MN-major)
 //
-// Tensor memory, all 512 columns: S_0, S_1 (128 each; P_i takes the first 64 of S_i's) and O_0, O_1 (D each).
+// Tensor memory, all 512 columns: S_0, S_1 (128 each; P_i takes the last 64 of S_i's) and O_0, O_1 (D each).
 // Roles: warps 0-3 and 4-7 are the softmax of row tile 0 and 1, a thread of warp 8 issues the products,
 // the warps after it fill a ring of key and value tiles (128 tokens x D, 128-byte swizzle).  The products go
 // PV_0(j), S_0(j+1), PV_1(j), S_1(j+1), so that each softmax works while the other tile's products run.
 //   bf16 cache: one warp, a lane per page, two tensor-map copies (64 channels each) per page and tile;
-//   4-bit cache: three warps convert on the way into shared memory, exactly: keys to fp16 (one instruction a
+//   4-bit cache: seven warps convert on the way into shared memory, exactly: keys to fp16 (one instruction a
 //   pair; the queries are fp16 then, each row divided by a power of two), values to bf16, whose range the
 //   weights need.
 // A rescaling of O happens only when a row's maximum grows by more than 2^8 since the last one; the S_i(j)
@@ -48,11 +48,8 @@ constexpr float kSlack = 8.0f;
 
 template <int D, bool FP4>
 struct Cfg {
-    static constexpr int kFillThreads = FP4 ? 96 : 32;
-    // Registers: the launch gives each of the 384 threads 168 (64,512 of the SM's 65,536); the last warpgroup
-    // gives back what it does not need, and 192 hold a row of 128 scores without spilling.
-    static constexpr int kThreads = 384, kSoftmaxRegs = 192, kOtherRegs = 112;
-    static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+    static constexpr int kFillThreads = FP4 ? 224 : 32;
+    static constexpr int kThreads = FP4 ? 512 : 384;
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kSlots = D == 128 ? 5 : 8;
     static constexpr int kPanel = kTile * 128;               // 64 channels of 128 rows
@@ -244,33 +241,47 @@ __device__ bool fill_fp4(const AttnCall& a, const Work& w, uint8_t* ring, Bars* 
     using C = Cfg<D, true>;
     constexpr int kUnits = D / 32, kAll = kTile * kUnits;                  // 32-channel units of a row, of a tile
     constexpr int kPer = (kAll + C::kFillThreads - 1) / C::kFillThreads;
-    const int shift = a.c.page_shift, total = 2 * (w.tile_hi - w.tile_lo);
+    const int shift = a.c.page_shift, page = 1 << shift, total = 2 * (w.tile_hi - w.tile_lo), lane = tid & 31;
     uint4 x[kPer], nx[kPer];
     uint32_t s[kPer], ns[kPer];
-    const auto load = [&](int idx, uint4* data, uint32_t* scale) {
+    // a lane's page of a tile: the cache row it starts at (rows are below 2^31), -1 where nobody looks
+    const auto page_of = [&](int i) {
+        const int j = attn::tile_base<kTile>(w.sp, i) + lane * page;
+        if (lane >= kTile >> shift || !page_needed(w.sp, j, page)) return -1;
+        const int64_t row = kv::token_slot(a.c, w.b, j);
+        return row < 0 ? -1 : (int32_t)(row + ((int64_t)w.h << shift));
+    };
+    int32_t here = page_of(w.tile_lo), ahead = -1;
+    const auto load = [&](int idx, int32_t pages, uint4* data, uint32_t* scale) {
         const int base = attn::tile_base<kTile>(w.sp, w.tile_lo + (idx >> 1));
         const uint8_t* src = idx & 1 ? a.c.v : a.c.k;
         const uint8_t* scl = idx & 1 ? a.c.vs : a.c.ks;
 #pragma unroll
         for (int n = 0; n < kPer; ++n) {
             const int at = tid + C::kFillThreads * n, r = at / kUnits, u = at % kUnits;
-            data[n] = make_uint4(0, 0, 0, 0);
+            const int32_t row = __shfl_sync(~0u, pages, (r & (kTile - 1)) >> shift);
+            data[n] = make_uint4(0, 0, 0, 0);                               // zeros where nobody looks
             scale[n] = 0;
-            if (at >= kAll || !seen_by_any(w.sp, base + r)) continue;       // zeros where nobody looks
-            const int64_t row = kv::token_slot(a.c, w.b, base + r);
-            if (row < 0) continue;
-            const int64_t t = row + ((int64_t)w.h << shift);
-            data[n] = __ldg(reinterpret_cast<const uint4*>(src + t * (D / 2) + u * 16));
-            scale[n] = __ldg(reinterpret_cast<const uint16_t*>(scl + t * (D / 16) + u * 2));
+            if (at < kAll && row >= 0 && seen_by_any(w.sp, base + r)) {
+                const int64_t t = row + (r & (page - 1));
+                data[n] = __ldg(reinterpret_cast<const uint4*>(src + t * (D / 2) + u * 16));
+                scale[n] = __ldg(reinterpret_cast<const uint16_t*>(scl + t * (D / 16) + u * 2));
+            }
         }
     };
-    load(0, x, s);
+    load(0, here, x, s);
     int slot = 0;
     uint32_t parity = 1;
     for (int idx = 0; idx < total; ++idx) {
-        if (idx + 1 < total) load(idx + 1, nx, ns);
+        if (!(idx & 1)) {
+            load(idx + 1, here, nx, ns);                                    // the tile's values; its successor's pages
+            if (idx + 2 < total) ahead = page_of(w.tile_lo + (idx >> 1) + 1);
+        } else if (idx + 1 < total) {
+            here = ahead;
+            load(idx + 1, here, nx, ns);
+        }
         uint8_t* dst = ring + slot * C::kTileBytes;
-        if (!warp_wait(&bars->empty[slot], parity, tid & 31)) return false;
+        if (!warp_wait(&bars->empty[slot], parity, lane)) return false;
 #pragma unroll
         for (int n = 0; n < kPer; ++n) {
             const int at = tid + C::kFillThreads * n, r = at / kUnits, u = at % kUnits;
@@ -296,7 +307,7 @@ __device__ bool fill_fp4(const AttnCall& a, const Work& w, uint8_t* ring, Bars* 
         }
         tc::fence_proxy_async();
         __syncwarp();
-        if ((tid & 31) == 0) tc::mbar_arrive(&bars->full[slot]);
+        if (lane == 0) tc::mbar_arrive(&bars->full[slot]);
         if (++slot == C::kSlots) slot = 0, parity ^= 1;
 #pragma unroll
         for (int n = 0; n < kPer; ++n) x[n] = nx[n], s[n] = ns[n];
@@ -346,7 +357,7 @@ __device__ bool issue(const int n_, const uint8_t* q, uint8_t* ring, Bars* bars,
                 tc::mma_f16_ss(tmem + 128 * i, dq + (i * kStep + off), b + off, id_s, s > 0);
             }
         }
-        part.look(&bars->p_ready[next_i][0], next_parity);
+        part.look(&bars->p_ready[next_i][1], next_parity);
         if (leader) {
 #pragma unroll
             for (int s = D / 16 - 2; s < D / 16; ++s) {
@@ -373,15 +384,15 @@ __device__ bool issue(const int n_, const uint8_t* q, uint8_t* ring, Bars* bars,
         for (int i = 0; i < NQ; ++i) {
             constexpr int kLast = NQ - 1;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 1; half >= 0; --half) {                        // the softmax hands over the high half first
                 if (!part.wait()) return false;
                 tc::tc_fence_after();
-                if (half == 0) part.look(&bars->p_ready[i][1], j & 1);
-                else if (i < kLast && !more) part.look(&bars->p_ready[kLast][0], j & 1);
+                if (half == 1) part.look(&bars->p_ready[i][0], j & 1);
+                else if (i < kLast && !more) part.look(&bars->p_ready[kLast][1], j & 1);
                 if (leader) {
 #pragma unroll
                 for (int s = 4 * half; s < 4 * half + 4; ++s)
-                    tc::mma_f16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * s, b + (s * 2048 >> 4), id_o, s > 0 ? 1u : (uint32_t)j);
+                    tc::mma_f16_ts(tmem + 256 + D * i, tmem + 128 * i + 64 + 8 * s, b + (s * 2048 >> 4), id_o, s != 4 ? 1u : (uint32_t)j);
                 }
             }
             if (more) {
@@ -512,32 +523,43 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
         const int base = attn::tile_base<kTile>(w.sp, w.tile_lo + j);
         if (!warp_wait(&bars->s_full[i], j & 1, lane)) return false;
         tc::tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s + 32 * x);
-        tmem_wait_ld();
-#pragma unroll
-        for (int x = 0; x < 4; ++x) pin32(s + 32 * x);
         const bool whole = base + kTile <= w.sp.hi && base + kTile - 1 <= p_lo && (a.window == 0 || base > p_hi - a.window || base + kTile <= a.sinks);
-        if (!whole) {
+        // Half a row of scores at a time: the low half for its maximum, then the high half, whose weights are
+        // taken and handed over first, then the low half again.  64 scores and 32 packed weights fit where 128
+        // scores spilled.
+        uint32_t s[64];
+        const auto load = [&](const int half) {
+            tmem_ld32(ts + 64 * half, s);
+            tmem_ld32(ts + 64 * half + 32, s + 32);
+            tmem_wait_ld();
+            pin32(s);
+            pin32(s + 32);
+            if (whole) return;
             // visible columns: those below `end` that are from `from` on or below `sink`, 32 to a word
             const int end = min(p + 1, w.sp.hi) - base, from = a.window ? p - a.window + 1 - base : 0, sink = a.sinks - base;
 #pragma unroll
-            for (int x = 0; x < 128; x += 32) {
-                const uint32_t on = low_bits(end - x) & (~low_bits(from - x) | low_bits(sink - x));
+            for (int x = 0; x < 64; x += 32) {
+                const int c = 64 * half + x;
+                const uint32_t on = low_bits(end - c) & (~low_bits(from - c) | low_bits(sink - c));
 #pragma unroll
                 for (int z = 0; z < 32; ++z)
                     if (!(on & (1u << z))) s[x + z] = 0xff800000u;
             }
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            load(half);
+            float t4[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) t4[z] = fmaxf(__uint_as_float(s[2 * z]), __uint_as_float(s[2 * z + 1]));
+#pragma unroll
+            for (int x = 8; x < 64; x += 8)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], __uint_as_float(s[x + 2 * z]), __uint_as_float(s[x + 2 * z + 1]));
+            top = max3(top, fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         }
-        float t4[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) t4[z] = fmaxf(__uint_as_float(s[2 * z]), __uint_as_float(s[2 * z + 1]));
-#pragma unroll
-        for (int x = 8; x < 128; x += 8)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], __uint_as_float(s[x + 2 * z]), __uint_as_float(s[x + 2 * z + 1]));
-        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * unit;
+        top *= unit;
         if (__any_sync(~0u, top > m + kSlack)) {
             const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.f : attn::ex2(m - mn);
             m = mn;
@@ -558,17 +580,17 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
         const float mu = m == -INFINITY ? 0.f : m;
         const uint64_t u2 = pack2(unit, unit), m2 = pack2(-mu, -mu);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 1; half >= 0; --half) {
+            if (half == 0) load(0);
             uint32_t pk[32];
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
-                const int e = 64 * half + 2 * x;
-                const float2 y = unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), u2, m2));
+                const float2 y = unpack2(fma2(pack2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), u2, m2));
                 const float e0 = attn::ex2(y.x), e1 = attn::ex2(y.y);
                 l2[x & 1] = add2(l2[x & 1], pack2(e0, e1));
                 pk[x] = kv::f32_to_bf16x2(e0, e1);
             }
-            tmem_st32(ts + 32 * half, pk);
+            tmem_st32(ts + 64 + 32 * half, pk);
             tc::tmem_wait_st();                                        // half of the product can start
             tc::tc_fence_before();
             __syncwarp();
@@ -729,10 +751,8 @@ __global__ void __launch_bounds__(Cfg<D, FP4>::kThreads, 1)
     }
     bool ok = true;
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         if (live && warp / 4 < w.nq) ok = softmax<D, FP4>(a, parts, w, parts_here, part, q, bars, tmem, warp / 4, threadIdx.x % 128);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (live && w.tile_hi > w.tile_lo) {
             if (warp == 8) {
                 const int n = w.tile_hi - w.tile_lo;
