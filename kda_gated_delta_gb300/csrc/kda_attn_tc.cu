@@ -458,6 +458,21 @@ __device__ __forceinline__ float load_queries(const AttnCall& a, const Work& w, 
     const int lane = tid & 31, chunk = lane % kLanes, G = a.c.G;
     float unit = a.scale * attn::kLog2e;
     uint8_t* tile = q + i * C::kTileBytes;
+    if constexpr (!FP4) {
+#pragma unroll 4
+        for (int x = 0; x < 32 / kAtOnce; ++x) {
+            const int r = (tid & 96) + x * kAtOnce + lane / kLanes, row = w.row0 + 128 * i + r, t = a.token_of(row);
+            const bool on = row < w.R;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (on ? (w.t0 + t) * a.q_stride + (int64_t)(w.h * G + row - t * G) * D + 8 * chunk : 0);
+            // 16 bytes, or zeros for a row past the last
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             tc::smem_u32(tile + (chunk >> 3) * C::kPanel + r * 128 + (((chunk & 7) ^ (r & 7)) << 4))),
+                         "l"(src), "r"(on ? 16 : 0)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return unit;
+    }
     constexpr int kBatch = 8;
 #pragma unroll 1
     for (int x0 = 0; x0 < 32 / kAtOnce; x0 += kBatch) {
@@ -526,62 +541,59 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
         const bool whole = base + kTile <= w.sp.hi && base + kTile - 1 <= p_lo && (a.window == 0 || base > p_hi - a.window || base + kTile <= a.sinks);
         // Half a row of scores at a time: the low half for its maximum, then the high half, whose weights are
         // taken and handed over first, then the low half again.  64 scores and 32 packed weights fit where 128
-        // scores spilled.
-        uint32_t s[64];
-        const auto load = [&](const int half) {
+        // scores spilled.  The steps are written out for tiles that every row sees whole; the others, one or
+        // two of a CTA, loop over one copy, which is fetched in less time than it takes to run.
+        float top = -INFINITY;
+        const auto run = [&](const int step, const bool edge) {
+            const int half = step & 1;
+            uint32_t s[64];
             tmem_ld32(ts + 64 * half, s);
             tmem_ld32(ts + 64 * half + 32, s + 32);
             tmem_wait_ld();
             pin32(s);
             pin32(s + 32);
-            if (whole) return;
-            // visible columns: those below `end` that are from `from` on or below `sink`, 32 to a word
-            const int end = min(p + 1, w.sp.hi) - base, from = a.window ? p - a.window + 1 - base : 0, sink = a.sinks - base;
+            if (edge) {
+                // visible columns: those below `end` that are from `from` on or below `sink`, 32 to a word
+                const int c = base + 64 * half, end = min(p + 1, w.sp.hi) - c, from = a.window ? p - a.window + 1 - c : 0, sink = a.sinks - c;
 #pragma unroll
-            for (int x = 0; x < 64; x += 32) {
-                const int c = 64 * half + x;
-                const uint32_t on = low_bits(end - c) & (~low_bits(from - c) | low_bits(sink - c));
+                for (int x = 0; x < 64; x += 32) {
+                    const uint32_t on = low_bits(end - x) & (~low_bits(from - x) | low_bits(sink - x));
 #pragma unroll
-                for (int z = 0; z < 32; ++z)
-                    if (!(on & (1u << z))) s[x + z] = 0xff800000u;
-            }
-        };
-        float top = -INFINITY;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            load(half);
-            float t4[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) t4[z] = fmaxf(__uint_as_float(s[2 * z]), __uint_as_float(s[2 * z + 1]));
-#pragma unroll
-            for (int x = 8; x < 64; x += 8)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], __uint_as_float(s[x + 2 * z]), __uint_as_float(s[x + 2 * z + 1]));
-            top = max3(top, fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-        }
-        top *= unit;
-        if (__any_sync(~0u, top > m + kSlack)) {
-            const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.f : attn::ex2(m - mn);
-            m = mn;
-            const uint64_t f2 = pack2(f, f);
-            l2[0] = fma2(l2[0], f2, pack2(0.f, 0.f));
-            l2[1] = fma2(l2[1], f2, pack2(0.f, 0.f));
-            if (j > 0) {
-#pragma unroll
-                for (int x = 0; x < D; x += 16) {                      // 16 at a time: the scores stay in registers
-                    float o[16];
-                    tc::tmem_ld16(to + x, o);
-#pragma unroll
-                    for (int z = 0; z < 16; ++z) o[z] *= f;
-                    tc::tmem_st16_nowait(to + x, o);
+                    for (int z = 0; z < 32; ++z)
+                        if (!(on & (1u << z))) s[x + z] = 0xff800000u;
                 }
             }
-        }
-        const float mu = m == -INFINITY ? 0.f : m;
-        const uint64_t u2 = pack2(unit, unit), m2 = pack2(-mu, -mu);
+            if (step < 2) {
+                float t4[4];
 #pragma unroll
-        for (int half = 1; half >= 0; --half) {
-            if (half == 0) load(0);
+                for (int z = 0; z < 4; ++z) t4[z] = fmaxf(__uint_as_float(s[2 * z]), __uint_as_float(s[2 * z + 1]));
+#pragma unroll
+                for (int x = 8; x < 64; x += 8)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], __uint_as_float(s[x + 2 * z]), __uint_as_float(s[x + 2 * z + 1]));
+                top = max3(top, fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                if (step == 0) return;
+                top *= unit;
+                if (__any_sync(~0u, top > m + kSlack)) {
+                    const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.f : attn::ex2(m - mn);
+                    m = mn;
+                    const uint64_t f2 = pack2(f, f);
+                    l2[0] = fma2(l2[0], f2, pack2(0.f, 0.f));
+                    l2[1] = fma2(l2[1], f2, pack2(0.f, 0.f));
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 16) {
+                            float o[16];
+                            tc::tmem_ld16(to + x, o);
+#pragma unroll
+                            for (int z = 0; z < 16; ++z) o[z] *= f;
+                            tc::tmem_st16_nowait(to + x, o);
+                        }
+                    }
+                }
+            }
+            const float mu = m == -INFINITY ? 0.f : m;
+            const uint64_t u2 = pack2(unit, unit), m2 = pack2(-mu, -mu);
             uint32_t pk[32];
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
@@ -595,6 +607,14 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars->p_ready[i][half]);
+        };
+        if (whole) {
+            run(0, false);
+            run(1, false);
+            run(2, false);
+        } else {
+#pragma unroll 1
+            for (int step = 0; step < 3; ++step) run(step, true);
         }
         // these scores were complete, so the products before them are: their keys and the last values are free
         // (a CTA of one row tile counts for both)
