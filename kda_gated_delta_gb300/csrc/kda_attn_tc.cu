@@ -449,25 +449,25 @@ __device__ __forceinline__ float max3(float x, float y, float z)
 }
 
 // A warp loads its 32 query rows of tile i into their swizzled places, D / 8 lanes to a row; returns the
-// factor from scores to log2 of the lane's own row.
+// factor from scores to log2 of the lane's own row.  `own_at`: where the lane's own row starts, in elements,
+// -1 past the last row; the lanes of a warp tell each other theirs.
 template <int D, bool FP4>
-__device__ __forceinline__ float load_queries(const AttnCall& a, const Work& w, uint8_t* q, int i, int tid)
+__device__ __forceinline__ float load_queries(const AttnCall& a, uint8_t* q, int i, int tid, int64_t own_at)
 {
     using C = Cfg<D, FP4>;
     constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;                    // lanes of a row, rows of a load
-    const int lane = tid & 31, chunk = lane % kLanes, G = a.c.G;
+    const int lane = tid & 31, chunk = lane % kLanes;
     float unit = a.scale * attn::kLog2e;
-    uint8_t* tile = q + i * C::kTileBytes;
+    uint8_t* tile = q + i * C::kTileBytes + (tid & 96) * 128 + (chunk >> 3) * C::kPanel;
+    const uint16_t* base = reinterpret_cast<const uint16_t*>(a.q) + 8 * chunk;
     if constexpr (!FP4) {
-#pragma unroll 4
-        for (int x = 0; x < 32 / kAtOnce; ++x) {
-            const int r = (tid & 96) + x * kAtOnce + lane / kLanes, row = w.row0 + 128 * i + r, t = a.token_of(row);
-            const bool on = row < w.R;
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (on ? (w.t0 + t) * a.q_stride + (int64_t)(w.h * G + row - t * G) * D + 8 * chunk : 0);
+#pragma unroll 2
+        for (int x = 0; x < 32; x += kAtOnce) {
+            const int r = x + lane / kLanes;
+            const int64_t at = __shfl_sync(~0u, own_at, r);
             // 16 bytes, or zeros for a row past the last
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             tc::smem_u32(tile + (chunk >> 3) * C::kPanel + r * 128 + (((chunk & 7) ^ (r & 7)) << 4))),
-                         "l"(src), "r"(on ? 16 : 0)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(tile + r * 128 + (((chunk & 7) ^ (r & 7)) << 4))),
+                         "l"(base + (at < 0 ? 0 : at)), "r"(at < 0 ? 0 : 16)
                          : "memory");
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -479,15 +479,13 @@ __device__ __forceinline__ float load_queries(const AttnCall& a, const Work& w, 
         uint4 v[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int row = w.row0 + 128 * i + (tid & 96) + (x0 + b) * kAtOnce + lane / kLanes, t = a.token_of(row);
+            const int64_t at = __shfl_sync(~0u, own_at, (x0 + b) * kAtOnce + lane / kLanes);
             v[b] = make_uint4(0, 0, 0, 0);
-            if (row < w.R)
-                v[b] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + (w.t0 + t) * a.q_stride +
-                                                       (int64_t)(w.h * G + row - t * G) * D + 8 * chunk);
+            if (at >= 0) v[b] = *reinterpret_cast<const uint4*>(base + at);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int r = (tid & 96) + (x0 + b) * kAtOnce + lane / kLanes;
+            const int r = (x0 + b) * kAtOnce + lane / kLanes;
             if constexpr (FP4) {
                 // fp16 operands: the row is divided by a power of two near its largest magnitude (see the few-rows form)
                 uint32_t y[4] = {v[b].x, v[b].y, v[b].z, v[b].w}, top = 0;
@@ -507,7 +505,7 @@ __device__ __forceinline__ float load_queries(const AttnCall& a, const Work& w, 
                 const float mine = __shfl_sync(~0u, up, lane % kAtOnce * kLanes);
                 if (lane / kAtOnce == x0 + b) unit *= mine;
             }
-            *reinterpret_cast<uint4*>(tile + (chunk >> 3) * C::kPanel + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)) = v[b];
+            *reinterpret_cast<uint4*>(tile + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)) = v[b];
         }
     }
     return unit;
@@ -518,16 +516,17 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
                         int i, int tid)
 {
     using C = Cfg<D, FP4>;
-    const int tile_row = 128 * i + tid, row = w.row0 + tile_row;
-    const float unit = load_queries<D, FP4>(a, w, q, i, tid);
-    const int lane = tid & 31;
+    const int row = w.row0 + 128 * i + tid, lane = tid & 31;
+    const bool live = row < w.R;
+    const int token = a.token_of(row), head = w.h * a.c.G + row - token * a.c.G;
+    const float unit = load_queries<D, FP4>(a, q, i, tid, live ? (w.t0 + token) * a.q_stride + (int64_t)head * D : -1);
     tc::fence_proxy_async();
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&bars->q_full[i]);
 
     const uint32_t lanes = (uint32_t)(tid & 96) << 16;                  // the warp's 32 tensor-memory lanes
     const uint32_t ts = tmem + 128 * i + lanes, to = tmem + 256 + D * i + lanes;
-    const int p = w.first + a.token_of(row);
+    const int p = w.first + token;
     const int p_lo = w.first + a.token_of(w.row0 + 128 * i);                // of the tile's first and last row
     const int p_hi = w.first + a.token_of(min(w.R - 1, w.row0 + 128 * i + 127));
     const int n = w.tile_hi - w.tile_lo;
@@ -539,12 +538,32 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
         if (!warp_wait(&bars->s_full[i], j & 1, lane)) return false;
         tc::tc_fence_after();
         const bool whole = base + kTile <= w.sp.hi && base + kTile - 1 <= p_lo && (a.window == 0 || base > p_hi - a.window || base + kTile <= a.sinks);
+        // A tile that some row sees only in part is masked where it lies, in a short loop, and then goes the way of
+        // all others: code that runs once or twice in a work is fetched anew each time, at some 200 cycles for
+        // eight instructions, and a masking copy of what follows took 5,000 cycles.
+        if (!whole) {
+#pragma unroll 1
+            for (int x = 0; x < 128; x += 32) {
+                uint32_t s[32];
+                tmem_ld32(ts + x, s);
+                tmem_wait_ld();
+                pin32(s);
+                // visible columns: those below `end` that are from `from` on or below `sink`
+                const int c = base + x;
+                const uint32_t on = low_bits(min(p + 1, w.sp.hi) - c) & ((a.window ? ~low_bits(p - a.window + 1 - c) : ~0u) | low_bits(a.sinks - c));
+#pragma unroll
+                for (int z = 0; z < 32; ++z)
+                    if (!(on & (1u << z))) s[z] = 0xff800000u;
+                tmem_st32(ts + x, s);
+            }
+            tc::tmem_wait_st();
+        }
         // Half a row of scores at a time: the low half for its maximum, then the high half, whose weights are
         // taken and handed over first, then the low half again.  64 scores and 32 packed weights fit where 128
-        // scores spilled.  The steps are written out for tiles that every row sees whole; the others, one or
-        // two of a CTA, loop over one copy, which is fetched in less time than it takes to run.
+        // scores spilled.
         float top = -INFINITY;
-        const auto run = [&](const int step, const bool edge) {
+#pragma unroll
+        for (int step = 0; step < 3; ++step) {
             const int half = step & 1;
             uint32_t s[64];
             tmem_ld32(ts + 64 * half, s);
@@ -552,17 +571,6 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
             tmem_wait_ld();
             pin32(s);
             pin32(s + 32);
-            if (edge) {
-                // visible columns: those below `end` that are from `from` on or below `sink`, 32 to a word
-                const int c = base + 64 * half, end = min(p + 1, w.sp.hi) - c, from = a.window ? p - a.window + 1 - c : 0, sink = a.sinks - c;
-#pragma unroll
-                for (int x = 0; x < 64; x += 32) {
-                    const uint32_t on = low_bits(end - x) & (~low_bits(from - x) | low_bits(sink - x));
-#pragma unroll
-                    for (int z = 0; z < 32; ++z)
-                        if (!(on & (1u << z))) s[x + z] = 0xff800000u;
-                }
-            }
             if (step < 2) {
                 float t4[4];
 #pragma unroll
@@ -572,7 +580,7 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
 #pragma unroll
                     for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], __uint_as_float(s[x + 2 * z]), __uint_as_float(s[x + 2 * z + 1]));
                 top = max3(top, fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-                if (step == 0) return;
+                if (step == 0) continue;
                 top *= unit;
                 if (__any_sync(~0u, top > m + kSlack)) {
                     const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.f : attn::ex2(m - mn);
@@ -607,14 +615,6 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars->p_ready[i][half]);
-        };
-        if (whole) {
-            run(0, false);
-            run(1, false);
-            run(2, false);
-        } else {
-#pragma unroll 1
-            for (int step = 0; step < 3; ++step) run(step, true);
         }
         // these scores were complete, so the products before them are: their keys and the last values are free
         // (a CTA of one row tile counts for both)
@@ -636,71 +636,61 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const float lse2 = l == 0.f ? -INFINITY : m + attn::lg2(l);
-    const int G = a.c.G;
-    const auto out_row = [&](int rw) {
-        const int t = a.token_of(rw);
-        return (w.t0 + t) * a.c.Hq + w.h * G + rw - t * G;
-    };
-    const bool live = row < w.R;
-    // 128 bytes of a row at a time through the tile's place among the queries, which no product reads any
-    // more, so that eight neighbouring lanes write them.
-    uint8_t* stage = q + i * C::kTileBytes + (tid & 96) * (C::kTileBytes / 128);
+    // the lane's own row of the output (or of its part), -1 past the last; the lanes tell each other theirs
+    const bool in_parts = parts_here > 1;
+    const int64_t out_row = (w.t0 + token) * a.c.Hq + head, own_at = !live ? -1 : in_parts ? out_row * parts.max_parts + part : out_row;
+    // 32 channels at a time through the warp's place among the queries, which no product reads any more, so
+    // that neighbouring lanes write a row.
+    uint8_t* stage = q + i * C::kTileBytes + (tid & 96) * 128;
 #pragma unroll 1
-    for (int x = 0; x < D; x += 64) {
-        uint32_t o[64];
+    for (int x = 0; x < D; x += 32) {
+        uint32_t o[32];
         if (n > 0) {
             tmem_ld32(to + x, o);
-            tmem_ld32(to + x + 32, o + 32);
             tmem_wait_ld();
-            pin32(o);
-            pin32(o + 32);
         }
-        // a row whose weights are all zero may stand beside non-finite products: its output is zero
+        pin32(o);
 #pragma unroll
-        for (int z = 0; z < 64; ++z) o[z] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[z]) * inv);
-        if (parts_here > 1) {
-            // a warp's 32 rows x 32 channels of fp32 at a time: 4 KB
+        for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * inv);
+        if (__any_sync(~0u, l == 0.f)) {
+            // a row whose weights are all zero may stand beside non-finite products: its output is zero
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int z = 0; z < 32; ++z) o[z] = l == 0.f ? 0u : o[z];
+        }
+        if (in_parts) {                                                // 128 bytes of fp32 a row
 #pragma unroll
-                for (int z = 0; z < 8; ++z)
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((z ^ (lane & 7)) << 4)) =
-                        make_uint4(o[32 * half + 4 * z], o[32 * half + 4 * z + 1], o[32 * half + 4 * z + 2], o[32 * half + 4 * z + 3]);
-                __syncwarp();
-                uint4 v[8];
-#pragma unroll
-                for (int z = 0; z < 8; ++z) v[z] = *reinterpret_cast<const uint4*>(stage + (z * 4 + lane / 8) * 128 + ((lane % 8 ^ (z * 4 + lane / 8 & 7)) << 4));
-#pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                    const int rw = w.row0 + 128 * i + (tid & 96) + z * 4 + lane / 8;
-                    if (rw < w.R) *reinterpret_cast<uint4*>(parts.o + (out_row(rw) * parts.max_parts + part) * D + x + 32 * half + 4 * (lane % 8)) = v[z];
-                }
-                __syncwarp();
+            for (int z = 0; z < 8; ++z)
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((z ^ (lane & 7)) << 4)) = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+            __syncwarp();
+#pragma unroll 2
+            for (int z = 0; z < 32; z += 4) {
+                const int r = z + lane / 8;
+                const int64_t at = __shfl_sync(~0u, own_at, r);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((lane % 8 ^ (r & 7)) << 4));
+                if (at >= 0) *reinterpret_cast<uint4*>(parts.o + at * D + x + 4 * (lane % 8)) = v;
             }
-        } else {
-            // 64 channels of bf16: 128 bytes a row
+        } else {                                                       // 64 bytes of bf16 a row, two rows to 128 bytes
 #pragma unroll
-            for (int z = 0; z < 8; ++z) {
+            for (int z = 0; z < 4; ++z) {
                 uint32_t y[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[k] = kv::f32_to_bf16x2(__uint_as_float(o[8 * z + 2 * k]), __uint_as_float(o[8 * z + 2 * k + 1]));
-                *reinterpret_cast<uint4*>(stage + lane * 128 + ((z ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(stage + (lane >> 1) * 128 + (((lane & 1) * 4 + z ^ (lane >> 1 & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
             }
             __syncwarp();
-            uint4 v[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z) v[z] = *reinterpret_cast<const uint4*>(stage + (z * 4 + lane / 8) * 128 + ((lane % 8 ^ (z * 4 + lane / 8 & 7)) << 4));
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-                const int rw = w.row0 + 128 * i + (tid & 96) + z * 4 + lane / 8;
-                if (rw < w.R) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + out_row(rw) * D + x + 8 * (lane % 8)) = v[z];
+#pragma unroll 2
+            for (int z = 0; z < 32; z += 8) {
+                const int r = z + lane / 4;
+                const int64_t at = __shfl_sync(~0u, own_at, r);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + (r >> 1) * 128 + (((r & 1) * 4 + lane % 4 ^ (r >> 1 & 7)) << 4));
+                if (at >= 0) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at * D + x + 8 * (lane % 4)) = v;
             }
-            __syncwarp();
         }
+        __syncwarp();
     }
     if (live) {
-        if (parts_here > 1) parts.lse2[out_row(row) * parts.max_parts + part] = lse2;
-        else if (a.lse) a.lse[out_row(row)] = lse2 * attn::kLn2;
+        if (in_parts) parts.lse2[own_at] = lse2;
+        else if (a.lse) a.lse[own_at] = lse2 * attn::kLn2;
     }
     return true;
 }
