@@ -30,8 +30,11 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kda_attn.cuh"
 #include "kda_internal.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 namespace {
@@ -95,34 +98,42 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return y;
 }
 
-// One warp's keys or values of TB x 16 tokens, as loaded.
+// One warp's keys or values of TB x 16 tokens, as loaded.  `lane_at` and `lane_scale` point at the lane's
+// part of cache row 0; row: cache row of token 0 of the 16.
+template <int D, bool FP4>
+__device__ __forceinline__ const uint8_t* row_at(const uint8_t* lane_at, int32_t row) { return lane_at + (int64_t)row * (FP4 ? D / 2 : 2 * D); }
+template <int D>
+__device__ __forceinline__ const uint8_t* scale_at(const uint8_t* lane_scale, int32_t row) { return lane_scale + (int64_t)row * (D / 16); }
+
 template <int D, bool FP4, int TB>
 struct KeyTile {
     static constexpr int kWords = FP4 ? D / 32 : D / 8;     // of one token, per lane
     uint32_t w[TB][2][kWords];
     uint32_t s[TB][2];                                        // 4 bits: the lane's scales
 
-    // row: cache row of token 0 of the 16; the lane reads tokens r and r + 8
-    __device__ __forceinline__ void load(int tb, const uint8_t* k, const uint8_t* ks, int64_t row, int r, int c)
+    // the lane reads tokens r and r + 8, the c-th quarter (bf16: the c-th 16 bytes of each 64)
+    static __device__ __forceinline__ int lane_offset(int r, int c) { return FP4 ? r * (D / 2) + c * (D / 8) : r * 2 * D + c * 16; }
+    static __device__ __forceinline__ int scale_offset(int r, int c) { return r * (D / 16) + c * (D / 64); }
+    __device__ __forceinline__ void load(int tb, const uint8_t* lane_at, const uint8_t* lane_scale, int32_t row)
     {
+        const uint8_t* p = row_at<D, FP4>(lane_at, row);
+        const uint8_t* q = scale_at<D>(lane_scale, row);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int64_t t = row + r + 8 * e;
             if constexpr (!FP4) {
-                const uint8_t* p = k + t * (2 * D) + c * 16;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
-                    const uint4 x = ld16(p + 64 * i);
+                    const uint4 x = ld16(p + e * 16 * D + 64 * i);
                     w[tb][e][4 * i] = x.x, w[tb][e][4 * i + 1] = x.y, w[tb][e][4 * i + 2] = x.z, w[tb][e][4 * i + 3] = x.w;
                 }
             } else if constexpr (D == 128) {
-                const uint4 x = ld16(k + t * 64 + c * 16);
+                const uint4 x = ld16(p + e * 4 * D);
                 w[tb][e][0] = x.x, w[tb][e][1] = x.y, w[tb][e][2] = x.z, w[tb][e][3] = x.w;
-                s[tb][e] = ld2(ks + t * 8 + 2 * c);
+                s[tb][e] = ld2(q + e * (D / 2));
             } else {
-                const uint2 x = ld8(k + t * 32 + c * 8);
+                const uint2 x = ld8(p + e * 4 * D);
                 w[tb][e][0] = x.x, w[tb][e][1] = x.y;
-                s[tb][e] = ld1(ks + t * 4 + c);
+                s[tb][e] = ld1(q + e * (D / 2));
             }
         }
     }
@@ -134,42 +145,54 @@ struct ValueTile {
     uint32_t w[TB][4][kWords];
     uint32_t s[TB][4];
 
-    // the lane reads tokens 2c, 2c + 1, 2c + 8, 2c + 9; those not in [lo, hi) or [0, sink_end) become zeros
-    __device__ __forceinline__ void load(int tb, const uint8_t* v, const uint8_t* vs, int64_t row, int base, const Span& sp, int r, int c)
+    // the lane reads tokens 2c, 2c + 1, 2c + 8, 2c + 9, the r-th eighth (bf16: the r-th 16 bytes of each 128)
+    static __device__ __forceinline__ int lane_offset(int r, int c) { return FP4 ? 2 * c * (D / 2) + r * (D / 16) : 2 * c * 2 * D + r * 16; }
+    static __device__ __forceinline__ int scale_offset(int r, int c) { return 2 * c * (D / 16) + (D == 128 ? r : r / 2); }
+    static __device__ __forceinline__ constexpr int token(int e) { return (e & 1) + 8 * (e >> 1); }
+    __device__ __forceinline__ void load_token(int tb, int e, const uint8_t* p, const uint8_t* q)
     {
+        if constexpr (!FP4) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int o = 2 * c + (e & 1) + 8 * (e >> 1);
-            const int64_t t = row + o;
-            const int j = base + o;
-            const bool on = row >= 0 && j < sp.hi && (j >= sp.lo || j < sp.sink_end);
+            for (int i = 0; i < D / 64; ++i) {
+                const uint4 x = ld16(p + token(e) * 2 * D + 128 * i);
+                w[tb][e][4 * i] = x.x, w[tb][e][4 * i + 1] = x.y, w[tb][e][4 * i + 2] = x.z, w[tb][e][4 * i + 3] = x.w;
+            }
+        } else if constexpr (D == 128) {
+            const uint2 x = ld8(p + token(e) * (D / 2));
+            w[tb][e][0] = x.x, w[tb][e][1] = x.y;
+            s[tb][e] = ld1(q + token(e) * (D / 16));
+        } else {
+            w[tb][e][0] = ld4(p + token(e) * (D / 2));
+            s[tb][e] = ld1(q + token(e) * (D / 16));
+        }
+    }
+    // tokens that nobody may see (not in [lo, hi) or [0, sink_end), or of a bad page) become zeros
+    __device__ __forceinline__ void load(int tb, const uint8_t* lane_at, const uint8_t* lane_scale, int32_t row, int base, const Span& sp, int c)
+    {
+        const uint8_t* p = row_at<D, FP4>(lane_at, row);
+        const uint8_t* q = scale_at<D>(lane_scale, row);
+        if (row >= 0 && base + 16 <= sp.hi && (base >= sp.lo || base + 16 <= sp.sink_end)) {
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) w[tb][e][i] = 0;
-            s[tb][e] = 0;
-            if (!on) continue;
-            if constexpr (!FP4) {
+            for (int e = 0; e < 4; ++e) load_token(tb, e, p, q);
+        } else {
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
-                    const uint4 x = ld16(v + t * (2 * D) + r * 16 + 128 * i);
-                    w[tb][e][4 * i] = x.x, w[tb][e][4 * i + 1] = x.y, w[tb][e][4 * i + 2] = x.z, w[tb][e][4 * i + 3] = x.w;
-                }
-            } else if constexpr (D == 128) {
-                const uint2 x = ld8(v + t * 64 + r * 8);
-                w[tb][e][0] = x.x, w[tb][e][1] = x.y;
-                s[tb][e] = ld1(vs + t * 8 + r);
-            } else {
-                w[tb][e][0] = ld4(v + t * 32 + r * 4);
-                s[tb][e] = ld1(vs + t * 4 + r / 2);
+            for (int e = 0; e < 4; ++e) {
+                const int j = base + 2 * c + token(e);
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) w[tb][e][i] = 0;
+                s[tb][e] = 0;
+                if (row >= 0 && j < sp.hi && (j >= sp.lo || j < sp.sink_end)) load_token(tb, e, p, q);
             }
         }
     }
 };
 
-// First row of the page of a token's 16-token block, -1 where the table holds none (recorded).
-__device__ __forceinline__ int64_t block_row(const AttnCall& a, int b, int base, int h)
+// First row of the page of a token's 16-token block, -1 where the table holds none (recorded)
+// (cache rows are below 2^31).
+__device__ __forceinline__ int32_t block_row(const AttnCall& a, int b, int base, int h)
 {
     const int64_t slot = kv::token_slot(a.c, b, base);
-    return slot < 0 ? -1 : slot + ((int64_t)h << a.c.page_shift);
+    return slot < 0 ? -1 : (int32_t)(slot + ((int64_t)h << a.c.page_shift));
 }
 
 template <int D, bool FP4, int NT, int TB>
@@ -259,9 +282,9 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
 
     KeyTile<D, FP4, TB> kt;
     ValueTile<D, FP4, TB> vt;
-    int64_t row_of[TB], next_row[TB];
+    int32_t row_of[TB], next_row[TB], far_row[TB];                        // of tiles i, i + kWarps, i + 2 kWarps
     int i = tile_lo + warp;
-    const auto rows_of = [&](int tile, int64_t* out) {
+    const auto rows_of = [&](int tile, int32_t* out) {
         const int base = attn::tile_base<kTile>(sp, tile);
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb) {
@@ -270,15 +293,30 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
             out[tb] = needed ? block_row(a, b, j, h) : -1;
         }
     };
-    const auto load_keys = [&](const int64_t* at) {
+    const uint8_t* const k_at = a.c.k + kt.lane_offset(r, c);
+    const uint8_t* const v_at = a.c.v + vt.lane_offset(r, c);
+    const uint8_t* const ks_at = a.c.ks + kt.scale_offset(r, c);
+    const uint8_t* const vs_at = a.c.vs + vt.scale_offset(r, c);
+    const auto load_keys = [&](const int32_t* at) {
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb)
-            if (at[tb] >= 0) kt.load(tb, a.c.k, a.c.ks, at[tb], r, c);
+            if (at[tb] >= 0) kt.load(tb, k_at, ks_at, at[tb]);
     };
-    const auto load_values = [&](int tile, const int64_t* at) {
+    const auto load_values = [&](int tile, const int32_t* at) {
         const int base = attn::tile_base<kTile>(sp, tile);
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb) vt.load(tb, a.c.v, a.c.vs, at[tb], base + 16 * tb, sp, r, c);
+        for (int tb = 0; tb < TB; ++tb) vt.load(tb, v_at, vs_at, at[tb], base + 16 * tb, sp, c);
+    };
+    // 16 tokens' keys and values into L2
+    const auto prefetch = [&](int64_t row) {
+        if (row < 0) return;
+        constexpr int64_t kRow = FP4 ? D / 2 : 2 * D;
+        tc::bulk_prefetch_l2(a.c.k + row * kRow, 16 * kRow);
+        tc::bulk_prefetch_l2(a.c.v + row * kRow, 16 * kRow);
+        if constexpr (FP4) {
+            tc::bulk_prefetch_l2(a.c.ks + row * (D / 16), D);
+            tc::bulk_prefetch_l2(a.c.vs + row * (D / 16), D);
+        }
     };
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb)
@@ -293,6 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
         load_keys(row_of);
         load_values(i, row_of);
         if (i + kWarps < tile_hi) rows_of(i + kWarps, next_row);
+        if (i + 2 * kWarps < tile_hi) rows_of(i + 2 * kWarps, far_row);
     }
     for (; i < tile_hi; i += kWarps) {
         const int base = attn::tile_base<kTile>(sp, i);
@@ -339,7 +378,14 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) row_of[tb] = next_row[tb];
             load_keys(row_of);
-            if (i + 2 * kWarps < tile_hi) rows_of(i + 2 * kWarps, next_row);
+            if (i + 2 * kWarps < tile_hi) {
+#pragma unroll
+                for (int tb = 0; tb < TB; ++tb) next_row[tb] = far_row[tb];
+                #pragma unroll
+                for (int tb = 0; tb < TB; ++tb)
+                    if (lane == tb) prefetch(far_row[tb]);
+                if (i + 3 * kWarps < tile_hi) rows_of(i + 3 * kWarps, far_row);
+            }
         }
         // ---- softmax -------------------------------------------------------------------------------------
 #pragma unroll
@@ -411,27 +457,32 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
                     for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt][mt], a0, a1, a2, a3, p[nt][0], p[nt][1]);
                 }
             } else {
-                // the scales of the lane's token pairs, as the two halves of a register
-                const float2 f01 = kv::f16x2_to_f32(kv::e4m3x2_to_f16x2(vt.s[tb][0] | vt.s[tb][1] << 8));
-                const float2 f23 = kv::f16x2_to_f32(kv::e4m3x2_to_f16x2(vt.s[tb][2] | vt.s[tb][3] << 8));
-                const uint32_t s01 = kv::f32_to_bf16x2(f01.x * kv::kBf16Up, f01.y * kv::kBf16Up);
-                const uint32_t s23 = kv::f32_to_bf16x2(f23.x * kv::kBf16Up, f23.y * kv::kBf16Up);
+                // to fp16 with the scale, exactly, then through fp32 to the bf16 pairs of two tokens
+                uint32_t sc[4];
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j)
+                for (int e = 0; e < 4; e += 2) {
+                    const uint32_t s2 = kv::e4m3x2_to_f16x2(vt.s[tb][e] | vt.s[tb][e + 1] << 8);
+                    sc[e] = __byte_perm(s2, 0, 0x1010), sc[e + 1] = __byte_perm(s2, 0, 0x3232);
+                }
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {             // channels 0..3 and 4..7 of the words
-                        const uint32_t pick = half ? 0x7632u : 0x5410u;
-                        uint32_t x[4], y[4];
-                        kv::e2m1_columns_to_bf16(__byte_perm(vt.w[tb][0][j], vt.w[tb][1][j], pick), x);
-                        kv::e2m1_columns_to_bf16(__byte_perm(vt.w[tb][2][j], vt.w[tb][3][j], pick), y);
+                for (int j = 0; j < D / 64; ++j) {
+                    uint32_t x[4][4];
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) x[z] = kv::mul_bf16x2(x[z], s01), y[z] = kv::mul_bf16x2(y[z], s23);
+                    for (int e = 0; e < 4; ++e) {
+                        kv::e2m1x8_to_f16(vt.w[tb][e][j], x[e]);
 #pragma unroll
-                        for (int z = 0; z < 2; ++z)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma<false>(o[nt][4 * j + 2 * half + z], x[2 * z], x[2 * z + 1], y[2 * z], y[2 * z + 1], p[nt][0], p[nt][1]);
+                        for (int z = 0; z < 4; ++z) x[e][z] = kv::mul_f16x2(x[e][z], sc[e]);
                     }
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const float2 f0 = kv::f16x2_to_f32(x[0][z]), f1 = kv::f16x2_to_f32(x[1][z]);
+                        const float2 f2 = kv::f16x2_to_f32(x[2][z]), f3 = kv::f16x2_to_f32(x[3][z]);
+                        const uint32_t a0 = kv::f32_to_bf16x2(f0.x, f1.x), a1 = kv::f32_to_bf16x2(f0.y, f1.y);
+                        const uint32_t a2 = kv::f32_to_bf16x2(f2.x, f3.x), a3 = kv::f32_to_bf16x2(f2.y, f3.y);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt][4 * j + z], a0, a1, a2, a3, p[nt][0], p[nt][1]);
+                    }
+                }
             }
         }
         if (more) load_values(i + kWarps, row_of);
@@ -478,7 +529,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             if (sm_l[w][row] != sm_l[w][row]) sum = acc.x = acc.y = acc.z = acc.w = sm_l[w][row];
-        const float inv = sum == 0.f ? 0.f : (FP4 ? kv::kBf16Rest : 1.f) / sum;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t out_row = (t0 + row / G) * a.c.Hq + h * G + row % G;
         const float lse2 = sum == 0.f ? -INFINITY : mx + attn::lg2(sum);
         if (parts_here > 1) {
@@ -493,14 +544,12 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     }
 }
 
-// Joins the parts of each row that has several: a warp per row.
+// Joins the parts of each row that has several: a CTA per row.
 template <int D, int kTile>
 __global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts)
 {
     a.c.err = &g_attn_error;
-    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    if (row >= a.c.T * a.c.Hq) return;
+    const int64_t row = blockIdx.x;
     int b;
     int64_t pos;
     const int64_t t = row / a.c.Hq;
@@ -511,7 +560,7 @@ __global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts)
     const int64_t first = len - (t1 - t0);
     const Span sp = attn::make_span<kTile>(first > 0 ? first : 0, len - 1, a.max_len, a.window, a.sinks);
     const int n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
-    if (n > 1) attn::join_row<D>(a, parts, row, n, lane);
+    if (n > 1) attn::join_row<D>(a, parts, row, n);
 }
 
 }  // namespace
@@ -521,15 +570,18 @@ namespace {
 constexpr int kFewRows = 16;
 
 // How a call of the few-rows form is cut along the cache.  An uncut call has one CTA per (request, kv
-// head).  The cut aims at kCtas CTAs for the longest histories the caller's bound allows, in parts of at
-// least kMinPart tokens.
-constexpr int kFewTile(bool fp4) { return fp4 ? 32 : 16; }
-constexpr int64_t kCtas = 2048;
+// head).  The cut aims at kCtas CTAs for the longest histories the caller's bound allows, so that ragged
+// histories spread evenly (16 histories of 4096 to 131072 tokens in 4 bits: 410 us with 2,048 CTAs, 380 with
+// 8,192), in parts whose fp32 outputs, written and read once, are at most 1/32 of the part's bytes (64
+// requests of 4 x 4 rows: 199 us in 16 parts of 256 tokens, 148 in 4 of 1,024).
+constexpr int kFewTile = 16;
+constexpr int64_t kCtas = 8192;
 constexpr int kMinPart = 256;
 
 attn::Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t max_len)
 {
-    const int tile = kFewTile(p.cache_dtype == KDA_CACHE_FP4);
+    const int tile = kFewTile, rows = max_new * (p.num_q_heads / p.num_kv_heads);
+    const int min_part = std::max(kMinPart, p.cache_dtype == KDA_CACHE_FP4 ? 228 * rows : 64 * rows);
     int64_t tokens = max_len;
     if (p.window) {
         const int64_t seen = (int64_t)p.window + max_new + p.num_sinks + 3 * tile;   // both runs, rounded out to tiles
@@ -538,7 +590,7 @@ attn::Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t ma
     const int64_t tiles = (tokens + tile - 1) / tile;
     const int64_t ctas = (int64_t)n * p.num_kv_heads;
     int64_t parts = (kCtas + ctas - 1) / ctas;
-    const int64_t most = tokens / kMinPart;
+    const int64_t most = tokens / min_part;
     if (parts > most) parts = most;
     if (parts > 256) parts = 256;
     if (parts < 1) parts = 1;
@@ -566,13 +618,13 @@ Parts make_parts(const kda_kv_params& p, int64_t T, const attn::Cut& c, void* wo
 template <int D, bool FP4, int NT>
 cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const attn::Cut& cut, void* workspace, cudaStream_t stream)
 {
-    constexpr int TB = kFewTile(FP4) / 16;
+    constexpr int TB = kFewTile / 16;
     const Parts parts = make_parts(p, a.c.T, cut, workspace);
     const size_t smem = (size_t)kWarps * 8 * NT * (D + 4) * 4;
     few_rows_kernel<D, FP4, NT, TB><<<dim3((unsigned)(a.c.n * a.c.Hkv), (unsigned)cut.parts), kWarps * 32, smem, stream>>>(a, parts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || cut.parts == 1) return e;
-    join_kernel<D, 16 * TB><<<(unsigned)((a.c.T * a.c.Hq + 3) / 4), 128, 0, stream>>>(a, parts);
+    join_kernel<D, 16 * TB><<<(unsigned)(a.c.T * a.c.Hq), 128, 0, stream>>>(a, parts);
     return cudaGetLastError();
 }
 

@@ -70,11 +70,14 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
-// One row's n > 1 parts joined by a warp, D / 32 channels a lane.
+// One row's n > 1 parts joined by the four warps of a CTA: each takes every fourth part, its lanes D / 32
+// channels each, and the first puts their sums together.
 template <int D>
-__device__ __forceinline__ void join_row(const AttnCall& a, const Parts& parts, int64_t row, int n, int lane)
+__device__ __forceinline__ void join_row(const AttnCall& a, const Parts& parts, int64_t row, int n)
 {
     constexpr int N = D / 32;
+    __shared__ float sm_o[4][D], sm_sum[4];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const float* lse = parts.lse2 + row * parts.max_parts;
     const float* src = parts.o + row * parts.max_parts * D + lane * N;
     float mx = -INFINITY, sum = 0.f, o[N] = {};
@@ -83,16 +86,27 @@ __device__ __forceinline__ void join_row(const AttnCall& a, const Parts& parts, 
     for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
     if (mx == -INFINITY) mx = 0.f;                                    // nothing seen, or NaN (which the weights carry on)
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
+    for (int i = warp; i < n; i += 4) {
         const float w = ex2(lse[i] - mx);
         sum += w;
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] += w * src[(int64_t)i * D + j];
     }
+#pragma unroll
+    for (int j = 0; j < N; ++j) sm_o[warp][lane * N + j] = o[j];
+    if (lane == 0) sm_sum[warp] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    sum = (sm_sum[0] + sm_sum[1]) + (sm_sum[2] + sm_sum[3]);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + row * D + lane * N;
 #pragma unroll
-    for (int j = 0; j < N; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = kv::f32_to_bf16x2(o[j] * inv, o[j + 1] * inv);
+    for (int j = 0; j < N; ++j) {
+        const int c = lane * N + j;
+        o[j] = ((sm_o[0][c] + sm_o[1][c]) + (sm_o[2][c] + sm_o[3][c])) * inv;
+    }
+#pragma unroll
+    for (int j = 0; j < N; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = kv::f32_to_bf16x2(o[j], o[j + 1]);
     if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + lg2(sum)) * kLn2;
 }
 

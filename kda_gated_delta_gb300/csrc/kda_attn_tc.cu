@@ -794,14 +794,12 @@ __global__ void __launch_bounds__(Cfg<D, FP4>::kThreads, 1)
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of each row that has several: a warp per row, D / 32 channels a lane.
+// Joins the parts of each row that has several: a CTA per row.
 template <int D>
 __global__ void __launch_bounds__(128) join_rows_kernel(AttnCall a, Parts parts)
 {
     a.c.err = &g_attn_tc_error;
-    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    if (row >= a.c.T * a.c.Hq) return;
+    const int64_t row = blockIdx.x;
     const int64_t t = row / a.c.Hq;
     int b = 0;
     int64_t pos;
@@ -815,7 +813,7 @@ __global__ void __launch_bounds__(128) join_rows_kernel(AttnCall a, Parts parts)
     const int64_t last = min((int64_t)fresh * G - 1, row0 + kRows - 1);
     const Span sp = attn::make_span<kTile>(max(first + row0 / G, (int64_t)0), first + last / G, a.max_len, a.window, a.sinks);
     const int n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
-    if (n > 1) attn::join_row<D>(a, parts, row, n, lane);
+    if (n > 1) attn::join_row<D>(a, parts, row, n);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder()
@@ -894,7 +892,7 @@ cudaError_t launch_many(const kda_kv_params& p, const AttnCall& a, const Parts& 
     many_rows_kernel<D, FP4><<<dim3((unsigned)(tiles * a.c.Hkv), (unsigned)parts.max_parts), C::kThreads, C::kSmem, stream>>>(a, parts, km, vm);
     e = cudaGetLastError();
     if (e != cudaSuccess || parts.max_parts == 1) return e;
-    join_rows_kernel<D><<<(unsigned)((a.c.T * a.c.Hq + 3) / 4), 128, 0, stream>>>(a, parts);
+    join_rows_kernel<D><<<(unsigned)(a.c.T * a.c.Hq), 128, 0, stream>>>(a, parts);
     return cudaGetLastError();
 }
 
