@@ -400,25 +400,36 @@ def _kv_params(Hq, Hkv, D, page, fp4, rot=0, interleaved=False, window=0, sinks=
     return ctypes.byref(p)
 
 
+# The calls below take a few microseconds, and a decode step makes them once a layer, so each argument is
+# first looked at in one expression; only one that fails it goes through the checks that say what is wrong.
+_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+
+
+def _need(t, name, dtype):
+    if not (t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        _dev(t, name, dtype)
+
+
 def _kv_cache_args(cache):
     """(kv heads, page size, head_dim, 4-bit?, k, v, k_scale and v_scale pointers, pages)."""
     k, v, ks, vs = cache
-    _dev(k, "cache.k")
-    fp4 = k.dtype == torch.uint8
-    if not fp4 and k.dtype != torch.bfloat16:
+    fp4 = k.dtype is _U8
+    if not fp4 and k.dtype is not _BF16:
         raise TypeError(f"cache.k must be torch.bfloat16 or torch.uint8 (4 bits), got {k.dtype}")
-    _dev(v, "cache.v", k.dtype)
-    if k.dim() != 4 or v.shape != k.shape:
+    _need(k, "cache.k", k.dtype)
+    _need(v, "cache.v", k.dtype)
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError("cache.k and cache.v must be [pages, kv heads, page size, channels], of one shape")
-    pages, Hkv, page, D = k.shape
+    pages, Hkv, page, D = shape
     if not fp4:
         return Hkv, page, D, False, k.data_ptr(), v.data_ptr(), None, None, pages
     for name, t in (("cache.k_scale", ks), ("cache.v_scale", vs)):
         if t is None:
             raise ValueError(f"{name} is missing")
-        _dev(t, name)
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        if t.dtype is not _E4M3 and t.dtype is not _U8:
             raise TypeError(f"{name} must be torch.float8_e4m3fn, got {t.dtype}")
+        _need(t, name, t.dtype)
         if t.shape != (pages, Hkv, page, D // 8):
             raise ValueError(f"{name} must be [pages, kv heads, page size, head_dim / 16]")
     return Hkv, page, 2 * D, True, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages
@@ -426,36 +437,43 @@ def _kv_cache_args(cache):
 
 def _kv_batch(cu_seqlens, kv_lens, block_table, T):
     """(cu_seqlens, kv_lens, block_table pointers, requests, pages per request, tokens)."""
-    _dev(kv_lens, "kv_lens", torch.int32)
-    _dev(block_table, "block_table", torch.int32)
-    n = kv_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != n:
+    _need(kv_lens, "kv_lens", _I32)
+    _need(block_table, "block_table", _I32)
+    n, shape = kv_lens.shape[0], block_table.shape
+    if len(shape) != 2 or shape[0] != n:
         raise ValueError("block_table must be [requests, pages per request]")
     if cu_seqlens is None:
         if T != n:
             raise ValueError("without cu_seqlens there is one token per request")
-        return None, kv_lens.data_ptr(), block_table.data_ptr(), n, block_table.shape[1], T
-    _dev(cu_seqlens, "cu_seqlens", torch.int32)
+        return None, kv_lens.data_ptr(), block_table.data_ptr(), n, shape[1], T
+    _need(cu_seqlens, "cu_seqlens", _I32)
     if cu_seqlens.shape[0] != n + 1:
         raise ValueError("cu_seqlens must have one entry more than kv_lens")
-    return cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, block_table.shape[1], T
+    return cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, shape[1], T
 
 
 def _rows(t, name, heads, D):
-    """Pointer and token stride of a bf16 [T, heads, D] tensor whose heads are contiguous (a slice of a
-    fused projection will do)."""
+    """Pointer, token stride, tokens and heads of a bf16 [T, heads, D] tensor whose heads are contiguous (a
+    slice of a fused projection will do)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {D}], got {tuple(shape)}")
     if t.is_contiguous():
-        return t.data_ptr(), t.shape[1] * D
+        return t.data_ptr(), shape[1] * D, shape[0], shape[1]
     s = t.stride()
-    if s[2] != 1 or (s[1] != D and t.shape[1] > 1):
+    if s[2] != 1 or (s[1] != D and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), s[0]
+    return t.data_ptr(), s[0], shape[0], shape[1]
+
+
+@functools.lru_cache(maxsize=None)
+def _fn(name):
+    """An entry point of the loaded library."""
+    return getattr(lib(), name)
 
 
 def _raw_stream(stream, t):
@@ -468,42 +486,42 @@ def kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, *, q=None, q_o
     keys rotated by the table ``rope`` ([positions, rot_dim], see :func:`rope_table`; None: no rotation).
     With ``q`` ([T, q heads, D]) returns it rotated (into ``q_out``, which may be ``q``)."""
     Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
-    kp, k_stride = _rows(k, "k", Hkv, D)
-    vp, v_stride = _rows(v, "v", Hkv, D)
-    T = k.shape[0]
-    if v.shape[0] != T:
+    kp, k_stride, T, _ = _rows(k, "k", Hkv, D)
+    vp, v_stride, Tv, _ = _rows(v, "v", Hkv, D)
+    if Tv != T:
         raise ValueError("k and v must have the same number of tokens")
-    batch = _kv_batch(cu_seqlens, kv_lens, block_table, T)
+    pc, pl, pt, n, max_pages, _ = _kv_batch(cu_seqlens, kv_lens, block_table, T)
     rot, rows, rp = 0, 0, None
     if rope is not None:
-        _dev(rope, "rope", torch.float32)
+        _need(rope, "rope", _F32)
         if rope.dim() != 2:
             raise ValueError("rope must be [positions, rot_dim]")
         rows, rot = rope.shape
         rp = rope.data_ptr()
     if positions is not None:
-        _dev(positions, "positions", torch.int32)
+        _need(positions, "positions", _I32)
         if positions.shape != (T,):
             raise ValueError("positions must hold one entry per token")
         positions = positions.data_ptr()
     Hq, qp, q_stride, qo = Hkv, None, 0, None
     if q is not None:
-        qp, q_stride = _rows(q, "q", None, D)
-        Hq = q.shape[1]
-        if q.shape[0] != T:
+        qp, q_stride, Tq, Hq = _rows(q, "q", None, D)
+        if Tq != T:
             raise ValueError("q and k must have the same number of tokens")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
         elif q_out.shape != q.shape:
             raise ValueError("q_out must have the shape of q")
         else:
-            _dev(q_out, "q_out", torch.bfloat16)
+            _need(q_out, "q_out", _BF16)
         qo = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    p = _kv_params(Hq, Hkv, D, page, fp4, rot, interleaved)
-    _check(lib().kda_kv_append(p, qp, q_stride, kp, k_stride, vp, v_stride, rp, rows, positions, *batch, pk, pv, pks,
-                               pvs, pages, qo, _raw_stream(stream, k)), "kda_kv_append")
+    rc = _fn("kda_kv_append")(_kv_params(Hq, Hkv, D, page, fp4, rot, interleaved), qp, q_stride, kp, k_stride, vp, v_stride,
+                              rp, rows, positions, pc, pl, pt, n, max_pages, T, pk, pv, pks, pvs, pages, qo,
+                              _raw_stream(stream, k))
+    if rc:
+        _check(rc, "kda_kv_append")
     return q_out
 
 
@@ -516,14 +534,17 @@ def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, ou
         raise ValueError("num_tokens is needed with cu_seqlens")
     batch = _kv_batch(cu_seqlens, kv_lens, block_table, int(T))
     if out is None:
-        out = tuple(torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=cache[0].device) for _ in range(2))
-    for name, t in (("out[0]", out[0]), ("out[1]", out[1])):
-        _dev(t, name, torch.bfloat16)
-        if t.shape != (T, Hkv, D):
-            raise ValueError(f"{name} must be [{T}, {Hkv}, {D}]")
-    p = _kv_params(Hkv, Hkv, D, page, fp4)
-    _check(lib().kda_kv_read(p, pk, pv, pks, pvs, pages, *batch, out[0].data_ptr(), out[1].data_ptr(),
-                             _raw_stream(stream, cache[0])), "kda_kv_read")
+        k_out = torch.empty((T, Hkv, D), dtype=_BF16, device=kv_lens.device)
+        out = k_out, torch.empty_like(k_out)
+    else:
+        for name, t in (("out[0]", out[0]), ("out[1]", out[1])):
+            _need(t, name, _BF16)
+            if t.shape != (T, Hkv, D):
+                raise ValueError(f"{name} must be [{T}, {Hkv}, {D}]")
+    rc = _fn("kda_kv_read")(_kv_params(Hkv, Hkv, D, page, fp4), pk, pv, pks, pvs, pages, *batch, out[0].data_ptr(),
+                            out[1].data_ptr(), _raw_stream(stream, kv_lens))
+    if rc:
+        _check(rc, "kda_kv_read")
     return out
 
 
@@ -540,37 +561,38 @@ def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0
     ``max_new`` bounds the new tokens of a request (default: all T; 1 without ``cu_seqlens``), ``max_len``
     bounds kv_lens (default: what block_table can hold): host numbers, the tighter the better."""
     Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
-    qp, q_stride = _rows(q, "q", None, D)
-    T, Hq, _ = q.shape
+    qp, q_stride, T, Hq = _rows(q, "q", None, D)
     batch = _kv_batch(cu_seqlens, kv_lens, block_table, T)
     if max_new is None or cu_seqlens is None:
         max_new = 1 if cu_seqlens is None else max(T, 1)
     if max_len is None:
         max_len = batch[4] * page
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
     else:
-        _dev(out, "out", torch.bfloat16)
+        _need(out, "out", _BF16)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
     if lse is not None:
-        _dev(lse, "lse", torch.float32)
+        _need(lse, "lse", _F32)
         if lse.shape != (T, Hq):
             raise ValueError("lse must be [tokens, q heads]")
     elif return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    p = _kv_params(Hq, Hkv, D, page, fp4, 0, False, int(window), int(sinks), scale)
+        lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
+    p = _kv_params(Hq, Hkv, D, page, fp4, 0, False, window, sinks, scale)
     need = _attention_workspace(p, batch[3], T, max_new, max_len)
-    if workspace is None:
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    else:
-        _dev(workspace, "workspace", torch.uint8)
-    _check(lib().kda_paged_attention(p, qp, q_stride, pk, pv, pks, pvs, pages, *batch, max_new, max_len, out.data_ptr(),
-                                     None if lse is None else lse.data_ptr(),
-                                     None if workspace is None else workspace.data_ptr(),
-                                     0 if workspace is None else workspace.numel(), _raw_stream(stream, q)),
-           "kda_paged_attention")
+    ws = None
+    if workspace is not None:
+        _need(workspace, "workspace", _U8)
+        need = workspace.numel()
+    elif need:
+        workspace = torch.empty(need, dtype=_U8, device=q.device)
+    if workspace is not None:
+        ws = workspace.data_ptr()
+    rc = _fn("kda_paged_attention")(p, qp, q_stride, pk, pv, pks, pvs, pages, *batch, max_new, max_len, out.data_ptr(),
+                                    None if lse is None else lse.data_ptr(), ws, need, _raw_stream(stream, q))
+    if rc:
+        _check(rc, "kda_paged_attention")
     return out if lse is None else (out, lse)
 
 

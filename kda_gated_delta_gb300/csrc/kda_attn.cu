@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
     const int G = a.c.G;
 
+    attn::let_next_launch();
     int64_t t0, t1;
     kv::request_rows(a.c, b, t0, t1);
     const int len = a.c.lens[b];
@@ -549,17 +550,18 @@ template <int D, int kTile>
 __global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts)
 {
     a.c.err = &g_attn_error;
-    const int64_t row = blockIdx.x;
-    int b;
+    const int64_t row = blockIdx.x, t = row / a.c.Hq;
+    int b, n = 1;
     int64_t pos;
-    const int64_t t = row / a.c.Hq;
-    if (!kv::token_place(a.c, t, b, pos)) return;                     // padding: written by the first part
-    int64_t t0, t1;
-    kv::request_rows(a.c, b, t0, t1);
-    const int len = a.c.lens[b];
-    const int64_t first = len - (t1 - t0);
-    const Span sp = attn::make_span<kTile>(first > 0 ? first : 0, len - 1, a.max_len, a.window, a.sinks);
-    const int n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
+    if (kv::token_place(a.c, t, b, pos)) {                            // padding: written by the first part
+        int64_t t0, t1;
+        kv::request_rows(a.c, b, t0, t1);
+        const int len = a.c.lens[b];
+        const int64_t first = len - (t1 - t0);
+        const Span sp = attn::make_span<kTile>(first > 0 ? first : 0, len - 1, a.max_len, a.window, a.sinks);
+        n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
+    }
+    attn::wait_for_last();
     if (n > 1) attn::join_row<D>(a, parts, row, n);
 }
 
@@ -574,13 +576,13 @@ constexpr int kFewRows = 16;
 // histories spread evenly (16 histories of 4096 to 131072 tokens in 4 bits: 410 us with 2,048 CTAs, 380 with
 // 8,192), in parts whose fp32 outputs, written and read once, are at most 1/32 of the part's bytes (64
 // requests of 4 x 4 rows: 199 us in 16 parts of 256 tokens, 148 in 4 of 1,024).
-constexpr int kFewTile = 16;
+constexpr int kFewTile(bool fp4) { return fp4 ? 32 : 16; }
 constexpr int64_t kCtas = 8192;
 constexpr int kMinPart = 256;
 
 attn::Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t max_len)
 {
-    const int tile = kFewTile, rows = max_new * (p.num_q_heads / p.num_kv_heads);
+    const int tile = kFewTile(p.cache_dtype == KDA_CACHE_FP4), rows = max_new * (p.num_q_heads / p.num_kv_heads);
     const int min_part = std::max(kMinPart, p.cache_dtype == KDA_CACHE_FP4 ? 228 * rows : 64 * rows);
     int64_t tokens = max_len;
     if (p.window) {
@@ -618,14 +620,13 @@ Parts make_parts(const kda_kv_params& p, int64_t T, const attn::Cut& c, void* wo
 template <int D, bool FP4, int NT>
 cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const attn::Cut& cut, void* workspace, cudaStream_t stream)
 {
-    constexpr int TB = kFewTile / 16;
+    constexpr int TB = kFewTile(FP4) / 16;
     const Parts parts = make_parts(p, a.c.T, cut, workspace);
     const size_t smem = (size_t)kWarps * 8 * NT * (D + 4) * 4;
     few_rows_kernel<D, FP4, NT, TB><<<dim3((unsigned)(a.c.n * a.c.Hkv), (unsigned)cut.parts), kWarps * 32, smem, stream>>>(a, parts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || cut.parts == 1) return e;
-    join_kernel<D, 16 * TB><<<(unsigned)(a.c.T * a.c.Hq), 128, 0, stream>>>(a, parts);
-    return cudaGetLastError();
+    return attn::launch_behind(join_kernel<D, 16 * TB>, a.c.T * a.c.Hq, 128, stream, a, parts);
 }
 
 template <int D, bool FP4>

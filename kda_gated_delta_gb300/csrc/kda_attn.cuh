@@ -70,6 +70,27 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
+// The joining kernel may be launched as soon as every CTA of the parts' kernel has begun, and waits there for
+// its end (programmatic dependent launch): its launch and its loads of the tables overlap the last CTAs.  Every CTA waits, also one with nothing to join, so
+// that whatever follows in the stream follows both kernels.
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), int64_t blocks, int threads, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // One row's n > 1 parts joined by the four warps of a CTA: each takes every fourth part, its lanes D / 32
 // channels each, and the first puts their sums together.
 template <int D>

@@ -736,6 +736,7 @@ __global__ void __launch_bounds__(Cfg<D, FP4>::kThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = bars->tmem;
+    attn::let_next_launch();
 
     Work w;
     bool live = bars->place[0] != 0;
@@ -799,20 +800,20 @@ template <int D>
 __global__ void __launch_bounds__(128) join_rows_kernel(AttnCall a, Parts parts)
 {
     a.c.err = &g_attn_tc_error;
-    const int64_t row = blockIdx.x;
-    const int64_t t = row / a.c.Hq;
-    int b = 0;
-    int64_t pos;
+    const int64_t row = blockIdx.x, t = row / a.c.Hq;
+    int b = 0, n = 1;
+    int64_t pos, t0, t1;
     const bool sees = kv::token_place(a.c, t, b, pos);
-    int64_t t0, t1;
     kv::request_rows(a.c, b, t0, t1);
     const int len = a.c.lens[b];
-    if ((!sees && (t < t0 || t >= t1)) || len <= 0) return;
-    const int fresh = (int)(t1 - t0), G = a.c.G, first = len - fresh;
-    const int64_t row0 = ((t - t0) * G + row % a.c.Hq % G) / kRows * kRows;
-    const int64_t last = min((int64_t)fresh * G - 1, row0 + kRows - 1);
-    const Span sp = attn::make_span<kTile>(max(first + row0 / G, (int64_t)0), first + last / G, a.max_len, a.window, a.sinks);
-    const int n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
+    if ((sees || (t >= t0 && t < t1)) && len > 0) {
+        const int fresh = (int)(t1 - t0), G = a.c.G, first = len - fresh;
+        const int64_t row0 = ((t - t0) * G + row % a.c.Hq % G) / kRows * kRows;
+        const int64_t last = min((int64_t)fresh * G - 1, row0 + kRows - 1);
+        const Span sp = attn::make_span<kTile>(max(first + row0 / G, (int64_t)0), first + last / G, a.max_len, a.window, a.sinks);
+        n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
+    }
+    attn::wait_for_last();
     if (n > 1) attn::join_row<D>(a, parts, row, n);
 }
 
@@ -892,8 +893,7 @@ cudaError_t launch_many(const kda_kv_params& p, const AttnCall& a, const Parts& 
     many_rows_kernel<D, FP4><<<dim3((unsigned)(tiles * a.c.Hkv), (unsigned)parts.max_parts), C::kThreads, C::kSmem, stream>>>(a, parts, km, vm);
     e = cudaGetLastError();
     if (e != cudaSuccess || parts.max_parts == 1) return e;
-    join_rows_kernel<D><<<(unsigned)(a.c.T * a.c.Hq), 128, 0, stream>>>(a, parts);
-    return cudaGetLastError();
+    return attn::launch_behind(join_rows_kernel<D>, a.c.T * a.c.Hq, 128, stream, a, parts);
 }
 
 template cudaError_t launch_many<64, false>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
