@@ -147,11 +147,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a)
             const uint4 zero = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(dst + c0) = live ? make_uint4(w0[0], w0[1], w0[2], w0[3]) : zero;
             *reinterpret_cast<uint4*>(dst + c1) = live ? make_uint4(w1[0], w1[1], w1[2], w1[3]) : zero;
+            continue;
         }
         const int h = is_v ? row - Hkv : row;
         const int64_t at = slot + ((int64_t)h << a.c.page_shift);    // row of the cache
         if constexpr (!FP4) {
-            if (!is_q && slot >= 0) {
+            if (slot >= 0) {
                 uint16_t* dst = reinterpret_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + at * D;
                 *reinterpret_cast<uint4*>(dst + c0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
                 *reinterpret_cast<uint4*>(dst + c1) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a)
             m1 = half_style ? fmaxf(m1, o1) : m0;
             const uint32_t e0 = kv::f32_to_e4m3(kv::settle(m0 * (1.0f / 6.0f)));
             const uint32_t e1 = kv::f32_to_e4m3(kv::settle(m1 * (1.0f / 6.0f)));
-            if (!is_q && slot >= 0) {
+            if (slot >= 0) {
                 const float2 s = kv::f16x2_to_f32(kv::e4m3x2_to_f16x2(e0 | e1 << 8));
                 const float s0 = s.x, s1 = s.y;
                 const uint32_t q0 = e0 ? quantise8(x, 1.0f / s0) : 0u, q1 = e1 ? quantise8(y, 1.0f / s1) : 0u;
