@@ -545,12 +545,12 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     }
 }
 
-// Joins the parts of each row that has several: a CTA per row.
+// Joins the parts of each row that has several.
 template <int D, int kTile>
-__global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts)
+__global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts, const int share)
 {
     a.c.err = &g_attn_error;
-    const int64_t row = blockIdx.x, t = row / a.c.Hq;
+    const int64_t rows = a.c.T * a.c.Hq, row = min(attn::join_row_index(share), rows - 1), t = row / a.c.Hq;
     int b, n = 1;
     int64_t pos;
     if (kv::token_place(a.c, t, b, pos)) {                            // padding: written by the first part
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts)
         n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
     }
     attn::wait_for_last();
-    if (n > 1) attn::join_row<D>(a, parts, row, n);
+    attn::join_row<D>(a, parts, row, attn::join_row_index(share) < rows ? n : 0, share);
 }
 
 }  // namespace
@@ -626,7 +626,7 @@ cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const attn::Cu
     few_rows_kernel<D, FP4, NT, TB><<<dim3((unsigned)(a.c.n * a.c.Hkv), (unsigned)cut.parts), kWarps * 32, smem, stream>>>(a, parts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || cut.parts == 1) return e;
-    return attn::launch_behind(join_kernel<D, 16 * TB>, a.c.T * a.c.Hq, 128, stream, a, parts);
+    return attn::launch_behind(join_kernel<D, 16 * TB>, attn::join_blocks(parts, a.c.T * a.c.Hq), 128, stream, a, parts, attn::join_warps(parts));
 }
 
 template <int D, bool FP4>

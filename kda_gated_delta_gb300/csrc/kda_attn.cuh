@@ -91,43 +91,54 @@ cudaError_t launch_behind(void (*kernel)(P...), int64_t blocks, int threads, cud
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// One row's n > 1 parts joined by the four warps of a CTA: each takes every fourth part, its lanes D / 32
-// channels each, and the first puts their sums together.
+// How many of a joining CTA's four warps share a row: one while there are few parts (a verify of 8,192 rows in
+// 4 parts takes 140 us with a warp a row, 146 with a CTA a row), all four when a row's parts are a long chain
+// of loads (a step of 512 rows in 64 parts: 380 us against 399).
+inline int join_warps(const Parts& p) { return p.max_parts > 8 ? 4 : 1; }
+inline int64_t join_blocks(const Parts& p, int64_t rows) { return p.max_parts > 8 ? rows : (rows + 3) / 4; }
+__device__ __forceinline__ int64_t join_row_index(int share) { return ((int64_t)blockIdx.x * 4 + threadIdx.x / 32) / share; }
+
+// One row's parts joined by `share` warps: each takes every share-th part, its lanes D / 32 channels each, and
+// the first puts their sums together.  n <= 1: nothing to join.  All warps of the CTA come here.
 template <int D>
-__device__ __forceinline__ void join_row(const AttnCall& a, const Parts& parts, int64_t row, int n)
+__device__ __forceinline__ void join_row(const AttnCall& a, const Parts& parts, int64_t row, int n, int share)
 {
     constexpr int N = D / 32;
     __shared__ float sm_o[4][D], sm_sum[4];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, first = warp % share;
     const float* lse = parts.lse2 + row * parts.max_parts;
     const float* src = parts.o + row * parts.max_parts * D + lane * N;
     float mx = -INFINITY, sum = 0.f, o[N] = {};
-    for (int i = lane; i < n; i += 32) mx = fmaxf(mx, lse[i]);
+    if (n > 1) {
+        for (int i = lane; i < n; i += 32) mx = fmaxf(mx, lse[i]);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-    if (mx == -INFINITY) mx = 0.f;                                    // nothing seen, or NaN (which the weights carry on)
+        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+        if (mx == -INFINITY) mx = 0.f;                                // nothing seen, or NaN (which the weights carry on)
 #pragma unroll 4
-    for (int i = warp; i < n; i += 4) {
-        const float w = ex2(lse[i] - mx);
-        sum += w;
+        for (int i = first; i < n; i += share) {
+            const float w = ex2(lse[i] - mx);
+            sum += w;
 #pragma unroll
-        for (int j = 0; j < N; ++j) o[j] += w * src[(int64_t)i * D + j];
+            for (int j = 0; j < N; ++j) o[j] += w * src[(int64_t)i * D + j];
+        }
     }
+    if (share > 1) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) sm_o[warp][lane * N + j] = o[j];
-    if (lane == 0) sm_sum[warp] = sum;
-    __syncthreads();
-    if (warp != 0) return;
-    sum = (sm_sum[0] + sm_sum[1]) + (sm_sum[2] + sm_sum[3]);
+        for (int j = 0; j < N; ++j) sm_o[warp][lane * N + j] = o[j];
+        if (lane == 0) sm_sum[warp] = sum;
+        __syncthreads();
+        sum = (sm_sum[0] + sm_sum[1]) + (sm_sum[2] + sm_sum[3]);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int c = lane * N + j;
+            o[j] = (sm_o[0][c] + sm_o[1][c]) + (sm_o[2][c] + sm_o[3][c]);
+        }
+    }
+    if (n <= 1 || first != 0) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + row * D + lane * N;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int c = lane * N + j;
-        o[j] = ((sm_o[0][c] + sm_o[1][c]) + (sm_o[2][c] + sm_o[3][c])) * inv;
-    }
-#pragma unroll
-    for (int j = 0; j < N; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = kv::f32_to_bf16x2(o[j], o[j + 1]);
+    for (int j = 0; j < N; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = kv::f32_to_bf16x2(o[j] * inv, o[j + 1] * inv);
     if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + lg2(sum)) * kLn2;
 }
 

@@ -795,12 +795,12 @@ __global__ void __launch_bounds__(Cfg<D, FP4>::kThreads, 1)
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of each row that has several: a CTA per row.
+// Joins the parts of each row that has several.
 template <int D>
-__global__ void __launch_bounds__(128) join_rows_kernel(AttnCall a, Parts parts)
+__global__ void __launch_bounds__(128) join_rows_kernel(AttnCall a, Parts parts, const int share)
 {
     a.c.err = &g_attn_tc_error;
-    const int64_t row = blockIdx.x, t = row / a.c.Hq;
+    const int64_t rows = a.c.T * a.c.Hq, row = min(attn::join_row_index(share), rows - 1), t = row / a.c.Hq;
     int b = 0, n = 1;
     int64_t pos, t0, t1;
     const bool sees = kv::token_place(a.c, t, b, pos);
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(128) join_rows_kernel(AttnCall a, Parts parts)
         n = min(parts.max_parts, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part);
     }
     attn::wait_for_last();
-    if (n > 1) attn::join_row<D>(a, parts, row, n);
+    attn::join_row<D>(a, parts, row, attn::join_row_index(share) < rows ? n : 0, share);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder()
@@ -893,7 +893,7 @@ cudaError_t launch_many(const kda_kv_params& p, const AttnCall& a, const Parts& 
     many_rows_kernel<D, FP4><<<dim3((unsigned)(tiles * a.c.Hkv), (unsigned)parts.max_parts), C::kThreads, C::kSmem, stream>>>(a, parts, km, vm);
     e = cudaGetLastError();
     if (e != cudaSuccess || parts.max_parts == 1) return e;
-    return attn::launch_behind(join_rows_kernel<D>, a.c.T * a.c.Hq, 128, stream, a, parts);
+    return attn::launch_behind(join_rows_kernel<D>, attn::join_blocks(parts, a.c.T * a.c.Hq), 128, stream, a, parts, attn::join_warps(parts));
 }
 
 template cudaError_t launch_many<64, false>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
