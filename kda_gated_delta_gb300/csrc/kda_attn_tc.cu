@@ -56,13 +56,19 @@ struct Cfg {
     static constexpr int kSmem = 2 * kTileBytes + kSlots * kTileBytes + 1024 /* alignment */ + 320 /* barriers */;
 };
 
+// A row tile: its request, that request's rows and length, and the tile's first row.
+struct Tile {
+    int32_t found, b, row0, len;
+    int64_t t0, t1;
+};
+
 struct __align__(8) Bars {
     uint64_t full[8], empty[8];
     uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2];
     uint64_t drain;
     uint64_t patch[4];                // arrival of the value tiles that are mended before use
     uint32_t tmem;
-    int32_t place[4];                 // request, first row of the CTA, found
+    Tile tile;                        // the CTA's
 };
 static_assert(sizeof(Bars) <= 320, "barrier block");
 
@@ -132,12 +138,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int la
     return __all_sync(~0u, ok);
 }
 
-// Request and first row of the CTA with index x among all row tiles; false past the last one.  One warp.
-__device__ __forceinline__ bool find_rows(const kv::Paged& c, int64_t x, int lane, int& b, int64_t& row0)
+// Row tile x among all row tiles of the batch (found = 0 past the last one), by one warp: a lane per request.
+__device__ __forceinline__ Tile find_rows(const kv::Paged& c, int64_t x, int lane)
 {
     for (int base = 0; base < c.n; base += 32) {
         int64_t t0 = 0, t1 = 0;
-        if (base + lane < c.n) kv::request_rows(c, base + lane, t0, t1);
+        int len = 0;
+        if (base + lane < c.n) {
+            len = c.lens[base + lane];
+            kv::request_rows(c, base + lane, t0, t1);
+        }
         const int64_t tiles = ((t1 - t0) * c.G + kRows - 1) / kRows;
         int64_t sum = tiles;
 #pragma unroll
@@ -149,13 +159,19 @@ __device__ __forceinline__ bool find_rows(const kv::Paged& c, int64_t x, int lan
         if (hit) {
             const int who = __ffs(hit) - 1;
             const int64_t before = __shfl_sync(~0u, sum - tiles, who), mine = __shfl_sync(~0u, tiles, who);
-            b = base + who;
-            row0 = (mine - 1 - (x - before)) * kRows;            // a request's last rows, which see most, first
-            return true;
+            Tile r;
+            r.found = 1;
+            r.b = base + who;
+            r.row0 = (int32_t)((mine - 1 - (x - before)) * kRows);   // a request's last rows, which see most, first
+            r.len = __shfl_sync(~0u, len, who);
+            r.t0 = __shfl_sync(~0u, t0, who);
+            r.t1 = __shfl_sync(~0u, t1, who);
+            return r;
         }
         x -= __shfl_sync(~0u, sum, 31);
     }
-    return false;
+    Tile none = {};
+    return none;
 }
 
 struct Work {
@@ -709,24 +725,25 @@ __global__ void __launch_bounds__(Cfg<D, FP4>::kThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     if (warp == 0) {
-        int b = 0;
-        int64_t row0 = 0;
-        const bool found = find_rows(a.c, blockIdx.x / a.c.Hkv, lane, b, row0);
-        if (lane == 0) bars->place[0] = found ? 1 : 0, bars->place[1] = b, bars->place[2] = (int32_t)row0;
-    } else if (warp == 1 && lane == 0) {
-        for (int i = 0; i < C::kSlots; ++i) {
-            tc::mbar_init(&bars->full[i], FP4 ? C::kFillThreads / 32 : 1);
-            tc::mbar_init(&bars->empty[i], 2);
-        }
-        for (int i = 0; i < 2; ++i) {
+        const Tile tile = find_rows(a.c, blockIdx.x / a.c.Hkv, lane);
+        if (lane == 0) bars->tile = tile;
+    } else if (warp == 1) {
+        // a lane per barrier
+        if (lane < C::kSlots) {
+            tc::mbar_init(&bars->full[lane], FP4 ? C::kFillThreads / 32 : 1);
+            tc::mbar_init(&bars->empty[lane], 2);
+        } else if (lane >= 8 && lane < 10) {
+            const int i = lane - 8;
             tc::mbar_init(&bars->q_full[i], 4);
             tc::mbar_init(&bars->s_full[i], 1);
             tc::mbar_init(&bars->p_ready[i][0], 4);
             tc::mbar_init(&bars->p_ready[i][1], 4);
             tc::mbar_init(&bars->o_full[i], 1);
+        } else if (lane >= 10 && lane < 14) {
+            tc::mbar_init(&bars->patch[lane - 10], 1);
+        } else if (lane == 14) {
+            tc::mbar_init(&bars->drain, 1);
         }
-        for (int i = 0; i < 4; ++i) tc::mbar_init(&bars->patch[i], 1);
-        tc::mbar_init(&bars->drain, 1);
         tc::fence_mbar_init();
     } else if (warp == 8) {
         tc::tmem_alloc(&bars->tmem, 512);
@@ -739,16 +756,16 @@ __global__ void __launch_bounds__(Cfg<D, FP4>::kThreads, 1)
     attn::let_next_launch();
 
     Work w;
-    bool live = bars->place[0] != 0;
+    const Tile tile = bars->tile;
+    bool live = tile.found != 0;
     int parts_here = 1;
     const int part = blockIdx.y;
     if (live) {
-        w.b = bars->place[1];
+        w.b = tile.b;
         w.h = blockIdx.x % a.c.Hkv;
-        w.row0 = bars->place[2];
-        int64_t t1;
-        kv::request_rows(a.c, w.b, w.t0, t1);
-        const int fresh = (int)(t1 - w.t0), len = a.c.lens[w.b];
+        w.row0 = tile.row0;
+        w.t0 = tile.t0;
+        const int fresh = (int)(tile.t1 - tile.t0), len = tile.len;
         w.R = fresh * a.c.G;
         if (threadIdx.x == 0 && part == 0 && w.h == 0 && (len > a.max_len || fresh > a.max_new)) kv::record(a.c, kv::kErrLength);
         w.first = len > 0 ? len - fresh : -1 - fresh;
