@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
     const int G = a.c.G;
 
-    attn::let_next_launch();
+    if (parts.o) attn::let_next_launch();
     int64_t t0, t1;
     kv::request_rows(a.c, b, t0, t1);
     const int len = a.c.lens[b];
@@ -217,10 +217,10 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     if (threadIdx.x == 0 && part == 0 && h == 0 && (len > room || fresh > a.max_new)) kv::record(a.c, kv::kErrLength);
     const int first = len > 0 ? len - fresh : -1 - fresh;          // position of the first new token; a padding request has none
     const Span sp = attn::make_span<kTile>(max(first, 0), len > 0 ? len - 1 : -1, room, a.window, a.sinks);
-    const int parts_here = parts.o ? min(parts.max_parts, max(1, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part)) : 1;
-    if (part >= parts_here) return;
+    const int parts_here = parts.max_parts > 1 ? min(parts.max_parts, max(1, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part)) : 1;
+    if (part >= parts_here && !parts.in_cluster) return;              // a cluster's CTA stays, with nothing to see
     const int tile_lo = parts_here > 1 ? part * parts.tiles_per_part : 0;
-    const int tile_hi = parts_here > 1 ? min(sp.tiles, tile_lo + parts.tiles_per_part) : sp.tiles;
+    const int tile_hi = part >= parts_here ? tile_lo : parts_here > 1 ? min(sp.tiles, tile_lo + parts.tiles_per_part) : sp.tiles;
 
     // ---- queries: B fragments in the channel order of the key loads -------------------------------------
     uint32_t q[NT][KS][2];
@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     // ---- join the four warps ------------------------------------------------------------------------------
     constexpr int N = 8 * NT, kPad = D + 4;
     __shared__ float sm_m[kWarps][N], sm_l[kWarps][N];
-    extern __shared__ float sm_o[];                                   // [warps][rows][kPad]
+    extern __shared__ float sm_o[];                                   // [warps][rows][kPad]; cluster: then [rows][D], [rows]
+    float* const mine = sm_o + kWarps * N * kPad;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -533,7 +534,10 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t out_row = (t0 + row / G) * a.c.Hq + h * G + row % G;
         const float lse2 = sum == 0.f ? -INFINITY : mx + attn::lg2(sum);
-        if (parts_here > 1) {
+        if (parts.in_cluster) {
+            *reinterpret_cast<float4*>(mine + row * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (d == 0) mine[N * D + row] = lse2;
+        } else if (parts_here > 1) {
             const int64_t at = out_row * parts.max_parts + part;
             *reinterpret_cast<float4*>(parts.o + at * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
             if (d == 0) parts.lse2[at] = lse2;
@@ -543,6 +547,31 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
             if (a.lse && d == 0) a.lse[out_row] = lse2 * attn::kLn2;
         }
     }
+    if (!parts.in_cluster) return;
+
+    // ---- join the cluster's parts: each CTA some of the rows ------------------------------------------------
+    attn::cluster_barrier();
+    const int P = gridDim.y;
+    for (int x = threadIdx.x; part + x / (D / 4) * P < rows; x += kWarps * 32) {
+        const int row = part + x / (D / 4) * P, d = x % (D / 4) * 4;
+        float mx = -INFINITY, sum = 0.f;
+        for (int w = 0; w < P; ++w) mx = fmaxf(mx, attn::ld_cluster(attn::cluster_addr(mine + N * D + row, w)));
+        if (mx == -INFINITY) mx = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < P; ++w) {
+            const float f = attn::ex2(attn::ld_cluster(attn::cluster_addr(mine + N * D + row, w)) - mx);
+            const float4 y = attn::ld_cluster4(attn::cluster_addr(mine + row * D + d, w));
+            sum += f;
+            acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t out_row = (t0 + row / G) * a.c.Hq + h * G + row % G;
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + out_row * D + d) =
+            make_uint2(kv::f32_to_bf16x2(acc.x * inv, acc.y * inv), kv::f32_to_bf16x2(acc.z * inv, acc.w * inv));
+        if (a.lse && d == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (mx + attn::lg2(sum)) * attn::kLn2;
+    }
+    attn::cluster_barrier();                                          // nobody leaves while its parts are read
 }
 
 // Joins the parts of each row that has several.
@@ -579,6 +608,11 @@ constexpr int kFewRows = 16;
 constexpr int kFewTile(bool fp4) { return fp4 ? 32 : 16; }
 constexpr int64_t kCtas = 8192;
 constexpr int kMinPart = 256;
+// Up to eight parts are the CTAs of a cluster, which join through each other's shared memory: no workspace and
+// no second launch (one token over 4096: 21 -> 17 us a call).  Only while all CTAs run at once: a cluster keeps
+// its SMs' places until its last part is done (64 ragged requests in clusters: 266 us against 192).  More parts,
+// worth it from kClusterPart tokens each on, go through the workspace.
+constexpr int64_t kCluster = 8, kClusterPart = 1024, kClusterCtas = 304;
 
 attn::Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t max_len)
 {
@@ -594,11 +628,13 @@ attn::Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t ma
     int64_t parts = (kCtas + ctas - 1) / ctas;
     const int64_t most = tokens / min_part;
     if (parts > most) parts = most;
+    if (parts > kCluster && tokens <= kCluster * kClusterPart && ctas * kCluster <= kClusterCtas) parts = kCluster;
     if (parts > 256) parts = 256;
     if (parts < 1) parts = 1;
     attn::Cut c;
     c.tiles_per_part = (int32_t)((tiles + parts - 1) / parts);
     c.parts = (int32_t)((tiles + c.tiles_per_part - 1) / c.tiles_per_part);
+    c.in_cluster = c.parts > 1 && c.parts <= kCluster && ctas * c.parts <= kClusterCtas;
     return c;
 }
 
@@ -612,8 +648,9 @@ Parts make_parts(const kda_kv_params& p, int64_t T, const attn::Cut& c, void* wo
     Parts x;
     x.max_parts = c.parts;
     x.tiles_per_part = c.tiles_per_part;
-    x.o = c.parts > 1 ? (float*)workspace : nullptr;
-    x.lse2 = c.parts > 1 ? (float*)workspace + (size_t)T * p.num_q_heads * c.parts * p.head_dim : nullptr;
+    x.in_cluster = c.in_cluster;
+    x.o = c.parts > 1 && !c.in_cluster ? (float*)workspace : nullptr;
+    x.lse2 = c.parts > 1 && !c.in_cluster ? (float*)workspace + (size_t)T * p.num_q_heads * c.parts * p.head_dim : nullptr;
     return x;
 }
 
@@ -623,7 +660,23 @@ cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const attn::Cu
     constexpr int TB = kFewTile(FP4) / 16;
     const Parts parts = make_parts(p, a.c.T, cut, workspace);
     const size_t smem = (size_t)kWarps * 8 * NT * (D + 4) * 4;
-    few_rows_kernel<D, FP4, NT, TB><<<dim3((unsigned)(a.c.n * a.c.Hkv), (unsigned)cut.parts), kWarps * 32, smem, stream>>>(a, parts);
+    const dim3 grid((unsigned)(a.c.n * a.c.Hkv), (unsigned)cut.parts);
+    if (cut.in_cluster) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kWarps * 32);
+        cfg.dynamicSmemBytes = smem + (size_t)8 * NT * (D + 1) * 4;
+        cfg.stream = stream;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 1;
+        at.val.clusterDim.y = (unsigned)cut.parts;
+        at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, few_rows_kernel<D, FP4, NT, TB>, a, parts);
+    }
+    few_rows_kernel<D, FP4, NT, TB><<<grid, kWarps * 32, smem, stream>>>(a, parts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || cut.parts == 1) return e;
     return attn::launch_behind(join_kernel<D, 16 * TB>, attn::join_blocks(parts, a.c.T * a.c.Hq), 128, stream, a, parts, attn::join_warps(parts));
@@ -648,7 +701,7 @@ size_t attention_workspace_bytes(const kda_kv_params& p, int32_t num_seqs, int64
 {
     const int64_t rows = (int64_t)max_new * (p.num_q_heads / p.num_kv_heads);
     const attn::Cut cut = rows <= kFewRows ? cut_few(p, num_seqs, max_new, max_len) : cut_many(p, num_seqs, total_tokens, max_new, max_len);
-    return cut.parts > 1 ? parts_bytes(p, total_tokens, cut.parts) : 0;
+    return cut.parts > 1 && !cut.in_cluster ? parts_bytes(p, total_tokens, cut.parts) : 0;
 }
 
 cudaError_t launch_attention(const kda_kv_params& p, const AttnCall& a, void* workspace, cudaStream_t stream)

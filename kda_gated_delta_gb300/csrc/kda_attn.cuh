@@ -50,11 +50,13 @@ struct Parts {
     float* lse2;
     int32_t max_parts;
     int32_t tiles_per_part;
+    int32_t in_cluster;        // the parts' CTAs are one cluster and join among themselves: o and lse2 are not used
 };
 
 // How the host cuts a call along the cache; parts = 1: not at all.
 struct Cut {
     int32_t parts, tiles_per_part;
+    bool in_cluster = false;
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -68,6 +70,31 @@ __device__ __forceinline__ float lg2(float x)
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Shared memory of the cluster's CTA `rank` at this CTA's address p.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+// All threads of all CTAs of the cluster, what they wrote to shared memory before included.
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // The joining kernel may be launched as soon as every CTA of the parts' kernel has begun, and waits there for

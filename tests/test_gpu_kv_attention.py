@@ -106,6 +106,17 @@ def test_decode_long_is_split(dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("past,D,window,sinks", [([3000, 100, -1], 128, 0, 0), ([900], 128, 0, 0), ([1700, 40, 650], 64, 0, 0), ([5000, 2049], 128, 1500, 70)])
+def test_few_requests_join_in_clusters(dtype, past, D, window, sinks):
+    """A few requests of some thousand tokens: up to eight parts, some of them empty, joined on the chip."""
+    b = ref.Batch([1] * len(past), past, 32, seed=len(past), drop=(window, sinks))
+    _attend(b, 8, 2, D, dtype, window=window, sinks=sinks, decode=True)
+    if min(past) > 4:
+        b = ref.Batch([3] * len(past), past, 32, seed=len(past), drop=(window, sinks))
+        _attend(b, 10, 2, D, dtype, window=window, sinks=sinks)
+
+
+@BOTH
 @pytest.mark.parametrize("new,G,D", [(2, 4, 128), (4, 4, 128), (3, 5, 64), (16, 1, 128), (16, 8, 64), (9, 16, 128)])
 def test_verify(dtype, new, G, D):
     b = ref.Batch([new] * 4, [0, 13, 130, 511], 32, seed=new)
