@@ -476,12 +476,24 @@ def _fn(name):
     return getattr(lib(), name)
 
 
-def _raw_stream(stream, t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+def _on_stream(f):
+    """With ``stream``, run ``f`` with it as the current stream: what the call allocates then belongs to it."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
 
 
+def _raw_stream(t):
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+@_on_stream
 def kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, *, q=None, q_out=None, rope=None,
-              interleaved=False, positions=None, stream=None):
+              interleaved=False, positions=None):
     """kda_kv_append: write the new tokens' keys and values ([T, kv heads, D] bf16) into the cache, the
     keys rotated by the table ``rope`` ([positions, rot_dim], see :func:`rope_table`; None: no rotation).
     With ``q`` ([T, q heads, D]) returns it rotated (into ``q_out``, which may be ``q``)."""
@@ -519,13 +531,14 @@ def kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, *, q=None, q_o
         raise ValueError("q_out without q")
     rc = _fn("kda_kv_append")(_kv_params(Hq, Hkv, D, page, fp4, rot, interleaved), qp, q_stride, kp, k_stride, vp, v_stride,
                               rp, rows, positions, pc, pl, pt, n, max_pages, T, pk, pv, pks, pvs, pages, qo,
-                              _raw_stream(stream, k))
+                              _raw_stream(k))
     if rc:
         _check(rc, "kda_kv_append")
     return q_out
 
 
-def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, out=None, stream=None):
+@_on_stream
+def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, out=None):
     """kda_kv_read: the last tokens of each request, as many as ``cu_seqlens`` gives it (None: one each),
     as bf16 (k, v) [T, kv heads, D].  ``num_tokens`` = cu_seqlens[-1] is needed with ``cu_seqlens``."""
     Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
@@ -542,7 +555,7 @@ def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, ou
             if t.shape != (T, Hkv, D):
                 raise ValueError(f"{name} must be [{T}, {Hkv}, {D}]")
     rc = _fn("kda_kv_read")(_kv_params(Hkv, Hkv, D, page, fp4), pk, pv, pks, pvs, pages, *batch, out[0].data_ptr(),
-                            out[1].data_ptr(), _raw_stream(stream, kv_lens))
+                            out[1].data_ptr(), _raw_stream(kv_lens))
     if rc:
         _check(rc, "kda_kv_read")
     return out
@@ -553,8 +566,9 @@ def _attention_workspace(p, n, T, max_new, max_len):
     return int(lib().kda_paged_attention_workspace_size(p, n, T, max_new, max_len))
 
 
+@_on_stream
 def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0, sinks=0, scale=None,
-                    max_new=None, max_len=None, out=None, lse=None, return_lse=False, workspace=None, stream=None):
+                    max_new=None, max_len=None, out=None, lse=None, return_lse=False, workspace=None):
     """kda_paged_attention: ``q`` [T, q heads, D] bf16 over the cache; returns ``out`` (or ``(out, lse)``).
 
     ``window`` 0: all tokens up to a query's own; w: the last w of them and the first ``sinks``.
@@ -590,7 +604,7 @@ def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0
     if workspace is not None:
         ws = workspace.data_ptr()
     rc = _fn("kda_paged_attention")(p, qp, q_stride, pk, pv, pks, pvs, pages, *batch, max_new, max_len, out.data_ptr(),
-                                    None if lse is None else lse.data_ptr(), ws, need, _raw_stream(stream, q))
+                                    None if lse is None else lse.data_ptr(), ws, need, _raw_stream(q))
     if rc:
         _check(rc, "kda_paged_attention")
     return out if lse is None else (out, lse)
