@@ -476,27 +476,19 @@ def _fn(name):
     return getattr(lib(), name)
 
 
-def _on_stream(f):
-    """With ``stream``, run ``f`` with it as the current stream: what the call allocates then belongs to it."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
-
-
 def _raw_stream(t):
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-@_on_stream
 def kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, *, q=None, q_out=None, rope=None,
-              interleaved=False, positions=None):
+              interleaved=False, positions=None, stream=None):
     """kda_kv_append: write the new tokens' keys and values ([T, kv heads, D] bf16) into the cache, the
     keys rotated by the table ``rope`` ([positions, rot_dim], see :func:`rope_table`; None: no rotation).
     With ``q`` ([T, q heads, D]) returns it rotated (into ``q_out``, which may be ``q``)."""
+    if stream is not None:                                    # what the call allocates belongs to its stream
+        with torch.cuda.stream(stream):
+            return kv_append(k, v, cache, block_table, kv_lens, cu_seqlens, q=q, q_out=q_out, rope=rope,
+                             interleaved=interleaved, positions=positions)
     Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
     kp, k_stride, T, _ = _rows(k, "k", Hkv, D)
     vp, v_stride, Tv, _ = _rows(v, "v", Hkv, D)
@@ -537,10 +529,12 @@ def kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, *, q=None, q_o
     return q_out
 
 
-@_on_stream
-def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, out=None):
+def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, out=None, stream=None):
     """kda_kv_read: the last tokens of each request, as many as ``cu_seqlens`` gives it (None: one each),
     as bf16 (k, v) [T, kv heads, D].  ``num_tokens`` = cu_seqlens[-1] is needed with ``cu_seqlens``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_read(cache, block_table, kv_lens, cu_seqlens, num_tokens=num_tokens, out=out)
     Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
     T = kv_lens.shape[0] if cu_seqlens is None else num_tokens
     if T is None:
@@ -566,14 +560,18 @@ def _attention_workspace(p, n, T, max_new, max_len):
     return int(lib().kda_paged_attention_workspace_size(p, n, T, max_new, max_len))
 
 
-@_on_stream
 def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0, sinks=0, scale=None,
-                    max_new=None, max_len=None, out=None, lse=None, return_lse=False, workspace=None):
+                    max_new=None, max_len=None, out=None, lse=None, return_lse=False, workspace=None, stream=None):
     """kda_paged_attention: ``q`` [T, q heads, D] bf16 over the cache; returns ``out`` (or ``(out, lse)``).
 
     ``window`` 0: all tokens up to a query's own; w: the last w of them and the first ``sinks``.
     ``max_new`` bounds the new tokens of a request (default: all T; 1 without ``cu_seqlens``), ``max_len``
     bounds kv_lens (default: what block_table can hold): host numbers, the tighter the better."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return paged_attention(q, cache, block_table, kv_lens, cu_seqlens, window=window, sinks=sinks, scale=scale,
+                                   max_new=max_new, max_len=max_len, out=out, lse=lse, return_lse=return_lse,
+                                   workspace=workspace)
     Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
     qp, q_stride, T, Hq = _rows(q, "q", None, D)
     batch = _kv_batch(cu_seqlens, kv_lens, block_table, T)
