@@ -116,26 +116,6 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* o)
         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
         : "r"(w));
 }
-// Four codes of two tokens (in the two halves of x, low code first) as four bf16 pairs of 2^-126 times the
-// values: a code's three magnitude bits, read as the lowest exponent and highest mantissa bits of a bf16
-// number, are that number exactly, 0.5 as a subnormal included.  The product with the scale puts the power
-// back (kBf16Up), but for 2^7 that would overflow and that the output's normalisation carries (kBf16Rest).
-constexpr float kBf16Up = 6.646139978924579e35f;   // 2^119
-constexpr float kBf16Rest = 128.0f;
-__device__ __forceinline__ void e2m1_columns_to_bf16(uint32_t x, uint32_t* o)
-{
-    constexpr uint32_t kSign = 0x80008000u, kMag = 0x01c001c0u;
-    o[0] = ((x << 12) & kSign) | ((x << 6) & kMag);
-    o[1] = ((x << 8) & kSign) | ((x << 2) & kMag);
-    o[2] = ((x << 4) & kSign) | ((x >> 2) & kMag);
-    o[3] = (x & kSign) | ((x >> 6) & kMag);
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t y;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-    return y;
-}
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair)
 {
     uint32_t r;
