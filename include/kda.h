@@ -325,7 +325,8 @@ int32_t kda_chunk_prefill_static_scratch(const kda_params* p,
  * The rows of q, k and v may be strided: *_stride is the distance between tokens in elements (the
  * heads of a token are contiguous), a multiple of 8.  Tensor pointers are 16-byte aligned.
  * Limits (KDA_ERR_UNSUPPORTED beyond them): total_tokens < 2^22, num_pages * num_kv_heads * page_size
- * < 2^31, max_pages * page_size < 2^31 - 256, num_q_heads <= 65535.
+ * < 2^31, max_pages * page_size < 2^31 - 256, num_q_heads <= 1024, num_seqs *
+ * num_kv_heads < 2^30.
  * ================================================================================================== */
 typedef enum kda_cache_dtype { KDA_CACHE_BF16 = 0, KDA_CACHE_FP4 = 1 } kda_cache_dtype;
 

@@ -22,7 +22,7 @@ int32_t check_params(const kda_kv_params* p)
     const int32_t s = p->page_size;
     if ((p->head_dim != 64 && p->head_dim != 128) || (s != 16 && s != 32 && s != 64 && s != 128) ||
         (p->cache_dtype != KDA_CACHE_BF16 && p->cache_dtype != KDA_CACHE_FP4) || p->rot_dim > p->head_dim ||
-        p->rot_dim % 32 != 0 || p->num_q_heads / p->num_kv_heads > 128 || p->num_q_heads > 65535)
+        p->rot_dim % 32 != 0 || p->num_q_heads / p->num_kv_heads > 128 || p->num_q_heads > 1024)
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
@@ -45,8 +45,8 @@ int32_t check_batch(const kda_kv_params* p, const void* kc, const void* vc, cons
     if (p->cache_dtype == KDA_CACHE_FP4 && (!ks || !vs)) return KDA_ERR_INVALID_ARG;
     if (misaligned(kc) || misaligned(vc)) return KDA_ERR_MISALIGNED;
     if (p->cache_dtype == KDA_CACHE_FP4 && (misaligned(ks) || misaligned(vs))) return KDA_ERR_MISALIGNED;
-    // token and page counts that the kernels' 32-bit grid and tensor-map coordinates can hold
-    if (T >= ((int64_t)1 << 31) / 512 || (int64_t)max_pages * p->page_size >= ((int64_t)1 << 31) - 256 ||
+    // counts that the kernels' 32-bit grids and tensor-map coordinates can hold
+    if ((int64_t)num_seqs * p->num_kv_heads >= ((int64_t)1 << 30) || T >= ((int64_t)1 << 31) / 512 || (int64_t)max_pages * p->page_size >= ((int64_t)1 << 31) - 256 ||
         num_pages * p->num_kv_heads * p->page_size >= ((int64_t)1 << 31))
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;

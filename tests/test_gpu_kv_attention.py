@@ -233,6 +233,39 @@ def test_step_in_a_graph(dtype):
     assert ((got[-1][0].cpu().double() - o).abs() <= ref.bounds(o, l, mag, big)[0]).all()
 
 
+@BOTH
+@pytest.mark.parametrize("new,past", [([1, 1], [9000, 20000]), ([1] * 40, [2000] * 40), ([1], [3000]), ([40, 3], [6000, 100]), ([300], [200])])
+def test_every_form_in_a_graph(dtype, new, past):
+    """Calls that are cut along the cache (joined by a kernel of their own or in a cluster) and prompts, captured:
+    a replay gives the bits of the plain call, also after the inputs changed in place."""
+    b = ref.Batch(new, past, 64, seed=21)
+    cache, _ = _filled_cache(b, 1, 128, dtype, 4)
+    table, lens, cu = b.on(DEV)
+    g = torch.Generator().manual_seed(6)
+    q = _bf(g, b.T, 4, 128).to(DEV)
+    kw = dict(max_new=max(new), max_len=int(b.lens.max()), return_lse=True)
+    kda.paged_attention(q, cache, table, lens, cu, **kw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = kda.paged_attention(q, cache, table, lens, cu, **kw)
+    for _ in range(2):
+        q.copy_(_bf(g, *q.shape))
+        graph.replay()
+        want = kda.paged_attention(q, cache, table, lens, cu, **kw)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@BOTH
+def test_limits_of_window_and_sinks(dtype):
+    """The largest values mean: everything."""
+    for new, past in (([1, 1], [100, 700]), ([40, 3], [100, 700])):
+        b = ref.Batch(new, past, 16, seed=22)
+        full = _attend(b, 8, 2, 128, dtype)
+        for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)):
+            assert torch.equal(_attend(b, 8, 2, 128, dtype, window=window, sinks=sinks), full)
+
+
 # ---- append and read ------------------------------------------------------------------------------------
 
 def _append_case(new, past, Hq, Hkv, D, page, dtype, rot, interleaved, seed=0, pad=0, with_positions=False, scale=None, decode=False):

@@ -60,6 +60,8 @@ def test_shared_checks(L, call):
     assert call(L, p=_p(rot_dim=16)) == -2
     assert call(L, p=_p(rot_dim=160)) == -2
     assert call(L, p=_p(Hq=258, Hkv=2), qs=258 * 128) == -2
+    assert call(L, p=_p(Hq=1032, Hkv=129), qs=1032 * 128) == -2
+    assert call(L, n=1 << 29) == -2
     assert call(L, n=-1) == -1 and call(L, T=-1) == -1 and call(L, mp=0) == -1
     assert call(L, cu=None) == -1                          # one token per request: T must equal n
     assert call(L, lens=None) == -1 and call(L, table=None) == -1
