@@ -25,7 +25,7 @@
 // rescaling.  The weights, at most 2^8 then, lose nothing by that in a floating-point format.
 //
 // Measured (8 kv and 32 query heads of 128): 64 requests of 512 to 8,192 tokens in 192 us, 6,380 GB/s of the 6,776
-// that a copy reaches; 16 requests of 4,096 to 131,072 tokens in 4 bits in 380 us, bound by the conversions (some
+// that a copy reaches; 16 requests of 4,096 to 131,072 tokens in 4 bits in 370 us, bound by the conversions (some
 // 500 instructions per 16 tokens).
 //
 // A warp takes every fourth tile of its CTA's part, with the next tile's keys requested as soon as the
@@ -199,7 +199,8 @@ __device__ __forceinline__ int32_t block_row(const AttnCall& a, int b, int base,
     return slot < 0 ? -1 : (int32_t)(slot + ((int64_t)h << a.c.page_shift));
 }
 
-template <int D, bool FP4, int NT, int TB>
+// CLUSTER: the parts' CTAs are one cluster and join among themselves (a variant of its own, for the registers).
+template <int D, bool FP4, int NT, int TB, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts parts)
 {
     a.c.err = &g_attn_error;
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
     const int G = a.c.G;
 
-    if (parts.o) attn::let_next_launch();
+    if (!CLUSTER && parts.o) attn::let_next_launch();
     int64_t t0, t1;
     kv::request_rows(a.c, b, t0, t1);
     const int len = a.c.lens[b];
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     const int first = len > 0 ? len - fresh : -1 - fresh;          // position of the first new token; a padding request has none
     const Span sp = attn::make_span<kTile>(max(first, 0), len > 0 ? len - 1 : -1, room, a.window, a.sinks);
     const int parts_here = parts.max_parts > 1 ? min(parts.max_parts, max(1, (sp.tiles + parts.tiles_per_part - 1) / parts.tiles_per_part)) : 1;
-    if (part >= parts_here && !parts.in_cluster) return;              // a cluster's CTA stays, with nothing to see
+    if (part >= parts_here && !CLUSTER) return;              // a cluster's CTA stays, with nothing to see
     const int tile_lo = parts_here > 1 ? part * parts.tiles_per_part : 0;
     const int tile_hi = part >= parts_here ? tile_lo : parts_here > 1 ? min(sp.tiles, tile_lo + parts.tiles_per_part) : sp.tiles;
 
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t out_row = (t0 + row / G) * a.c.Hq + h * G + row % G;
         const float lse2 = sum == 0.f ? -INFINITY : mx + attn::lg2(sum);
-        if (parts.in_cluster) {
+        if constexpr (CLUSTER) {
             *reinterpret_cast<float4*>(mine + row * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
             if (d == 0) mine[N * D + row] = lse2;
         } else if (parts_here > 1) {
@@ -551,7 +552,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
             if (a.lse && d == 0) a.lse[out_row] = lse2 * attn::kLn2;
         }
     }
-    if (!parts.in_cluster) return;
+    if constexpr (!CLUSTER) return;
 
     // ---- join the cluster's parts: each CTA some of the rows ------------------------------------------------
     attn::cluster_barrier();
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts, cons
 
 namespace {
 
-// Rows of a (request, kv head) up to which this form is taken: 64 requests of 16 rows take 136 us here and 148
+// Rows of a (request, kv head) up to which this form is taken: 64 requests of 16 rows take 140 us here and 148
 // in the tcgen05 form; more rows would not fit the registers.
 constexpr int kFewRows = 16;
 
@@ -655,7 +656,6 @@ Parts make_parts(const kda_kv_params& p, int64_t T, const attn::Cut& c, void* wo
     Parts x;
     x.max_parts = c.parts;
     x.tiles_per_part = c.tiles_per_part;
-    x.in_cluster = c.in_cluster;
     x.o = c.parts > 1 && !c.in_cluster ? (float*)workspace : nullptr;
     x.lse2 = c.parts > 1 && !c.in_cluster ? (float*)workspace + (size_t)T * p.num_q_heads * c.parts * p.head_dim : nullptr;
     return x;
@@ -681,9 +681,9 @@ cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const attn::Cu
         at.val.clusterDim.z = 1;
         cfg.attrs = &at;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, few_rows_kernel<D, FP4, NT, TB>, a, parts);
+        return cudaLaunchKernelEx(&cfg, few_rows_kernel<D, FP4, NT, TB, true>, a, parts);
     }
-    few_rows_kernel<D, FP4, NT, TB><<<grid, kWarps * 32, smem, stream>>>(a, parts);
+    few_rows_kernel<D, FP4, NT, TB, false><<<grid, kWarps * 32, smem, stream>>>(a, parts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || cut.parts == 1) return e;
     return attn::launch_behind(join_kernel<D, 16 * TB>, attn::join_blocks(parts, a.c.T * a.c.Hq), 128, stream, a, parts, attn::join_warps(parts));

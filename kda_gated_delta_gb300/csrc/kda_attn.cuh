@@ -46,11 +46,10 @@ __device__ __forceinline__ int32_t tile_base(const Span& s, int32_t i)
 // Parts of a row that several CTAs worked on: [row][part][D] fp32 outputs, each normalised by its own
 // sum, and their log2 of the sum of exponentials [row][part], -inf for an empty part.
 struct Parts {
-    float* o;
+    float* o;                  // null where the parts' CTAs join in a cluster, and where there is one part
     float* lse2;
     int32_t max_parts;
     int32_t tiles_per_part;
-    int32_t in_cluster;        // the parts' CTAs are one cluster and join among themselves: o and lse2 are not used
 };
 
 // How the host cuts a call along the cache; parts = 1: not at all.
