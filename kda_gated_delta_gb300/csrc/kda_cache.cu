@@ -7,8 +7,8 @@
 // loads in flight at once, and the rotation's cosines and sines are loaded once for them.
 //
 // Measured: 16,412 tokens of 32 query and 8 kv heads of 128, bf16, in 72 us, 6,500 GB/s of the 6,776 that a copy
-// reaches; 16,411 tokens into a 4-bit cache in 67 us (5,300 GB/s; the quantiser's instructions), and back in 21.
-// Rows per thread, 4-bit cache: 2 take 84 us, 6 take 77.
+// reaches; 16,411 tokens into a 4-bit cache in 63 us (5,600 GB/s; the quantiser's instructions), and back in 22.
+// Into the 4-bit cache 2 rows per thread take 84 us and 6 take 77; CTAs of 256 threads 67 and of 64 threads 66.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -23,7 +23,7 @@ namespace {
 
 __device__ int32_t g_cache_error = 0;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kRows = 4;
 
 struct AppendArgs {
