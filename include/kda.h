@@ -395,7 +395,8 @@ int32_t kda_kv_read(const kda_kv_params* p,
  * A query that sees no token (padding) gets zeros and lse = -infinity.  What masked and unwritten cache
  * slots hold, NaN included, does not matter, with one exception: a non-finite VALUE that some query of a
  * call may see can make the outputs of other queries of its request in that call non-finite.
- *   max_new_tokens  host bound on the new tokens of any one request (1 when cu_seqlens is NULL)
+ *   max_new_tokens  host bound on the new tokens of any one request (1 when cu_seqlens is NULL); anything
+ *                   from total_tokens up bounds nothing
  *   max_kv_len      host bound on kv_lens; at most max_pages * page_size.  A tight bound means less
  *                   workspace and better-sized work.
  *   workspace       kda_paged_attention_workspace_size(...) bytes, 256-byte aligned, contents garbage

@@ -605,7 +605,8 @@ namespace {
 
 // Rows of a (request, kv head) up to which this form is taken: 64 requests of 16 rows take 140 us here and 148
 // in the tcgen05 form; more rows would not fit the registers.
-constexpr int kFewRows = 16;
+constexpr int64_t kFewRows = 16;
+int64_t rows_of(const kda_kv_params& p, int32_t max_new) { return (int64_t)max_new * (p.num_q_heads / p.num_kv_heads); }
 
 // How a call of the few-rows form is cut along the cache.  An uncut call has one CTA per (request, kv
 // head).  The cut aims at kCtas CTAs for the longest histories the caller's bound allows, so that ragged
@@ -615,7 +616,7 @@ constexpr int kFewRows = 16;
 // Tokens of a tile; in 4 bits two blocks of 16, whose shared softmax steps save instructions (380 -> 372 us).
 constexpr int kFewTile(bool fp4) { return fp4 ? 32 : 16; }
 constexpr int64_t kCtas = 8192;
-constexpr int kMinPart = 256;
+constexpr int64_t kMinPart = 256;
 // Up to eight parts are the CTAs of a cluster, which join through each other's shared memory: no workspace and
 // no second launch (one token over 4096: 21 -> 17 us a call).  Only while all CTAs run at once: a cluster keeps
 // its SMs' places until its last part is done (64 ragged requests in clusters: 266 us against 192).  More parts,
@@ -624,8 +625,8 @@ constexpr int64_t kCluster = 8, kClusterPart = 1024, kClusterCtas = 304;
 
 attn::Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t max_len)
 {
-    const int tile = kFewTile(p.cache_dtype == KDA_CACHE_FP4), rows = max_new * (p.num_q_heads / p.num_kv_heads);
-    const int min_part = std::max(kMinPart, p.cache_dtype == KDA_CACHE_FP4 ? 228 * rows : 64 * rows);
+    const int tile = kFewTile(p.cache_dtype == KDA_CACHE_FP4);
+    const int64_t rows = rows_of(p, max_new), min_part = std::max(kMinPart, p.cache_dtype == KDA_CACHE_FP4 ? 228 * rows : 64 * rows);
     int64_t tokens = max_len;
     if (p.window) {
         const int64_t seen = (int64_t)p.window + max_new + p.num_sinks + 3 * tile;   // both runs, rounded out to tiles
@@ -692,7 +693,7 @@ cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const attn::Cu
 template <int D, bool FP4>
 cudaError_t launch_typed(const kda_kv_params& p, const AttnCall& a, void* workspace, cudaStream_t stream)
 {
-    const int rows = a.max_new * a.c.G;
+    const int64_t rows = rows_of(p, a.max_new);
     if (rows <= kFewRows) {
         const attn::Cut cut = cut_few(p, a.c.n, a.max_new, a.max_len);
         return rows <= 8 ? launch_few<D, FP4, 1>(p, a, cut, workspace, stream) : launch_few<D, FP4, 2>(p, a, cut, workspace, stream);
@@ -706,8 +707,7 @@ cudaError_t launch_typed(const kda_kv_params& p, const AttnCall& a, void* worksp
 size_t attention_workspace_bytes(const kda_kv_params& p, int32_t num_seqs, int64_t total_tokens, int32_t max_new,
                                  int32_t max_len)
 {
-    const int64_t rows = (int64_t)max_new * (p.num_q_heads / p.num_kv_heads);
-    const attn::Cut cut = rows <= kFewRows ? cut_few(p, num_seqs, max_new, max_len) : cut_many(p, num_seqs, total_tokens, max_new, max_len);
+    const attn::Cut cut = rows_of(p, max_new) <= kFewRows ? cut_few(p, num_seqs, max_new, max_len) : cut_many(p, num_seqs, total_tokens, max_new, max_len);
     return cut.parts > 1 && !cut.in_cluster ? parts_bytes(p, total_tokens, cut.parts) : 0;
 }
 

@@ -66,6 +66,13 @@ kda::kv::Paged paged(const kda_kv_params* p, const void* kc, const void* vc, con
     return c;
 }
 
+// The bound on a request's new tokens that every size and form goes by, in the workspace query and in the call
+// alike: a caller without one may pass any large number, and no request has more than all tokens.
+int32_t new_tokens_bound(int32_t max_new_tokens, int64_t total_tokens)
+{
+    return total_tokens < max_new_tokens ? (int32_t)total_tokens : max_new_tokens;
+}
+
 bool bad_stride(int64_t stride, int heads, int D) { return stride < (int64_t)heads * D || stride % 8 != 0; }
 
 }  // namespace
@@ -130,7 +137,7 @@ size_t kda_paged_attention_workspace_size(const kda_kv_params* p, int32_t num_se
                                           int32_t max_new_tokens, int32_t max_kv_len)
 {
     if (check_params(p) != KDA_OK || num_seqs <= 0 || total_tokens <= 0 || max_new_tokens <= 0 || max_kv_len <= 0) return 0;
-    return kda::attention_workspace_bytes(*p, num_seqs, total_tokens, max_new_tokens, max_kv_len);
+    return kda::attention_workspace_bytes(*p, num_seqs, total_tokens, new_tokens_bound(max_new_tokens, total_tokens), max_kv_len);
 }
 
 int32_t kda_paged_attention(const kda_kv_params* p, const void* q, int64_t q_stride, const void* k_cache,
@@ -150,6 +157,7 @@ int32_t kda_paged_attention(const kda_kv_params* p, const void* q, int64_t q_str
         return KDA_ERR_INVALID_ARG;
     if (bad_stride(q_stride, p->num_q_heads, p->head_dim)) return KDA_ERR_INVALID_ARG;
     if (misaligned(q) || misaligned(out)) return KDA_ERR_MISALIGNED;
+    max_new_tokens = new_tokens_bound(max_new_tokens, total_tokens);
     const size_t need = kda::attention_workspace_bytes(*p, num_seqs, total_tokens, max_new_tokens, max_kv_len);
     if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return KDA_ERR_WORKSPACE;

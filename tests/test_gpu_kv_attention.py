@@ -266,6 +266,24 @@ def test_limits_of_window_and_sinks(dtype):
             assert torch.equal(_attend(b, 8, 2, 128, dtype, window=window, sinks=sinks), full)
 
 
+@BOTH
+@pytest.mark.parametrize("new,past", [([2, 1], [3000, 20]), ([300, 40], [100, 9000]), ([5, 3, 4], [9, 40, 0])])
+def test_bounds_that_bound_nothing(dtype, new, past):
+    """Numbers whose product with the heads of a group passes 32 bits, and every other from all tokens up."""
+    b = ref.Batch(new, past, 32, seed=30)
+    cache, _ = _filled_cache(b, 2, 128, dtype, 5)
+    table, lens, cu = b.on(DEV)
+    q = _bf(torch.Generator().manual_seed(7), b.T, 8, 128).to(DEV)
+    want = _attend(b, 8, 2, 128, dtype, tight=False)           # by default all tokens
+    assert torch.isfinite(want).all()
+    first = kda.paged_attention(q, cache, table, lens, cu, max_new=b.T, return_lse=True)
+    for bound in (b.T + 1, 2 ** 29, 2 ** 30, 2 ** 31 - 1):
+        out, lse = torch.full_like(q, NAN), torch.full((b.T, 8), NAN, device=DEV)
+        kda.paged_attention(q, cache, table, lens, cu, max_new=bound, out=out, lse=lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert kda.check_device_errors() == 0
+
+
 # ---- append and read ------------------------------------------------------------------------------------
 
 def _append_case(new, past, Hq, Hkv, D, page, dtype, rot, interleaved, seed=0, pad=0, with_positions=False, scale=None, decode=False):

@@ -104,6 +104,21 @@ def test_attention_checks(L):
         assert _attend(L, ws=FAKE + 16, **args) == -4
 
 
+def test_any_large_bound_on_new_tokens_means_all_tokens(L):
+    """The form and its workspace go by one bound, whose products with the heads of a group stay whole numbers."""
+    size = L.kda_paged_attention_workspace_size
+    for Hq, Hkv, n, T, length in ((8, 2, 1, 3, 65536), (32, 8, 2, 5, 65536), (128, 1, 1, 40, 65536), (32, 8, 8, 16384, 4096), (5, 5, 1, 16, 70000)):
+        p = _p(Hq=Hq, Hkv=Hkv)
+        want = size(ctypes.byref(p), n, T, T, length)
+        for new in (T + 1, (1 << 24) + 1, 1 << 25, 1 << 28, 1 << 29, 1 << 30, (1 << 31) - 1):
+            assert size(ctypes.byref(p), n, T, new, length) == want, (Hq, T, new)
+    args = dict(T=3, n=1, mp=1024, length=65536, pages=1024)    # 12 rows a kv head
+    need = size(ctypes.byref(_p()), 1, 3, 3, 65536)
+    assert need > 0
+    for new in (3, 1 << 29, (1 << 31) - 1):
+        assert _attend(L, new=new, wsb=need - 1, **args) == -4 and _attend(L, new=new, ws=None, **args) == -4
+
+
 def test_python_refusals():
     with pytest.raises(ValueError):
         kda.kv_cache(4, 2, 64, 128, dtype="int8", device="cpu")
