@@ -321,7 +321,7 @@ int32_t kda_chunk_prefill_static_scratch(const kda_params* p,
  *   code 6  a page index outside [0, num_pages)
  *   code 7  a position outside the rotation table
  *   code 8  kv_lens[b] > max_pages * page_size; attention: kv_lens[b] > max_kv_len, or more new tokens than
- *           max_new_tokens (whose outputs are then unspecified)
+ *           max_new_tokens (that request's outputs are then unspecified, the others' are not)
  * The rows of q, k and v may be strided: *_stride is the distance between tokens in elements (the
  * heads of a token are contiguous), a multiple of 8.  Tensor pointers are 16-byte aligned.
  * Limits (KDA_ERR_UNSUPPORTED beyond them): total_tokens < 2^22, num_pages * num_kv_heads * page_size

@@ -145,7 +145,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int la
 }
 
 // Row tile x among all row tiles of the batch (found = 0 past the last one), by one warp: a lane per request.
-__device__ __forceinline__ Tile find_rows(const kv::Paged& c, int64_t x, int lane)
+// The grid holds the tiles of `max_new` tokens a request: one that brings more has its further tiles left out, so
+// that the other requests keep theirs.
+__device__ __forceinline__ Tile find_rows(const kv::Paged& c, int64_t x, int32_t max_new, int lane)
 {
     for (int base = 0; base < c.n; base += 32) {
         int64_t t0 = 0, t1 = 0;
@@ -154,7 +156,7 @@ __device__ __forceinline__ Tile find_rows(const kv::Paged& c, int64_t x, int lan
             len = c.lens[base + lane];
             kv::request_rows(c, base + lane, t0, t1);
         }
-        const int64_t tiles = ((t1 - t0) * c.G + kRows - 1) / kRows;
+        const int64_t tiles = (min(t1 - t0, (int64_t)max_new) * c.G + kRows - 1) / kRows;
         int64_t sum = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(Cfg<D, FP4>::kThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     if (warp == 0) {
-        const Tile tile = find_rows(a.c, blockIdx.x / a.c.Hkv, lane);
+        const Tile tile = find_rows(a.c, blockIdx.x / a.c.Hkv, a.max_new, lane);
         if (lane == 0) bars->tile = tile;
     } else if (warp == 1) {
         // a lane per barrier

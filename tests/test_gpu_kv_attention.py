@@ -476,3 +476,24 @@ def test_bad_tables_are_recorded(dtype, new, what, code):
     b, cache, q, k, table, lens, cu = _small(dtype, new)       # and the next call is as ever
     kda.paged_attention(q, cache, table, lens, cu)
     assert kda.check_device_errors() == 0
+
+
+@BOTH
+@pytest.mark.parametrize("new,G,bound", [([600, 100], 1, 100), ([30, 700, 5, 64], 4, 64), ([300, 17, 17], 8, 17)])
+def test_a_request_above_the_bound_leaves_the_others(dtype, new, G, bound):
+    """Its own outputs are unspecified, every other request's are right."""
+    b = ref.Batch(new, [50] * len(new), 32, seed=31)
+    cache, k_of = _filled_cache(b, 2, 128, dtype, 5)
+    table, lens, cu = b.on(DEV)
+    q = _bf(torch.Generator().manual_seed(7), b.T, 2 * G, 128)
+    out = torch.full((b.T, 2 * G, 128), NAN, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((b.T, 2 * G), NAN, device=DEV)
+    kda.paged_attention(q.to(DEV), cache, table, lens, cu, max_new=bound, max_len=int(b.lens.max()), out=out, lse=lse)
+    assert kda.check_device_errors() == 8
+    o, l, mag, big = ref.attention(q, k_of, b, 0, 0, 128 ** -0.5)
+    tol_o, tol_l = ref.bounds(o, l, mag, big)
+    for i, n in enumerate(new):
+        if n <= bound:
+            at = slice(int(b.cu[i]), int(b.cu[i + 1]))
+            assert ((out[at].cpu().double() - o[at]).abs() <= tol_o[at]).all()
+            assert ((lse[at].cpu().double() - l[at]).abs() <= tol_l[at]).all()
