@@ -354,7 +354,8 @@ void kda_kv_params_init(kda_kv_params* p, int32_t num_q_heads, int32_t num_kv_he
  * With cos_i, sin_i = rope[position][i], rope[position][rot_dim / 2 + i], a rotated pair (x, y) becomes
  * (x cos_i - y sin_i, y cos_i + x sin_i), rounded to bf16 (what a key in 4 bits is quantised from).
  *   4 bits: s = e4m3(min(max|x| / 6, 448)) per 16 channels, code = e2m1(x / s), both to nearest, ties
- *   to even, saturating; s = 0 gives zeros.  Non-finite values saturate.
+ *   to even, saturating; s = 0 gives zeros.  An infinity saturates (6 * 448 with its sign); a NaN makes its
+ *   group of 16 channels NaN (s = 0x7f), as visible to readers of the cache as a NaN in bf16.
  *   q, q_out   [total_tokens][num_q_heads][head_dim]: the queries, rotated like the keys into q_out
  *              (contiguous; may be q itself when q is contiguous).  Both NULL: keys and values only.
  *   rope       device fp32 [rope_rows][rot_dim], cosines then sines; may be NULL when rot_dim = 0.

@@ -55,8 +55,15 @@ __device__ __forceinline__ float max8(const float* x)
 {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+    for (int i = 0; i < 8; ++i) m = kv::max_nan(m, fabsf(x[i]));
     return m;
+}
+
+// e4m3 scale of a group whose largest magnitude is m.  A group that holds a NaN gets a NaN scale: like in a bf16
+// cache it then shows to whoever reads it.
+__device__ __forceinline__ uint32_t scale_of(float m)
+{
+    return m == m ? kv::f32_to_e4m3(kv::settle(m * (1.0f / 6.0f))) : kv::kNanScale;
 }
 
 template <int D, bool FP4>
@@ -172,14 +179,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a)
             const unsigned mask = 3u << (threadIdx.x & 30);
             float m0 = max8(x), m1 = max8(y);
             const float o0 = __shfl_xor_sync(mask, m0, 1), o1 = __shfl_xor_sync(mask, m1, 1);
-            m0 = fmaxf(m0, half_style ? o0 : m1);
-            m1 = half_style ? fmaxf(m1, o1) : m0;
-            const uint32_t e0 = kv::f32_to_e4m3(kv::settle(m0 * (1.0f / 6.0f)));
-            const uint32_t e1 = kv::f32_to_e4m3(kv::settle(m1 * (1.0f / 6.0f)));
+            m0 = kv::max_nan(m0, half_style ? o0 : m1);
+            m1 = half_style ? kv::max_nan(m1, o1) : m0;
+            const uint32_t e0 = scale_of(m0), e1 = scale_of(m1);
             if (slot >= 0) {
                 const float2 s = kv::f16x2_to_f32(kv::e4m3x2_to_f16x2(e0 | e1 << 8));
                 const float s0 = s.x, s1 = s.y;
-                const uint32_t q0 = e0 ? quantise8(x, 1.0f / s0) : 0u, q1 = e1 ? quantise8(y, 1.0f / s1) : 0u;
+                // codes of a group without a finite scale above zero: zeros
+                const uint32_t q0 = e0 - 1 < kv::kNanScale - 1 ? quantise8(x, 1.0f / s0) : 0u;
+                const uint32_t q1 = e1 - 1 < kv::kNanScale - 1 ? quantise8(y, 1.0f / s1) : 0u;
                 uint8_t* dst = (is_v ? a.c.v : a.c.k) + at * (D / 2);
                 *reinterpret_cast<uint32_t*>(dst + c0 / 2) = q0;
                 *reinterpret_cast<uint32_t*>(dst + c1 / 2) = q1;

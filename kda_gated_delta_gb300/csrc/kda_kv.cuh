@@ -134,10 +134,19 @@ __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi)   // nea
     asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tmov.b32 %0, {b, b, b, b};\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
     return r & 0xffu;
 }
+// The larger of two magnitudes, NaN where either is (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+constexpr uint32_t kNanScale = 0x7f;   // e4m3: a group with this scale is NaN whatever its codes are
 // A quotient computed by a product with a reciprocal is off by some 2^-23; one whose exact value has at
-// most 7 significant bits is made exact again by rounding to 13.  The operands here have 8 bits (bf16)
+// most 7 significant bits is made exact again by rounding to 12.  The operands here have 8 bits (bf16)
 // and 4 (e4m3) or 2 (6): a quotient that is not a rounding border of e4m3 or e2m1 (5 and 3 bits; times
 // the divisor at most 7) is at least 2^-8 from one, so ties, which do occur, go the way of exact division.
+// Infinities stay what they are; a NaN must not come here (the sum would carry its bits into the sign).
 __device__ __forceinline__ float settle(float x)
 {
     return __uint_as_float((__float_as_uint(x) + 0x800u) & 0xfffff000u);

@@ -395,6 +395,35 @@ def test_append_fp4_ties():
         assert torch.equal(out.cpu().double(), ref.dequantise(code, s))
 
 
+@pytest.mark.parametrize("D,rot,interleaved", [(128, 0, False), (128, 128, False), (128, 64, True), (64, 32, False)])
+def test_append_fp4_non_finite(D, rot, interleaved):
+    """A NaN in a key or value makes its group NaN, as it would a bf16 cache; infinities saturate."""
+    T, inf = 40, math.inf
+    g = torch.Generator().manual_seed(9)
+    k, v = _bf(g, T, 2, D), _bf(g, T, 2, D)
+    for x in (k, v):
+        x[3, 0, 5], x[4, 1, D - 1], x[5, 0, :] = NAN, NAN, NAN
+        x[6, 1, 17], x[7, 0, 30], x[8, 1, :] = inf, -inf, inf
+        x[9, 0, 2], x[9, 0, 3] = inf, NAN
+        x[10, 1, 0:16] = torch.tensor([inf, 5000.0] + 14 * [300.0])
+    rope = kda.rope_table(100, rot, device=DEV) if rot else None
+    table = torch.arange(4, dtype=torch.int32, device=DEV)[None]
+    lens, cu = torch.tensor([T], dtype=torch.int32, device=DEV), torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    full, cache = kda.kv_cache(4, 2, 16, D, "bf16", DEV), kda.kv_cache(4, 2, 16, D, "fp4", DEV)
+    for c in (full, cache):
+        kda.kv_append(k.to(DEV), v.to(DEV), c, table, lens, cu, rope=rope, interleaved=interleaved)
+    for x, got in zip(kda.kv_read(full, table, lens, cu, num_tokens=T), kda.kv_read(cache, table, lens, cu, num_tokens=T)):
+        x, got = x.cpu().unflatten(-1, (-1, 16)), got.cpu().double().unflatten(-1, (-1, 16))
+        bad = torch.isnan(x).any(-1)
+        assert bad.any() and torch.isnan(got[bad]).all()
+        code, s = ref.quantise(x.clamp(-2688, 2688).nan_to_num(0.0).flatten(-2))
+        want = ref.dequantise(code, s).unflatten(-1, (-1, 16))
+        assert torch.equal(got[~bad], want[~bad])
+    q = _bf(g, 1, 4, D).to(DEV)                               # both kv heads hold a NaN that the last token sees
+    assert torch.isnan(kda.paged_attention(q, cache, table, lens)).all()
+    assert kda.check_device_errors() == 0
+
+
 @BOTH
 def test_append_decode_form_and_in_place_queries(dtype):
     for B in (1, 37):
