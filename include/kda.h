@@ -316,8 +316,9 @@ int32_t kda_chunk_prefill_static_scratch(const kda_params* p,
  *                read (pages that fell out of every window may be reused or hold -1).
  * Bad tables never cause an access out of range; they are recorded as device errors, and the tokens
  * concerned are not appended (attention: not visible, or visible with unspecified values):
- *   code 2  cu_seqlens not non-decreasing within [0, total_tokens] (as far as the tokens' own entries
- *           show it)
+ *   code 2  cu_seqlens not non-decreasing from 0 to total_tokens (as far as the tokens' own entries
+ *           show it).  Rows before its first entry and from its last one on belong to no request and are
+ *           treated as padding; an attention call whose cu_seqlens decreases has unspecified outputs
  *   code 6  a page index outside [0, num_pages)
  *   code 7  a position outside the rotation table
  *   code 8  kv_lens[b] > max_pages * page_size; attention: kv_lens[b] > max_kv_len, or more new tokens than

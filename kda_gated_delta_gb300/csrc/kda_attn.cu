@@ -212,6 +212,10 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(AttnCall a, Parts
     const int G = a.c.G;
 
     if (!CLUSTER && parts.o) attn::let_next_launch();
+    if (a.c.cu && b == a.c.n) {                                 // the CTA past the last request
+        if (part == 0) attn::clear_unowned<D>(a);
+        return;
+    }
     int64_t t0, t1;
     kv::request_rows(a.c, b, t0, t1);
     const int len = a.c.lens[b];
@@ -668,7 +672,7 @@ cudaError_t launch_few(const kda_kv_params& p, const AttnCall& a, const attn::Cu
     constexpr int TB = kFewTile(FP4) / 16;
     const Parts parts = make_parts(p, a.c.T, cut, workspace);
     const size_t smem = (size_t)kWarps * 8 * NT * (D + 4) * 4;
-    const dim3 grid((unsigned)(a.c.n * a.c.Hkv), (unsigned)cut.parts);
+    const dim3 grid((unsigned)(a.c.n * a.c.Hkv) + attn::extra_cta(a.c), (unsigned)cut.parts);
     if (cut.in_cluster) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;

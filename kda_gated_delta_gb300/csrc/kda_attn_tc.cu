@@ -786,6 +786,8 @@ __global__ void __launch_bounds__(Cfg<D, FP4>::kThreads, 1)
         w.tile_lo = parts_here > 1 ? part * parts.tiles_per_part : 0;
         w.tile_hi = parts_here > 1 ? min(w.sp.tiles, w.tile_lo + parts.tiles_per_part) : w.sp.tiles;
         live = part < parts_here;
+    } else if (a.c.cu && part == 0 && blockIdx.x == gridDim.x - 1) {
+        attn::clear_unowned_call<D>(a.c.cu, a.c.n, (int32_t)a.c.T, a.c.Hq, reinterpret_cast<uint4*>(a.out), a.lse, a.c.err);
     }
     bool ok = true;
     if (warp < 8) {
@@ -917,7 +919,7 @@ cudaError_t launch_many(const kda_kv_params& p, const AttnCall& a, const Parts& 
     cudaError_t e = cudaFuncSetAttribute(many_rows_kernel<D, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = row_tiles(p, a.c.n, a.c.T, a.max_new);
-    many_rows_kernel<D, FP4><<<dim3((unsigned)(tiles * a.c.Hkv), (unsigned)parts.max_parts), C::kThreads, C::kSmem, stream>>>(a, parts, km, vm);
+    many_rows_kernel<D, FP4><<<dim3((unsigned)(tiles * a.c.Hkv) + attn::extra_cta(a.c), (unsigned)parts.max_parts), C::kThreads, C::kSmem, stream>>>(a, parts, km, vm);
     e = cudaGetLastError();
     if (e != cudaSuccess || parts.max_parts == 1) return e;
     return attn::launch_behind(join_rows_kernel<D>, attn::join_blocks(parts, a.c.T * a.c.Hq), 128, stream, a, parts, attn::join_warps(parts));

@@ -526,3 +526,39 @@ def test_a_request_above_the_bound_leaves_the_others(dtype, new, G, bound):
             at = slice(int(b.cu[i]), int(b.cu[i + 1]))
             assert ((out[at].cpu().double() - o[at]).abs() <= tol_o[at]).all()
             assert ((lse[at].cpu().double() - l[at]).abs() <= tol_l[at]).all()
+
+
+@BOTH
+@pytest.mark.parametrize("new,past,max_new", [([1, 1], [20, 30], 1), ([2, 1], [3000, 2000], 2), ([2, 2], [9000, 20000], 2), ([40, 30], [100, 20], 40),
+                                              ([40, 30], [6000, 900], 40)])
+def test_rows_that_no_request_owns(dtype, new, past, max_new):
+    """Rows before cu_seqlens[0] and from cu_seqlens[-1] on: recorded, with zeros, in uncut calls, clusters and cut calls
+    of both forms; append and read agree."""
+    b = ref.Batch(new, past, 64, seed=32)
+    cache, k_of = _filled_cache(b, 2, 128, dtype, 6)
+    table, lens, cu = b.on(DEV)
+    q = _bf(torch.Generator().manual_seed(8), b.T, 8, 128)
+    o, l, mag, big = ref.attention(q, k_of, b, 0, 0, 128 ** -0.5)
+    tol_o, tol_l = ref.bounds(o, l, mag, big)
+    for front, back in ((0, 5), (3, 0), (2, 70)):
+        T = front + b.T + back
+        qd = torch.full((T, 8, 128), NAN, dtype=torch.bfloat16, device=DEV)
+        qd[front:front + b.T] = q.to(DEV)
+        out, lse = torch.full_like(qd, NAN), torch.full((T, 8), NAN, device=DEV)
+        kda.paged_attention(qd, cache, table, lens, cu + front, max_new=max_new, max_len=int(b.lens.max()), out=out, lse=lse)
+        assert kda.check_device_errors() == 2
+        kda.paged_attention(qd, cache, table, lens, cu + front, max_new=max_new, max_len=int(b.lens.max()))   # without lse
+        assert kda.check_device_errors() == 2
+        own = torch.zeros(T, dtype=torch.bool)
+        own[front:front + b.T] = True
+        out, lse = out.cpu(), lse.cpu()
+        assert (out[~own] == 0).all() and (lse[~own] == -math.inf).all()
+        assert ((out[own].double() - o).abs() <= tol_o).all()
+        assert ((lse[own].double() - l).abs() <= tol_l).all()
+        k = _bf(torch.Generator().manual_seed(10), T, 2, 128).to(DEV)
+        scratch = kda.kv_cache(b.num_pages, 2, 64, 128, dtype, DEV)
+        qo = kda.kv_append(k, k, scratch, table, lens, cu + front, q=qd)
+        assert kda.check_device_errors() == 2 and (qo.cpu()[~own] == 0).all() and torch.equal(qo.cpu()[own], q)
+        for x in kda.kv_read(scratch, table, lens, cu + front, num_tokens=T):
+            assert (x.cpu()[~own] == 0).all()
+        assert kda.check_device_errors() == 2
