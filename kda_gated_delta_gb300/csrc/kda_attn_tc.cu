@@ -519,7 +519,7 @@ __device__ __forceinline__ float load_queries(const AttnCall& a, uint8_t* q, int
                 for (int z = 0; z < 4; ++z) top = max(top, max(y[z] & 0x7fffu, (y[z] >> 16) & 0x7fffu));
 #pragma unroll
                 for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
-                const int e = min(max((int)(top >> 7), 1), 253);
+                const int e = min(max((int)(top >> 7), a.min_exp), 253);
                 const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {

@@ -190,6 +190,8 @@ struct AttnCall {
     int32_t max_new, max_len;  // host bounds
     int32_t window, sinks;
     float scale;
+    int32_t min_exp;           // least biased exponent e with scale * log2(e) * 2^(e - 127) >= 2^-126: 4-bit caches divide
+                               // no query row by less, or its factor would be zero and NaN beside a masked score's -inf
     void* out;
     float* lse;
     uint64_t by_group;         // 2^36 / G rounded up: row / G for row < 2^22 G is (row * by_group) >> 36

@@ -171,6 +171,9 @@ int32_t kda_paged_attention(const kda_kv_params* p, const void* q, int64_t q_str
     a.window = p->window;
     a.sinks = p->num_sinks;
     a.scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / sqrtf((float)p->head_dim);
+    int exponent = 0;
+    if (isfinite(a.scale)) frexp(a.scale * 1.4426950408889634, &exponent);   // a product of at least 2^(exponent - 1)
+    a.min_exp = 2 - exponent > 1 ? 2 - exponent : 1;
     a.out = out;
     a.lse = lse;
     a.by_group = (((uint64_t)1 << 36) + a.c.G - 1) / a.c.G;

@@ -267,6 +267,15 @@ def test_limits_of_window_and_sinks(dtype):
 
 
 @BOTH
+def test_small_scales(dtype):
+    """Factors of the scores that underflow: the weights are uniform over what is visible, masked tokens stay out."""
+    b = ref.Batch([1, 40], [100, 100], 32, seed=33)
+    _attend(b, 8, 2, 128, dtype, q_std=0.0, scale=1e-9)
+    _attend(b, 8, 2, 128, dtype, q_std=1e-30, scale=1e-20)
+    _attend(b, 8, 2, 128, dtype, window=30, sinks=2, scale=1e-30)
+
+
+@BOTH
 @pytest.mark.parametrize("new,past", [([2, 1], [3000, 20]), ([300, 40], [100, 9000]), ([5, 3, 4], [9, 40, 0])])
 def test_bounds_that_bound_nothing(dtype, new, past):
     """Numbers whose product with the heads of a group passes 32 bits, and every other from all tokens up."""
