@@ -170,11 +170,18 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current device: kernels are launched there, whatever the tensors' device, so the two must agree.
+_device = torch._C._cuda_getDevice
+
+
 def _dev(t, name, dtype=None):
     if t is None:
         return
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    at = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if at < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if at != _device():
+        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -184,6 +191,8 @@ def _dev(t, name, dtype=None):
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
+    elif stream.device_index != _device():
+        raise ValueError(f"stream is of cuda:{stream.device_index}, the current device is cuda:{_device()}")
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -405,40 +414,44 @@ def _kv_params(Hq, Hkv, D, page, fp4, rot=0, interleaved=False, window=0, sinks=
 _BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 
 
-def _need(t, name, dtype):
-    if not (t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+def _need(t, name, dtype, dev):
+    if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
         _dev(t, name, dtype)
+        raise ValueError(f"{name} must be on cuda:{dev}, with the cache")
 
 
 def _kv_cache_args(cache):
-    """(kv heads, page size, head_dim, 4-bit?, k, v, k_scale and v_scale pointers, pages)."""
+    """(device, kv heads, page size, head_dim, 4-bit?, k, v, k_scale and v_scale pointers, pages)."""
     k, v, ks, vs = cache
     fp4 = k.dtype is _U8
     if not fp4 and k.dtype is not _BF16:
         raise TypeError(f"cache.k must be torch.bfloat16 or torch.uint8 (4 bits), got {k.dtype}")
-    _need(k, "cache.k", k.dtype)
-    _need(v, "cache.v", k.dtype)
+    dev = k.get_device()
+    if dev < 0:
+        raise ValueError("cache.k must be a CUDA tensor")
+    _need(k, "cache.k", k.dtype, dev)
+    _need(v, "cache.v", k.dtype, dev)
     shape = k.shape
     if len(shape) != 4 or v.shape != shape:
         raise ValueError("cache.k and cache.v must be [pages, kv heads, page size, channels], of one shape")
     pages, Hkv, page, D = shape
     if not fp4:
-        return Hkv, page, D, False, k.data_ptr(), v.data_ptr(), None, None, pages
+        return dev, Hkv, page, D, False, k.data_ptr(), v.data_ptr(), None, None, pages
     for name, t in (("cache.k_scale", ks), ("cache.v_scale", vs)):
         if t is None:
             raise ValueError(f"{name} is missing")
         if t.dtype is not _E4M3 and t.dtype is not _U8:
             raise TypeError(f"{name} must be torch.float8_e4m3fn, got {t.dtype}")
-        _need(t, name, t.dtype)
+        _need(t, name, t.dtype, dev)
         if t.shape != (pages, Hkv, page, D // 8):
             raise ValueError(f"{name} must be [pages, kv heads, page size, head_dim / 16]")
-    return Hkv, page, 2 * D, True, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages
+    return dev, Hkv, page, 2 * D, True, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages
 
 
-def _kv_batch(cu_seqlens, kv_lens, block_table, T):
+def _kv_batch(cu_seqlens, kv_lens, block_table, T, dev):
     """(cu_seqlens, kv_lens, block_table pointers, requests, pages per request, tokens)."""
-    _need(kv_lens, "kv_lens", _I32)
-    _need(block_table, "block_table", _I32)
+    _need(kv_lens, "kv_lens", _I32, dev)
+    _need(block_table, "block_table", _I32, dev)
     n, shape = kv_lens.shape[0], block_table.shape
     if len(shape) != 2 or shape[0] != n:
         raise ValueError("block_table must be [requests, pages per request]")
@@ -446,17 +459,17 @@ def _kv_batch(cu_seqlens, kv_lens, block_table, T):
         if T != n:
             raise ValueError("without cu_seqlens there is one token per request")
         return None, kv_lens.data_ptr(), block_table.data_ptr(), n, shape[1], T
-    _need(cu_seqlens, "cu_seqlens", _I32)
+    _need(cu_seqlens, "cu_seqlens", _I32, dev)
     if cu_seqlens.shape[0] != n + 1:
         raise ValueError("cu_seqlens must have one entry more than kv_lens")
     return cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, shape[1], T
 
 
-def _rows(t, name, heads, D):
+def _rows(t, name, heads, D, dev):
     """Pointer, token stride, tokens and heads of a bf16 [T, heads, D] tensor whose heads are contiguous (a
     slice of a fused projection will do)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}, with the cache")
     if t.dtype is not _BF16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     shape = t.shape
@@ -476,8 +489,11 @@ def _fn(name):
     return getattr(lib(), name)
 
 
-def _raw_stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _raw_stream(dev):
+    """The current stream of the call's device, which has to be the current one."""
+    if dev != _device():
+        raise ValueError(f"the cache is on cuda:{dev}, the current device is cuda:{_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, *, q=None, q_out=None, rope=None,
@@ -489,27 +505,27 @@ def kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, *, q=None, q_o
         with torch.cuda.stream(stream):
             return kv_append(k, v, cache, block_table, kv_lens, cu_seqlens, q=q, q_out=q_out, rope=rope,
                              interleaved=interleaved, positions=positions)
-    Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
-    kp, k_stride, T, _ = _rows(k, "k", Hkv, D)
-    vp, v_stride, Tv, _ = _rows(v, "v", Hkv, D)
+    dev, Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
+    kp, k_stride, T, _ = _rows(k, "k", Hkv, D, dev)
+    vp, v_stride, Tv, _ = _rows(v, "v", Hkv, D, dev)
     if Tv != T:
         raise ValueError("k and v must have the same number of tokens")
-    pc, pl, pt, n, max_pages, _ = _kv_batch(cu_seqlens, kv_lens, block_table, T)
+    pc, pl, pt, n, max_pages, _ = _kv_batch(cu_seqlens, kv_lens, block_table, T, dev)
     rot, rows, rp = 0, 0, None
     if rope is not None:
-        _need(rope, "rope", _F32)
+        _need(rope, "rope", _F32, dev)
         if rope.dim() != 2:
             raise ValueError("rope must be [positions, rot_dim]")
         rows, rot = rope.shape
         rp = rope.data_ptr()
     if positions is not None:
-        _need(positions, "positions", _I32)
+        _need(positions, "positions", _I32, dev)
         if positions.shape != (T,):
             raise ValueError("positions must hold one entry per token")
         positions = positions.data_ptr()
     Hq, qp, q_stride, qo = Hkv, None, 0, None
     if q is not None:
-        qp, q_stride, Tq, Hq = _rows(q, "q", None, D)
+        qp, q_stride, Tq, Hq = _rows(q, "q", None, D, dev)
         if Tq != T:
             raise ValueError("q and k must have the same number of tokens")
         if q_out is None:
@@ -517,13 +533,13 @@ def kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, *, q=None, q_o
         elif q_out.shape != q.shape:
             raise ValueError("q_out must have the shape of q")
         else:
-            _need(q_out, "q_out", _BF16)
+            _need(q_out, "q_out", _BF16, dev)
         qo = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     rc = _fn("kda_kv_append")(_kv_params(Hq, Hkv, D, page, fp4, rot, interleaved), qp, q_stride, kp, k_stride, vp, v_stride,
                               rp, rows, positions, pc, pl, pt, n, max_pages, T, pk, pv, pks, pvs, pages, qo,
-                              _raw_stream(k))
+                              _raw_stream(dev))
     if rc:
         _check(rc, "kda_kv_append")
     return q_out
@@ -535,21 +551,21 @@ def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, ou
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_read(cache, block_table, kv_lens, cu_seqlens, num_tokens=num_tokens, out=out)
-    Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
+    dev, Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
     T = kv_lens.shape[0] if cu_seqlens is None else num_tokens
     if T is None:
         raise ValueError("num_tokens is needed with cu_seqlens")
-    batch = _kv_batch(cu_seqlens, kv_lens, block_table, int(T))
+    batch = _kv_batch(cu_seqlens, kv_lens, block_table, int(T), dev)
     if out is None:
         k_out = torch.empty((T, Hkv, D), dtype=_BF16, device=kv_lens.device)
         out = k_out, torch.empty_like(k_out)
     else:
         for name, t in (("out[0]", out[0]), ("out[1]", out[1])):
-            _need(t, name, _BF16)
+            _need(t, name, _BF16, dev)
             if t.shape != (T, Hkv, D):
                 raise ValueError(f"{name} must be [{T}, {Hkv}, {D}]")
     rc = _fn("kda_kv_read")(_kv_params(Hkv, Hkv, D, page, fp4), pk, pv, pks, pvs, pages, *batch, out[0].data_ptr(),
-                            out[1].data_ptr(), _raw_stream(kv_lens))
+                            out[1].data_ptr(), _raw_stream(dev))
     if rc:
         _check(rc, "kda_kv_read")
     return out
@@ -572,9 +588,9 @@ def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0
             return paged_attention(q, cache, block_table, kv_lens, cu_seqlens, window=window, sinks=sinks, scale=scale,
                                    max_new=max_new, max_len=max_len, out=out, lse=lse, return_lse=return_lse,
                                    workspace=workspace)
-    Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
-    qp, q_stride, T, Hq = _rows(q, "q", None, D)
-    batch = _kv_batch(cu_seqlens, kv_lens, block_table, T)
+    dev, Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
+    qp, q_stride, T, Hq = _rows(q, "q", None, D, dev)
+    batch = _kv_batch(cu_seqlens, kv_lens, block_table, T, dev)
     if max_new is None or cu_seqlens is None:
         max_new = 1 if cu_seqlens is None else max(T, 1)
     if max_len is None:
@@ -582,11 +598,11 @@ def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0
     if out is None:
         out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
     else:
-        _need(out, "out", _BF16)
+        _need(out, "out", _BF16, dev)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
     if lse is not None:
-        _need(lse, "lse", _F32)
+        _need(lse, "lse", _F32, dev)
         if lse.shape != (T, Hq):
             raise ValueError("lse must be [tokens, q heads]")
     elif return_lse:
@@ -595,14 +611,14 @@ def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0
     need = _attention_workspace(p, batch[3], T, max_new, max_len)
     ws = None
     if workspace is not None:
-        _need(workspace, "workspace", _U8)
+        _need(workspace, "workspace", _U8, dev)
         need = workspace.numel()
     elif need:
         workspace = torch.empty(need, dtype=_U8, device=q.device)
     if workspace is not None:
         ws = workspace.data_ptr()
     rc = _fn("kda_paged_attention")(p, qp, q_stride, pk, pv, pks, pvs, pages, *batch, max_new, max_len, out.data_ptr(),
-                                    None if lse is None else lse.data_ptr(), ws, need, _raw_stream(q))
+                                    None if lse is None else lse.data_ptr(), ws, need, _raw_stream(dev))
     if rc:
         _check(rc, "kda_paged_attention")
     return out if lse is None else (out, lse)
