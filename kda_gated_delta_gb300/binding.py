@@ -402,10 +402,19 @@ def rope_table(num_positions, rot_dim, theta=10000.0, device="cuda") -> torch.Te
     return torch.ldexp(torch.round(m * 65536.0), e - 16).float().contiguous()
 
 
+_TOP = 2 ** 31 - 1
+
+
+def _clip(x):
+    """x as an int32 argument.  ctypes would take it modulo 2^32; all numbers past either end mean the same here:
+    more than any length, or an error."""
+    return x if -_TOP <= x <= _TOP else _TOP if x > 0 else -_TOP
+
+
 @functools.lru_cache(maxsize=256)
 def _kv_params(Hq, Hkv, D, page, fp4, rot=0, interleaved=False, window=0, sinks=0, scale=None):
-    p = KvParams(Hq, Hkv, D, page, CACHE_FP4 if fp4 else CACHE_BF16, rot, 1 if interleaved else 0, window, sinks,
-                 0.0 if scale is None else scale)
+    p = KvParams(_clip(Hq), _clip(Hkv), _clip(D), _clip(page), CACHE_FP4 if fp4 else CACHE_BF16, _clip(rot), 1 if interleaved else 0,
+                 _clip(window), _clip(sinks), 0.0 if scale is None else scale)
     return ctypes.byref(p)
 
 
@@ -573,7 +582,7 @@ def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, ou
 
 @functools.lru_cache(maxsize=4096)
 def _attention_workspace(p, n, T, max_new, max_len):
-    return int(lib().kda_paged_attention_workspace_size(p, n, T, max_new, max_len))
+    return int(lib().kda_paged_attention_workspace_size(p, _clip(n), T, _clip(max_new), _clip(max_len)))
 
 
 def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0, sinks=0, scale=None,
@@ -617,7 +626,7 @@ def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0
         workspace = torch.empty(need, dtype=_U8, device=q.device)
     if workspace is not None:
         ws = workspace.data_ptr()
-    rc = _fn("kda_paged_attention")(p, qp, q_stride, pk, pv, pks, pvs, pages, *batch, max_new, max_len, out.data_ptr(),
+    rc = _fn("kda_paged_attention")(p, qp, q_stride, pk, pv, pks, pvs, pages, *batch, _clip(max_new), _clip(max_len), out.data_ptr(),
                                     None if lse is None else lse.data_ptr(), ws, need, _raw_stream(dev))
     if rc:
         _check(rc, "kda_paged_attention")

@@ -91,6 +91,17 @@ def test_cache_calls(reached, name):
     assert reached == [name]
 
 
+def test_bounds_past_32_bits(reached, monkeypatch):
+    base, calls = kv_calls(0)
+    got = []
+    monkeypatch.setattr(binding, "_fn", lambda name: lambda *args: got.append(args[14:16]) or 0)
+    for new, length in ((2 ** 32 + 1, 2 ** 32 + 64), (2 ** 63, 2 ** 31), (-2 ** 32 + 1, -2 ** 32 + 64)):
+        kda.paged_attention(base["q"], (base["ck"], base["cv"], base["ks"], base["vs"]), base["table"], base["lens"], base["cu"],
+                            max_new=new, max_len=length)
+    top = 2 ** 31 - 1
+    assert got == [(top, top), (top, top), (-top, -top)]
+
+
 def state_calls(at):
     H, D, B = 2, 128, 2
     x = [on(at, B, H, D, dtype=BF) for _ in range(3)]

@@ -119,6 +119,22 @@ def test_any_large_bound_on_new_tokens_means_all_tokens(L):
         assert _attend(L, new=new, wsb=need - 1, **args) == -4 and _attend(L, new=new, ws=None, **args) == -4
 
 
+def test_python_numbers_past_32_bits(L, monkeypatch):
+    """They are not taken modulo 2^32: a window of 2^32 + 5 is no window of 5."""
+    def seen(**kw):
+        return binding._kv_params(8, 2, 128, 64, False, **kw)._obj
+
+    for big in (2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1, 2 ** 70):
+        p = seen(window=big, sinks=big)
+        assert p.window == p.num_sinks == 2 ** 31 - 1
+        assert seen(window=-big).window < 0 and seen(sinks=-big).num_sinks < 0       # refused by the library
+        size = kda.attention_workspace_size
+        assert size(8, 2, 128, 64, 1, 3, big, 65536) == size(8, 2, 128, 64, 1, 3, 3, 65536) > 0
+        assert size(8, 2, 128, 64, 1, 1, 1, -big) == size(8, 2, 128, 64, 1, 1, -big, 256) == 0
+    p = seen(window=2 ** 31 - 1, sinks=5)
+    assert (p.window, p.num_sinks) == (2 ** 31 - 1, 5)
+
+
 def test_python_refusals():
     with pytest.raises(ValueError):
         kda.kv_cache(4, 2, 64, 128, dtype="int8", device="cpu")
