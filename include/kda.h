@@ -394,6 +394,7 @@ int32_t kda_kv_read(const kda_kv_params* p,
  *   out  [total_tokens][num_q_heads][head_dim] bf16
  *   lse  [total_tokens][num_q_heads] fp32, log(sum_j exp(s_j)), for merging with attention over other
  *        tokens; or NULL
+ * total_tokens = 0 or num_seqs = 0 is a no-op.
  * A query that sees no token (padding) gets zeros and lse = -infinity.  What masked and unwritten cache
  * slots hold, NaN included, does not matter, with one exception: a non-finite VALUE that some query of a
  * call may see can make the outputs of other queries of its request in that call non-finite.

@@ -461,16 +461,18 @@ def _kv_batch(cu_seqlens, kv_lens, block_table, T, dev):
     """(cu_seqlens, kv_lens, block_table pointers, requests, pages per request, tokens)."""
     _need(kv_lens, "kv_lens", _I32, dev)
     _need(block_table, "block_table", _I32, dev)
-    n, shape = kv_lens.shape[0], block_table.shape
+    n, shape = kv_lens.numel(), block_table.shape
     if len(shape) != 2 or shape[0] != n:
-        raise ValueError("block_table must be [requests, pages per request]")
+        raise ValueError("block_table must be [requests, pages per request], with one entry of kv_lens per request")
     if cu_seqlens is None:
         if T != n:
             raise ValueError("without cu_seqlens there is one token per request")
         return None, kv_lens.data_ptr(), block_table.data_ptr(), n, shape[1], T
     _need(cu_seqlens, "cu_seqlens", _I32, dev)
-    if cu_seqlens.shape[0] != n + 1:
+    if cu_seqlens.numel() != n + 1:
         raise ValueError("cu_seqlens must have one entry more than kv_lens")
+    if n == 0 and T > 0:
+        raise ValueError("tokens without a request")           # the library would leave their outputs unwritten
     return cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, shape[1], T
 
 
@@ -561,7 +563,7 @@ def kv_read(cache, block_table, kv_lens, cu_seqlens=None, *, num_tokens=None, ou
         with torch.cuda.stream(stream):
             return kv_read(cache, block_table, kv_lens, cu_seqlens, num_tokens=num_tokens, out=out)
     dev, Hkv, page, D, fp4, pk, pv, pks, pvs, pages = _kv_cache_args(cache)
-    T = kv_lens.shape[0] if cu_seqlens is None else num_tokens
+    T = kv_lens.numel() if cu_seqlens is None else num_tokens
     if T is None:
         raise ValueError("num_tokens is needed with cu_seqlens")
     batch = _kv_batch(cu_seqlens, kv_lens, block_table, int(T), dev)

@@ -91,6 +91,21 @@ def test_cache_calls(reached, name):
     assert reached == [name]
 
 
+@pytest.mark.parametrize("name", ["kda_kv_append", "kda_kv_read", "kda_paged_attention"])
+def test_shapes_of_the_tables(reached, name):
+    """One length and one table row per request: further entries would be read as other requests'."""
+    base, calls = kv_calls(0)
+    call, _ = calls[name]
+    for bad in (dict(lens=on(0, 2, 3, dtype=I32)), dict(lens=on(0, dtype=I32)), dict(lens=on(0, 1, dtype=I32)), dict(table=on(0, 8, dtype=I32)),
+                dict(cu=on(0, 3, 2, dtype=I32)), dict(cu=on(0, dtype=I32)), dict(cu=on(0, 2, dtype=I32)),
+                dict(lens=on(0, 0, dtype=I32), table=on(0, 0, 4, dtype=I32), cu=on(0, 1, dtype=I32))):
+        with pytest.raises(ValueError):
+            call({**base, **bad})
+    assert reached == []
+    call({**base, "lens": on(0, 2, 1, dtype=I32)})
+    assert reached == [name]
+
+
 def test_bounds_past_32_bits(reached, monkeypatch):
     base, calls = kv_calls(0)
     got = []
