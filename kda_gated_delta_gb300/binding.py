@@ -378,14 +378,18 @@ class KVCache(NamedTuple):
     v_scale: torch.Tensor | None = None
 
 
+def _is_fp4(dtype) -> bool:
+    if dtype not in ("bf16", "fp4"):
+        raise ValueError(f"dtype must be 'bf16' or 'fp4', got {dtype!r}")
+    return dtype == "fp4"
+
+
 def kv_cache(num_pages, num_kv_heads, page_size, head_dim, dtype="bf16", device="cuda") -> KVCache:
     """Allocate a zeroed cache; ``dtype`` "bf16" or "fp4"."""
     shape = (int(num_pages), int(num_kv_heads), int(page_size))
-    if dtype == "bf16":
+    if not _is_fp4(dtype):
         k = torch.zeros(*shape, int(head_dim), dtype=torch.bfloat16, device=device)
         return KVCache(k, torch.zeros_like(k))
-    if dtype != "fp4":
-        raise ValueError(f"dtype must be 'bf16' or 'fp4', got {dtype!r}")
     k = torch.zeros(*shape, head_dim // 2, dtype=torch.uint8, device=device)
     s = torch.zeros(*shape, head_dim // 16, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
     return KVCache(k, torch.zeros_like(k), s, s.clone())
@@ -639,7 +643,7 @@ def attention_workspace_size(num_q_heads, num_kv_heads, head_dim, page_size, num
                              dtype="bf16", window=0, sinks=0) -> int:
     """Bytes of ``workspace`` that :func:`paged_attention` needs for these sizes (it allocates them itself
     when none is given)."""
-    p = _kv_params(num_q_heads, num_kv_heads, head_dim, page_size, dtype == "fp4", 0, False, window, sinks)
+    p = _kv_params(num_q_heads, num_kv_heads, head_dim, page_size, _is_fp4(dtype), 0, False, window, sinks)
     return _attention_workspace(p, num_seqs, num_tokens, max_new, max_len)
 
 

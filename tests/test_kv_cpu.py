@@ -135,6 +135,14 @@ def test_python_numbers_past_32_bits(L, monkeypatch):
     assert (p.window, p.num_sinks) == (2 ** 31 - 1, 5)
 
 
+def test_workspace_of_an_unknown_cache_type(L):
+    for dtype in ("int8", "FP4", torch.bfloat16, None):       # none of them means bf16
+        with pytest.raises(ValueError):
+            kda.attention_workspace_size(8, 2, 128, 64, 1, 1, 1, 65536, dtype=dtype)
+    assert kda.attention_workspace_size(8, 2, 128, 64, 1, 1, 1, 65536) > 0
+    assert kda.attention_workspace_size(8, 2, 128, 64, 1, 1, 1, 65536, dtype="fp4") > 0
+
+
 def test_python_refusals():
     with pytest.raises(ValueError):
         kda.kv_cache(4, 2, 64, 128, dtype="int8", device="cpu")
