@@ -19,7 +19,7 @@ class Claims(torch.Tensor):
 
 
 def on(at, *shape, dtype=torch.float32):
-    t = torch.zeros(*shape, dtype=dtype).as_subclass(Claims)
+    t = torch.zeros(shape, dtype=dtype).as_subclass(Claims)
     t.at = at
     return t
 
