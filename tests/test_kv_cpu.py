@@ -104,6 +104,20 @@ def test_attention_checks(L):
         assert _attend(L, ws=FAKE + 16, **args) == -4
 
 
+@pytest.mark.parametrize("fp4", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,new", [(1, 1), (4, 4), (40, 40), (300, 300)])
+def test_cut_calls_need_their_workspace(L, T, new, D, fp4):
+    """One request over a long history is cut into more parts than a cluster joins, with few and with many query rows."""
+    p = _p(D=D, cache_dtype=fp4)
+    need = L.kda_paged_attention_workspace_size(ctypes.byref(p), 1, T, new, 65536)
+    assert need > 8 * T * 8 * (D + 1) * 4                  # more than eight parts of 8 heads, in fp32
+    args = dict(p=p, qs=8 * D, ksc=FAKE, vsc=FAKE, T=T, n=1, new=new, mp=1024, length=65536, pages=1024)
+    if new == 1:
+        args["cu"] = None
+    assert _attend(L, ws=None, **args) == -4 and _attend(L, wsb=need - 1, **args) == -4 and _attend(L, ws=FAKE + 16, **args) == -4
+
+
 def test_any_large_bound_on_new_tokens_means_all_tokens(L):
     """The form and its workspace go by one bound, whose products with the heads of a group stay whole numbers."""
     size = L.kda_paged_attention_workspace_size
