@@ -724,9 +724,8 @@ cudaError_t launch_attention(const kda_kv_params& p, const AttnCall& a, void* wo
 
 cudaError_t attn_read_and_clear_error(int32_t* code)
 {
-    int32_t zero = 0, many = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_error, sizeof(int32_t));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(int32_t));
+    int32_t many = 0;
+    cudaError_t e = read_and_clear(g_attn_error, code);
     if (e == cudaSuccess) e = attn_tc_read_and_clear_error(&many);
     if (*code == 0) *code = many;
     return e;

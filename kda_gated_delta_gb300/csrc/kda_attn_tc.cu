@@ -930,12 +930,6 @@ template cudaError_t launch_many<64, true>(const kda_kv_params&, const AttnCall&
 template cudaError_t launch_many<128, false>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
 template cudaError_t launch_many<128, true>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
 
-cudaError_t attn_tc_read_and_clear_error(int32_t* code)
-{
-    int32_t zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_tc_error, sizeof(int32_t));
-    if (e != cudaSuccess) return e;
-    return cudaMemcpyToSymbol(g_attn_tc_error, &zero, sizeof(int32_t));
-}
+cudaError_t attn_tc_read_and_clear_error(int32_t* code) { return read_and_clear(g_attn_tc_error, code); }
 
 }  // namespace kda

@@ -308,12 +308,6 @@ cudaError_t launch_kv_read(const kda_kv_params& p, kv::Paged c, void* k_out, voi
     });
 }
 
-cudaError_t cache_read_and_clear_error(int32_t* code)
-{
-    int32_t zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_cache_error, sizeof(int32_t));
-    if (e != cudaSuccess) return e;
-    return cudaMemcpyToSymbol(g_cache_error, &zero, sizeof(int32_t));
-}
+cudaError_t cache_read_and_clear_error(int32_t* code) { return read_and_clear(g_cache_error, code); }
 
 }  // namespace kda

@@ -58,6 +58,16 @@ __device__ __forceinline__ float gate_log_decay(float x, float rate, const GateP
 
 __device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + expf(-x)); }
 
+// ---- error words --------------------------------------------------------------------------------
+// Read a translation unit's device error word, and clear it if it holds a code.  A word without one is not written:
+// a copy takes some 10 us, and there are six words (a check takes 61 us; with all of them cleared always it took 83).
+inline cudaError_t read_and_clear(int32_t& word, int32_t* code)
+{
+    const int32_t zero = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(code, word, sizeof(int32_t));
+    return e != cudaSuccess || *code == 0 ? e : cudaMemcpyToSymbol(word, &zero, sizeof(int32_t));
+}
+
 // ---- host-side argument handling (kda_api.cu) ----------------------------------------------------
 GateParams gate_params(const kda_params& p);
 // The host-side checks of a chunk-prefill call, in one place for every prefill entry point (the

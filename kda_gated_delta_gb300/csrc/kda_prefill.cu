@@ -1995,12 +1995,6 @@ cudaError_t launch_prefill(const kda_params& p, const GateParams& gp, const void
     return cudaErrorInvalidValue;
 }
 
-cudaError_t prefill_read_and_clear_error(int32_t* code)
-{
-    int32_t zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_prefill_error, sizeof(int32_t));
-    if (e != cudaSuccess) return e;
-    return cudaMemcpyToSymbol(g_prefill_error, &zero, sizeof(int32_t));
-}
+cudaError_t prefill_read_and_clear_error(int32_t* code) { return read_and_clear(g_prefill_error, code); }
 
 }  // namespace kda

@@ -654,12 +654,6 @@ cudaError_t launch_commit(int H, int D, const float* inter, int32_t batch, int32
     return cudaGetLastError();
 }
 
-cudaError_t recurrent_read_and_clear_error(int32_t* code)
-{
-    int32_t zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_recurrent_error, sizeof(int32_t));
-    if (e != cudaSuccess) return e;
-    return cudaMemcpyToSymbol(g_recurrent_error, &zero, sizeof(int32_t));
-}
+cudaError_t recurrent_read_and_clear_error(int32_t* code) { return read_and_clear(g_recurrent_error, code); }
 
 }  // namespace kda

@@ -60,12 +60,6 @@ cudaError_t launch_wait_selftest(uint32_t polls, int32_t* result, cudaStream_t s
     return cudaGetLastError();
 }
 
-cudaError_t selftest_read_and_clear_error(int32_t* code)
-{
-    int32_t zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_selftest_error, sizeof(int32_t));
-    if (e != cudaSuccess) return e;
-    return cudaMemcpyToSymbol(g_selftest_error, &zero, sizeof(int32_t));
-}
+cudaError_t selftest_read_and_clear_error(int32_t* code) { return read_and_clear(g_selftest_error, code); }
 
 }  // namespace kda
