@@ -47,7 +47,7 @@ int32_t check_batch(const kda_kv_params* p, const void* kc, const void* vc, cons
     if (p->cache_dtype == KDA_CACHE_FP4 && (misaligned(ks) || misaligned(vs))) return KDA_ERR_MISALIGNED;
     // counts that the kernels' 32-bit grids and tensor-map coordinates can hold
     if ((int64_t)num_seqs * p->num_kv_heads >= ((int64_t)1 << 30) || T >= ((int64_t)1 << 31) / 512 || (int64_t)max_pages * p->page_size >= ((int64_t)1 << 31) - 256 ||
-        num_pages * p->num_kv_heads * p->page_size >= ((int64_t)1 << 31))
+        num_pages >= ((int64_t)1 << 31) || num_pages * p->num_kv_heads * p->page_size >= ((int64_t)1 << 31))   // no product past 2^48
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }

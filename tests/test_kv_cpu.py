@@ -74,6 +74,15 @@ def test_shared_checks(L, call):
     assert call(L, T=0) == 0 and call(L, n=0) == 0
 
 
+@pytest.mark.parametrize("call", [_append, _attend])
+def test_page_counts_whose_product_passes_64_bits(L, call):
+    """A caller without a bound on its pages gets a refusal, not a call that takes every page index for good."""
+    for pages in (1 << 27, 1 << 31, 1 << 47, 1 << 57, (1 << 62) + 1, (1 << 63) - 1):
+        assert call(L, pages=pages) == -2
+        assert call(L, pages=pages, p=_p(Hq=1, Hkv=1), qs=128) == -2 or pages == 1 << 27
+    assert call(L, pages=-1) == -1
+
+
 def test_append_checks(L):
     assert _append(L, k=None) == -1 and _append(L, v=None) == -1
     assert _append(L, q=None) == -1 and _append(L, qo=None) == -1
