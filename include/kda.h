@@ -406,8 +406,9 @@ int32_t kda_kv_read(const kda_kv_params* p,
  *                   before and after; may be NULL when that size is 0.  It must not be shared with a
  *                   call that overlaps in time.
  * Scores, softmax statistics and outputs are accumulated in fp32; the weights exp(s_j - max) enter the
- * product with the values rounded to bf16.  Results do not depend on timing: the
- * same call gives the same bits.
+ * product with the values rounded to bf16.  Over a 4-bit cache a query row is held in fp16, divided by a power
+ * of two near its largest magnitude: its elements below 2^-14 of that lose low bits.  Results do not depend
+ * on timing: the same call gives the same bits.
  */
 size_t kda_paged_attention_workspace_size(const kda_kv_params* p, int32_t num_seqs, int64_t total_tokens,
                                           int32_t max_new_tokens, int32_t max_kv_len);

@@ -24,8 +24,13 @@
 // exceeds the current one by 8 in log2 (one vote), so that the common tile has no shuffles and no
 // rescaling.  The weights, at most 2^8 then, lose nothing by that in a floating-point format.
 //
-// Measured (8 kv and 32 query heads of 128): 64 requests of 512 to 8,192 tokens in 192 us, 6,380 GB/s of the 6,776
-// that a copy reaches; 16 requests of 4,096 to 131,072 tokens in 4 bits in 370 us, bound by the conversions (some
+// The weights are rounded to bf16 for their product with the values, half a step or 2^-8 of a weight at most; their
+// sum takes them unrounded.  mma.sync has no wider operand beside bf16 values, and two products (a weight as the sum
+// of two bf16 numbers) would double the tensor work; the output, rounded to bf16 once more, is off by 2.1e-3 to
+// 2.3e-3 of its size in the mean, where its own rounding alone gives 1.7e-3.
+//
+// Measured (8 kv and 32 query heads of 128): 64 requests of 512 to 8,192 tokens in 193 us, 6,350 GB/s of the 6,776
+// that a copy reaches; 16 requests of 4,096 to 131,072 tokens in 4 bits in 373 us, bound by the conversions (some
 // 500 instructions per 16 tokens).
 //
 // A warp takes every fourth tile of its CTA's part, with the next tile's keys requested as soon as the
@@ -607,7 +612,7 @@ __global__ void __launch_bounds__(128) join_kernel(AttnCall a, Parts parts, cons
 
 namespace {
 
-// Rows of a (request, kv head) up to which this form is taken: 64 requests of 16 rows take 140 us here and 148
+// Rows of a (request, kv head) up to which this form is taken: 64 requests of 16 rows take 136 us here and 148
 // in the tcgen05 form; more rows would not fit the registers.
 constexpr int64_t kFewRows = 16;
 int64_t rows_of(const kda_kv_params& p, int32_t max_new) { return (int64_t)max_new * (p.num_q_heads / p.num_kv_heads); }
@@ -616,15 +621,17 @@ int64_t rows_of(const kda_kv_params& p, int32_t max_new) { return (int64_t)max_n
 // head).  The cut aims at kCtas CTAs for the longest histories the caller's bound allows, so that ragged
 // histories spread evenly (16 histories of 4096 to 131072 tokens in 4 bits: 410 us with 2,048 CTAs, 380 with
 // 8,192), in parts whose fp32 outputs, written and read once, are at most 1/32 of the part's bytes (64
-// requests of 4 x 4 rows: 199 us in 16 parts of 256 tokens, 148 in 4 of 1,024).
+// requests of 4 x 4 rows: 199 us in 16 parts of 256 tokens, 148 in 4 of 1,024).  That rule does not look at how many
+// CTAs result: 16 rows of one request leave most SMs idle (4 drafts over 32,768 tokens: 35 us in bf16, 66 in 4 bits).
 // Tokens of a tile; in 4 bits two blocks of 16, whose shared softmax steps save instructions (380 -> 372 us).
 constexpr int kFewTile(bool fp4) { return fp4 ? 32 : 16; }
 constexpr int64_t kCtas = 8192;
 constexpr int64_t kMinPart = 256;
 // Up to eight parts are the CTAs of a cluster, which join through each other's shared memory: no workspace and
-// no second launch (one token over 4096: 21 -> 17 us a call).  Only while all CTAs run at once: a cluster keeps
-// its SMs' places until its last part is done (64 ragged requests in clusters: 266 us against 192).  More parts,
-// worth it from kClusterPart tokens each on, go through the workspace.
+// no second launch (one token over 4,096: 12.9 -> 11.5 us on the GPU; calls in a row 20 -> 16 us, an allocation
+// among them).  Only while all CTAs run at once: a cluster keeps its SMs' places until its last part is done (64
+// ragged requests in clusters: 266 us against 192).  More parts, worth it from kClusterPart tokens each on, go
+// through the workspace.
 constexpr int64_t kCluster = 8, kClusterPart = 1024, kClusterCtas = 304;
 
 attn::Cut cut_few(const kda_kv_params& p, int32_t n, int32_t max_new, int32_t max_len)

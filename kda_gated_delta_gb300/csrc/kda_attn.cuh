@@ -45,8 +45,8 @@ __device__ __forceinline__ int32_t tile_base(const Span& s, int32_t i)
 
 // Rows before the first request's and after the last one's belong to nobody; there are none with a good
 // cu_seqlens.  The grid of a call with one has a CTA more than its work, which looks, and gives such rows what a
-// query that sees nothing gets.  Others meet no instruction more for it: what every CTA runs once costs it some 200
-// cycles per eight instructions, and a look at the kernels' start took 1 to 2% of a call.  Still the 4-bit kernels'
+// query that sees nothing gets.  Others meet one comparison more for it at most: what every CTA runs once costs it
+// some 200 cycles per eight instructions, and a look at the kernels' start took 1 to 2% of a call.  Still the 4-bit kernels'
 // code came out 1% slower beside it (373 -> 376, 364 -> 370 us), with few query rows in bf16 1% faster.
 inline unsigned extra_cta(const kv::Paged& c) { return c.cu ? 1 : 0; }
 template <int D>

@@ -6,7 +6,9 @@
 // tokens that any of them may see in tiles of 128:
 //
 //   S_i = Q_i K_j^T      M 128 (rows) x N 128 (tokens) x K D, both operands K-major in shared memory
-//   P_i = exp2(S_i - m)  one thread per row: no shuffles; packed over half of S_i's own columns
+//   P_i = exp2(S_i - m)  one thread per row: no shuffles; packed in bf16 over half of S_i's own columns (half a
+//                        step, 2^-8 of a weight at most, for one operand type with the values; the sum of the
+//                        weights takes them unrounded)
 //   O_i += P_i V_j       A from tensor memory, V_j as it lies in the cache (MN-major)
 //
 // Tensor memory, all 512 columns: S_0, S_1 (128 each; P_i takes the last 64 of S_i's) and O_0, O_1 (D each).
@@ -24,10 +26,10 @@
 // shared memory before their product, by a warp of its own: what lies there may be NaN, which a weight of
 // zero does not stop.
 //
-// Measured (8 kv and 32 query heads of 128): 4,096 tokens over 32,768 in 1.51 ms, 1,360 TFLOP/s, bound by the
+// Measured (8 kv and 32 query heads of 128): 4,096 tokens over 32,768 in 1.52 ms, 1,360 TFLOP/s, bound by the
 // chain scores - softmax - products of a tile, some 3,000 cycles where the products alone take 2,080; eight
 // prompts of 512 to 4,096 tokens through a window of 1,024 in 0.34 ms, a third of it a CTA's start and end;
-// 4 x 500..1,030 tokens over a 4-bit past of 2,000..9,000 in 0.36 ms, bound by the conversion.  Shared memory is
+// 4 x 500..1,030 tokens over a 4-bit past of 2,000..9,000 in 0.37 ms, bound by the conversion.  Shared memory is
 // the busiest unit beside the tensor cores: a product of 128 x 128 x 16 reads 8 KB of it in 64 cycles.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -585,8 +587,8 @@ __device__ bool softmax(const AttnCall& a, const Parts& parts, const Work& w, in
             tc::tmem_wait_st();
         }
         // Half a row of scores at a time: the low half for its maximum, then the high half, whose weights are
-        // taken and handed over first, then the low half again.  64 scores and 32 packed weights fit where 128
-        // scores spilled.
+        // taken and handed over first, then the low half again: 64 scores and 32 packed weights at a time.  28 to 88
+        // bytes a thread still spill (by the variant); with 128 scores at a time the calls were slower.
         float top = -INFINITY;
 #pragma unroll
         for (int step = 0; step < 3; ++step) {

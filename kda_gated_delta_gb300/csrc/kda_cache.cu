@@ -7,7 +7,8 @@
 // loads in flight at once, and the rotation's cosines and sines are loaded once for them.
 //
 // Measured: 16,412 tokens of 32 query and 8 kv heads of 128, bf16, in 72 us, 6,500 GB/s of the 6,776 that a copy
-// reaches; 16,411 tokens into a 4-bit cache in 63 us (5,600 GB/s; the quantiser's instructions), and back in 22.
+// reaches; 16,411 tokens into a 4-bit cache in 64 us (5,600 GB/s; the quantiser's instructions), and back in 24.5;
+// back from a bf16 cache in 27.5 (4,900 GB/s).
 // Into the 4-bit cache 2 rows per thread take 84 us and 6 take 77; CTAs of 256 threads 67 and of 64 threads 66.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
