@@ -423,6 +423,136 @@ int32_t kda_paged_attention(const kda_kv_params* p,
                             void* out, float* lse,
                             void* workspace, size_t workspace_bytes, kda_stream_t stream);
 
+/* ==================================================================================================
+ * Around a recurrence: the short causal convolution before it, the group norm with an activation behind
+ * it, and the selective state space recurrence, the per-head-gated sibling without the delta correction.
+ *
+ * A KDA layer takes its queries, keys and values through a short convolution and its outputs through a
+ * per-head norm times an activated gate; layers of the selective recurrence have the same two around
+ * theirs.  The pages describe the layers' projections and norms only in passing ("KDA inference
+ * components"); formulas and layouts below are this library's own.
+ *
+ * Packed batch and padding are as in kda_chunk_prefill: request i owns rows cu_seqlens[i] ..
+ * cu_seqlens[i+1]-1, state_idx[i] is its slot, a negative slot marks padding (zero outputs, no state read
+ * or written), slots of distinct requests are distinct, a slot >= num_slots is padding and recorded
+ * (code 1), a malformed cu_seqlens is recorded (code 2) and never causes an access out of range: rows that
+ * belong to no request get zeros, a table that decreases has unspecified outputs.  A request without
+ * tokens leaves its state as it is.
+ * The rows of x, dt, B, C and gate may be strided: *_stride is the distance between tokens in elements
+ * (what belongs to one token is contiguous).  Parameters (weight, bias, A_log, dt_bias, D) are fp32.
+ * Outputs may not overlap inputs.  Results do not depend on timing: the same call gives the same bits.
+ * ================================================================================================== */
+typedef enum kda_activation {
+    KDA_ACT_NONE = 0,
+    KDA_ACT_SILU = 1,           /* x sigmoid(x) */
+    KDA_ACT_SIGMOID = 2
+} kda_activation;
+
+typedef struct kda_conv_params {
+    int32_t num_channels;       /* C >= 1 */
+    int32_t width;              /* W: 2, 3 or 4 taps */
+    int32_t io_dtype;           /* kda_dtype of x, the outputs and the pool */
+    int32_t activation;         /* KDA_ACT_NONE or KDA_ACT_SILU */
+} kda_conv_params;
+
+/*
+ * Short causal convolution of each channel over a request's tokens:
+ *     y_t[c] = act(bias[c] + sum_{i < W} weight[c][i] x_{t-W+1+i}[c])       (sums in fp32)
+ * Inputs before the call's first token come from the request's state, its last W - 1 inputs, which the
+ * call then replaces: a prompt may be taken in parts, and decoding continues it.  A zeroed state starts a
+ * request.
+ *   x           [total_tokens][C], weight [C][W], bias [C] or NULL
+ *   state_pool  io_dtype [num_slots][W - 1][C], the oldest input first
+ *   cu_seqlens  as in kda_chunk_prefill, or NULL: one token per request, total_tokens = num_seqs
+ *   outs        host array of num_outs (1 to 4) device pointers; output j is contiguous
+ *               [total_tokens][out_channels[j]] and receives the next out_channels[j] channels (host
+ *               int32 array of sum C): the parts of a fused projection come out ready for what follows
+ * Rows of 16-byte aligned x, pool and outputs whose stride and channel counts are multiples of 16 bytes go
+ * by vectors; all others by single elements.  total_tokens < 2^31 - 64, C <= 2^20, num_seqs < 2^30.
+ * total_tokens = 0 or num_seqs = 0 is a no-op.
+ */
+int32_t kda_causal_conv(const kda_conv_params* p, const void* x, int64_t x_stride,
+                        const float* weight, const float* bias,
+                        const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                        void* state_pool, int64_t num_slots, const int32_t* state_idx,
+                        void* const* outs, const int32_t* out_channels, int32_t num_outs,
+                        kda_stream_t stream);
+
+typedef struct kda_ssm_params {
+    int32_t num_heads;          /* H, a multiple of num_groups */
+    int32_t head_dim;           /* P: 16, 32, 64 or 128 channels of x and y per head */
+    int32_t state_dim;          /* N: 16, 32, 64, 128 or 256 states per channel */
+    int32_t num_groups;         /* G: head h reads B and C of group h / (H / G) */
+    int32_t io_dtype;           /* kda_dtype of x, B and C */
+    int32_t dt_dtype;           /* kda_dtype of dt */
+    int32_t out_dtype;          /* kda_dtype of out */
+    float softplus_threshold;   /* 20: softplus(x) = x above it */
+} kda_ssm_params;
+
+/* Fill `p`: bf16 x, B, C and out, fp32 dt, threshold 20. */
+void kda_ssm_params_init(kda_ssm_params* p, int32_t num_heads, int32_t head_dim, int32_t state_dim,
+                         int32_t num_groups);
+
+/*
+ * Selective state space recurrence.  Per head, with state S in R^{P x N}:
+ *     dt_t = softplus(dt_raw_t + dt_bias),   a_t = exp(-dt_t exp(A_log))
+ *     S_t  = a_t S_{t-1} + dt_t x_t B_t^T,   y_t = S_t C_t + D x_t
+ * kda_ssm_prefill takes packed prompts, kda_ssm_decode one token per request (row b is request b's); both
+ * start from and update state_pool[state_idx[i]], and decoding continues a prompt.
+ *   x    [T][H][P], dt [T][H], B, C [T][G][N], A_log [H], dt_bias [H] or NULL, D [H] or NULL
+ *   state_pool   fp32 [num_slots][H][P][N], as the delta-rule pool (value row, key channel contiguous)
+ *   out          [T][H][P] out_dtype
+ *   workspace    kda_ssm_prefill_workspace_size(...) bytes, 256-byte aligned, contents garbage before and
+ *                after; it must not be shared with a call that overlaps in time.
+ * x, B, C, the pool and out are 16-byte aligned; x_stride, b_stride and c_stride are multiples of 8.
+ * States are held and updated in fp32.  Limits (KDA_ERR_UNSUPPORTED beyond them): total_tokens < 2^31 - 64,
+ * H <= 4096, num_seqs * H < 2^30.
+ * total_tokens = 0 or num_seqs = 0 is a no-op.
+ */
+size_t kda_ssm_prefill_workspace_size(const kda_ssm_params* p, int32_t num_seqs, int64_t total_tokens);
+
+int32_t kda_ssm_prefill(const kda_ssm_params* p, const void* x, int64_t x_stride,
+                        const void* dt, int64_t dt_stride, const void* B, int64_t b_stride,
+                        const void* C, int64_t c_stride,
+                        const float* A_log, const float* dt_bias, const float* D,
+                        const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                        float* state_pool, int64_t num_slots, const int32_t* state_idx, void* out,
+                        void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+int32_t kda_ssm_decode(const kda_ssm_params* p, const void* x, int64_t x_stride,
+                       const void* dt, int64_t dt_stride, const void* B, int64_t b_stride,
+                       const void* C, int64_t c_stride,
+                       const float* A_log, const float* dt_bias, const float* D,
+                       int32_t batch, float* state_pool, int64_t num_slots, const int32_t* state_idx,
+                       void* out, kda_stream_t stream);
+
+typedef struct kda_norm_params {
+    int32_t num_groups;         /* G >= 1 groups of a token's channels */
+    int32_t group_size;         /* n: 1 to 16384 channels per group */
+    int32_t io_dtype;           /* kda_dtype of x */
+    int32_t out_dtype;          /* kda_dtype of out and of gate */
+    int32_t activation;         /* kda_activation */
+    int32_t gate_first;         /* 1: the gate multiplies x before the norm */
+    int32_t center;             /* 1: group norm (mean taken out); 0: by the root mean square only */
+    float eps;
+} kda_norm_params;
+
+/*
+ * Group norm of each token's channels (channels last) with an activation:
+ *     norm(x) = (x - m) / sqrt(mean((x - m)^2) + eps) * weight + bias,   m = mean(x) if center, else 0
+ *     gate given, gate_first = 0:   out = norm(x) * act(gate)
+ *     gate given, gate_first = 1:   out = norm(x * act(gate))
+ *     no gate:                      out = act(norm(x))
+ * Each (token, group) has its own mean and square: no token reaches another's output.  With groups = heads
+ * it is the output norm of a KDA layer.  Statistics in fp32, the squares taken from the centered values.
+ *   x, gate   [tokens][G][n], gate may be NULL;  weight, bias [G][n] or NULL;  out [tokens][G][n]
+ * Rows of 16-byte aligned tensors whose strides and n are multiples of 8 go by vectors, all others by
+ * single elements.  tokens * G < 2^31 (KDA_ERR_UNSUPPORTED beyond).  tokens = 0 is a no-op.
+ */
+int32_t kda_group_norm(const kda_norm_params* p, const void* x, int64_t x_stride,
+                       const void* gate, int64_t gate_stride, const float* weight, const float* bias,
+                       int64_t tokens, void* out, kda_stream_t stream);
+
 /*
  * Synchronise `stream`, then read and clear the device error word that the kernels set when
  * they meet an out-of-range state_idx (code 1), a malformed cu_seqlens or a snapshot table too

@@ -8,9 +8,11 @@ from .binding import (  # noqa: F401
     KdaError,
     Params,
     attention_workspace_size,
+    causal_conv,
     chunk_prefill,
     check_device_errors,
     commit_verified_states,
+    group_norm,
     kv_append,
     kv_cache,
     kv_read,
@@ -24,5 +26,8 @@ from .binding import (  # noqa: F401
     replay_rings,
     rope_table,
     selftest_wait_timeout,
+    ssm_decode,
+    ssm_prefill,
+    ssm_prefill_workspace_size,
     status_string,
 )

@@ -66,6 +66,23 @@ class KvParams(ctypes.Structure):
     ]
 
 
+class ConvParams(ctypes.Structure):
+    """Mirror of ``kda_conv_params``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_channels", "width", "io_dtype", "activation")]
+
+
+class SsmParams(ctypes.Structure):
+    """Mirror of ``kda_ssm_params``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_heads", "head_dim", "state_dim", "num_groups", "io_dtype", "dt_dtype", "out_dtype")]
+    _fields_ += [("softplus_threshold", ctypes.c_float)]
+
+
+class NormParams(ctypes.Structure):
+    """Mirror of ``kda_norm_params``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_groups", "group_size", "io_dtype", "out_dtype", "activation", "gate_first", "center")]
+    _fields_ += [("eps", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _lock = threading.Lock()
 _lib = None
@@ -128,6 +145,20 @@ def lib() -> ctypes.CDLL:
         L.kda_paged_attention_workspace_size.argtypes = [KP, i32, i64, i32, i32]
         L.kda_paged_attention.restype = i32
         L.kda_paged_attention.argtypes = [KP, _P, i64, *cache, i64, *batch, i32, i32, _P, _P, _P, ctypes.c_size_t, _P]
+        CP, SP, NP = ctypes.POINTER(ConvParams), ctypes.POINTER(SsmParams), ctypes.POINTER(NormParams)
+        L.kda_causal_conv.restype = i32
+        L.kda_causal_conv.argtypes = [CP, _P, i64, _P, _P, _P, i32, i64, _P, i64, _P, _P, _P, i32, _P]
+        L.kda_ssm_params_init.restype = None
+        L.kda_ssm_params_init.argtypes = [SP, i32, i32, i32, i32]
+        L.kda_ssm_prefill_workspace_size.restype = ctypes.c_size_t
+        L.kda_ssm_prefill_workspace_size.argtypes = [SP, i32, i64]
+        rows = [SP, _P, i64, _P, i64, _P, i64, _P, i64, _P, _P, _P]
+        L.kda_ssm_prefill.restype = i32
+        L.kda_ssm_prefill.argtypes = rows + [_P, i32, i64, _P, i64, _P, _P, _P, ctypes.c_size_t, _P]
+        L.kda_ssm_decode.restype = i32
+        L.kda_ssm_decode.argtypes = rows + [i32, _P, i64, _P, _P, _P]
+        L.kda_group_norm.restype = i32
+        L.kda_group_norm.argtypes = [NP, _P, i64, _P, i64, _P, _P, i64, _P, _P]
         _lib = L
         return L
 
@@ -645,6 +676,269 @@ def attention_workspace_size(num_q_heads, num_kv_heads, head_dim, page_size, num
     when none is given)."""
     p = _kv_params(num_q_heads, num_kv_heads, head_dim, page_size, _is_fp4(dtype), 0, False, window, sinks)
     return _attention_workspace(p, num_seqs, num_tokens, max_new, max_len)
+
+
+# ---- around a recurrence: short convolution, selective recurrence, group norm ---------------------------
+
+_CODES = {_F32: KDA_F32, _BF16: KDA_BF16}
+_ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
+
+
+def _code(dtype, name):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
+    return code
+
+
+def _tokens(t, name, shape, dtype, dev):
+    """Pointer and token stride of a [T, ...] tensor of which one token's values are contiguous (a slice of a fused
+    projection will do).  ``shape``: what follows T."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}, with x")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape[1:] != shape:
+        raise ValueError(f"{name} must be [tokens, {', '.join(map(str, shape))}], got {tuple(t.shape)}")
+    if t.is_contiguous():
+        n = 1
+        for d in shape:
+            n *= d
+        return t.data_ptr(), n
+    s, n = t.stride(), 1
+    for i in range(len(shape), 0, -1):
+        if shape[i - 1] > 1 and s[i] != n:
+            raise ValueError(f"{name}: the values of a token must be contiguous")
+        n *= shape[i - 1]
+    if t.shape[0] > 1 and s[0] < n:
+        raise ValueError(f"{name}: the rows of two tokens overlap")
+    return t.data_ptr(), max(s[0], n)
+
+
+def _need_with_x(t, name, dtype, dev, shape=None):
+    if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        _dev(t, name, dtype)
+        raise ValueError(f"{name} must be on cuda:{dev}, with x")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _here(t, name):
+    """The device of x, which has to be the current one."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_device()}")
+    return dev
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_params(C, W, code, act):
+    return ctypes.byref(ConvParams(_clip(C), _clip(W), code, act))
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_split(parts):
+    return (ctypes.c_int32 * len(parts))(*(_clip(n) for n in parts)), ctypes.c_void_p * len(parts)
+
+
+def causal_conv(x, weight, state_pool, state_idx, cu_seqlens=None, *, bias=None, activation=None, split=None, out=None, stream=None):
+    """kda_causal_conv: short causal convolution of each channel of ``x`` ([T, C] bf16 or fp32, rows may be strided) with
+    ``weight`` ([C, W] fp32, W 2 to 4); ``activation`` None or "silu".  ``state_pool`` ([slots, W - 1, C], the type of x)
+    holds each request's last inputs and is updated in place; without ``cu_seqlens`` there is one token per request.
+
+    Returns [T, C], or with ``split`` (channel counts, up to four) a tuple of contiguous [T, n]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return causal_conv(x, weight, state_pool, state_idx, cu_seqlens, bias=bias, activation=activation, split=split, out=out)
+    dev = _here(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, channels]")
+    T, C = x.shape
+    dtype = x.dtype
+    code = _code(dtype, "x")
+    xp, x_stride = _tokens(x, "x", x.shape[1:], dtype, dev)
+    wp = _need_with_x(weight, "weight", _F32, dev)
+    if weight.dim() != 2 or weight.shape[0] != C:
+        raise ValueError(f"weight must be [{C}, width]")
+    W = weight.shape[1]
+    bp = None if bias is None else _need_with_x(bias, "bias", _F32, dev, (C,))
+    pool = _need_with_x(state_pool, "state_pool", dtype, dev)
+    if state_pool.dim() != 3 or state_pool.shape[1:] != (W - 1, C):
+        raise ValueError(f"state_pool must be [slots, {W - 1}, {C}]")
+    idx, n = _need_with_x(state_idx, "state_idx", _I32, dev), state_idx.numel()
+    cu = None
+    if cu_seqlens is not None:
+        cu = _need_with_x(cu_seqlens, "cu_seqlens", _I32, dev, (n + 1,))
+        if n == 0 and T > 0:
+            raise ValueError("tokens without a request")
+    elif T != n:
+        raise ValueError("without cu_seqlens there is one token per request")
+    act = _ACTIVATIONS.get(activation, -1)
+    if act < 0 or act > 1:
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    parts = (C,) if split is None else tuple(split)
+    if sum(parts) != C or not 1 <= len(parts) <= 4 or min(parts) < 1:
+        raise ValueError(f"split must be one to four channel counts with the sum {C}, got {split}")
+    if out is None:
+        outs = [torch.empty((T, m), dtype=dtype, device=x.device) for m in parts]
+    else:
+        outs = [out] if split is None else list(out)
+        if len(outs) != len(parts):
+            raise ValueError("out must have one tensor per part")
+        for i, (o, m) in enumerate(zip(outs, parts)):
+            _need_with_x(o, f"out[{i}]", dtype, dev, (T, m))
+    counts, pointers = _conv_split(parts)
+    rc = _fn("kda_causal_conv")(_conv_params(C, W, code, act), xp, x_stride, wp, bp, cu, n, T, pool, state_pool.shape[0], idx,
+                                pointers(*[o.data_ptr() for o in outs]), counts, len(parts), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, "kda_causal_conv")
+    return outs[0] if split is None else tuple(outs)
+
+
+@functools.lru_cache(maxsize=256)
+def _ssm_params(H, P, N, G, io, dt, out, threshold):
+    return ctypes.byref(SsmParams(_clip(H), _clip(P), _clip(N), _clip(G), io, dt, out, threshold))
+
+
+@functools.lru_cache(maxsize=4096)
+def _ssm_workspace(p, n, T):
+    return int(lib().kda_ssm_prefill_workspace_size(p, _clip(n), T))
+
+
+def ssm_prefill_workspace_size(num_heads, head_dim, state_dim, num_groups, num_seqs, num_tokens, *, dtype=torch.bfloat16,
+                               out_dtype=None) -> int:
+    """Bytes of ``workspace`` that :func:`ssm_prefill` needs for these sizes (it allocates them itself when none is
+    given)."""
+    io = _code(dtype, "dtype")
+    p = _ssm_params(num_heads, head_dim, state_dim, num_groups, io, KDA_F32, io if out_dtype is None else _code(out_dtype, "out_dtype"), 20.0)
+    return _ssm_workspace(p, num_seqs, num_tokens)
+
+
+def _ssm_args(x, dt, B, C, A_log, state_pool, state_idx, dt_bias, D, out, out_dtype, threshold):
+    """(device, params, the entry points' shared pointers, requests, pool, slots, indices, out)."""
+    dev = _here(x, "x")
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be [tokens, heads, head_dim], B and C [tokens, groups, states]")
+    T, H, P = x.shape
+    G, N = B.shape[1:]
+    dtype = x.dtype
+    code = _code(dtype, "x")
+    xp, xs = _tokens(x, "x", x.shape[1:], dtype, dev)
+    bp, bs = _tokens(B, "B", B.shape[1:], dtype, dev)
+    cp, cs = _tokens(C, "C", B.shape[1:], dtype, dev)
+    dt_code = _code(dt.dtype, "dt")
+    dp, ds = _tokens(dt, "dt", (H,), dt.dtype, dev)
+    if not T == B.shape[0] == C.shape[0] == dt.shape[0]:
+        raise ValueError("x, dt, B and C must have the same number of tokens")
+    al = _need_with_x(A_log, "A_log", _F32, dev, (H,))
+    db = None if dt_bias is None else _need_with_x(dt_bias, "dt_bias", _F32, dev, (H,))
+    dd = None if D is None else _need_with_x(D, "D", _F32, dev, (H,))
+    pool = _need_with_x(state_pool, "state_pool", _F32, dev)
+    if state_pool.dim() != 4 or state_pool.shape[1:] != (H, P, N):
+        raise ValueError(f"state_pool must be [slots, {H}, {P}, {N}]")
+    idx = _need_with_x(state_idx, "state_idx", _I32, dev)
+    if out is None:
+        out_dtype = dtype if out_dtype is None else out_dtype
+        out_code = _code(out_dtype, "out_dtype")
+        out = torch.empty((T, H, P), dtype=out_dtype, device=x.device)
+    else:
+        out_code = _code(out.dtype, "out")
+        _need_with_x(out, "out", out.dtype, dev, (T, H, P))
+    p = _ssm_params(H, P, N, G, code, dt_code, out_code, threshold)
+    return dev, T, p, (p, xp, xs, dp, ds, bp, bs, cp, cs, al, db, dd), state_idx.numel(), (pool, state_pool.shape[0], idx, out.data_ptr()), out
+
+
+def ssm_prefill(x, dt, B, C, A_log, cu_seqlens, state_pool, state_idx, *, dt_bias=None, D=None, out=None, out_dtype=None,
+                softplus_threshold=20.0, workspace=None, stream=None):
+    """kda_ssm_prefill: selective state space recurrence over packed prompts.  ``x`` [T, H, P], ``B``, ``C`` [T, G, N] (bf16
+    or fp32), ``dt`` [T, H] (bf16 or fp32, before softplus); rows may be strided.  ``state_pool`` [slots, H, P, N] fp32
+    is updated in place.  Returns ``out`` [T, H, P]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ssm_prefill(x, dt, B, C, A_log, cu_seqlens, state_pool, state_idx, dt_bias=dt_bias, D=D, out=out, out_dtype=out_dtype,
+                               softplus_threshold=softplus_threshold, workspace=workspace)
+    dev, T, p, rows, n, state, out = _ssm_args(x, dt, B, C, A_log, state_pool, state_idx, dt_bias, D, out, out_dtype, softplus_threshold)
+    cu = _need_with_x(cu_seqlens, "cu_seqlens", _I32, dev, (n + 1,))
+    if n == 0 and T > 0:
+        raise ValueError("tokens without a request")
+    need, ws = _ssm_workspace(p, n, T), None
+    if workspace is not None:
+        ws, need = _need_with_x(workspace, "workspace", _U8, dev), workspace.numel()
+    elif need:
+        workspace = torch.empty(need, dtype=_U8, device=x.device)
+        ws = workspace.data_ptr()
+    rc = _fn("kda_ssm_prefill")(*rows, cu, n, T, *state, ws, need, torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, "kda_ssm_prefill")
+    return out
+
+
+def ssm_decode(x, dt, B, C, A_log, state_pool, state_idx, *, dt_bias=None, D=None, out=None, out_dtype=None,
+               softplus_threshold=20.0, stream=None):
+    """kda_ssm_decode: one token per request (row b is request b's), see :func:`ssm_prefill`."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ssm_decode(x, dt, B, C, A_log, state_pool, state_idx, dt_bias=dt_bias, D=D, out=out, out_dtype=out_dtype,
+                              softplus_threshold=softplus_threshold)
+    dev, T, p, rows, n, state, out = _ssm_args(x, dt, B, C, A_log, state_pool, state_idx, dt_bias, D, out, out_dtype, softplus_threshold)
+    if T != n:
+        raise ValueError("there must be one token per request")
+    rc = _fn("kda_ssm_decode")(*rows, n, *state, torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, "kda_ssm_decode")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_params(G, n, io, out, act, first, center, eps):
+    return ctypes.byref(NormParams(_clip(G), _clip(n), io, out, act, first, center, eps))
+
+
+def group_norm(x, weight=None, bias=None, *, gate=None, activation=None, gate_first=False, center=True, eps=1e-5, out=None,
+               out_dtype=None, stream=None):
+    """kda_group_norm: norm of each group of a token's channels.  ``x`` [T, G, n] (bf16 or fp32, rows may be strided),
+    ``weight`` and ``bias`` [G, n] fp32 or None; ``center`` False: by the root mean square only.  ``activation`` None, "silu"
+    or "sigmoid" is applied to the result, or with ``gate`` ([T, G, n], the type of the output) to the gate, which multiplies
+    the result, or x before the norm (``gate_first``).  Returns ``out`` [T, G, n] (default: the type of x)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return group_norm(x, weight, bias, gate=gate, activation=activation, gate_first=gate_first, center=center, eps=eps, out=out,
+                              out_dtype=out_dtype)
+    dev = _here(x, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be [tokens, groups, channels]")
+    shape = x.shape
+    T, G, n = shape
+    code = _code(x.dtype, "x")
+    xp, xs = _tokens(x, "x", shape[1:], x.dtype, dev)
+    wp = None if weight is None else _need_with_x(weight, "weight", _F32, dev, shape[1:])
+    bp = None if bias is None else _need_with_x(bias, "bias", _F32, dev, shape[1:])
+    if out is None:
+        out_dtype = x.dtype if out_dtype is None else out_dtype
+        out_code = _code(out_dtype, "out_dtype")
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    else:
+        out_dtype = out.dtype
+        out_code = _code(out_dtype, "out")
+        _need_with_x(out, "out", out_dtype, dev, shape)
+    gp, gs = None, 0
+    if gate is not None:
+        if gate.shape != shape:
+            raise ValueError("gate must have the shape of x")
+        gp, gs = _tokens(gate, "gate", shape[1:], out_dtype, dev)
+    elif gate_first:
+        raise ValueError("gate_first without gate")
+    act = _ACTIVATIONS.get(activation, -1)
+    if act < 0:
+        raise ValueError(f"activation must be None, 'silu' or 'sigmoid', got {activation!r}")
+    rc = _fn("kda_group_norm")(_norm_params(G, n, code, out_code, act, 1 if gate_first else 0, 1 if center else 0, eps), xp, xs, gp, gs, wp, bp,
+                               T, out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, "kda_group_norm")
+    return out
 
 
 def selftest_wait_timeout(polls: int, result=None, stream=None) -> None:

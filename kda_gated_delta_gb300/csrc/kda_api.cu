@@ -8,6 +8,7 @@
 #include "kda.h"
 #include "kda_internal.cuh"
 #include "kda_kv.cuh"
+#include "kda_layer.cuh"
 
 namespace {
 
@@ -251,13 +252,14 @@ int32_t kda_check_device_errors(kda_stream_t stream, int32_t* code)
     if (!code) return KDA_ERR_INVALID_ARG;
     *code = 0;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return KDA_ERR_CUDA;
-    int32_t c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0;
+    int32_t c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0, c6 = 0;
     if (kda::recurrent_read_and_clear_error(&c1) != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::prefill_read_and_clear_error(&c2) != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::selftest_read_and_clear_error(&c3) != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::cache_read_and_clear_error(&c4) != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::attn_read_and_clear_error(&c5) != cudaSuccess) return KDA_ERR_CUDA;
-    *code = c1 ? c1 : c2 ? c2 : c3 ? c3 : c4 ? c4 : c5;
+    if (kda::layer_read_and_clear_error(&c6) != cudaSuccess) return KDA_ERR_CUDA;
+    *code = c1 ? c1 : c2 ? c2 : c3 ? c3 : c4 ? c4 : c5 ? c5 : c6;
     return *code ? KDA_ERR_DEVICE_CHECK : KDA_OK;
 }
 

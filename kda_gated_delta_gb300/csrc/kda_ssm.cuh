@@ -1,0 +1,332 @@
+// kda_ssm.cuh -- the selective state space recurrence token by token:
+//
+//     S_t = a_t S_{t-1} + (dt_t x_t) B_t^T,   y_t = S_t C_t + D x_t,   a_t = exp(-dt_t exp(A_log))
+//
+// Rows of S (channels of x) are independent.  A row is split over LPR lanes with CPL states each (16-byte
+// groups 4 * (li + LPR * j), so that a load instruction of a warp reads whole rows), held in registers
+// across the tokens; y_t takes log2(LPR) shuffles a row.
+//
+//   ssm_token_kernel   one token per request: bound by the state's bytes, read and written once.
+//   ssm_rows_kernel    packed prompts, tokens staged through shared memory: 3 fp32 operations a state and
+//                      token, bound by the fp32 pipes; the path of fp32 inputs and of the shapes that the
+//                      tensor-core form (kda_ssm_tc.cuh) does not take.
+#pragma once
+
+#include <atomic>
+
+#include "kda_layer.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+
+constexpr int kSsmThreads = 128;
+
+template <int N>
+struct SsmShape {
+    static constexpr int CPL = N <= 32 ? 4 : N == 64 ? 8 : 16;   // states of a lane
+    static constexpr int LPR = N / CPL;                          // lanes of a row
+    static constexpr int RPS = 32 / LPR;                         // rows of a warp at once
+    static constexpr int ROWS = kSsmThreads / LPR;               // rows of a CTA at once
+    static constexpr int NV4 = CPL / 4;
+};
+
+// dt_t and a_t of one head and token.
+__device__ __forceinline__ void ssm_step_size(const SsmCall& a, int64_t t, int h, float rate, float bias, float& dt, float& decay)
+{
+    const int64_t i = t * a.dt_stride + h;
+    const float raw = a.dt_bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.dt)[i]) : reinterpret_cast<const float*>(a.dt)[i];
+    dt = softplus_f32(raw + bias, a.threshold);
+    decay = expf(-dt * rate);
+}
+
+// One token per request.  A CTA has STEPS * ROWS rows of one (request, head).
+template <int N, int STEPS, typename TIn, typename TOut>
+__global__ void __launch_bounds__(kSsmThreads, STEPS >= 4 ? 4 : 8) ssm_token_kernel(const SsmCall a, int splits, int64_t ahead)
+{
+    using Sh = SsmShape<N>;
+    constexpr int NV4 = Sh::NV4, LPR = Sh::LPR;
+    const int64_t bh = blockIdx.x / splits;
+    const int row0 = (int)(blockIdx.x - bh * splits) * Sh::ROWS * STEPS;
+    const int64_t b = bh / a.H;
+    const int h = (int)(bh - b * a.H);
+    const int li = threadIdx.x % LPR, r0 = row0 + threadIdx.x / LPR;
+    int64_t slot = a.idx[b];
+    if (slot >= a.num_slots) {
+        if (threadIdx.x == 0) record_layer_error(kDevErrStateIndex);
+        slot = -1;
+    }
+    TOut* out = reinterpret_cast<TOut*>(a.out) + (b * a.H + h) * a.P;
+    if (slot < 0) {
+        for (int r = row0 + threadIdx.x; r < a.P && r < row0 + Sh::ROWS * STEPS; r += kSsmThreads) out[r] = from_f32<TOut>(0.f);
+        return;
+    }
+    float* state = a.pool + ((slot * a.H + h) * a.P + r0) * N + 4 * li;
+    float4 st[STEPS][NV4];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int j = 0; j < NV4; ++j)
+            st[s][j] = r0 + s * Sh::ROWS < a.P ? __ldcs(reinterpret_cast<const float4*>(state + (int64_t)s * Sh::ROWS * N + 4 * LPR * j))
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ahead > 0 && threadIdx.x == 0 && blockIdx.x + ahead < gridDim.x) {
+        // the state of the CTA one wave of resident CTAs ahead: it is in L2 when that CTA starts
+        const int64_t nb = blockIdx.x + ahead, nbh = nb / splits, q = nbh / a.H;
+        const int64_t ns = a.idx[q];
+        if (ns >= 0 && ns < a.num_slots) {
+            const int nr = (int)(nb - nbh * splits) * Sh::ROWS * STEPS;
+            const int rows = a.P - nr < Sh::ROWS * STEPS ? a.P - nr : Sh::ROWS * STEPS;
+            tc::bulk_prefetch_l2(a.pool + ((ns * a.H + (nbh - q * a.H)) * a.P + nr) * N, (uint32_t)rows * N * 4);
+        }
+    }
+    const int g = h / (a.H / a.G);
+    const TIn* Bp = reinterpret_cast<const TIn*>(a.B) + b * a.b_stride + (int64_t)g * N + 4 * li;
+    const TIn* Cp = reinterpret_cast<const TIn*>(a.C) + b * a.c_stride + (int64_t)g * N + 4 * li;
+    const TIn* xp = reinterpret_cast<const TIn*>(a.x) + b * a.x_stride + (int64_t)h * a.P;
+    float Bv[4 * NV4], Cv[4 * NV4], xv[STEPS];
+#pragma unroll
+    for (int j = 0; j < NV4; ++j) {
+        load_floats<TIn, 4>(Bp + 4 * LPR * j, Bv + 4 * j);
+        load_floats<TIn, 4>(Cp + 4 * LPR * j, Cv + 4 * j);
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) xv[s] = r0 + s * Sh::ROWS < a.P ? to_f32(xp[r0 + s * Sh::ROWS]) : 0.f;
+    float dt, decay;
+    ssm_step_size(a, b, h, expf(a.A_log[h]), a.dt_bias ? a.dt_bias[h] : 0.f, dt, decay);
+    const float D = a.D ? a.D[h] : 0.f;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int r = r0 + s * Sh::ROWS;
+        const float u = dt * xv[s];
+        float y = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV4; ++j) {
+            float* e = reinterpret_cast<float*>(&st[s][j]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                e[k] = fmaf(u, Bv[4 * j + k], decay * e[k]);
+                y = fmaf(e[k], Cv[4 * j + k], y);
+            }
+        }
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+        if (r < a.P) {
+#pragma unroll
+            for (int j = 0; j < NV4; ++j) __stcs(reinterpret_cast<float4*>(state + (int64_t)s * Sh::ROWS * N + 4 * LPR * j), st[s][j]);
+            if (li == 0) out[r] = from_f32<TOut>(fmaf(D, xv[s], y));
+        }
+    }
+}
+
+__device__ __forceinline__ void ssm_cp_async16(void* dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+
+constexpr int kSsmTile = 16;        // tokens staged at once
+
+// Packed prompts.  blockIdx.x: (request, head, slab of STEPS * ROWS rows); one CTA more gives zeros to rows of
+// no request.
+template <int N, int STEPS, typename TIn, typename TOut>
+__global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, int splits)
+{
+    using Sh = SsmShape<N>;
+    constexpr int NV4 = Sh::NV4, LPR = Sh::LPR, R = Sh::ROWS * STEPS, E = 16 / (int)sizeof(TIn);
+    constexpr int XR = R < 16 ? 16 : R;
+    __shared__ __align__(16) TIn sB[2][kSsmTile][N], sC[2][kSsmTile][N], sx[2][kSsmTile][XR];
+    __shared__ float sdt[2][kSsmTile], sa[2][kSsmTile];
+    __shared__ __align__(16) TOut sy[kSsmTile][XR];
+    const int tid = threadIdx.x;
+    const int64_t bh = blockIdx.x / splits;
+    const int64_t b = bh / a.H;
+    TOut* out = reinterpret_cast<TOut*>(a.out);
+    const int64_t width = (int64_t)a.H * a.P;
+    if (b >= a.n) {                                     // rows before the first request and behind the last
+        int64_t lo = a.cu[0], hi = a.cu[a.n];
+        lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+        hi = hi < 0 ? 0 : hi > a.T ? a.T : hi;
+        if ((lo > 0 || hi < a.T) && tid == 0) record_layer_error(kDevErrSeqlens);
+        for (int64_t i = tid; i < lo * width; i += kSsmThreads) out[i] = from_f32<TOut>(0.f);
+        for (int64_t i = hi * width + tid; i < a.T * width; i += kSsmThreads) out[i] = from_f32<TOut>(0.f);
+        return;
+    }
+    const int h = (int)(bh - b * a.H);
+    const int row0 = (int)(blockIdx.x - bh * splits) * R;
+    const int rows = a.P - row0 < R ? a.P - row0 : R;    // a multiple of 16
+    int64_t first, last;
+    if (!layer_rows(a.cu, (int32_t)b, a.T, first, last) && tid == 0) record_layer_error(kDevErrSeqlens);
+    if (first == last) return;
+    int64_t slot = a.idx[b];
+    if (slot >= a.num_slots) {
+        if (tid == 0) record_layer_error(kDevErrStateIndex);
+        slot = -1;
+    }
+    out += (int64_t)h * a.P + row0;
+    if (slot < 0) {
+        for (int64_t t = first; t < last; ++t)
+            for (int r = tid; r < rows; r += kSsmThreads) out[t * width + r] = from_f32<TOut>(0.f);
+        return;
+    }
+    const int g = h / (a.H / a.G);
+    const TIn* Bp = reinterpret_cast<const TIn*>(a.B) + (int64_t)g * N;
+    const TIn* Cp = reinterpret_cast<const TIn*>(a.C) + (int64_t)g * N;
+    const TIn* xp = reinterpret_cast<const TIn*>(a.x) + (int64_t)h * a.P + row0;
+    const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
+
+    auto stage = [&](int buf, int64_t t0) {
+        const int count = last - t0 < kSsmTile ? (int)(last - t0) : kSsmTile;
+        for (int i = tid; i < count * (N / E); i += kSsmThreads) {
+            const int k = i / (N / E), c = i % (N / E) * E;
+            ssm_cp_async16(&sB[buf][k][c], Bp + (t0 + k) * a.b_stride + c);
+            ssm_cp_async16(&sC[buf][k][c], Cp + (t0 + k) * a.c_stride + c);
+        }
+        for (int i = tid; i < count * (rows / E); i += kSsmThreads) {
+            const int k = i / (rows / E), c = i % (rows / E) * E;
+            ssm_cp_async16(&sx[buf][k][c], xp + (t0 + k) * a.x_stride + c);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (tid < count) ssm_step_size(a, t0 + tid, h, rate, bias, sdt[buf][tid], sa[buf][tid]);
+    };
+
+    const int li = tid % LPR, r0 = tid / LPR;
+    float* state = a.pool + ((slot * a.H + h) * a.P + row0 + r0) * N + 4 * li;
+    float st[STEPS][4 * NV4];
+    stage(0, first);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int j = 0; j < NV4; ++j) {
+            const float4 v = r0 + s * Sh::ROWS < rows ? *reinterpret_cast<const float4*>(state + (int64_t)s * Sh::ROWS * N + 4 * LPR * j)
+                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+            st[s][4 * j] = v.x; st[s][4 * j + 1] = v.y; st[s][4 * j + 2] = v.z; st[s][4 * j + 3] = v.w;
+        }
+    int buf = 0;
+    for (int64_t t0 = first; t0 < last; t0 += kSsmTile, buf ^= 1) {
+        const int count = last - t0 < kSsmTile ? (int)(last - t0) : kSsmTile;
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();                                 // this tile is in, the last one's outputs are out
+        if (t0 + kSsmTile < last) stage(buf ^ 1, t0 + kSsmTile);
+#pragma unroll 2
+        for (int k = 0; k < count; ++k) {
+            const float decay = sa[buf][k], dt = sdt[buf][k];
+            float Bv[4 * NV4], Cv[4 * NV4];
+#pragma unroll
+            for (int j = 0; j < NV4; ++j) {
+                load_floats<TIn, 4>(&sB[buf][k][4 * (li + LPR * j)], Bv + 4 * j);
+                load_floats<TIn, 4>(&sC[buf][k][4 * (li + LPR * j)], Cv + 4 * j);
+            }
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int r = r0 + s * Sh::ROWS;
+                const float x = to_f32(sx[buf][k][r]);
+                const float u = dt * x;
+                float y = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4 * NV4; ++i) {
+                    st[s][i] = fmaf(u, Bv[i], decay * st[s][i]);
+                    y = fmaf(st[s][i], Cv[i], y);
+                }
+#pragma unroll
+                for (int off = LPR / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+                if (li == 0) sy[k][r] = from_f32<TOut>(fmaf(D, x, y));
+            }
+        }
+        __syncthreads();
+        constexpr int O = 16 / (int)sizeof(TOut);
+        for (int i = tid; i < count * (rows / O); i += kSsmThreads) {
+            const int k = i / (rows / O), c = i % (rows / O) * O;
+            *reinterpret_cast<uint4*>(out + (t0 + k) * width + c) = *reinterpret_cast<const uint4*>(&sy[k][c]);
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int j = 0; j < NV4; ++j)
+            if (r0 + s * Sh::ROWS < rows)
+                *reinterpret_cast<float4*>(state + (int64_t)s * Sh::ROWS * N + 4 * LPR * j) =
+                    make_float4(st[s][4 * j], st[s][4 * j + 1], st[s][4 * j + 2], st[s][4 * j + 3]);
+}
+
+namespace {
+
+int sm_count()
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <int N, int STEPS, typename TIn, typename TOut>
+cudaError_t ssm_token_launch(const SsmCall& a, cudaStream_t s)
+{
+    constexpr int R = SsmShape<N>::ROWS * STEPS;
+    const int splits = (a.P + R - 1) / R;
+    const int64_t blocks = (int64_t)a.n * a.H * splits;
+    const int64_t resident = (int64_t)sm_count() * (STEPS >= 4 ? 4 : 8);
+    ssm_token_kernel<N, STEPS, TIn, TOut><<<(unsigned)blocks, kSsmThreads, 0, s>>>(a, splits, blocks > resident ? resident : 0);
+    return cudaGetLastError();
+}
+
+// Rows of a CTA: four steps keep 64 states a thread in flight; few requests take one step each, so that
+// more SMs have work.
+template <int N, typename TIn, typename TOut>
+cudaError_t ssm_token_steps(const SsmCall& a, cudaStream_t s)
+{
+    constexpr int R = SsmShape<N>::ROWS;
+    const int64_t rows = (int64_t)a.n * a.H * a.P;
+    if (a.P >= 4 * R && rows >= (int64_t)sm_count() * 4 * 4 * R) return ssm_token_launch<N, 4, TIn, TOut>(a, s);
+    if (a.P >= 2 * R && rows >= (int64_t)sm_count() * 4 * 2 * R) return ssm_token_launch<N, 2, TIn, TOut>(a, s);
+    return ssm_token_launch<N, 1, TIn, TOut>(a, s);
+}
+
+template <int N, int STEPS, typename TIn, typename TOut>
+cudaError_t ssm_rows_launch(const SsmCall& a, cudaStream_t s)
+{
+    constexpr int R = SsmShape<N>::ROWS * STEPS;
+    const int splits = (a.P + R - 1) / R;
+    const int64_t blocks = (int64_t)a.n * a.H * splits + 1;
+    ssm_rows_kernel<N, STEPS, TIn, TOut><<<(unsigned)blocks, kSsmThreads, 0, s>>>(a, splits);
+    return cudaGetLastError();
+}
+
+template <int N, typename TIn, typename TOut>
+cudaError_t ssm_rows_steps(const SsmCall& a, cudaStream_t s)
+{
+    constexpr int R = SsmShape<N>::ROWS;
+    if (a.P >= 2 * R && (int64_t)a.n * a.H * a.P >= (int64_t)sm_count() * 4 * R) return ssm_rows_launch<N, 2, TIn, TOut>(a, s);
+    return ssm_rows_launch<N, 1, TIn, TOut>(a, s);
+}
+
+template <bool TOKEN, typename TIn, typename TOut>
+cudaError_t ssm_states(const SsmCall& a, cudaStream_t s)
+{
+#define KDA_SSM_N(n) case n: return TOKEN ? ssm_token_steps<n, TIn, TOut>(a, s) : ssm_rows_steps<n, TIn, TOut>(a, s)
+    switch (a.N) {
+        KDA_SSM_N(16);
+        KDA_SSM_N(32);
+        KDA_SSM_N(64);
+        KDA_SSM_N(128);
+        KDA_SSM_N(256);
+    default: return cudaErrorInvalidValue;
+    }
+#undef KDA_SSM_N
+}
+
+template <bool TOKEN>
+cudaError_t ssm_dispatch(const kda_ssm_params& p, const SsmCall& a, cudaStream_t s)
+{
+    if (p.io_dtype == KDA_BF16)
+        return p.out_dtype == KDA_BF16 ? ssm_states<TOKEN, __nv_bfloat16, __nv_bfloat16>(a, s) : ssm_states<TOKEN, __nv_bfloat16, float>(a, s);
+    return p.out_dtype == KDA_BF16 ? ssm_states<TOKEN, float, __nv_bfloat16>(a, s) : ssm_states<TOKEN, float, float>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_decode(const kda_ssm_params& p, const SsmCall& a, cudaStream_t s) { return ssm_dispatch<true>(p, a, s); }
+
+}  // namespace kda
