@@ -48,6 +48,11 @@ __device__ int32_t g_attn_tc_error = 0;
 
 using attn::Parts;
 using attn::Span;
+using tc::desc_sw128;
+using tc::pin32;
+using tc::tmem_ld32;
+using tc::tmem_st32;
+using tc::tmem_wait_ld;
 
 constexpr int kRows = 256;            // query rows of a CTA
 constexpr int kTile = 128;            // cache tokens of a tile
@@ -80,49 +85,12 @@ struct __align__(8) Bars {
 };
 static_assert(sizeof(Bars) <= 320, "barrier block");
 
-// Matrix descriptor of a 128-byte-swizzled operand: 8 rows of 128 bytes make an atom, `sbo` the distance of
-// atoms along the strided dimension, `lbo` (MN-major only) that of 64-element panels.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
-{
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
 template <bool FP16>
 __host__ __device__ constexpr uint32_t idesc(uint32_t N, bool b_mn)
 {
     return (1u << 4) | (FP16 ? 0u : 1u << 7 | 1u << 10) | (b_mn ? 1u << 16 : 0u) | (N >> 3) << 17 | (128u >> 4) << 24;
 }
 
-#define KDA_X8(p, i) p(r[i]), p(r[i + 1]), p(r[i + 2]), p(r[i + 3]), p(r[i + 4]), p(r[i + 5]), p(r[i + 6]), p(r[i + 7])
-#define KDA_OUT(x) "=r"(x)
-#define KDA_IN(x) "r"(x)
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : KDA_X8(KDA_OUT, 0), KDA_X8(KDA_OUT, 8), KDA_X8(KDA_OUT, 16), KDA_X8(KDA_OUT, 24)
-        : "r"(addr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        KDA_X8(KDA_IN, 0), KDA_X8(KDA_IN, 8), KDA_X8(KDA_IN, 16), KDA_X8(KDA_IN, 24)
-        : "memory");
-}
-// Waits for the loads; the empty statements keep every use of their registers after the wait.
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-#define KDA_BOTH(x) "+r"(x)
-__device__ __forceinline__ void pin32(uint32_t* r)
-{
-    asm volatile("" : KDA_X8(KDA_BOTH, 0), KDA_X8(KDA_BOTH, 8), KDA_X8(KDA_BOTH, 16), KDA_X8(KDA_BOTH, 24)::"memory");
-}
-#undef KDA_X8
-#undef KDA_OUT
-#undef KDA_IN
-#undef KDA_BOTH
 // Whether the phase with the given parity is complete, without waiting (try_wait may suspend the thread).
 __device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity)
 {
@@ -848,22 +816,10 @@ __global__ void __launch_bounds__(128) join_rows_kernel(AttnCall a, Parts parts,
     attn::join_row<D>(a, parts, row, attn::join_row_index(share) < rows ? n : 0, share);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess || r != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
-}
-
 // The cache as rows of D channels, read in boxes of one page x 64 channels, 128-byte swizzle.
 cudaError_t encode_pages(CUtensorMap* m, const void* base, int64_t rows, int D, int page)
 {
-    const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tc::tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)D * 2};

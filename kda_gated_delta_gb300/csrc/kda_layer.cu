@@ -13,10 +13,4 @@ cudaError_t layer_read_and_clear_error(int32_t* code) { return read_and_clear(g_
 #include "kda_conv.cuh"
 #include "kda_norm.cuh"
 #include "kda_ssm.cuh"
-
-namespace kda {
-
-size_t ssm_workspace_bytes(const kda_ssm_params&, int32_t, int64_t) { return 0; }
-cudaError_t launch_ssm_prefill(const kda_ssm_params& p, const SsmCall& a, void*, cudaStream_t s) { return ssm_dispatch<false>(p, a, s); }
-
-}  // namespace kda
+#include "kda_ssm_tc.cuh"

@@ -1,0 +1,735 @@
+// kda_ssm_tc.cuh -- the selective state space recurrence over packed prompts on the tensor cores (bf16
+// inputs, head_dim 64 or 128, 64 or 128 states).
+//
+// Unrolled over a chunk of 128 tokens that a state S [N][P] enters, with l_t = log2 a_t and G_r = sum_{i<=r} l_i:
+//
+//     y_r  = 2^{G_r} S^T C_r + sum_{j<=r} 2^{G_r - G_j} dt_j (C_r . B_j) x_j + D x_r
+//     S'   = 2^{G_L} S + sum_j 2^{G_L - G_j} dt_j B_j x_j^T
+//
+// so a chunk is four products of matrices, and the state runs through elementwise operations only:
+//
+//     Gram = C B^T            M 128 (r) x N 128 (j) x K states, shared by the heads of a group
+//     Y    = C S, scaled by 2^{G_r} and D x added in tensor memory, then += M X with
+//            M_rj = Gram_rj 2^{G_r - G_j} dt_j (j <= r), from tensor memory
+//     dS   = B^T X',  X'_j = 2^{G_L - G_j} dt_j x_j
+//
+// No exponent is positive, so nothing overflows, and none is a difference of long sums, which would lose the small
+// steps behind large ones: G_L - G_j is a sum of its own from the chunk's end, G_r - G_j for rows of different
+// warps is (j to the end of its block of 32) + (blocks between) + (start of its block to r).  Only inside a block
+// it is a difference of sums over at most 32 steps.
+// Roundings: M and S (for C S) to bf16 once, 2^-8 of a factor at most, for one operand type with x, B and C, which
+// are exact.  X' is kept as the sum of two bf16 numbers, 2^-16, because its errors stay in the state: with one
+// the states would be off by 2e-3.  S itself stays in fp32 registers from a segment's first chunk to its last.
+//
+// A CTA takes the tokens of one request (or a segment of them) for two slices of 64 channels of x that share B
+// and C: two heads of 64 channels or the halves of one of 128.  One warpgroup per slice, thread = token row, and
+// for the state thread = state index.  All 512 tensor-memory columns: Gram 128, and per slice M 64, Y 64, dS 64.
+// Warp 8 issues the products, warp 9 the tensor-map copies.
+//
+// Long requests are cut into segments when there are fewer (request, slice pair) than SMs: a first pass
+// computes each segment's own state from zero (dS only), a small kernel chains them, and every segment then
+// starts from its true state.
+#pragma once
+
+#include <atomic>
+#include <cstddef>
+
+#include "kda_layer.cuh"
+#include "kda_ssm.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace ssm {
+
+constexpr int kChunk = 128;
+constexpr int kSlice = 64;                       // channels of a slice
+constexpr int kTcThreads = 320;
+constexpr uint32_t kPolls = 1u << 24;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFarStep = -128.f;               // log2 of a step's decay, bounded: 2^-128 leaves nothing either way
+
+// One segment of a request.
+struct Segment {
+    int32_t b, slot;                             // slot < 0: padding, zeros
+    int32_t first, len;
+    int32_t k, count;                            // segment k of count
+    int32_t base;                                // count > 1: the request's first state in the workspace
+    int32_t pad;
+};
+
+// The call's segments, the states between them and how the slices are paired.
+struct Plan {
+    Segment* segments;
+    int32_t* found;                              // number of segments
+    float* states;                               // [..][H][P][N]: state before segment k of a request at base + k
+    float* decays;                               // [..][H]: log2 of a segment's whole decay, at base + k + 1
+    int32_t max_segments;
+    int32_t pairs_per_group, pairs;              // slice pairs
+    int32_t want;                                // tokens of a segment that fill the SMs
+};
+
+// Lists the segments, the longest first (by 64 classes of length), so that no long one starts last.
+__global__ void __launch_bounds__(1024) ssm_plan_kernel(const SsmCall a, const Plan plan)
+{
+    __shared__ int32_t bucket[65], longest, states;
+    const int tid = threadIdx.x;
+    if (tid < 65) bucket[tid] = 0;
+    if (tid == 0) longest = 1, states = 0;
+    __syncthreads();
+    // request b: its rows, slot, and the number of its segments, `size` tokens each but the last
+    auto cut = [&](int32_t b, int64_t& first, int64_t& len, int32_t& slot, int64_t& size) -> int32_t {
+        int64_t last;
+        if (!layer_rows(a.cu, b, a.T, first, last)) record_layer_error(kDevErrSeqlens);
+        len = last - first;
+        slot = a.idx[b];
+        if (slot >= a.num_slots) {
+            record_layer_error(kDevErrStateIndex);
+            slot = -1;
+        }
+        size = len;
+        if (len == 0) return 0;
+        const int64_t n = slot < 0 ? 1 : len / plan.want;
+        if (n <= 1) return 1;
+        size = ((len + n - 1) / n + kChunk - 1) / kChunk * kChunk;
+        return (int32_t)((len + size - 1) / size);                           // whole chunks may need fewer
+    };
+    int64_t first, len, size;
+    int32_t slot;
+    for (int32_t b = tid; b < a.n; b += 1024)
+        if (cut(b, first, len, slot, size) > 0) atomicMax(&longest, (int32_t)size);
+    __syncthreads();
+    const int64_t top = longest;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int32_t b = tid; b < a.n; b += 1024) {
+            const int32_t n = cut(b, first, len, slot, size);
+            const int32_t base = pass == 1 && n > 1 ? atomicAdd(&states, n) : 0;
+            for (int32_t k = 0; k < n; ++k) {
+                const int64_t at = k * size, part = len - at < size ? len - at : size;
+                const int key = 63 - (int)(part * 63 / top);
+                const int32_t place = atomicAdd(&bucket[pass == 0 ? key + 1 : key], 1);
+                if (pass == 1 && place < plan.max_segments) {
+                    Segment s;
+                    s.b = b; s.slot = slot; s.first = (int32_t)(first + at); s.len = (int32_t)part;
+                    s.k = k; s.count = n; s.base = base; s.pad = 0;
+                    plan.segments[place] = s;
+                }
+            }
+        }
+        __syncthreads();
+        if (pass == 0 && tid == 0) {
+            for (int i = 1; i < 65; ++i) bucket[i] += bucket[i - 1];         // first place of each class
+            *plan.found = bucket[64] < plan.max_segments ? bucket[64] : plan.max_segments;
+        }
+        __syncthreads();
+    }
+}
+
+// ---- the chunk kernel ------------------------------------------------------------------------------
+template <int N>
+struct TcCfg {
+    static constexpr int kPanel = kChunk * 128;                 // 64 columns of 128 rows
+    static constexpr int kSteps = N / 16;                       // products along the states
+    static constexpr int kC = 0, kB = 2 * kPanel, kX = 4 * kPanel;       // X: [slice][buffer]
+    static constexpr int kXs = 8 * kPanel;                      // X': [slice][high, low]
+    static constexpr int kS = 12 * kPanel;                      // S: [slice]
+    static constexpr int kEnd = 14 * kPanel;
+    static constexpr int kSmem = kEnd + 3072;
+};
+
+struct __align__(16) TcBars {
+    uint64_t full_c, full_b, full_x[2][2];
+    uint64_t gram, y_first[2], ds[2], y_full[2][2];             // products done
+    uint64_t next[2], xs[2], ready[2];                          // a slice's operands written
+    uint64_t drain;
+    uint32_t tmem;
+    float total[2][2][4], tail[2][2][4];                        // [parity][slice][warp]: sums of the warps' steps
+    __align__(16) float col[2][2][kChunk];                                    // [parity][slice]: log2 of dt_j and the decay to its block's end
+};
+static_assert(sizeof(TcBars) <= 3072 && offsetof(TcBars, col) % 16 == 0, "barrier block; columns are read by 16 bytes");
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Barriers of a slice's warpgroup; the second also tells all whether any of them gave a true flag.
+__device__ __forceinline__ void slice_sync(int s) { asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory"); }
+__device__ __forceinline__ bool slice_any(int s, bool flag)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred pi, po;\n\t"
+        "setp.ne.u32 pi, %1, 0;\n\t"
+        "bar.red.or.pred po, %2, 128, pi;\n\t"
+        "selp.u32 %0, 1, 0, po;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)flag), "r"(1 + s)
+        : "memory");
+    return r != 0;
+}
+
+__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t n, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+struct TcWork {
+    Segment seg;
+    int chunks, slices;
+    int g;
+    int head[2], channel[2];                                     // of each slice: its head, its first channel there
+};
+
+// One lane issues the products of all chunks, in the order of their operands.
+template <int N, bool ENDS>
+__device__ bool tc_issue(const TcWork& w, uint32_t smem, TcBars* bars, uint32_t tmem)
+{
+    using K = TcCfg<N>;
+    constexpr uint32_t id_gram = idesc_bf16(128, false, false), id_y = idesc_bf16(64, false, true), id_ds = idesc_bf16(64, true, true);
+    const uint64_t c_k = tc::desc_sw128(smem + K::kC, 16, 1024), b_k = tc::desc_sw128(smem + K::kB, 16, 1024);
+    const uint64_t b_mn = tc::desc_sw128(smem + K::kB, K::kPanel, 1024);
+    for (int c = 0; c < w.chunks; ++c) {
+        const uint32_t par = c & 1;
+        if constexpr (!ENDS) {
+            if (!tc::mbar_wait(&bars->full_c, par, kPolls)) return false;
+        }
+        if (!tc::mbar_wait(&bars->full_b, par, kPolls)) return false;
+        tc::tc_fence_after();
+        if constexpr (!ENDS) {
+#pragma unroll
+            for (int k = 0; k < K::kSteps; ++k) {
+                const uint32_t off = ((k / 4) * K::kPanel + (k % 4) * 32) >> 4;
+                tc::mma_f16_ss(tmem, c_k + off, b_k + off, id_gram, k > 0);
+            }
+            tc::mma_commit(&bars->gram);
+            for (int s = 0; s < w.slices; ++s) {
+                if (!tc::mbar_wait(&bars->next[s], par, kPolls)) return false;
+                tc::tc_fence_after();
+                const uint64_t sb = tc::desc_sw128(smem + K::kS + s * K::kPanel, K::kPanel, 1024);
+#pragma unroll
+                for (int k = 0; k < K::kSteps; ++k) {
+                    const uint32_t off = ((k / 4) * K::kPanel + (k % 4) * 32) >> 4;
+                    tc::mma_f16_ss(tmem + 128 + 192 * s + 64, c_k + off, sb + (k * 2048 >> 4), id_y, k > 0);
+                }
+                tc::mma_commit(&bars->y_first[s]);
+            }
+        }
+        for (int s = 0; s < w.slices; ++s) {
+            if (!tc::mbar_wait(&bars->xs[s], par, kPolls)) return false;
+            tc::tc_fence_after();
+            const uint64_t xs = tc::desc_sw128(smem + K::kXs + 2 * s * K::kPanel, K::kPanel, 1024);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)                              // eight steps with the high parts, eight with the low
+                tc::mma_f16_ss(tmem + 128 + 192 * s + 128, b_mn + ((k % 8) * 2048 >> 4), xs + (((k / 8) * K::kPanel + (k % 8) * 2048) >> 4), id_ds,
+                               k > 0);
+            tc::mma_commit(&bars->ds[s]);
+        }
+        if constexpr (!ENDS) {
+            for (int s = 0; s < w.slices; ++s) {
+                if (!tc::mbar_wait(&bars->ready[s], par, kPolls)) return false;
+                tc::tc_fence_after();
+                const uint64_t x = tc::desc_sw128(smem + K::kX + (2 * s + par) * K::kPanel, K::kPanel, 1024);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    tc::mma_f16_ts(tmem + 128 + 192 * s + 64, tmem + 128 + 192 * s + 8 * k, x + (k * 2048 >> 4), id_y, 1);
+                tc::mma_commit(&bars->y_full[s][par]);
+            }
+        }
+    }
+    return true;
+}
+
+// One lane copies the chunks' tiles.  What a barrier is waited for here completes again only after the copy that
+// follows, so no phase can be missed.
+template <int N, bool ENDS>
+__device__ bool tc_load(const SsmCall& a, const TcWork& w, uint8_t* smem, TcBars* bars, const CUtensorMap* xm, const CUtensorMap* bm,
+                        const CUtensorMap* cm)
+{
+    using K = TcCfg<N>;
+    for (int c = 0; c < w.chunks; ++c) {
+        const int32_t t = w.seg.first + c * kChunk;
+        const uint32_t par = c & 1;
+        auto load_x = [&]() {
+            for (int s = 0; s < w.slices; ++s) {
+                tc::mbar_arrive_expect_tx(&bars->full_x[s][par], K::kPanel);
+                tc::tma_load_2d(smem + K::kX + (2 * s + par) * K::kPanel, xm, w.head[s] * a.P + w.channel[s], t, &bars->full_x[s][par]);
+            }
+        };
+        auto load_tile = [&](uint64_t* bar, int at, const CUtensorMap* m) {
+            tc::mbar_arrive_expect_tx(bar, K::kPanel * (N / 64));
+#pragma unroll
+            for (int p = 0; p < N / 64; ++p) tc::tma_load_2d(smem + at + p * K::kPanel, m, w.g * N + 64 * p, t, bar);
+        };
+        if constexpr (ENDS) {
+            if (c > 0 && !tc::mbar_wait(&bars->ds[w.slices - 1], (c - 1) & 1, kPolls)) return false;
+            load_x();                                             // X' of the chunk before the last one is done, too
+            load_tile(&bars->full_b, K::kB, bm);
+        } else {
+            for (int s = 0; s < w.slices && c > 1; ++s)
+                if (!tc::mbar_wait(&bars->y_full[s][par], ((c >> 1) - 1) & 1, kPolls)) return false;
+            load_x();
+            if (c > 0 && !tc::mbar_wait(&bars->y_first[w.slices - 1], (c - 1) & 1, kPolls)) return false;
+            load_tile(&bars->full_c, K::kC, cm);
+            if (c > 0 && !tc::mbar_wait(&bars->ds[w.slices - 1], (c - 1) & 1, kPolls)) return false;
+            load_tile(&bars->full_b, K::kB, bm);
+        }
+    }
+    return true;
+}
+
+// One warpgroup: a slice's operands, state and results.  A wait that gave up leaves the loop at the next barrier of
+// the group, for all its threads at once.
+template <int N, bool ENDS, typename TOut>
+__device__ bool tc_slice(const SsmCall& a, const Plan& plan, const TcWork& w, uint8_t* smem, TcBars* bars, uint32_t tmem_base, int s, int r)
+{
+    using K = TcCfg<N>;
+    const int warp = r >> 5, lane = r & 31, h = w.head[s];
+    const uint32_t tmem = tmem_base + ((uint32_t)(r & 96) << 16);
+    const uint32_t t_gram = tmem, t_m = tmem + 128 + 192 * s, t_y = t_m + 64, t_ds = t_m + 128;
+    uint8_t* x_tile = smem + K::kX + 2 * s * K::kPanel;
+    uint8_t* xs_tile = smem + K::kXs + 2 * s * K::kPanel;
+    uint8_t* s_tile = smem + K::kS + s * K::kPanel;
+    const float rate = expf(a.A_log[h]) * kLog2e, bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
+
+    // the state: this thread has S[r][0 .. 63] of the slice
+    float S[kSlice];
+    const int64_t tile = ((int64_t)h * a.P + w.channel[s]) * N + r, all = (int64_t)a.H * a.P * N;
+    const bool own = r < N;
+    if (ENDS) {
+#pragma unroll
+        for (int i = 0; i < kSlice; ++i) S[i] = 0.f;
+    } else {
+        const float* from = (w.seg.count > 1 ? plan.states + (w.seg.base + w.seg.k) * all : a.pool + w.seg.slot * all) + tile;
+#pragma unroll
+        for (int i = 0; i < kSlice; ++i) S[i] = own ? from[(int64_t)i * N] : 0.f;
+    }
+    auto store_s = [&]() {                                        // S in bf16, as the product with C takes it
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(s_tile + r * 128 + ((c ^ (r & 7)) << 4)) =
+                make_uint4(pack_bf16(S[8 * c], S[8 * c + 1]), pack_bf16(S[8 * c + 2], S[8 * c + 3]), pack_bf16(S[8 * c + 4], S[8 * c + 5]),
+                           pack_bf16(S[8 * c + 6], S[8 * c + 7]));
+        tc::fence_proxy_async();
+    };
+    auto arrive = [&](uint64_t* bar) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
+    };
+    bool bad = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!bad) bad = !tc::mbar_wait(bar, parity, kPolls);
+        __syncwarp();
+    };
+    if constexpr (!ENDS) {
+        store_s();
+        const uint32_t zero[16] = {};
+        for (int b = warp + 1; b < 4; ++b) tc::tmem_st16u_nowait(t_m + 16 * b, zero);      // M above the diagonal stays zero
+        tc::tmem_wait_st();
+        arrive(&bars->next[s]);
+    }
+
+    const int64_t t_row = (int64_t)w.seg.first + r;
+    auto raw_step = [&](int c) -> float {
+        if (c * kChunk + r >= w.seg.len) return 0.f;
+        const int64_t i = (t_row + c * kChunk) * a.dt_stride + h;
+        return a.dt_bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.dt)[i]) : reinterpret_cast<const float*>(a.dt)[i];
+    };
+    float raw = raw_step(0), all_steps = 0.f;
+    for (int c = 0; c < w.chunks; ++c) {
+        const uint32_t par = c & 1;
+        const int len = w.seg.len - c * kChunk < kChunk ? w.seg.len - c * kChunk : kChunk;
+        const bool live = r < len;
+        // ---- steps and decays: prefix sums for M, sums from the end for the state
+        const float dt = live ? softplus_f32(raw + bias, a.threshold) : 0.f;
+        if (c + 1 < w.chunks) raw = raw_step(c + 1);
+        const float l = live ? fmaxf(-dt * rate, kFarStep) : 0.f;
+        float head = l, tail = l;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float u = __shfl_up_sync(~0u, head, off), v = __shfl_down_sync(~0u, tail, off);
+            if (lane >= off) head += u;
+            if (lane + off < 32) tail += v;
+        }
+        if (lane == 31) bars->total[par][s][warp] = head;
+        if (lane == 0) bars->tail[par][s][warp] = tail;
+        tail = __shfl_down_sync(~0u, tail, 1);
+        if (lane == 31) tail = 0.f;
+        if (slice_any(s, bad)) return false;
+        float G = head, whole = 0.f, after = 0.f;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const float f = bars->total[par][s][i];
+            if (i < warp) G += f;
+            whole += f;
+        }
+#pragma unroll
+        for (int i = 3; i > 0; --i)
+            if (i > warp) after += bars->tail[par][s][i];
+        const float weight = live ? dt * exp2_fast(tail + after) : 0.f;
+        const float gamma = exp2_fast(whole);
+        all_steps += whole;
+        const float log_dt = __log2f(dt);
+        if constexpr (!ENDS) bars->col[par][s][r] = tail + log_dt;
+
+        // ---- X' = weight x, in two parts
+        wait(&bars->full_x[s][par], (c >> 1) & 1);
+        uint8_t* x_row = x_tile + par * K::kPanel + r * 128;
+        uint8_t* xs_row = xs_tile + r * 128;
+        if (len < kChunk) wait(&bars->full_b, par);
+        if (live) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int at = (q ^ (r & 7)) << 4;
+                float x[8];
+                to_floats<__nv_bfloat16, 8>(*reinterpret_cast<const uint4*>(x_row + at), x);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float u = x[2 * z] * weight, v = x[2 * z + 1] * weight;
+                    float f[2];
+                    hi[z] = pack_bf16(u, v);
+                    unpack_bf16(hi[z], f);
+                    lo[z] = pack_bf16(u - f[0], v - f[1]);
+                }
+                *reinterpret_cast<uint4*>(xs_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(xs_row + K::kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        } else {
+            // rows behind the request's last: another's, or nobody's; zeros, for a weight of zero does not stop a NaN
+            const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                *reinterpret_cast<uint4*>(x_row + 16 * q) = none;
+                *reinterpret_cast<uint4*>(xs_row + 16 * q) = none;
+                *reinterpret_cast<uint4*>(xs_row + K::kPanel + 16 * q) = none;
+#pragma unroll
+                for (int p = 0; p < N / 64; ++p) *reinterpret_cast<uint4*>(smem + K::kB + p * K::kPanel + r * 128 + 16 * q) = none;
+            }
+        }
+        tc::fence_proxy_async();
+        arrive(&bars->xs[s]);
+
+        if constexpr (!ENDS) {
+            slice_sync(s);                                         // the columns' exponents
+            // ---- M
+            wait(&bars->gram, par);
+            tc::tc_fence_after();
+            const float* col = bars->col[par][s];
+            float base = head;                                     // decay from the end of block b to this row
+            for (int b = warp; b >= 0; --b) {
+                uint32_t g[32], m[16];
+                tc::tmem_ld32(t_gram + 32 * b, g);
+                tc::tmem_wait_ld();
+                tc::pin32(g);
+                if (b == warp) {                                   // the diagonal block: columns are the warp's own rows
+                    const float mine = log_dt - head;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float e0 = head + __shfl_sync(~0u, mine, i), e1 = head + __shfl_sync(~0u, mine, i + 1);
+                        const float v0 = i > lane ? 0.f : exp2_fast(e0) * __uint_as_float(g[i]);
+                        const float v1 = i + 1 > lane ? 0.f : exp2_fast(e1) * __uint_as_float(g[i + 1]);
+                        m[i / 2] = pack_bf16(v0, v1);
+                    }
+                } else {
+                    if (b + 1 < warp) base += bars->total[par][s][b + 1];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 e = *reinterpret_cast<const float4*>(col + 32 * b + i);
+                        m[i / 2] = pack_bf16(exp2_fast(base + e.x) * __uint_as_float(g[i]), exp2_fast(base + e.y) * __uint_as_float(g[i + 1]));
+                        m[i / 2 + 1] = pack_bf16(exp2_fast(base + e.z) * __uint_as_float(g[i + 2]), exp2_fast(base + e.w) * __uint_as_float(g[i + 3]));
+                    }
+                }
+                tc::tmem_st16u_nowait(t_m + 16 * b, m);
+            }
+            // ---- Y = 2^G C S + D x; the product M X is added to it
+            const float grow = exp2_fast(G);
+            wait(&bars->y_first[s], par);
+            tc::tc_fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t y[32];
+                tc::tmem_ld32(t_y + 32 * half, y);
+                tc::tmem_wait_ld();
+                tc::pin32(y);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float x[8];
+                    to_floats<__nv_bfloat16, 8>(*reinterpret_cast<const uint4*>(x_row + (((4 * half + q) ^ (r & 7)) << 4)), x);
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) y[8 * q + z] = __float_as_uint(fmaf(__uint_as_float(y[8 * q + z]), grow, D * x[z]));
+                }
+                tc::tmem_st32(t_y + 32 * half, y);
+            }
+            tc::tmem_wait_st();
+            arrive(&bars->ready[s]);
+        }
+        // ---- S = gamma S + dS
+        wait(&bars->ds[s], par);
+        tc::tc_fence_after();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t d[32];
+            tc::tmem_ld32(t_ds + 32 * half, d);
+            tc::tmem_wait_ld();
+            tc::pin32(d);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[32 * half + i] = fmaf(gamma, S[32 * half + i], __uint_as_float(d[i]));
+        }
+        if constexpr (!ENDS) {
+            store_s();
+            // ---- results
+            wait(&bars->y_full[s][par], (c >> 1) & 1);
+            tc::tc_fence_after();
+            uint32_t y[64];
+            tc::tmem_ld32(t_y, y);
+            tc::tmem_ld32(t_y + 32, y + 32);
+            tc::tmem_wait_ld();
+            tc::pin32(y);
+            tc::pin32(y + 32);
+            arrive(&bars->next[s]);
+            if (live) {
+                TOut* out = reinterpret_cast<TOut*>(a.out) + ((t_row + c * kChunk) * a.H + h) * a.P + w.channel[s];
+                constexpr int E = 16 / (int)sizeof(TOut);
+#pragma unroll
+                for (int i = 0; i < kSlice; i += E) {
+                    float f[E];
+#pragma unroll
+                    for (int z = 0; z < E; ++z) f[z] = __uint_as_float(y[i + z]);
+                    store_raw<TOut, E>(out + i, from_floats<TOut, E>(f));
+                }
+            }
+        }
+    }
+    if (ENDS) {
+        if (own) {
+            float* to = plan.states + (w.seg.base + w.seg.k + 1) * all + tile;
+#pragma unroll
+            for (int i = 0; i < kSlice; ++i) to[(int64_t)i * N] = S[i];
+        }
+        if (r == 0 && w.channel[s] == 0) plan.decays[(int64_t)(w.seg.base + w.seg.k + 1) * a.H + h] = all_steps;
+    } else if (w.seg.k == w.seg.count - 1 && own) {
+        float* to = a.pool + w.seg.slot * all + tile;
+#pragma unroll
+        for (int i = 0; i < kSlice; ++i) to[(int64_t)i * N] = S[i];
+    }
+    return !bad;
+}
+
+// blockIdx.x: (segment, slice pair); one CTA more gives zeros to rows of no request.
+template <int N, bool ENDS, typename TOut>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    ssm_chunk_kernel(const SsmCall a, const Plan plan, const __grid_constant__ CUtensorMap xm, const __grid_constant__ CUtensorMap bm,
+                     const __grid_constant__ CUtensorMap cm)
+{
+    using K = TcCfg<N>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    TcBars* bars = reinterpret_cast<TcBars*>(smem + K::kEnd);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t place = blockIdx.x / plan.pairs, pair = blockIdx.x % plan.pairs;
+    TOut* out = reinterpret_cast<TOut*>(a.out);
+    if (!ENDS && blockIdx.x == gridDim.x - 1) {
+        ssm_clear_unowned<TOut>(a, tid, kTcThreads);
+        return;
+    }
+    if (place >= *plan.found) return;
+    TcWork w;
+    w.seg = plan.segments[place];
+    if (ENDS && w.seg.k + 1 >= w.seg.count) return;              // nothing starts from a last segment's state
+    const int per_head = a.P / kSlice, hpg = a.H / a.G;
+    w.g = pair / plan.pairs_per_group;
+    const int first = (pair % plan.pairs_per_group) * 2;        // slice of the group
+    w.slices = hpg * per_head - first < 2 ? 1 : 2;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        w.head[s] = w.g * hpg + (first + s) / per_head;
+        w.channel[s] = (first + s) % per_head * kSlice;
+    }
+    w.chunks = (w.seg.len + kChunk - 1) / kChunk;
+    if (w.seg.slot < 0) {                                         // padding
+        for (int s = 0; s < w.slices; ++s)
+            for (int64_t i = tid; i < (int64_t)w.seg.len * kSlice; i += kTcThreads)
+                out[((w.seg.first + i / kSlice) * a.H + w.head[s]) * a.P + w.channel[s] + i % kSlice] = from_f32<TOut>(0.f);
+        return;
+    }
+    if (tc::smem_u32(smem) & 1023u) {                             // the swizzled tiles want whole kilobytes
+        if (tid == 0) record_layer_error(kDevErrTimeout);
+        return;
+    }
+    if (warp == 0) {
+        if (lane == 0) {
+            tc::mbar_init(&bars->full_c, 1);
+            tc::mbar_init(&bars->full_b, 1);
+            tc::mbar_init(&bars->gram, 1);
+            tc::mbar_init(&bars->drain, 1);
+            for (int s = 0; s < 2; ++s) {
+                tc::mbar_init(&bars->y_first[s], 1);
+                tc::mbar_init(&bars->ds[s], 1);
+                tc::mbar_init(&bars->next[s], 4);
+                tc::mbar_init(&bars->xs[s], 4);
+                tc::mbar_init(&bars->ready[s], 4);
+                for (int i = 0; i < 2; ++i) {
+                    tc::mbar_init(&bars->full_x[s][i], 1);
+                    tc::mbar_init(&bars->y_full[s][i], 1);
+                }
+            }
+            tc::fence_mbar_init();
+        }
+    } else if (warp == 8) {
+        tc::tmem_alloc(&bars->tmem, 512);
+        tc::tmem_relinquish();
+    }
+    if constexpr (N < 128) {                                      // the states that are not there: zero rows of dS
+        for (int i = tid; i < K::kPanel / 16; i += kTcThreads) reinterpret_cast<uint4*>(smem + K::kB + K::kPanel)[i] = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    bool ok = true;
+    if (warp < 8) {
+        if (warp / 4 < w.slices) ok = tc_slice<N, ENDS, TOut>(a, plan, w, smem, bars, tmem, warp / 4, tid & 127);
+    } else if (lane == 0) {
+        if (warp == 8) {
+            ok = tc_issue<N, ENDS>(w, tc::smem_u32(smem), bars, tmem);
+            tc::mma_commit(&bars->drain);                          // everything issued ends before the exit
+            ok = tc::mbar_wait(&bars->drain, 0, kPolls) && ok;
+        } else {
+            ok = tc_load<N, ENDS>(a, w, smem, bars, &xm, &bm, &cm);
+            if (!ok) {                                             // and the copies in flight land
+                for (uint32_t p = 0; p < 2; ++p) {
+                    tc::mbar_wait(&bars->full_c, p, 1u << 16);
+                    tc::mbar_wait(&bars->full_b, p, 1u << 16);
+                    for (int i = 0; i < 4; ++i) tc::mbar_wait(&bars->full_x[i / 2][i % 2], p, 1u << 16);
+                }
+            }
+        }
+    }
+    if (!ok) record_layer_error(kDevErrTimeout);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    __syncwarp();
+    if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+// The state before each segment: of the first the pool's, then S = decay S + (the segment's own).
+// blockIdx.x: (segment, head, 1024 states); only a request's first segment has work.
+__global__ void __launch_bounds__(256) ssm_chain_kernel(const SsmCall a, const Plan plan)
+{
+    const int per = a.P * a.N / 1024;
+    const int64_t bh = blockIdx.x / per;
+    const int32_t place = (int32_t)(bh / a.H), h = (int32_t)(bh - (int64_t)place * a.H);
+    if (place >= *plan.found) return;
+    const Segment seg = plan.segments[place];
+    if (seg.k != 0 || seg.count < 2) return;
+    const int64_t all = (int64_t)a.H * a.P * a.N, at = (int64_t)h * a.P * a.N + (blockIdx.x % per) * 1024 + threadIdx.x * 4;
+    float4 v = *reinterpret_cast<const float4*>(a.pool + seg.slot * all + at);
+    float* to = plan.states + seg.base * all + at;
+    *reinterpret_cast<float4*>(to) = v;
+    for (int k = 1; k < seg.count; ++k) {
+        to += all;
+        const float decay = exp2_fast(plan.decays[(int64_t)(seg.base + k) * a.H + h]);
+        const float4 e = *reinterpret_cast<const float4*>(to);
+        v = make_float4(fmaf(decay, v.x, e.x), fmaf(decay, v.y, e.y), fmaf(decay, v.z, e.z), fmaf(decay, v.w, e.w));
+        *reinterpret_cast<float4*>(to) = v;
+    }
+}
+
+}  // namespace ssm
+
+namespace {
+
+bool ssm_on_tensor_cores(const kda_ssm_params& p)
+{
+    return p.io_dtype == KDA_BF16 && (p.head_dim == 64 || p.head_dim == 128) && (p.state_dim == 64 || p.state_dim == 128);
+}
+
+struct SsmLayout {
+    ssm::Plan plan;
+    bool cut;                        // some request may have several segments
+    size_t segments, states, decays, total;
+};
+
+SsmLayout ssm_layout(const kda_ssm_params& p, int32_t n, int64_t T)
+{
+    SsmLayout w = {};
+    const int sms = sm_count(), per_head = p.head_dim / ssm::kSlice;
+    w.plan.pairs_per_group = (p.num_heads / p.num_groups * per_head + 1) / 2;
+    w.plan.pairs = w.plan.pairs_per_group * p.num_groups;
+    // segments so long that all of them, times the pairs, just fill the SMs; at least eight chunks
+    int64_t want = (T * w.plan.pairs + sms - 1) / sms;
+    if (want < 8 * ssm::kChunk) want = 8 * ssm::kChunk;
+    w.cut = T >= 2 * want;
+    w.plan.want = (int32_t)(want < (int64_t)1 << 30 ? want : (int64_t)1 << 30);
+    const int64_t more = T / w.plan.want;                          // a request of k > 1 segments has k * want tokens or more
+    w.plan.max_segments = (int32_t)(n + more);
+    auto round = [](size_t x) { return (x + 255) / 256 * 256; };
+    w.segments = 256;
+    w.states = w.segments + round(sizeof(ssm::Segment) * (size_t)w.plan.max_segments);
+    const size_t held = w.cut ? (size_t)more : 0;
+    w.decays = w.states + round(held * 4 * p.num_heads * p.head_dim * p.state_dim);
+    w.total = w.decays + round(held * 4 * p.num_heads);
+    return w;
+}
+
+cudaError_t ssm_map(CUtensorMap* m, const void* base, int64_t rows, int64_t width, int64_t stride)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tc::tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)ssm::kChunk};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int N, typename TOut>
+cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* workspace, cudaStream_t s)
+{
+    SsmLayout w = ssm_layout(p, a.n, a.T);
+    uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
+    w.plan.found = reinterpret_cast<int32_t*>(base);
+    w.plan.segments = reinterpret_cast<ssm::Segment*>(base + w.segments);
+    w.plan.states = reinterpret_cast<float*>(base + w.states);
+    w.plan.decays = reinterpret_cast<float*>(base + w.decays);
+    CUtensorMap xm, bm, cm;
+    cudaError_t e = ssm_map(&xm, a.x, a.T, (int64_t)a.H * a.P, a.x_stride);
+    if (e == cudaSuccess) e = ssm_map(&bm, a.B, a.T, (int64_t)a.G * a.N, a.b_stride);
+    if (e == cudaSuccess) e = ssm_map(&cm, a.C, a.T, (int64_t)a.G * a.N, a.c_stride);
+    if (e != cudaSuccess) return e;
+    constexpr int smem = ssm::TcCfg<N>::kSmem;
+    ssm::ssm_plan_kernel<<<1, 1024, 0, s>>>(a, w.plan);
+    const unsigned blocks = (unsigned)((int64_t)w.plan.max_segments * w.plan.pairs);
+    if (w.cut) {
+        e = cudaFuncSetAttribute(ssm::ssm_chunk_kernel<N, true, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ssm::ssm_chunk_kernel<N, true, TOut><<<blocks, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm);
+        ssm::ssm_chain_kernel<<<(unsigned)((int64_t)w.plan.max_segments * a.H * (a.P * a.N / 1024)), 256, 0, s>>>(a, w.plan);
+    }
+    e = cudaFuncSetAttribute(ssm::ssm_chunk_kernel<N, false, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ssm::ssm_chunk_kernel<N, false, TOut><<<blocks + 1, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t ssm_workspace_bytes(const kda_ssm_params& p, int32_t num_seqs, int64_t total_tokens)
+{
+    return ssm_on_tensor_cores(p) ? ssm_layout(p, num_seqs, total_tokens).total : 0;
+}
+
+cudaError_t launch_ssm_prefill(const kda_ssm_params& p, const SsmCall& a, void* workspace, cudaStream_t s)
+{
+    if (!ssm_on_tensor_cores(p)) return ssm_dispatch<false>(p, a, s);
+    if (p.state_dim == 64)
+        return p.out_dtype == KDA_BF16 ? ssm_tc_launch<64, __nv_bfloat16>(p, a, workspace, s) : ssm_tc_launch<64, float>(p, a, workspace, s);
+    return p.out_dtype == KDA_BF16 ? ssm_tc_launch<128, __nv_bfloat16>(p, a, workspace, s) : ssm_tc_launch<128, float>(p, a, workspace, s);
+}
+
+}  // namespace kda

@@ -11,7 +11,9 @@
 // advances by 256 bytes per step.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <stdint.h>
 
 namespace kda {
@@ -82,6 +84,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Matrix descriptor of a 128-byte-swizzled operand: 8 rows of 128 bytes make an atom, `sbo` the distance of
+// atoms along the strided dimension, `lbo` (MN-major only) that of 64-element panels.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
 // ---- mbarriers ----------------------------------------------------------------------------------
@@ -312,6 +321,38 @@ __device__ __forceinline__ void tmem_st8u_nowait(uint32_t taddr, const uint32_t*
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+#define KDA_X8(p, i) p(r[i]), p(r[i + 1]), p(r[i + 2]), p(r[i + 3]), p(r[i + 4]), p(r[i + 5]), p(r[i + 6]), p(r[i + 7])
+#define KDA_OUT(x) "=r"(x)
+#define KDA_IN(x) "r"(x)
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : KDA_X8(KDA_OUT, 0), KDA_X8(KDA_OUT, 8), KDA_X8(KDA_OUT, 16), KDA_X8(KDA_OUT, 24)
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        KDA_X8(KDA_IN, 0), KDA_X8(KDA_IN, 8), KDA_X8(KDA_IN, 16), KDA_X8(KDA_IN, 24)
+        : "memory");
+}
+// Waits for the loads; the empty statements keep every use of their registers after the wait.
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+#define KDA_BOTH(x) "+r"(x)
+__device__ __forceinline__ void pin32(uint32_t* r)
+{
+    asm volatile("" : KDA_X8(KDA_BOTH, 0), KDA_X8(KDA_BOTH, 8), KDA_X8(KDA_BOTH, 16), KDA_X8(KDA_BOTH, 24)::"memory");
+}
+#undef KDA_X8
+#undef KDA_OUT
+#undef KDA_IN
+#undef KDA_BOTH
+
 // Eight fp32 values rounded to fp16 (nearest even) as one 16-byte vector, element i at bytes 2i.
 __device__ __forceinline__ uint4 pack8_f16(const float* x)
 {
@@ -324,6 +365,19 @@ __device__ __forceinline__ void unpack_f16x2(uint32_t p, float& lo, float& hi)
     asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
         : "=f"(lo), "=f"(hi)
         : "r"(p));
+}
+
+// The driver's tensor-map encoder, looked up once; null where it is missing.
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess || r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
 }
 
 }  // namespace tc

@@ -134,7 +134,9 @@ def ssm_inputs(seed, lens, H, P, N, G, dtype, dt_dtype=F32, strided=False, big_s
 # Bounds of the recurrence in fp32: a step adds at most 6 half steps to a state (decay's own error 3, the product,
 # the sum, dt's share), a result's sum N + 2 half steps and dt x B's own error some 8, all of the sums of magnitudes.
 # On the tensor-core form (bf16 inputs, dims of 64 or 128, states of 64 or 128) a state's increments are products of
-# halves of 16 bits together, 2^-16, and the factors of a result are rounded to bf16 once, 2^-8, of the magnitudes.
+# halves of 16 bits together, 2^-16, and the factors of a result are rounded to bf16 once, 2^-8, of the magnitudes; an
+# exponent inside 32 tokens is the difference of two sums of up to 32 steps of at most 128 each: six additions of half
+# a step of 4096, 6 * 2^-13, twice, 1.5e-3 or 1.0e-3 of a factor (times ln 2).
 
 def on_tensor_cores(dtype, P, N):
     return dtype is BF16 and P in (64, 128) and N in (64, 128)
@@ -142,7 +144,7 @@ def on_tensor_cores(dtype, P, N):
 
 def ssm_bounds(want, y_mag, mags, longest, N, out, tc):
     tau = (6 * longest + N + 16) * ref.F32
-    b = (tau + (ref.half_step(BF16) if tc else 0)) * y_mag
+    b = (tau + (ref.half_step(BF16) + 2.0 ** -9.9 if tc else 0)) * y_mag
     return b + ref.half_step(out) * (want.abs() + b) + 1e-40, (tau + (2.0 ** -16 if tc else 0)) * mags + 1e-40
 
 
@@ -179,6 +181,22 @@ def test_ssm_decode(H, P, N, G, dtype, out, batch):
     want, state, y_mag, mags = ref.ssm(x, dt, B, C, A_log, pool, slots, [1] * batch, dt_bias, D)
     got = kda.ssm_decode(x, dt, B, C, A_log, pool, idx(slots), dt_bias=dt_bias, D=D, out_dtype=out)
     yb, sb = ssm_bounds(want, y_mag, mags, 1, N, out, False)
+    ref.within(got, want, yb)
+    ref.within(pool, state, sb)
+
+
+@pytest.mark.parametrize("lens", [[2300], [700, 3333, 0, 1, 2048, 4100]], ids=str)
+@pytest.mark.parametrize("H,P,N,G", [(3, 64, 128, 1), (1, 128, 64, 1)])
+def test_ssm_requests_in_segments(lens, H, P, N, G):
+    """Long requests of few heads are cut into segments that start from chained states; the pool is updated in place."""
+    x, dt, B, C, A_log, dt_bias, D = ssm_inputs(20, lens, H, P, N, G, BF16)
+    A_log = A_log - 3                                       # states that last over thousands of tokens
+    slots = [len(lens) - i for i in range(len(lens))]
+    pool = normal(gen(21), len(lens) + 2, H, P, N)
+    want, state, y_mag, mags = ref.ssm(x, dt, B, C, A_log, pool, slots, lens, dt_bias, D)
+    kda.ssm_prefill(x, dt, B, C, A_log, ref.lengths_to_cu(lens, DEV), pool.clone(), idx(slots), dt_bias=dt_bias, D=D)
+    got = kda.ssm_prefill(x, dt, B, C, A_log, ref.lengths_to_cu(lens, DEV), pool, idx(slots), dt_bias=dt_bias, D=D)
+    yb, sb = ssm_bounds(want, y_mag, mags, max(lens), N, BF16, True)
     ref.within(got, want, yb)
     ref.within(pool, state, sb)
 
