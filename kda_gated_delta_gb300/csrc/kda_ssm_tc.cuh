@@ -22,9 +22,9 @@
 // the states would be off by 2e-3.  S itself stays in fp32 registers from a segment's first chunk to its last.
 //
 // A CTA takes the tokens of one request (or a segment of them) for two slices of 64 channels of x that share B
-// and C: two heads of 64 channels or the halves of one of 128.  One warpgroup per slice, thread = token row, and
-// for the state thread = state index.  All 512 tensor-memory columns: Gram 128, and per slice M 64, Y 64, dS 64.
-// Warp 8 issues the products, warp 9 the tensor-map copies.
+// and C: two heads of 64 channels or the halves of one of 128.  A slice has two warpgroups, one for its results (M, Y)
+// and one for its state (X', S), thread = token row, and for S thread = state index.  All 512 tensor-memory columns:
+// Gram 128, and per slice M 64, Y 64, dS 64.  Warp 16 issues the products, warp 17 the tensor-map copies.
 //
 // Long requests are cut into segments when there are fewer (request, slice pair) than SMs: a first pass
 // computes each segment's own state from zero (dS only), a small kernel chains them, and every segment then
@@ -43,7 +43,13 @@ namespace ssm {
 
 constexpr int kChunk = 128;
 constexpr int kSlice = 64;                       // channels of a slice
-constexpr int kTcThreads = 320;
+// tensor-memory columns; Y and dS of the two slices side by side, so that one product makes both
+constexpr uint32_t kGramCol = 0, kMCol = 128, kYCol = 256, kDsCol = 384;
+constexpr int kTcThreads = 640;                  // state, results of two slices: 4 warps each; products, copies, two idle
+// Registers: 96 a thread at launch; the state's groups take 120 (64 of them S), the last gives 48 back:
+// 256 * 120 + 256 * 96 + 128 * 48 = 640 * 96.
+template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 constexpr uint32_t kPolls = 1u << 24;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFarStep = -128.f;               // log2 of a step's decay, bounded: 2^-128 leaves nothing either way
@@ -130,22 +136,25 @@ struct TcCfg {
     static constexpr int kPanel = kChunk * 128;                 // 64 columns of 128 rows
     static constexpr int kSteps = N / 16;                       // products along the states
     static constexpr int kC = 0, kB = 2 * kPanel, kX = 4 * kPanel;       // X: [slice][buffer]
-    static constexpr int kXs = 8 * kPanel;                      // X': [slice][high, low]
+    static constexpr int kXs = 8 * kPanel;                      // X': [high, low][slice]
     static constexpr int kS = 12 * kPanel;                      // S: [slice]
     static constexpr int kEnd = 14 * kPanel;
     static constexpr int kSmem = kEnd + 3072;
 };
 
 struct __align__(16) TcBars {
-    uint64_t full_c, full_b, full_x[2][2];
-    uint64_t gram, y_first[2], ds[2], y_full[2][2];             // products done
-    uint64_t next[2], xs[2], ready[2];                          // a slice's operands written
+    uint64_t full_c, full_b, full_x[2];
+    uint64_t gram, y_first, ds, y_full[2];                      // products done
     uint64_t drain;
+    // what a warp each of all slices arrives at:
+    uint64_t next_s, next_y, xs, ready;                         // S written, Y read, X' written, M and Y written
+    uint64_t x_free[2];                                         // an X tile is no longer needed
     uint32_t tmem;
-    float total[2][2][4], tail[2][2][4];                        // [parity][slice][warp]: sums of the warps' steps
-    __align__(16) float col[2][2][kChunk];                                    // [parity][slice]: log2 of dt_j and the decay to its block's end
+    float total[2][2][4], tail[2][2][4];                        // [parity][slice][warp]: sums of the blocks' steps
+    __align__(16) float col[2][kChunk];                         // [slice]: dt_j times the decay from j to its block's end
+    __align__(16) float diag[2][kChunk];                        // [slice]: log2 dt_j less the steps of its block up to j
 };
-static_assert(sizeof(TcBars) <= 3072 && offsetof(TcBars, col) % 16 == 0, "barrier block; columns are read by 16 bytes");
+static_assert(sizeof(TcBars) <= 3072 && offsetof(TcBars, col) % 16 == 0 && offsetof(TcBars, diag) % 16 == 0, "barrier block; columns are read by 16 bytes");
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -153,9 +162,33 @@ __device__ __forceinline__ float exp2_fast(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// Barriers of a slice's warpgroup; the second also tells all whether any of them gave a true flag.
-__device__ __forceinline__ void slice_sync(int s) { asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory"); }
-__device__ __forceinline__ bool slice_any(int s, bool flag)
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+// Barriers of a warpgroup; the second also tells all whether any of them gave a true flag.
+__device__ __forceinline__ void slice_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool slice_any(int id, bool flag)
 {
     uint32_t r;
     asm volatile(
@@ -164,7 +197,7 @@ __device__ __forceinline__ bool slice_any(int s, bool flag)
         "bar.red.or.pred po, %2, 128, pi;\n\t"
         "selp.u32 %0, 1, 0, po;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)flag), "r"(1 + s)
+        : "r"((uint32_t)flag), "r"(id)
         : "memory");
     return r != 0;
 }
@@ -178,18 +211,29 @@ struct TcWork {
     Segment seg;
     int chunks, slices;
     int g;
-    int head[2], channel[2];                                     // of each slice: its head, its first channel there
+    int first, halves;                                            // first slice of the pair; 1: two slices make a head
+    int head0;                                                    // of the group
+    __device__ __forceinline__ int head(int s) const { return head0 + ((first + s) >> halves); }
+    __device__ __forceinline__ int channel(int s) const { return ((first + s) & halves) * kSlice; }
 };
 
-// One lane issues the products of all chunks, in the order of their operands.
-template <int N, bool ENDS>
-__device__ bool tc_issue(const TcWork& w, uint32_t smem, TcBars* bars, uint32_t tmem)
+// One warp issues the products of all chunks, in the order of their operands.  It runs as one, with uniform bounds and
+// addresses, so that the descriptors are uniform registers; only the products themselves are one lane's.  (One lane
+// alone takes 100 to 170 cycles a product, most of them for its addresses.)
+template <int N, bool ENDS, int SLICES>
+__device__ bool tc_issue(const int chunks_, uint32_t smem_, TcBars* bars, uint32_t tmem_, const bool leader)
 {
     using K = TcCfg<N>;
-    constexpr uint32_t id_gram = idesc_bf16(128, false, false), id_y = idesc_bf16(64, false, true), id_ds = idesc_bf16(64, true, true);
+    constexpr uint32_t id_gram = idesc_bf16(128, false, false), id_y = idesc_bf16(64 * SLICES, false, true);
+    constexpr uint32_t id_ds = idesc_bf16(64 * SLICES, true, true), id_mx = idesc_bf16(64, false, true);
+    constexpr uint32_t kTile = K::kPanel >> 4;                       // descriptors count in units of 16 bytes
+    const int chunks = (int)__reduce_max_sync(~0u, (unsigned)chunks_);
+    const uint32_t tmem = __reduce_max_sync(~0u, tmem_), smem = __reduce_max_sync(~0u, smem_);
     const uint64_t c_k = tc::desc_sw128(smem + K::kC, 16, 1024), b_k = tc::desc_sw128(smem + K::kB, 16, 1024);
-    const uint64_t b_mn = tc::desc_sw128(smem + K::kB, K::kPanel, 1024);
-    for (int c = 0; c < w.chunks; ++c) {
+    const uint64_t b_mn = tc::desc_sw128(smem + K::kB, K::kPanel, 1024), s_mn = tc::desc_sw128(smem + K::kS, K::kPanel, 1024);
+    const uint64_t xs_mn = tc::desc_sw128(smem + K::kXs, K::kPanel, 1024), x_mn = tc::desc_sw128(smem + K::kX, K::kPanel, 1024);
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
         const uint32_t par = c & 1;
         if constexpr (!ENDS) {
             if (!tc::mbar_wait(&bars->full_c, par, kPolls)) return false;
@@ -197,43 +241,43 @@ __device__ bool tc_issue(const TcWork& w, uint32_t smem, TcBars* bars, uint32_t 
         if (!tc::mbar_wait(&bars->full_b, par, kPolls)) return false;
         tc::tc_fence_after();
         if constexpr (!ENDS) {
-#pragma unroll
-            for (int k = 0; k < K::kSteps; ++k) {
-                const uint32_t off = ((k / 4) * K::kPanel + (k % 4) * 32) >> 4;
-                tc::mma_f16_ss(tmem, c_k + off, b_k + off, id_gram, k > 0);
-            }
-            tc::mma_commit(&bars->gram);
-            for (int s = 0; s < w.slices; ++s) {
-                if (!tc::mbar_wait(&bars->next[s], par, kPolls)) return false;
-                tc::tc_fence_after();
-                const uint64_t sb = tc::desc_sw128(smem + K::kS + s * K::kPanel, K::kPanel, 1024);
+            if (leader) {
 #pragma unroll
                 for (int k = 0; k < K::kSteps; ++k) {
-                    const uint32_t off = ((k / 4) * K::kPanel + (k % 4) * 32) >> 4;
-                    tc::mma_f16_ss(tmem + 128 + 192 * s + 64, c_k + off, sb + (k * 2048 >> 4), id_y, k > 0);
+                    const uint32_t off = (k / 4) * kTile + (k % 4) * 2;
+                    tc::mma_f16_ss(tmem + kGramCol, c_k + off, b_k + off, id_gram, k > 0);
                 }
-                tc::mma_commit(&bars->y_first[s]);
+                tc::mma_commit(&bars->gram);
+            }
+            if (!tc::mbar_wait(&bars->next_s, par, kPolls)) return false;
+            if (c > 0 && !tc::mbar_wait(&bars->next_y, par ^ 1, kPolls)) return false;
+            tc::tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < K::kSteps; ++k)
+                    tc::mma_f16_ss(tmem + kYCol, c_k + ((k / 4) * kTile + (k % 4) * 2), s_mn + k * 128, id_y, k > 0);
+                tc::mma_commit(&bars->y_first);
             }
         }
-        for (int s = 0; s < w.slices; ++s) {
-            if (!tc::mbar_wait(&bars->xs[s], par, kPolls)) return false;
-            tc::tc_fence_after();
-            const uint64_t xs = tc::desc_sw128(smem + K::kXs + 2 * s * K::kPanel, K::kPanel, 1024);
+        if (!tc::mbar_wait(&bars->xs, par, kPolls)) return false;
+        tc::tc_fence_after();
+        if (leader) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)                              // eight steps with the high parts, eight with the low
-                tc::mma_f16_ss(tmem + 128 + 192 * s + 128, b_mn + ((k % 8) * 2048 >> 4), xs + (((k / 8) * K::kPanel + (k % 8) * 2048) >> 4), id_ds,
-                               k > 0);
-            tc::mma_commit(&bars->ds[s]);
+                tc::mma_f16_ss(tmem + kDsCol, b_mn + (k % 8) * 128, xs_mn + (k / 8) * 2 * kTile + (k % 8) * 128, id_ds, k > 0);
+            tc::mma_commit(&bars->ds);
         }
         if constexpr (!ENDS) {
-            for (int s = 0; s < w.slices; ++s) {
-                if (!tc::mbar_wait(&bars->ready[s], par, kPolls)) return false;
-                tc::tc_fence_after();
-                const uint64_t x = tc::desc_sw128(smem + K::kX + (2 * s + par) * K::kPanel, K::kPanel, 1024);
+            if (!tc::mbar_wait(&bars->ready, par, kPolls)) return false;
+            tc::tc_fence_after();
+            if (leader) {
+                const uint64_t x = x_mn + par * kTile;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    tc::mma_f16_ts(tmem + 128 + 192 * s + 64, tmem + 128 + 192 * s + 8 * k, x + (k * 2048 >> 4), id_y, 1);
-                tc::mma_commit(&bars->y_full[s][par]);
+#pragma unroll
+                    for (int s = 0; s < SLICES; ++s)                  // the two slices' sums in turn
+                        tc::mma_f16_ts(tmem + kYCol + 64 * s, tmem + kMCol + 64 * s + 8 * k, x + 2 * s * kTile + k * 128, id_mx, 1);
+                tc::mma_commit(&bars->y_full[par]);
             }
         }
     }
@@ -251,10 +295,9 @@ __device__ bool tc_load(const SsmCall& a, const TcWork& w, uint8_t* smem, TcBars
         const int32_t t = w.seg.first + c * kChunk;
         const uint32_t par = c & 1;
         auto load_x = [&]() {
-            for (int s = 0; s < w.slices; ++s) {
-                tc::mbar_arrive_expect_tx(&bars->full_x[s][par], K::kPanel);
-                tc::tma_load_2d(smem + K::kX + (2 * s + par) * K::kPanel, xm, w.head[s] * a.P + w.channel[s], t, &bars->full_x[s][par]);
-            }
+            tc::mbar_arrive_expect_tx(&bars->full_x[par], K::kPanel * w.slices);
+            for (int s = 0; s < w.slices; ++s)
+                tc::tma_load_2d(smem + K::kX + (2 * s + par) * K::kPanel, xm, w.head(s) * a.P + w.channel(s), t, &bars->full_x[par]);
         };
         auto load_tile = [&](uint64_t* bar, int at, const CUtensorMap* m) {
             tc::mbar_arrive_expect_tx(bar, K::kPanel * (N / 64));
@@ -262,39 +305,87 @@ __device__ bool tc_load(const SsmCall& a, const TcWork& w, uint8_t* smem, TcBars
             for (int p = 0; p < N / 64; ++p) tc::tma_load_2d(smem + at + p * K::kPanel, m, w.g * N + 64 * p, t, bar);
         };
         if constexpr (ENDS) {
-            if (c > 0 && !tc::mbar_wait(&bars->ds[w.slices - 1], (c - 1) & 1, kPolls)) return false;
+            if (c > 0 && !tc::mbar_wait(&bars->ds, par ^ 1, kPolls)) return false;
             load_x();                                             // X' of the chunk before the last one is done, too
             load_tile(&bars->full_b, K::kB, bm);
         } else {
-            for (int s = 0; s < w.slices && c > 1; ++s)
-                if (!tc::mbar_wait(&bars->y_full[s][par], ((c >> 1) - 1) & 1, kPolls)) return false;
+            if (c > 1 && !tc::mbar_wait(&bars->x_free[par], ((c >> 1) - 1) & 1, kPolls)) return false;
             load_x();
-            if (c > 0 && !tc::mbar_wait(&bars->y_first[w.slices - 1], (c - 1) & 1, kPolls)) return false;
+            if (c > 0 && !tc::mbar_wait(&bars->y_first, par ^ 1, kPolls)) return false;
             load_tile(&bars->full_c, K::kC, cm);
-            if (c > 0 && !tc::mbar_wait(&bars->ds[w.slices - 1], (c - 1) & 1, kPolls)) return false;
+            if (c > 0 && !tc::mbar_wait(&bars->ds, par ^ 1, kPolls)) return false;
             load_tile(&bars->full_b, K::kB, bm);
         }
     }
     return true;
 }
 
-// One warpgroup: a slice's operands, state and results.  A wait that gave up leaves the loop at the next barrier of
-// the group, for all its threads at once.
-template <int N, bool ENDS, typename TOut>
-__device__ bool tc_slice(const SsmCall& a, const Plan& plan, const TcWork& w, uint8_t* smem, TcBars* bars, uint32_t tmem_base, int s, int r)
+// What the two warpgroups of a slice share: thread r is token row r of a chunk and state r.
+struct TcThread {
+    TcBars* bars;
+    int s, r, warp, lane, id;                                     // slice, row, its block of 32, barrier of the group
+    int h, channel;
+    uint32_t tmem;                                                // this warp's lanes
+    float rate, bias;
+    bool bad = false;                                             // a wait gave up
+
+    __device__ __forceinline__ TcThread(const SsmCall& a, const TcWork& w, TcBars* bars_, uint32_t tmem_base, int s_, int r_, int id_)
+        : bars(bars_), s(s_), r(r_), warp(r_ >> 5), lane(r_ & 31), id(id_), h(w.head(s_)), channel(w.channel(s_)),
+          tmem(tmem_base + ((uint32_t)(r_ & 96) << 16)), rate(expf(a.A_log[h]) * kLog2e), bias(a.dt_bias ? a.dt_bias[h] : 0.f)
+    {
+    }
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity)
+    {
+        if (!bad) bad = !tc::mbar_wait(bar, parity, kPolls);
+        __syncwarp();
+    }
+    __device__ __forceinline__ void arrive(uint64_t* bar) const
+    {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
+    }
+    __device__ __forceinline__ float raw_step(const SsmCall& a, const TcWork& w, int c) const
+    {
+        if (c * kChunk + r >= w.seg.len) return 0.f;
+        const int64_t i = ((int64_t)w.seg.first + c * kChunk + r) * a.dt_stride + h;
+        return a.dt_bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.dt)[i]) : reinterpret_cast<const float*>(a.dt)[i];
+    }
+};
+
+// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1, by the series of log(1 + e) = 2 artanh(e / (2 + e)), whose argument is at
+// most 1 / 3: the first term left out is below 2^-25 of the sum.
+__device__ __forceinline__ float softplus_series(float x, float threshold)
+{
+    const float e = exp2_fast(-fabsf(x) * kLog2e);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(2.0f + e));
+    const float u = e * r, q = u * u;
+    float p = fmaf(q, 1.f / 15, 1.f / 13);
+    p = fmaf(q, p, 1.f / 11);
+    p = fmaf(q, p, 1.f / 9);
+    p = fmaf(q, p, 1.f / 7);
+    p = fmaf(q, p, 1.f / 5);
+    p = fmaf(q, p, 1.f / 3);
+    p = fmaf(q, p, 1.f);
+    return x > threshold ? x : fmaf(2.f * u, p, fmaxf(x, 0.f));
+}
+
+// The warpgroup of a slice's state: X' and S.  A wait that gave up leaves the loop at the next barrier of the group, for
+// all its threads at once.
+template <int N, bool ENDS>
+__device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, uint8_t* smem, TcThread t)
 {
     using K = TcCfg<N>;
-    const int warp = r >> 5, lane = r & 31, h = w.head[s];
-    const uint32_t tmem = tmem_base + ((uint32_t)(r & 96) << 16);
-    const uint32_t t_gram = tmem, t_m = tmem + 128 + 192 * s, t_y = t_m + 64, t_ds = t_m + 128;
-    uint8_t* x_tile = smem + K::kX + 2 * s * K::kPanel;
-    uint8_t* xs_tile = smem + K::kXs + 2 * s * K::kPanel;
-    uint8_t* s_tile = smem + K::kS + s * K::kPanel;
-    const float rate = expf(a.A_log[h]) * kLog2e, bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
+    TcBars* bars = t.bars;
+    const int s = t.s, r = t.r, warp = t.warp, lane = t.lane;
+    const uint32_t t_ds = t.tmem + kDsCol + 64 * s;
+    uint8_t* xs_row = smem + K::kXs + s * K::kPanel + r * 128;
+    uint8_t* s_row = smem + K::kS + s * K::kPanel + r * 128;
 
-    // the state: this thread has S[r][0 .. 63] of the slice
+    // this thread has S[r][0 .. 63] of the slice
     float S[kSlice];
-    const int64_t tile = ((int64_t)h * a.P + w.channel[s]) * N + r, all = (int64_t)a.H * a.P * N;
+    const int64_t tile = ((int64_t)t.h * a.P + t.channel) * N + r, all = (int64_t)a.H * a.P * N;
     const bool own = r < N;
     if (ENDS) {
 #pragma unroll
@@ -307,167 +398,89 @@ __device__ bool tc_slice(const SsmCall& a, const Plan& plan, const TcWork& w, ui
     auto store_s = [&]() {                                        // S in bf16, as the product with C takes it
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(s_tile + r * 128 + ((c ^ (r & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(s_row + ((c ^ (r & 7)) << 4)) =
                 make_uint4(pack_bf16(S[8 * c], S[8 * c + 1]), pack_bf16(S[8 * c + 2], S[8 * c + 3]), pack_bf16(S[8 * c + 4], S[8 * c + 5]),
                            pack_bf16(S[8 * c + 6], S[8 * c + 7]));
         tc::fence_proxy_async();
     };
-    auto arrive = [&](uint64_t* bar) {
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar);
-    };
-    bool bad = false;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!bad) bad = !tc::mbar_wait(bar, parity, kPolls);
-        __syncwarp();
-    };
     if constexpr (!ENDS) {
         store_s();
-        const uint32_t zero[16] = {};
-        for (int b = warp + 1; b < 4; ++b) tc::tmem_st16u_nowait(t_m + 16 * b, zero);      // M above the diagonal stays zero
-        tc::tmem_wait_st();
-        arrive(&bars->next[s]);
+        t.arrive(&bars->next_s);
     }
-
-    const int64_t t_row = (int64_t)w.seg.first + r;
-    auto raw_step = [&](int c) -> float {
-        if (c * kChunk + r >= w.seg.len) return 0.f;
-        const int64_t i = (t_row + c * kChunk) * a.dt_stride + h;
-        return a.dt_bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.dt)[i]) : reinterpret_cast<const float*>(a.dt)[i];
-    };
-    float raw = raw_step(0), all_steps = 0.f;
+    float raw = t.raw_step(a, w, 0), all_steps = 0.f;
     for (int c = 0; c < w.chunks; ++c) {
         const uint32_t par = c & 1;
         const int len = w.seg.len - c * kChunk < kChunk ? w.seg.len - c * kChunk : kChunk;
         const bool live = r < len;
-        // ---- steps and decays: prefix sums for M, sums from the end for the state
-        const float dt = live ? softplus_f32(raw + bias, a.threshold) : 0.f;
-        if (c + 1 < w.chunks) raw = raw_step(c + 1);
-        const float l = live ? fmaxf(-dt * rate, kFarStep) : 0.f;
-        float head = l, tail = l;
+        // ---- steps from each token to the chunk's end
+        const float dt = live ? softplus_series(raw + t.bias, a.threshold) : 0.f;
+        if (c + 1 < w.chunks) raw = t.raw_step(a, w, c + 1);
+        float tail = live ? fmaxf(-dt * t.rate, kFarStep) : 0.f;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const float u = __shfl_up_sync(~0u, head, off), v = __shfl_down_sync(~0u, tail, off);
-            if (lane >= off) head += u;
+            const float v = __shfl_down_sync(~0u, tail, off);
             if (lane + off < 32) tail += v;
         }
-        if (lane == 31) bars->total[par][s][warp] = head;
         if (lane == 0) bars->tail[par][s][warp] = tail;
         tail = __shfl_down_sync(~0u, tail, 1);
         if (lane == 31) tail = 0.f;
-        if (slice_any(s, bad)) return false;
-        float G = head, whole = 0.f, after = 0.f;
+        if (slice_any(t.id, t.bad)) return false;
+        float whole = 0.f;
 #pragma unroll
         for (int i = 3; i >= 0; --i) {
-            const float f = bars->total[par][s][i];
-            if (i < warp) G += f;
+            const float f = bars->tail[par][s][i];
+            if (i > warp) tail += f;
             whole += f;
         }
-#pragma unroll
-        for (int i = 3; i > 0; --i)
-            if (i > warp) after += bars->tail[par][s][i];
-        const float weight = live ? dt * exp2_fast(tail + after) : 0.f;
+        const float weight = live ? dt * exp2_fast(tail) : 0.f;
         const float gamma = exp2_fast(whole);
         all_steps += whole;
-        const float log_dt = __log2f(dt);
-        if constexpr (!ENDS) bars->col[par][s][r] = tail + log_dt;
 
         // ---- X' = weight x, in two parts
-        wait(&bars->full_x[s][par], (c >> 1) & 1);
-        uint8_t* x_row = x_tile + par * K::kPanel + r * 128;
-        uint8_t* xs_row = xs_tile + r * 128;
-        if (len < kChunk) wait(&bars->full_b, par);
+        t.wait(&bars->full_x[par], (c >> 1) & 1);
+        uint8_t* x_row = smem + K::kX + (2 * s + par) * K::kPanel + r * 128;
+        if (len < kChunk) t.wait(&bars->full_b, par);
         if (live) {
-#pragma unroll
+            const uint64_t ww = pack2(weight, weight), minus = pack2(-1.f, -1.f);
+#pragma unroll 2
             for (int q = 0; q < 8; ++q) {
                 const int at = (q ^ (r & 7)) << 4;
-                float x[8];
-                to_floats<__nv_bfloat16, 8>(*reinterpret_cast<const uint4*>(x_row + at), x);
+                const uint4 raw_x = *reinterpret_cast<const uint4*>(x_row + at);
+                const uint32_t xw[4] = {raw_x.x, raw_x.y, raw_x.z, raw_x.w};
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
-                    const float u = x[2 * z] * weight, v = x[2 * z + 1] * weight;
                     float f[2];
-                    hi[z] = pack_bf16(u, v);
+                    unpack_bf16(xw[z], f);
+                    const uint64_t v = mul2(pack2(f[0], f[1]), ww);
+                    const float2 vf = unpack2(v);
+                    hi[z] = pack_bf16(vf.x, vf.y);
                     unpack_bf16(hi[z], f);
-                    lo[z] = pack_bf16(u - f[0], v - f[1]);
+                    const float2 rest = unpack2(fma2(pack2(f[0], f[1]), minus, v));
+                    lo[z] = pack_bf16(rest.x, rest.y);
                 }
                 *reinterpret_cast<uint4*>(xs_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(xs_row + K::kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                *reinterpret_cast<uint4*>(xs_row + 2 * K::kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         } else {
             // rows behind the request's last: another's, or nobody's; zeros, for a weight of zero does not stop a NaN
             const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int q = 0; q < 128; q += 16) {
+                *reinterpret_cast<uint4*>(x_row + q) = none;
+                *reinterpret_cast<uint4*>(xs_row + q) = none;
+                *reinterpret_cast<uint4*>(xs_row + 2 * K::kPanel + q) = none;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                *reinterpret_cast<uint4*>(x_row + 16 * q) = none;
-                *reinterpret_cast<uint4*>(xs_row + 16 * q) = none;
-                *reinterpret_cast<uint4*>(xs_row + K::kPanel + 16 * q) = none;
-#pragma unroll
-                for (int p = 0; p < N / 64; ++p) *reinterpret_cast<uint4*>(smem + K::kB + p * K::kPanel + r * 128 + 16 * q) = none;
+                for (int p = 0; p < N / 64; ++p) *reinterpret_cast<uint4*>(smem + K::kB + p * K::kPanel + r * 128 + q) = none;
             }
         }
         tc::fence_proxy_async();
-        arrive(&bars->xs[s]);
+        t.arrive(&bars->xs);
 
-        if constexpr (!ENDS) {
-            slice_sync(s);                                         // the columns' exponents
-            // ---- M
-            wait(&bars->gram, par);
-            tc::tc_fence_after();
-            const float* col = bars->col[par][s];
-            float base = head;                                     // decay from the end of block b to this row
-            for (int b = warp; b >= 0; --b) {
-                uint32_t g[32], m[16];
-                tc::tmem_ld32(t_gram + 32 * b, g);
-                tc::tmem_wait_ld();
-                tc::pin32(g);
-                if (b == warp) {                                   // the diagonal block: columns are the warp's own rows
-                    const float mine = log_dt - head;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float e0 = head + __shfl_sync(~0u, mine, i), e1 = head + __shfl_sync(~0u, mine, i + 1);
-                        const float v0 = i > lane ? 0.f : exp2_fast(e0) * __uint_as_float(g[i]);
-                        const float v1 = i + 1 > lane ? 0.f : exp2_fast(e1) * __uint_as_float(g[i + 1]);
-                        m[i / 2] = pack_bf16(v0, v1);
-                    }
-                } else {
-                    if (b + 1 < warp) base += bars->total[par][s][b + 1];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 e = *reinterpret_cast<const float4*>(col + 32 * b + i);
-                        m[i / 2] = pack_bf16(exp2_fast(base + e.x) * __uint_as_float(g[i]), exp2_fast(base + e.y) * __uint_as_float(g[i + 1]));
-                        m[i / 2 + 1] = pack_bf16(exp2_fast(base + e.z) * __uint_as_float(g[i + 2]), exp2_fast(base + e.w) * __uint_as_float(g[i + 3]));
-                    }
-                }
-                tc::tmem_st16u_nowait(t_m + 16 * b, m);
-            }
-            // ---- Y = 2^G C S + D x; the product M X is added to it
-            const float grow = exp2_fast(G);
-            wait(&bars->y_first[s], par);
-            tc::tc_fence_after();
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t y[32];
-                tc::tmem_ld32(t_y + 32 * half, y);
-                tc::tmem_wait_ld();
-                tc::pin32(y);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float x[8];
-                    to_floats<__nv_bfloat16, 8>(*reinterpret_cast<const uint4*>(x_row + (((4 * half + q) ^ (r & 7)) << 4)), x);
-#pragma unroll
-                    for (int z = 0; z < 8; ++z) y[8 * q + z] = __float_as_uint(fmaf(__uint_as_float(y[8 * q + z]), grow, D * x[z]));
-                }
-                tc::tmem_st32(t_y + 32 * half, y);
-            }
-            tc::tmem_wait_st();
-            arrive(&bars->ready[s]);
-        }
         // ---- S = gamma S + dS
-        wait(&bars->ds[s], par);
+        t.wait(&bars->ds, par);
         tc::tc_fence_after();
+        const uint64_t gg = pack2(gamma, gamma);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t d[32];
@@ -475,31 +488,17 @@ __device__ bool tc_slice(const SsmCall& a, const Plan& plan, const TcWork& w, ui
             tc::tmem_wait_ld();
             tc::pin32(d);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) S[32 * half + i] = fmaf(gamma, S[32 * half + i], __uint_as_float(d[i]));
+            for (int i = 0; i < 32; i += 2) {
+                float* e = &S[32 * half + i];
+                const float2 v = unpack2(fma2(pack2(e[0], e[1]), gg, pack2(__uint_as_float(d[i]), __uint_as_float(d[i + 1]))));
+                e[0] = v.x;
+                e[1] = v.y;
+            }
         }
         if constexpr (!ENDS) {
+            t.wait(&bars->y_first, par);                        // the product with the last S is done
             store_s();
-            // ---- results
-            wait(&bars->y_full[s][par], (c >> 1) & 1);
-            tc::tc_fence_after();
-            uint32_t y[64];
-            tc::tmem_ld32(t_y, y);
-            tc::tmem_ld32(t_y + 32, y + 32);
-            tc::tmem_wait_ld();
-            tc::pin32(y);
-            tc::pin32(y + 32);
-            arrive(&bars->next[s]);
-            if (live) {
-                TOut* out = reinterpret_cast<TOut*>(a.out) + ((t_row + c * kChunk) * a.H + h) * a.P + w.channel[s];
-                constexpr int E = 16 / (int)sizeof(TOut);
-#pragma unroll
-                for (int i = 0; i < kSlice; i += E) {
-                    float f[E];
-#pragma unroll
-                    for (int z = 0; z < E; ++z) f[z] = __uint_as_float(y[i + z]);
-                    store_raw<TOut, E>(out + i, from_floats<TOut, E>(f));
-                }
-            }
+            t.arrive(&bars->next_s);
         }
     }
     if (ENDS) {
@@ -508,13 +507,159 @@ __device__ bool tc_slice(const SsmCall& a, const Plan& plan, const TcWork& w, ui
 #pragma unroll
             for (int i = 0; i < kSlice; ++i) to[(int64_t)i * N] = S[i];
         }
-        if (r == 0 && w.channel[s] == 0) plan.decays[(int64_t)(w.seg.base + w.seg.k + 1) * a.H + h] = all_steps;
+        if (r == 0 && t.channel == 0) plan.decays[(int64_t)(w.seg.base + w.seg.k + 1) * a.H + t.h] = all_steps;
     } else if (w.seg.k == w.seg.count - 1 && own) {
         float* to = a.pool + w.seg.slot * all + tile;
 #pragma unroll
         for (int i = 0; i < kSlice; ++i) to[(int64_t)i * N] = S[i];
     }
-    return !bad;
+    return !t.bad;
+}
+
+// The warpgroup of a slice's results: M and Y.
+template <int N, typename TOut>
+__device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcThread t)
+{
+    using K = TcCfg<N>;
+    TcBars* bars = t.bars;
+    const int s = t.s, r = t.r, warp = t.warp, lane = t.lane;
+    const uint32_t t_gram = t.tmem + kGramCol, t_m = t.tmem + kMCol + 64 * s, t_y = t.tmem + kYCol + 64 * s;
+    const float D = a.D ? a.D[t.h] : 0.f;
+    const uint32_t zero[16] = {};
+    for (int b = warp + 1; b < 4; ++b) tc::tmem_st16u_nowait(t_m + 16 * b, zero);              // M above the diagonal stays zero
+    tc::tmem_wait_st();
+
+    float raw = t.raw_step(a, w, 0);
+    float head = 0.f, G = 0.f;                                     // steps of the block, of the chunk, up to this row
+    // prefix sums of a chunk's steps, and its columns' factors; false: a wait gave up
+    auto steps = [&](int c) -> bool {
+        const bool live = c * kChunk + r < w.seg.len;
+        const float dt = live ? softplus_series(raw + t.bias, a.threshold) : 0.f;
+        if (c + 1 < w.chunks) raw = t.raw_step(a, w, c + 1);
+        float tail = head = live ? fmaxf(-dt * t.rate, kFarStep) : 0.f;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float u = __shfl_up_sync(~0u, head, off), v = __shfl_down_sync(~0u, tail, off);
+            if (lane >= off) head += u;
+            if (lane + off < 32) tail += v;
+        }
+        if (lane == 31) bars->total[c & 1][s][warp] = head;
+        tail = __shfl_down_sync(~0u, tail, 1);
+        if (lane == 31) tail = 0.f;
+        if (slice_any(t.id, t.bad)) return false;                  // all warps are through with the last chunk's M
+        G = head;
+#pragma unroll
+        for (int i = 2; i >= 0; --i)
+            if (i < warp) G += bars->total[c & 1][s][i];
+        bars->col[s][r] = dt * exp2_fast(tail);
+        bars->diag[s][r] = __log2f(dt) - head;
+        return true;
+    };
+    if (!steps(0)) return false;
+    for (int c = 0; c < w.chunks; ++c) {
+        const uint32_t par = c & 1;
+        const int len = w.seg.len - c * kChunk < kChunk ? w.seg.len - c * kChunk : kChunk;
+        uint8_t* x_row = smem + K::kX + (2 * s + par) * K::kPanel + r * 128;
+        slice_sync(t.id);                                          // the columns' factors
+        // ---- M
+        t.wait(&bars->gram, par);
+        tc::tc_fence_after();
+        float base = head;                                         // steps from the end of block b to this row
+#pragma unroll 1
+        for (int b = 2 * warp + 1; b >= 0; --b) {                  // 16 columns at a time
+            float g[16];
+            uint32_t m[8];
+            const bool own = b >> 1 == warp;                       // the diagonal block
+            const float* col = (own ? bars->diag[s] : bars->col[s]) + 16 * b;
+            if ((b & 1) && b < 2 * warp - 1) base += bars->total[par][s][(b >> 1) + 1];
+            tc::tmem_ld16(t_gram + 16 * b, g);
+            if (own) {
+                const int past = lane - 16 * (b & 1);              // columns up to this one are seen
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 e = *reinterpret_cast<const float4*>(col + i);
+                    const float v0 = i > past ? 0.f : exp2_fast(head + e.x) * g[i];
+                    const float v1 = i + 1 > past ? 0.f : exp2_fast(head + e.y) * g[i + 1];
+                    const float v2 = i + 2 > past ? 0.f : exp2_fast(head + e.z) * g[i + 2];
+                    const float v3 = i + 3 > past ? 0.f : exp2_fast(head + e.w) * g[i + 3];
+                    m[i / 2] = pack_bf16(v0, v1);
+                    m[i / 2 + 1] = pack_bf16(v2, v3);
+                }
+            } else {                                               // two factors, neither above dt
+                const float row = exp2_fast(base);
+                const uint64_t rr = pack2(row, row);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(col + i);
+                    const float2 u = unpack2(mul2(mul2(e.x, rr), pack2(g[i], g[i + 1])));
+                    const float2 v = unpack2(mul2(mul2(e.y, rr), pack2(g[i + 2], g[i + 3])));
+                    m[i / 2] = pack_bf16(u.x, u.y);
+                    m[i / 2 + 1] = pack_bf16(v.x, v.y);
+                }
+            }
+            tc::tmem_st8u_nowait(t_m + 8 * b, m);
+        }
+        // ---- Y = 2^G C S + D x; the product M X is added to it
+        const float grow = exp2_fast(G);
+        t.wait(&bars->full_x[par], (c >> 1) & 1);
+        t.wait(&bars->y_first, par);
+        tc::tc_fence_after();
+        const uint64_t gg = pack2(grow, grow), dd = pack2(D, D);
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+            float y[16];
+            tc::tmem_ld16(t_y + 16 * x, y);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const uint4 raw_x = *reinterpret_cast<const uint4*>(x_row + (((2 * x + q) ^ (r & 7)) << 4));
+                const uint32_t xw[4] = {raw_x.x, raw_x.y, raw_x.z, raw_x.w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    float f[2], *e = y + 8 * q + 2 * z;
+                    unpack_bf16(xw[z], f);
+                    const float2 v = unpack2(fma2(pack2(e[0], e[1]), gg, mul2(pack2(f[0], f[1]), dd)));
+                    e[0] = v.x;
+                    e[1] = v.y;
+                }
+            }
+            tc::tmem_st16_nowait(t_y + 16 * x, y);
+        }
+        tc::tmem_wait_st();
+        t.arrive(&bars->ready);
+        if (c + 1 < w.chunks && !steps(c + 1)) return false;       // while the product runs
+        // ---- results
+        t.wait(&bars->y_full[par], (c >> 1) & 1);
+        tc::tc_fence_after();
+        // through the X tile's rows, which nobody needs any more, so that a warp writes whole lines
+        constexpr int E = 16 / (int)sizeof(TOut);
+        TOut* out = reinterpret_cast<TOut*>(a.out) + ((int64_t)(w.seg.first + c * kChunk + (r & 96)) * a.H + t.h) * a.P + t.channel + lane % 8 * E;
+        const uint8_t* warp_rows = x_row - lane * 128;
+        const int left = len - (r & 96);                           // rows of this warp that are the request's
+#pragma unroll 1
+        for (int part = 0; part < kSlice; part += 8 * E) {
+            if (part) __syncwarp();
+#pragma unroll 1
+            for (int x = 0; x < 8 * E; x += 16) {
+                float y[16];
+                tc::tmem_ld16(t_y + part + x, y);
+#pragma unroll
+                for (int q = 0; q < 16 / E; ++q)
+                    *reinterpret_cast<typename Vec<TOut, E>::Raw*>(x_row + (((x / E + q) ^ (r & 7)) << 4)) = from_floats<TOut, E>(y + E * q);
+            }
+            if (part + 8 * E >= kSlice) t.arrive(&bars->next_y);
+            __syncwarp();
+#pragma unroll 2
+            for (int i = 0; i < 32; i += 4) {
+                const int row = i + lane / 8;
+                if (row < left)
+                    *reinterpret_cast<uint4*>(out + (int64_t)row * a.H * a.P + part) =
+                        *reinterpret_cast<const uint4*>(warp_rows + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+            }
+        }
+        tc::fence_proxy_async();
+        t.arrive(&bars->x_free[par]);
+    }
+    return !t.bad;
 }
 
 // blockIdx.x: (segment, slice pair); one CTA more gives zeros to rows of no request.
@@ -539,18 +684,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (ENDS && w.seg.k + 1 >= w.seg.count) return;              // nothing starts from a last segment's state
     const int per_head = a.P / kSlice, hpg = a.H / a.G;
     w.g = pair / plan.pairs_per_group;
-    const int first = (pair % plan.pairs_per_group) * 2;        // slice of the group
-    w.slices = hpg * per_head - first < 2 ? 1 : 2;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        w.head[s] = w.g * hpg + (first + s) / per_head;
-        w.channel[s] = (first + s) % per_head * kSlice;
-    }
+    w.first = (pair % plan.pairs_per_group) * 2;
+    w.halves = per_head - 1;
+    w.head0 = w.g * hpg;
+    w.slices = hpg * per_head - w.first < 2 ? 1 : 2;
     w.chunks = (w.seg.len + kChunk - 1) / kChunk;
     if (w.seg.slot < 0) {                                         // padding
         for (int s = 0; s < w.slices; ++s)
             for (int64_t i = tid; i < (int64_t)w.seg.len * kSlice; i += kTcThreads)
-                out[((w.seg.first + i / kSlice) * a.H + w.head[s]) * a.P + w.channel[s] + i % kSlice] = from_f32<TOut>(0.f);
+                out[((w.seg.first + i / kSlice) * a.H + w.head(s)) * a.P + w.channel(s) + i % kSlice] = from_f32<TOut>(0.f);
         return;
     }
     if (tc::smem_u32(smem) & 1023u) {                             // the swizzled tiles want whole kilobytes
@@ -559,24 +701,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (warp == 0) {
         if (lane == 0) {
-            tc::mbar_init(&bars->full_c, 1);
-            tc::mbar_init(&bars->full_b, 1);
-            tc::mbar_init(&bars->gram, 1);
-            tc::mbar_init(&bars->drain, 1);
-            for (int s = 0; s < 2; ++s) {
-                tc::mbar_init(&bars->y_first[s], 1);
-                tc::mbar_init(&bars->ds[s], 1);
-                tc::mbar_init(&bars->next[s], 4);
-                tc::mbar_init(&bars->xs[s], 4);
-                tc::mbar_init(&bars->ready[s], 4);
-                for (int i = 0; i < 2; ++i) {
-                    tc::mbar_init(&bars->full_x[s][i], 1);
-                    tc::mbar_init(&bars->y_full[s][i], 1);
-                }
-            }
+            for (uint64_t* bar = &bars->full_c; bar <= &bars->drain; ++bar) tc::mbar_init(bar, 1);
+            for (uint64_t* bar = &bars->next_s; bar <= &bars->x_free[1]; ++bar) tc::mbar_init(bar, 4 * w.slices);
             tc::fence_mbar_init();
         }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         tc::tmem_alloc(&bars->tmem, 512);
         tc::tmem_relinquish();
     }
@@ -590,19 +719,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t tmem = bars->tmem;
     bool ok = true;
     if (warp < 8) {
-        if (warp / 4 < w.slices) ok = tc_slice<N, ENDS, TOut>(a, plan, w, smem, bars, tmem, warp / 4, tid & 127);
-    } else if (lane == 0) {
-        if (warp == 8) {
-            ok = tc_issue<N, ENDS>(w, tc::smem_u32(smem), bars, tmem);
-            tc::mma_commit(&bars->drain);                          // everything issued ends before the exit
+        const int s = warp / 4;
+        if (!ENDS && s < w.slices) ok = tc_results<N, TOut>(a, w, smem, TcThread(a, w, bars, tmem, s, tid & 127, 1 + s));
+    } else if (warp < 16) {
+        more_registers<120>();
+        const int s = warp / 4 - 2;
+        if (s < w.slices) ok = tc_state<N, ENDS>(a, plan, w, smem, TcThread(a, w, bars, tmem, s, tid & 127, 3 + s));
+    } else {
+        fewer_registers<48>();
+        if (warp == 16) {
+            uint32_t leader = 0;
+            asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+            ok = w.slices == 2 ? tc_issue<N, ENDS, 2>(w.chunks, tc::smem_u32(smem), bars, tmem, leader) : tc_issue<N, ENDS, 1>(w.chunks, tc::smem_u32(smem), bars, tmem, leader);
+            if (leader) tc::mma_commit(&bars->drain);             // everything issued ends before the exit
+            __syncwarp();
             ok = tc::mbar_wait(&bars->drain, 0, kPolls) && ok;
-        } else {
+        } else if (lane == 0 && warp == 17) {
             ok = tc_load<N, ENDS>(a, w, smem, bars, &xm, &bm, &cm);
             if (!ok) {                                             // and the copies in flight land
                 for (uint32_t p = 0; p < 2; ++p) {
                     tc::mbar_wait(&bars->full_c, p, 1u << 16);
                     tc::mbar_wait(&bars->full_b, p, 1u << 16);
-                    for (int i = 0; i < 4; ++i) tc::mbar_wait(&bars->full_x[i / 2][i % 2], p, 1u << 16);
+                    tc::mbar_wait(&bars->full_x[0], p, 1u << 16);
+                    tc::mbar_wait(&bars->full_x[1], p, 1u << 16);
                 }
             }
         }
@@ -612,7 +751,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     __syncwarp();
-    if (warp == 8) tc::tmem_dealloc(tmem, 512);
+    if (warp == 16) tc::tmem_dealloc(tmem, 512);
 }
 
 // The state before each segment: of the first the pool's, then S = decay S + (the segment's own).
