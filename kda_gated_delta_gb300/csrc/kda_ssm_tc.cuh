@@ -146,7 +146,7 @@ struct __align__(16) TcBars {
     uint64_t full_c, full_b, full_x[2];
     uint64_t gram, y_first, ds, y_full[2];                      // products done
     uint64_t drain;
-    // what a warp each of all slices arrives at:
+    // what each warp of the group concerned (M and Y: of both groups) arrives at, for all slices:
     uint64_t next_s, next_y, xs, ready;                         // S written, Y read, X' written, M and Y written
     uint64_t x_free[2];                                         // an X tile is no longer needed
     uint32_t tmem;
@@ -379,7 +379,8 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
     using K = TcCfg<N>;
     TcBars* bars = t.bars;
     const int s = t.s, r = t.r, warp = t.warp, lane = t.lane;
-    const uint32_t t_ds = t.tmem + kDsCol + 64 * s;
+    const uint32_t t_ds = t.tmem + kDsCol + 64 * s, t_y = t.tmem + kYCol + 64 * s;
+    const float D = a.D ? a.D[t.h] : 0.f;
     uint8_t* xs_row = smem + K::kXs + s * K::kPanel + r * 128;
     uint8_t* s_row = smem + K::kS + s * K::kPanel + r * 128;
 
@@ -408,41 +409,49 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         t.arrive(&bars->next_s);
     }
     float raw = t.raw_step(a, w, 0), all_steps = 0.f;
-    for (int c = 0; c < w.chunks; ++c) {
-        const uint32_t par = c & 1;
-        const int len = w.seg.len - c * kChunk < kChunk ? w.seg.len - c * kChunk : kChunk;
-        const bool live = r < len;
-        // ---- steps from each token to the chunk's end
+    float weight = 0.f, gamma = 0.f, grow = 0.f;                  // of this row's X', of the state, of this row's C S
+    // the steps from each token of a chunk to its end; false: a wait gave up
+    auto steps = [&](int c) -> bool {
+        const bool live = c * kChunk + r < w.seg.len;
         const float dt = live ? softplus_series(raw + t.bias, a.threshold) : 0.f;
         if (c + 1 < w.chunks) raw = t.raw_step(a, w, c + 1);
-        float tail = live ? fmaxf(-dt * t.rate, kFarStep) : 0.f;
+        float head = live ? fmaxf(-dt * t.rate, kFarStep) : 0.f, tail = head;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const float v = __shfl_down_sync(~0u, tail, off);
+            const float u = ENDS ? 0.f : __shfl_up_sync(~0u, head, off), v = __shfl_down_sync(~0u, tail, off);
+            if (lane >= off) head += u;
             if (lane + off < 32) tail += v;
         }
-        if (lane == 0) bars->tail[par][s][warp] = tail;
+        if (lane == 0) bars->tail[c & 1][s][warp] = tail;
         tail = __shfl_down_sync(~0u, tail, 1);
         if (lane == 31) tail = 0.f;
         if (slice_any(t.id, t.bad)) return false;
         float whole = 0.f;
 #pragma unroll
         for (int i = 3; i >= 0; --i) {
-            const float f = bars->tail[par][s][i];
+            const float f = bars->tail[c & 1][s][i];
             if (i > warp) tail += f;
+            if (i < warp) head += f;
             whole += f;
         }
-        const float weight = live ? dt * exp2_fast(tail) : 0.f;
-        const float gamma = exp2_fast(whole);
+        weight = live ? dt * exp2_fast(tail) : 0.f;
+        gamma = exp2_fast(whole);
+        grow = exp2_fast(head);
         all_steps += whole;
-
+        return true;
+    };
+    if (!steps(0)) return false;
+    for (int c = 0; c < w.chunks; ++c) {
+        const uint32_t par = c & 1;
+        const int len = w.seg.len - c * kChunk < kChunk ? w.seg.len - c * kChunk : kChunk;
+        const bool live = r < len;
         // ---- X' = weight x, in two parts
         t.wait(&bars->full_x[par], (c >> 1) & 1);
         uint8_t* x_row = smem + K::kX + (2 * s + par) * K::kPanel + r * 128;
         if (len < kChunk) t.wait(&bars->full_b, par);
         if (live) {
             const uint64_t ww = pack2(weight, weight), minus = pack2(-1.f, -1.f);
-#pragma unroll 2
+#pragma unroll 4
             for (int q = 0; q < 8; ++q) {
                 const int at = (q ^ (r & 7)) << 4;
                 const uint4 raw_x = *reinterpret_cast<const uint4*>(x_row + at);
@@ -477,10 +486,41 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         tc::fence_proxy_async();
         t.arrive(&bars->xs);
 
+        // ---- Y = 2^G C S + D x; the product M X is added to it
+        if constexpr (!ENDS) {
+            t.wait(&bars->y_first, par);
+            tc::tc_fence_after();
+            const uint64_t gg = pack2(grow, grow), dd = pack2(D, D);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                uint32_t y[32];
+                tc::tmem_ld32(t_y + 32 * half, y);
+                tc::tmem_wait_ld();
+                tc::pin32(y);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 raw_x = *reinterpret_cast<const uint4*>(x_row + (((4 * half + q) ^ (r & 7)) << 4));
+                    const uint32_t xw[4] = {raw_x.x, raw_x.y, raw_x.z, raw_x.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        float f[2];
+                        unpack_bf16(xw[z], f);
+                        uint32_t* e = y + 8 * q + 2 * z;
+                        const float2 v = unpack2(fma2(pack2(__uint_as_float(e[0]), __uint_as_float(e[1])), gg, mul2(pack2(f[0], f[1]), dd)));
+                        e[0] = __float_as_uint(v.x);
+                        e[1] = __float_as_uint(v.y);
+                    }
+                }
+                tc::tmem_st32(t_y + 32 * half, y);
+            }
+            tc::tmem_wait_st();
+            t.arrive(&bars->ready);
+        }
         // ---- S = gamma S + dS
+        const uint64_t gg = pack2(gamma, gamma);
+        if (c + 1 < w.chunks && !steps(c + 1)) return false;      // while the product runs
         t.wait(&bars->ds, par);
         tc::tc_fence_after();
-        const uint64_t gg = pack2(gamma, gamma);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t d[32];
@@ -496,8 +536,7 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
             }
         }
         if constexpr (!ENDS) {
-            t.wait(&bars->y_first, par);                        // the product with the last S is done
-            store_s();
+            store_s();                                             // (the product with the last S is done)
             t.arrive(&bars->next_s);
         }
     }
@@ -518,19 +557,18 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
 
 // The warpgroup of a slice's results: M and Y.
 template <int N, typename TOut>
-__device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcThread t)
+__device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcThread t, const CUtensorMap* om)
 {
     using K = TcCfg<N>;
     TcBars* bars = t.bars;
     const int s = t.s, r = t.r, warp = t.warp, lane = t.lane;
     const uint32_t t_gram = t.tmem + kGramCol, t_m = t.tmem + kMCol + 64 * s, t_y = t.tmem + kYCol + 64 * s;
-    const float D = a.D ? a.D[t.h] : 0.f;
     const uint32_t zero[16] = {};
     for (int b = warp + 1; b < 4; ++b) tc::tmem_st16u_nowait(t_m + 16 * b, zero);              // M above the diagonal stays zero
     tc::tmem_wait_st();
 
     float raw = t.raw_step(a, w, 0);
-    float head = 0.f, G = 0.f;                                     // steps of the block, of the chunk, up to this row
+    float head = 0.f;                                              // steps of the block up to this row
     // prefix sums of a chunk's steps, and its columns' factors; false: a wait gave up
     auto steps = [&](int c) -> bool {
         const bool live = c * kChunk + r < w.seg.len;
@@ -547,10 +585,6 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
         tail = __shfl_down_sync(~0u, tail, 1);
         if (lane == 31) tail = 0.f;
         if (slice_any(t.id, t.bad)) return false;                  // all warps are through with the last chunk's M
-        G = head;
-#pragma unroll
-        for (int i = 2; i >= 0; --i)
-            if (i < warp) G += bars->total[c & 1][s][i];
         bars->col[s][r] = dt * exp2_fast(tail);
         bars->diag[s][r] = __log2f(dt) - head;
         return true;
@@ -564,65 +598,48 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
         // ---- M
         t.wait(&bars->gram, par);
         tc::tc_fence_after();
+        if (c > 0) {                                               // the last chunk's results are out of their X tile
+            if (lane == 0) tc::bulk_wait_read();
+            t.arrive(&bars->x_free[par ^ 1]);
+        }
+        uint32_t g[32], m[16];
+        tc::tmem_ld32(t_gram + 32 * warp, g);
+        tc::tmem_wait_ld();
+        tc::pin32(g);
+        {                                                          // the diagonal block
+            const float* col = bars->diag[s] + 32 * warp;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 e = *reinterpret_cast<const float4*>(col + i);
+                const float v0 = i > lane ? 0.f : exp2_fast(head + e.x) * __uint_as_float(g[i]);
+                const float v1 = i + 1 > lane ? 0.f : exp2_fast(head + e.y) * __uint_as_float(g[i + 1]);
+                const float v2 = i + 2 > lane ? 0.f : exp2_fast(head + e.z) * __uint_as_float(g[i + 2]);
+                const float v3 = i + 3 > lane ? 0.f : exp2_fast(head + e.w) * __uint_as_float(g[i + 3]);
+                m[i / 2] = pack_bf16(v0, v1);
+                m[i / 2 + 1] = pack_bf16(v2, v3);
+            }
+        }
+        if (warp > 0) tc::tmem_ld32(t_gram + 32 * (warp - 1), g);
+        tc::tmem_st16u_nowait(t_m + 16 * warp, m);
         float base = head;                                         // steps from the end of block b to this row
 #pragma unroll 1
-        for (int b = 2 * warp + 1; b >= 0; --b) {                  // 16 columns at a time
-            float g[16];
-            uint32_t m[8];
-            const bool own = b >> 1 == warp;                       // the diagonal block
-            const float* col = (own ? bars->diag[s] : bars->col[s]) + 16 * b;
-            if ((b & 1) && b < 2 * warp - 1) base += bars->total[par][s][(b >> 1) + 1];
-            tc::tmem_ld16(t_gram + 16 * b, g);
-            if (own) {
-                const int past = lane - 16 * (b & 1);              // columns up to this one are seen
+        for (int b = warp - 1; b >= 0; --b) {                      // the blocks before it: two factors, neither above dt
+            if (b < warp - 1) base += bars->total[par][s][b + 1];
+            const float row = exp2_fast(base);
+            const uint64_t rr = pack2(row, row);
+            const float* col = bars->col[s] + 32 * b;
+            tc::tmem_wait_ld();
+            tc::pin32(g);
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 e = *reinterpret_cast<const float4*>(col + i);
-                    const float v0 = i > past ? 0.f : exp2_fast(head + e.x) * g[i];
-                    const float v1 = i + 1 > past ? 0.f : exp2_fast(head + e.y) * g[i + 1];
-                    const float v2 = i + 2 > past ? 0.f : exp2_fast(head + e.z) * g[i + 2];
-                    const float v3 = i + 3 > past ? 0.f : exp2_fast(head + e.w) * g[i + 3];
-                    m[i / 2] = pack_bf16(v0, v1);
-                    m[i / 2 + 1] = pack_bf16(v2, v3);
-                }
-            } else {                                               // two factors, neither above dt
-                const float row = exp2_fast(base);
-                const uint64_t rr = pack2(row, row);
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(col + i);
-                    const float2 u = unpack2(mul2(mul2(e.x, rr), pack2(g[i], g[i + 1])));
-                    const float2 v = unpack2(mul2(mul2(e.y, rr), pack2(g[i + 2], g[i + 3])));
-                    m[i / 2] = pack_bf16(u.x, u.y);
-                    m[i / 2 + 1] = pack_bf16(v.x, v.y);
-                }
+            for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(col + i);
+                const float2 u = unpack2(mul2(mul2(e.x, rr), pack2(__uint_as_float(g[i]), __uint_as_float(g[i + 1]))));
+                const float2 v = unpack2(mul2(mul2(e.y, rr), pack2(__uint_as_float(g[i + 2]), __uint_as_float(g[i + 3]))));
+                m[i / 2] = pack_bf16(u.x, u.y);
+                m[i / 2 + 1] = pack_bf16(v.x, v.y);
             }
-            tc::tmem_st8u_nowait(t_m + 8 * b, m);
-        }
-        // ---- Y = 2^G C S + D x; the product M X is added to it
-        const float grow = exp2_fast(G);
-        t.wait(&bars->full_x[par], (c >> 1) & 1);
-        t.wait(&bars->y_first, par);
-        tc::tc_fence_after();
-        const uint64_t gg = pack2(grow, grow), dd = pack2(D, D);
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-            float y[16];
-            tc::tmem_ld16(t_y + 16 * x, y);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const uint4 raw_x = *reinterpret_cast<const uint4*>(x_row + (((2 * x + q) ^ (r & 7)) << 4));
-                const uint32_t xw[4] = {raw_x.x, raw_x.y, raw_x.z, raw_x.w};
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    float f[2], *e = y + 8 * q + 2 * z;
-                    unpack_bf16(xw[z], f);
-                    const float2 v = unpack2(fma2(pack2(e[0], e[1]), gg, mul2(pack2(f[0], f[1]), dd)));
-                    e[0] = v.x;
-                    e[1] = v.y;
-                }
-            }
-            tc::tmem_st16_nowait(t_y + 16 * x, y);
+            if (b > 0) tc::tmem_ld32(t_gram + 32 * (b - 1), g);
+            tc::tmem_st16u_nowait(t_m + 16 * b, m);
         }
         tc::tmem_wait_st();
         t.arrive(&bars->ready);
@@ -635,19 +652,34 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
         TOut* out = reinterpret_cast<TOut*>(a.out) + ((int64_t)(w.seg.first + c * kChunk + (r & 96)) * a.H + t.h) * a.P + t.channel + lane % 8 * E;
         const uint8_t* warp_rows = x_row - lane * 128;
         const int left = len - (r & 96);                           // rows of this warp that are the request's
+        const bool whole = sizeof(TOut) == 2 && left >= 32;        // all rows of the warp: one tensor-map copy
 #pragma unroll 1
         for (int part = 0; part < kSlice; part += 8 * E) {
             if (part) __syncwarp();
-#pragma unroll 1
-            for (int x = 0; x < 8 * E; x += 16) {
-                float y[16];
-                tc::tmem_ld16(t_y + part + x, y);
 #pragma unroll
-                for (int q = 0; q < 16 / E; ++q)
-                    *reinterpret_cast<typename Vec<TOut, E>::Raw*>(x_row + (((x / E + q) ^ (r & 7)) << 4)) = from_floats<TOut, E>(y + E * q);
+            for (int x = 0; x < 8 * E; x += 32) {
+                uint32_t y[32];
+                tc::tmem_ld32(t_y + part + x, y);
+                tc::tmem_wait_ld();
+                tc::pin32(y);
+#pragma unroll
+                for (int q = 0; q < 32 / E; ++q) {
+                    float f[E];
+#pragma unroll
+                    for (int z = 0; z < E; ++z) f[z] = __uint_as_float(y[E * q + z]);
+                    *reinterpret_cast<typename Vec<TOut, E>::Raw*>(x_row + (((x / E + q) ^ (r & 7)) << 4)) = from_floats<TOut, E>(f);
+                }
             }
+            if (whole) tc::fence_proxy_async();
             if (part + 8 * E >= kSlice) t.arrive(&bars->next_y);
             __syncwarp();
+            if (whole) {
+                if (lane == 0) {
+                    tc::tma_store_2d(om, t.h * a.P + t.channel, w.seg.first + c * kChunk + (r & 96), warp_rows);
+                    tc::bulk_commit();
+                }
+                continue;
+            }
 #pragma unroll 2
             for (int i = 0; i < 32; i += 4) {
                 const int row = i + lane / 8;
@@ -656,9 +688,9 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
                         *reinterpret_cast<const uint4*>(warp_rows + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
             }
         }
-        tc::fence_proxy_async();
-        t.arrive(&bars->x_free[par]);
+        if (!whole) tc::fence_proxy_async();
     }
+    if (lane == 0) tc::bulk_wait_read();                           // before the tile's memory goes
     return !t.bad;
 }
 
@@ -666,7 +698,7 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
 template <int N, bool ENDS, typename TOut>
 __global__ void __launch_bounds__(kTcThreads, 1)
     ssm_chunk_kernel(const SsmCall a, const Plan plan, const __grid_constant__ CUtensorMap xm, const __grid_constant__ CUtensorMap bm,
-                     const __grid_constant__ CUtensorMap cm)
+                     const __grid_constant__ CUtensorMap cm, const __grid_constant__ CUtensorMap om)
 {
     using K = TcCfg<N>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -702,7 +734,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             for (uint64_t* bar = &bars->full_c; bar <= &bars->drain; ++bar) tc::mbar_init(bar, 1);
-            for (uint64_t* bar = &bars->next_s; bar <= &bars->x_free[1]; ++bar) tc::mbar_init(bar, 4 * w.slices);
+            for (uint64_t* bar = &bars->next_s; bar <= &bars->x_free[1]; ++bar) tc::mbar_init(bar, (bar == &bars->ready ? 8 : 4) * w.slices);
             tc::fence_mbar_init();
         }
     } else if (warp == 16) {
@@ -720,7 +752,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     if (warp < 8) {
         const int s = warp / 4;
-        if (!ENDS && s < w.slices) ok = tc_results<N, TOut>(a, w, smem, TcThread(a, w, bars, tmem, s, tid & 127, 1 + s));
+        if (!ENDS && s < w.slices) ok = tc_results<N, TOut>(a, w, smem, TcThread(a, w, bars, tmem, s, tid & 127, 1 + s), &om);
     } else if (warp < 16) {
         more_registers<120>();
         const int s = warp / 4 - 2;
@@ -814,13 +846,13 @@ SsmLayout ssm_layout(const kda_ssm_params& p, int32_t n, int64_t T)
     return w;
 }
 
-cudaError_t ssm_map(CUtensorMap* m, const void* base, int64_t rows, int64_t width, int64_t stride)
+cudaError_t ssm_map(CUtensorMap* m, const void* base, int64_t rows, int64_t width, int64_t stride, int box_rows)
 {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = tc::tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)ssm::kChunk};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -836,10 +868,11 @@ cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* works
     w.plan.segments = reinterpret_cast<ssm::Segment*>(base + w.segments);
     w.plan.states = reinterpret_cast<float*>(base + w.states);
     w.plan.decays = reinterpret_cast<float*>(base + w.decays);
-    CUtensorMap xm, bm, cm;
-    cudaError_t e = ssm_map(&xm, a.x, a.T, (int64_t)a.H * a.P, a.x_stride);
-    if (e == cudaSuccess) e = ssm_map(&bm, a.B, a.T, (int64_t)a.G * a.N, a.b_stride);
-    if (e == cudaSuccess) e = ssm_map(&cm, a.C, a.T, (int64_t)a.G * a.N, a.c_stride);
+    CUtensorMap xm, bm, cm, om = {};
+    cudaError_t e = ssm_map(&xm, a.x, a.T, (int64_t)a.H * a.P, a.x_stride, ssm::kChunk);
+    if (e == cudaSuccess) e = ssm_map(&bm, a.B, a.T, (int64_t)a.G * a.N, a.b_stride, ssm::kChunk);
+    if (e == cudaSuccess) e = ssm_map(&cm, a.C, a.T, (int64_t)a.G * a.N, a.c_stride, ssm::kChunk);
+    if (e == cudaSuccess && sizeof(TOut) == 2) e = ssm_map(&om, a.out, a.T, (int64_t)a.H * a.P, (int64_t)a.H * a.P, 32);
     if (e != cudaSuccess) return e;
     constexpr int smem = ssm::TcCfg<N>::kSmem;
     ssm::ssm_plan_kernel<<<1, 1024, 0, s>>>(a, w.plan);
@@ -847,12 +880,12 @@ cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* works
     if (w.cut) {
         e = cudaFuncSetAttribute(ssm::ssm_chunk_kernel<N, true, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        ssm::ssm_chunk_kernel<N, true, TOut><<<blocks, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm);
+        ssm::ssm_chunk_kernel<N, true, TOut><<<blocks, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm, om);
         ssm::ssm_chain_kernel<<<(unsigned)((int64_t)w.plan.max_segments * a.H * (a.P * a.N / 1024)), 256, 0, s>>>(a, w.plan);
     }
     e = cudaFuncSetAttribute(ssm::ssm_chunk_kernel<N, false, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    ssm::ssm_chunk_kernel<N, false, TOut><<<blocks + 1, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm);
+    ssm::ssm_chunk_kernel<N, false, TOut><<<blocks + 1, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm, om);
     return cudaGetLastError();
 }
 

@@ -167,6 +167,14 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int32_t
         : "memory");
 }
 
+// The same way back, in the issuing thread's bulk group; rows outside the tensor are not written.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int32_t x, int32_t y, const void* src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+}
+
 // ---- bulk async copy shared -> global (bulk-group completion) -------------------------------------
 // src and dst 16-byte aligned, bytes a multiple of 16.  The issuing thread tracks completion with
 // bulk_commit / bulk_wait_read (the shared source may be reused) / bulk_wait (writes done).
