@@ -46,8 +46,11 @@ constexpr int kSlice = 64;                       // channels of a slice
 // tensor-memory columns; Y and dS of the two slices side by side, so that one product makes both
 constexpr uint32_t kGramCol = 0, kMCol = 128, kYCol = 256, kDsCol = 384;
 constexpr int kTcThreads = 640;                  // state, results of two slices: 4 warps each; products, copies, two idle
-// Registers: 96 a thread at launch; the state's groups take 120 (64 of them S), the last gives 48 back:
-// 256 * 120 + 256 * 96 + 128 * 48 = 640 * 96.
+// Registers of a thread at launch, and then of the state's groups (64 of them S), of the results' and of the last one.  A
+// group that asks for more than the others have left waits forever, so the sum is checked here, and the launch's share
+// before the launch.
+constexpr int kLaunchRegs = 96, kStateRegs = 128, kResultRegs = 88, kOtherRegs = 48;
+static_assert(256 * kStateRegs + 256 * kResultRegs + 128 * kOtherRegs <= kTcThreads * kLaunchRegs, "register shares");
 template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 constexpr uint32_t kPolls = 1u << 24;
@@ -152,7 +155,7 @@ struct __align__(16) TcBars {
     uint32_t tmem;
     float total[2][2][4], tail[2][2][4];                        // [parity][slice][warp]: sums of the blocks' steps
     __align__(16) float col[2][kChunk];                         // [slice]: dt_j times the decay from j to its block's end
-    __align__(16) float diag[2][kChunk];                        // [slice]: log2 dt_j less the steps of its block up to j
+    __align__(16) float diag[2][kChunk];                        // [slice]: dt_j against the steps of its block up to j, or their log2
 };
 static_assert(sizeof(TcBars) <= 3072 && offsetof(TcBars, col) % 16 == 0 && offsetof(TcBars, diag) % 16 == 0, "barrier block; columns are read by 16 bytes");
 
@@ -345,6 +348,7 @@ struct TcThread {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
     }
+    // dt of this row in chunk c, before softplus
     __device__ __forceinline__ float raw_step(const SsmCall& a, const TcWork& w, int c) const
     {
         if (c * kChunk + r >= w.seg.len) return 0.f;
@@ -408,13 +412,12 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         store_s();
         t.arrive(&bars->next_s);
     }
-    float raw = t.raw_step(a, w, 0), all_steps = 0.f;
+    float all_steps = 0.f;
     float weight = 0.f, gamma = 0.f, grow = 0.f;                  // of this row's X', of the state, of this row's C S
     // the steps from each token of a chunk to its end; false: a wait gave up
-    auto steps = [&](int c) -> bool {
+    auto steps = [&](int c, float raw) -> bool {
         const bool live = c * kChunk + r < w.seg.len;
         const float dt = live ? softplus_series(raw + t.bias, a.threshold) : 0.f;
-        if (c + 1 < w.chunks) raw = t.raw_step(a, w, c + 1);
         float head = live ? fmaxf(-dt * t.rate, kFarStep) : 0.f, tail = head;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -440,7 +443,7 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         all_steps += whole;
         return true;
     };
-    if (!steps(0)) return false;
+    if (!steps(0, t.raw_step(a, w, 0))) return false;
     for (int c = 0; c < w.chunks; ++c) {
         const uint32_t par = c & 1;
         const int len = w.seg.len - c * kChunk < kChunk ? w.seg.len - c * kChunk : kChunk;
@@ -486,6 +489,7 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         tc::fence_proxy_async();
         t.arrive(&bars->xs);
 
+        const float raw = t.raw_step(a, w, c + 1);                 // wanted further down
         // ---- Y = 2^G C S + D x; the product M X is added to it
         if constexpr (!ENDS) {
             t.wait(&bars->y_first, par);
@@ -518,7 +522,7 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         }
         // ---- S = gamma S + dS
         const uint64_t gg = pack2(gamma, gamma);
-        if (c + 1 < w.chunks && !steps(c + 1)) return false;      // while the product runs
+        if (c + 1 < w.chunks && !steps(c + 1, raw)) return false;      // while the product runs
         t.wait(&bars->ds, par);
         tc::tc_fence_after();
 #pragma unroll
@@ -567,13 +571,12 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
     for (int b = warp + 1; b < 4; ++b) tc::tmem_st16u_nowait(t_m + 16 * b, zero);              // M above the diagonal stays zero
     tc::tmem_wait_st();
 
-    float raw = t.raw_step(a, w, 0);
     float head = 0.f;                                              // steps of the block up to this row
+    bool mild = false;                                             // the block's whole steps are no more than 60
     // prefix sums of a chunk's steps, and its columns' factors; false: a wait gave up
-    auto steps = [&](int c) -> bool {
+    auto steps = [&](int c, float raw) -> bool {
         const bool live = c * kChunk + r < w.seg.len;
         const float dt = live ? softplus_series(raw + t.bias, a.threshold) : 0.f;
-        if (c + 1 < w.chunks) raw = t.raw_step(a, w, c + 1);
         float tail = head = live ? fmaxf(-dt * t.rate, kFarStep) : 0.f;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -586,14 +589,17 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
         if (lane == 31) tail = 0.f;
         if (slice_any(t.id, t.bad)) return false;                  // all warps are through with the last chunk's M
         bars->col[s][r] = dt * exp2_fast(tail);
-        bars->diag[s][r] = __log2f(dt) - head;
+        // inside a block: with few steps two factors again, 2^head and dt_j 2^-head_j, neither past 2^64
+        mild = __shfl_sync(~0u, head, 31) > -60.f;
+        bars->diag[s][r] = mild ? dt * exp2_fast(-head) : __log2f(dt) - head;
         return true;
     };
-    if (!steps(0)) return false;
+    if (!steps(0, t.raw_step(a, w, 0))) return false;
     for (int c = 0; c < w.chunks; ++c) {
         const uint32_t par = c & 1;
         const int len = w.seg.len - c * kChunk < kChunk ? w.seg.len - c * kChunk : kChunk;
         uint8_t* x_row = smem + K::kX + (2 * s + par) * K::kPanel + r * 128;
+        const float raw = t.raw_step(a, w, c + 1);                 // wanted behind M
         slice_sync(t.id);                                          // the columns' factors
         // ---- M
         t.wait(&bars->gram, par);
@@ -606,17 +612,21 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
         tc::tmem_ld32(t_gram + 32 * warp, g);
         tc::tmem_wait_ld();
         tc::pin32(g);
-        {                                                          // the diagonal block
-            const float* col = bars->diag[s] + 32 * warp;
+        const float* own = bars->diag[s] + 32 * warp;              // the diagonal block
+        const float first = mild ? exp2_fast(head) : head;
+        if (mild) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-                const float4 e = *reinterpret_cast<const float4*>(col + i);
-                const float v0 = i > lane ? 0.f : exp2_fast(head + e.x) * __uint_as_float(g[i]);
-                const float v1 = i + 1 > lane ? 0.f : exp2_fast(head + e.y) * __uint_as_float(g[i + 1]);
-                const float v2 = i + 2 > lane ? 0.f : exp2_fast(head + e.z) * __uint_as_float(g[i + 2]);
-                const float v3 = i + 3 > lane ? 0.f : exp2_fast(head + e.w) * __uint_as_float(g[i + 3]);
-                m[i / 2] = pack_bf16(v0, v1);
-                m[i / 2 + 1] = pack_bf16(v2, v3);
+                const float4 e = *reinterpret_cast<const float4*>(own + i);
+                m[i / 2] = pack_bf16(i > lane ? 0.f : e.x * first * __uint_as_float(g[i]), i + 1 > lane ? 0.f : e.y * first * __uint_as_float(g[i + 1]));
+                m[i / 2 + 1] = pack_bf16(i + 2 > lane ? 0.f : e.z * first * __uint_as_float(g[i + 2]), i + 3 > lane ? 0.f : e.w * first * __uint_as_float(g[i + 3]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 e = *reinterpret_cast<const float4*>(own + i);
+                m[i / 2] = pack_bf16(i > lane ? 0.f : exp2_fast(first + e.x) * __uint_as_float(g[i]), i + 1 > lane ? 0.f : exp2_fast(first + e.y) * __uint_as_float(g[i + 1]));
+                m[i / 2 + 1] = pack_bf16(i + 2 > lane ? 0.f : exp2_fast(first + e.z) * __uint_as_float(g[i + 2]), i + 3 > lane ? 0.f : exp2_fast(first + e.w) * __uint_as_float(g[i + 3]));
             }
         }
         if (warp > 0) tc::tmem_ld32(t_gram + 32 * (warp - 1), g);
@@ -643,7 +653,7 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
         }
         tc::tmem_wait_st();
         t.arrive(&bars->ready);
-        if (c + 1 < w.chunks && !steps(c + 1)) return false;       // while the product runs
+        if (c + 1 < w.chunks && !steps(c + 1, raw)) return false;       // while the product runs
         // ---- results
         t.wait(&bars->y_full[par], (c >> 1) & 1);
         tc::tc_fence_after();
@@ -751,14 +761,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t tmem = bars->tmem;
     bool ok = true;
     if (warp < 8) {
+        fewer_registers<kResultRegs>();
         const int s = warp / 4;
         if (!ENDS && s < w.slices) ok = tc_results<N, TOut>(a, w, smem, TcThread(a, w, bars, tmem, s, tid & 127, 1 + s), &om);
     } else if (warp < 16) {
-        more_registers<120>();
+        more_registers<kStateRegs>();
         const int s = warp / 4 - 2;
         if (s < w.slices) ok = tc_state<N, ENDS>(a, plan, w, smem, TcThread(a, w, bars, tmem, s, tid & 127, 3 + s));
     } else {
-        fewer_registers<48>();
+        fewer_registers<kOtherRegs>();
         if (warp == 16) {
             uint32_t leader = 0;
             asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
@@ -859,6 +870,22 @@ cudaError_t ssm_map(CUtensorMap* m, const void* base, int64_t rows, int64_t widt
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The kernel with its shared memory, if it was built with the registers that its groups share out.
+template <int N, bool ENDS, typename TOut>
+cudaError_t ssm_chunk_ready()
+{
+    const auto kernel = ssm::ssm_chunk_kernel<N, ENDS, TOut>;
+    static std::atomic<int> registers;
+    if (registers.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes f;
+        const cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+        if (e != cudaSuccess) return e;
+        registers.store(f.numRegs, std::memory_order_relaxed);
+    }
+    if (registers.load(std::memory_order_relaxed) != ssm::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ssm::TcCfg<N>::kSmem);
+}
+
 template <int N, typename TOut>
 cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* workspace, cudaStream_t s)
 {
@@ -878,12 +905,12 @@ cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* works
     ssm::ssm_plan_kernel<<<1, 1024, 0, s>>>(a, w.plan);
     const unsigned blocks = (unsigned)((int64_t)w.plan.max_segments * w.plan.pairs);
     if (w.cut) {
-        e = cudaFuncSetAttribute(ssm::ssm_chunk_kernel<N, true, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = ssm_chunk_ready<N, true, TOut>();
         if (e != cudaSuccess) return e;
         ssm::ssm_chunk_kernel<N, true, TOut><<<blocks, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm, om);
         ssm::ssm_chain_kernel<<<(unsigned)((int64_t)w.plan.max_segments * a.H * (a.P * a.N / 1024)), 256, 0, s>>>(a, w.plan);
     }
-    e = cudaFuncSetAttribute(ssm::ssm_chunk_kernel<N, false, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = ssm_chunk_ready<N, false, TOut>();
     if (e != cudaSuccess) return e;
     ssm::ssm_chunk_kernel<N, false, TOut><<<blocks + 1, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm, om);
     return cudaGetLastError();
