@@ -15,7 +15,6 @@
 namespace kda {
 
 constexpr int kConvThreads = 128;
-constexpr int kConvTile = 32;        // tokens of a thread
 
 // The V channels from `c` on, their output and the parameters of their taps.
 template <typename T, int V, int W>
@@ -26,10 +25,18 @@ struct ConvLane {
 
     __device__ __forceinline__ ConvLane(const ConvCall& a, int c)
     {
+        float flat[V * W];                            // [channel][tap], as they lie
+        if constexpr (V > 1) {
+#pragma unroll
+            for (int i = 0; i < V * W; i += 4) load_floats<float, 4>(a.weight + (int64_t)c * W + i, flat + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) flat[i] = a.weight[(int64_t)c * W + i];
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) w[i][v] = a.weight[(int64_t)(c + v) * W + i];
+            for (int i = 0; i < W; ++i) w[i][v] = flat[v * W + i];
             bias[v] = a.bias ? a.bias[c + v] : 0.f;
         }
         void* base = a.out[0];
@@ -45,21 +52,20 @@ struct ConvLane {
         out = reinterpret_cast<T*>(base) + (c - first);
     }
 
-    // window[0 .. W - 2] holds the inputs before this token, oldest first; x is its own
+    // The window holds the last W - 1 inputs, the oldest at `at`; x takes its place.  A caller that unrolls over tokens
+    // passes constants, and nothing moves.
     template <bool SILU>
-    __device__ __forceinline__ void step(float (&window)[W - 1][V], const float* x, int64_t t)
+    __device__ __forceinline__ void step(float (&window)[W - 1][V], int at, const float* x, int64_t t)
     {
         float y[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float s = fmaf(window[0][v], w[0][v], bias[v]);
+            float s = bias[v];
 #pragma unroll
-            for (int i = 1; i < W - 1; ++i) s = fmaf(window[i][v], w[i][v], s);
+            for (int i = 0; i < W - 1; ++i) s = fmaf(window[(at + i) % (W - 1)][v], w[i][v], s);
             s = fmaf(x[v], w[W - 1][v], s);
             y[v] = SILU ? s * fast_sigmoid(s) : s;
-#pragma unroll
-            for (int i = 0; i < W - 2; ++i) window[i][v] = window[i + 1][v];
-            window[W - 2][v] = x[v];
+            window[at][v] = x[v];
         }
         store_raw<T, V>(out + t * out_stride, from_floats<T, V>(y));
     }
@@ -70,35 +76,56 @@ struct ConvLane {
     }
 };
 
-// One token per request: blockIdx.x the request, blockIdx.y the channels.
-template <typename T, int V, int W, bool SILU>
+// One token per request: blockIdx.x the requests, R of them to a thread (its taps are loaded once and more rows are
+// in flight), blockIdx.y the channels.
+template <typename T, int V, int W, bool SILU, int R>
 __global__ void __launch_bounds__(kConvThreads) conv_token_kernel(const ConvCall a)
 {
     const int c = (blockIdx.y * kConvThreads + threadIdx.x) * V;
     if (c >= a.C) return;
-    const int64_t b = blockIdx.x;
-    int64_t slot = a.idx[b];
-    const auto raw = load_raw<T, V>(reinterpret_cast<const T*>(a.x) + b * a.x_stride + c);
+    const int64_t b0 = (int64_t)blockIdx.x * R;
+    int64_t slot[R];
+    typename Vec<T, V>::Raw raw[R], old[R][W - 1];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t b = b0 + i < a.n ? b0 + i : a.n - 1;
+        slot[i] = a.idx[b];
+        raw[i] = load_raw<T, V>(reinterpret_cast<const T*>(a.x) + b * a.x_stride + c);
+    }
     ConvLane<T, V, W> lane(a, c);
-    if (slot >= a.num_slots) {
-        if (threadIdx.x == 0) record_layer_error(kDevErrStateIndex);
-        slot = -1;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (slot[i] >= a.num_slots) {
+            if (threadIdx.x == 0) record_layer_error(kDevErrStateIndex);
+            slot[i] = -1;
+        }
+        const T* state = reinterpret_cast<const T*>(a.pool) + slot[i] * (W - 1) * a.C + c;
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            if (slot[i] >= 0) old[i][k] = load_raw<T, V>(state + (int64_t)k * a.C);
     }
-    if (slot < 0) {
-        lane.zero(b);
-        return;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (b0 + i >= a.n) break;
+        if (slot[i] < 0) {
+            lane.zero(b0 + i);
+            continue;
+        }
+        T* state = reinterpret_cast<T*>(a.pool) + slot[i] * (W - 1) * a.C + c;
+        float window[W - 1][V], x[V];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            to_floats<T, V>(old[i][k], window[k]);
+            store_raw<T, V>(state + (int64_t)k * a.C, k < W - 2 ? old[i][k < W - 2 ? k + 1 : 0] : raw[i]);
+        }
+        to_floats<T, V>(raw[i], x);
+        lane.template step<SILU>(window, 0, x, b0 + i);
     }
-    T* state = reinterpret_cast<T*>(a.pool) + slot * (W - 1) * a.C + c;
-    typename Vec<T, V>::Raw old[W - 1];
-#pragma unroll
-    for (int i = 0; i < W - 1; ++i) old[i] = load_raw<T, V>(state + (int64_t)i * a.C);
-    float window[W - 1][V], x[V];
-#pragma unroll
-    for (int i = 0; i < W - 1; ++i) to_floats<T, V>(old[i], window[i]);
-    to_floats<T, V>(raw, x);
-#pragma unroll
-    for (int i = 0; i < W - 1; ++i) store_raw<T, V>(state + (int64_t)i * a.C, i < W - 2 ? old[i < W - 2 ? i + 1 : 0] : raw);
-    lane.template step<SILU>(window, x, b);
+}
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
 // Where the tile that would end before row e ends: a request's first W - 1 tokens, whose outputs depend on
@@ -114,80 +141,124 @@ __device__ __forceinline__ int64_t conv_tile_edge(const ConvCall& a, int64_t e)
     return first + (W - 1) < last ? first + (W - 1) : last;
 }
 
-// Packed prompts: blockIdx.x the tile of kConvTile tokens, blockIdx.y the channels.
+// Packed prompts: blockIdx.x the tile of `tile` tokens, blockIdx.y the channels.
 template <typename T, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kConvThreads) conv_rows_kernel(const ConvCall a)
+__global__ void __launch_bounds__(kConvThreads, 4) conv_rows_kernel(const ConvCall a, int tile)
 {
     const int c = (blockIdx.y * kConvThreads + threadIdx.x) * V;
     if (c >= a.C) return;
-    const int64_t t0 = conv_tile_edge<W>(a, (int64_t)blockIdx.x * kConvTile);
-    const int64_t t1 = conv_tile_edge<W>(a, ((int64_t)blockIdx.x + 1) * kConvTile);
+    const int64_t t0 = conv_tile_edge<W>(a, (int64_t)blockIdx.x * tile);
+    const int64_t t1 = conv_tile_edge<W>(a, ((int64_t)blockIdx.x + 1) * tile);
     if (t0 >= t1) return;
     const T* x = reinterpret_cast<const T*>(a.x) + c;
     ConvLane<T, V, W> lane(a, c);
 
-    float window[W - 1][V];
+    float window[W - 1][V];                         // the oldest first at every step's start
     int32_t b = layer_owner(a.cu, a.n, t0);
     int64_t last = t0, slot = -1;                   // the stretch of rows that t is in ends at `last`; slot < 0: zeros
-    constexpr int U = 4;                            // rows in flight
-    for (int64_t t = t0; t < t1; t += U) {
-        typename Vec<T, V>::Raw raw[U];
+    constexpr int U = W == 4 ? 6 : 4;               // rows of a step, whole rounds of the window
+    // Whole vectors come through shared memory, where three further steps' rows are on their way meanwhile, each thread
+    // its own (in registers there is room for one: 184 us for the eight prompts).  A group of copies a step, empty ones
+    // past the tile's end, so that all but the last two being complete covers the step's rows.
+    constexpr bool kRing = V * sizeof(T) == 16;
+    constexpr int R = kRing ? 4 * U : 1;
+    __shared__ uint4 ring[R][kConvThreads];
+    int64_t asked = t0;                             // rows before this one have been asked for
+    int at = 0, put = 0;                            // places of rows t and `asked` in the ring
+    const auto ask = [&](int64_t t) {
+        if constexpr (kRing) {
+            while (asked - t <= R - U) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = load_raw<T, V>(x + (t + u < t1 ? t + u : t1 - 1) * a.x_stride);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t now = t + u;
-            if (now >= t1) break;
-            if (now >= last) {                       // a stretch begins, or the tile begins inside one
-                while (b < a.n && a.cu[b + 1] <= now) ++b;
-                int64_t first = now;
-                slot = -1;
-                bool ok = b >= 0 && b < a.n && layer_rows(a.cu, b, a.T, first, last);
-                if (ok) {
-                    slot = a.idx[b];
-                    if (slot >= a.num_slots) {
-                        if (threadIdx.x == 0) record_layer_error(kDevErrStateIndex);
-                        slot = -1;
-                    }
-                } else {                             // rows of no request
-                    if (threadIdx.x == 0) record_layer_error(kDevErrSeqlens);
-                    last = b < 0 ? a.cu[0] : b < a.n ? now + 1 : a.T;
+                for (int u = 0; u < U; ++u)
+                    if (asked + u < t1) copy_async16(&ring[put + u][threadIdx.x], x + (asked + u) * a.x_stride);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asked += U;
+                put = put + U == R ? 0 : put + U;
+            }
+        }
+    };
+    ask(t0);
+#pragma unroll 1
+    for (int64_t t = t0; t < t1;) {
+        if (t >= last) {                             // a stretch begins, or the tile begins inside one
+            while (b < a.n && a.cu[b + 1] <= t) ++b;
+            int64_t first = t;
+            slot = -1;
+            const bool ok = b >= 0 && b < a.n && layer_rows(a.cu, b, a.T, first, last);
+            if (ok) {
+                slot = a.idx[b];
+                if (slot >= a.num_slots) {
+                    if (threadIdx.x == 0) record_layer_error(kDevErrStateIndex);
+                    slot = -1;
                 }
-                if (last <= now) last = now + 1;
-                if (slot >= 0) {
-                    T* state = reinterpret_cast<T*>(a.pool) + slot * (W - 1) * a.C + c;
-                    typename Vec<T, V>::Raw old[W - 1];
+            } else {                                 // rows of no request
+                if (threadIdx.x == 0) record_layer_error(kDevErrSeqlens);
+                last = b < 0 ? a.cu[0] : b < a.n ? t + 1 : a.T;
+            }
+            if (last <= t) last = t + 1;
+            if (slot >= 0) {
+                T* state = reinterpret_cast<T*>(a.pool) + slot * (W - 1) * a.C + c;
+                typename Vec<T, V>::Raw old[W - 1];
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i) {
+                    old[i] = load_raw<T, V>(t == first ? state + (int64_t)i * a.C : x + (t - (W - 1) + i) * a.x_stride);
+                    to_floats<T, V>(old[i], window[i]);
+                }
+                if (t == first) {                    // the new state: the last W - 1 inputs
 #pragma unroll
                     for (int i = 0; i < W - 1; ++i) {
-                        old[i] = load_raw<T, V>(now == first ? state + (int64_t)i * a.C : x + (now - (W - 1) + i) * a.x_stride);
-                        to_floats<T, V>(old[i], window[i]);
-                    }
-                    if (now == first) {              // the new state: the last W - 1 inputs
+                        const int64_t row = last - (W - 1) + i;
+                        typename Vec<T, V>::Raw r = old[i];
+                        if (row >= first) {
+                            r = load_raw<T, V>(x + row * a.x_stride);
+                        } else {                     // fewer tokens than that: the old state moves up
 #pragma unroll
-                        for (int i = 0; i < W - 1; ++i) {
-                            const int64_t row = last - (W - 1) + i;
-                            typename Vec<T, V>::Raw r = old[i];
-                            if (row >= first) {
-                                r = load_raw<T, V>(x + row * a.x_stride);
-                            } else {                 // fewer tokens than that: the old state moves up
-#pragma unroll
-                                for (int k = 1; k < W - 1; ++k)
-                                    if (row - first + (W - 1) == k) r = old[k];
-                            }
-                            store_raw<T, V>(state + (int64_t)i * a.C, r);
+                            for (int k = 1; k < W - 1; ++k)
+                                if (row - first + (W - 1) == k) r = old[k];
                         }
+                        store_raw<T, V>(state + (int64_t)i * a.C, r);
                     }
                 }
             }
-            if (slot < 0) {
-                lane.zero(now);
-                continue;
-            }
-            float xv[V];
-            to_floats<T, V>(raw[u], xv);
-            lane.template step<SILU>(window, xv, now);
         }
+        if (slot >= 0 && t + U <= last && t + U <= t1) {
+            if constexpr (kRing) asm volatile("cp.async.wait_group 2;" ::: "memory");
+            typename Vec<T, V>::Raw raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if constexpr (kRing) raw[u] = ring[at + u < R ? at + u : at + u - R][threadIdx.x];
+                else raw[u] = load_raw<T, V>(x + (t + u) * a.x_stride);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float xv[V];
+                to_floats<T, V>(raw[u], xv);
+                lane.template step<SILU>(window, u % (W - 1), xv, t + u);
+            }
+            at = at + U < R ? at + U : at + U - R;
+            ask(t + U);
+            t += U;
+            continue;
+        }
+        if (slot < 0) {
+            lane.zero(t);
+        } else {                                     // few rows of the stretch or the tile are left
+            float xv[V];
+            to_floats<T, V>(load_raw<T, V>(x + t * a.x_stride), xv);
+            lane.template step<SILU>(window, 0, xv, t);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {            // the oldest first again
+                const float newest = window[0][v];
+#pragma unroll
+                for (int i = 0; i < W - 2; ++i) window[i][v] = window[i + 1][v];
+                window[W - 2][v] = newest;
+            }
+        }
+        ++t;
+        at = at + 1 < R ? at + 1 : 0;
+        ask(t);
     }
+    if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 namespace {
@@ -195,7 +266,7 @@ namespace {
 bool conv_vectors(const ConvCall& a, int elem)
 {
     const int V = 16 / elem;
-    if ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.pool)) & 15u || a.x_stride % V || a.C % V) return false;
+    if ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.pool) | reinterpret_cast<uintptr_t>(a.weight)) & 15u || a.x_stride % V || a.C % V) return false;
     for (int j = 0; j < a.num_outs; ++j)
         if ((reinterpret_cast<uintptr_t>(a.out[j]) & 15u) || (a.out_first[j + 1] - a.out_first[j]) % V) return false;
     return true;
@@ -204,9 +275,17 @@ bool conv_vectors(const ConvCall& a, int elem)
 template <typename T, int V, int W, bool SILU>
 cudaError_t conv_launch(const ConvCall& a, cudaStream_t s)
 {
-    const unsigned slabs = (unsigned)((a.C / V + kConvThreads - 1) / kConvThreads);
-    if (a.cu == nullptr) conv_token_kernel<T, V, W, SILU><<<dim3((unsigned)a.n, slabs), kConvThreads, 0, s>>>(a);
-    else conv_rows_kernel<T, V, W, SILU><<<dim3((unsigned)((a.T + kConvTile - 1) / kConvTile), slabs), kConvThreads, 0, s>>>(a);
+    const int64_t slabs = (a.C / V + kConvThreads - 1) / kConvThreads, few = 8 * (int64_t)sm_count();
+    if (a.cu == nullptr) {
+        // four requests a thread while that leaves several CTAs an SM
+        if (a.n * slabs >= 2 * few) conv_token_kernel<T, V, W, SILU, 4><<<dim3((unsigned)((a.n + 3) / 4), (unsigned)slabs), kConvThreads, 0, s>>>(a);
+        else conv_token_kernel<T, V, W, SILU, 1><<<dim3((unsigned)a.n, (unsigned)slabs), kConvThreads, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    // long tiles read less twice (the first rows, the taps), short ones make more CTAs
+    int tile = 96;                                                  // whole steps of either width
+    while (tile > 12 && (a.T + tile - 1) / tile * slabs < few) tile /= 2;
+    conv_rows_kernel<T, V, W, SILU><<<dim3((unsigned)((a.T + tile - 1) / tile), (unsigned)slabs), kConvThreads, 0, s>>>(a, tile);
     return cudaGetLastError();
 }
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda.h"
 #include "kda_internal.cuh"
 
@@ -200,6 +202,20 @@ __device__ __forceinline__ int32_t layer_owner(const int32_t* cu, int32_t n, int
         else hi = mid;
     }
     return lo - 1;
+}
+
+// SMs of the current device, looked up once each.
+inline int sm_count()
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 }  // namespace kda

@@ -257,19 +257,6 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
 
 namespace {
 
-int sm_count()
-{
-    static std::atomic<int> known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    int n = known[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-        known[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
 template <int N, int STEPS, typename TIn, typename TOut>
 cudaError_t ssm_token_launch(const SsmCall& a, cudaStream_t s)
 {
