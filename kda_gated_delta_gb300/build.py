@@ -19,7 +19,7 @@ LIB = os.path.join(BUILD, "libkda.so")
 
 SOURCES = ["kda_api.cu", "kda_recurrent.cu", "kda_prefill.cu", "kda_prefill_static.cu",
            "kda_selftest.cu", "kda_kv_api.cu", "kda_cache.cu", "kda_attn.cu",
-           "kda_attn_tc.cu", "kda_layer_api.cu", "kda_layer.cu"]
+           "kda_attn_tc.cu", "kda_layer_api.cu", "kda_layer.cu", "kda_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

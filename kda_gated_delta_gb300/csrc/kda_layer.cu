@@ -1,5 +1,5 @@
-// kda_layer.cu -- the operators around a recurrence, in one translation unit so that they share one device
-// error word: the short convolution, the selective recurrence and the group norm.
+// kda_layer.cu -- the operators around a recurrence that record errors, in one translation unit so that they share one device
+// error word: the short convolution and the selective recurrence.
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -11,6 +11,5 @@ cudaError_t layer_read_and_clear_error(int32_t* code) { return read_and_clear(g_
 }  // namespace kda
 
 #include "kda_conv.cuh"
-#include "kda_norm.cuh"
 #include "kda_ssm.cuh"
 #include "kda_ssm_tc.cuh"
