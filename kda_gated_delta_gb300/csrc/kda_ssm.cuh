@@ -12,7 +12,7 @@
 //                      tensor-core form (kda_ssm_tc.cuh) does not take.
 #pragma once
 
-#include <atomic>
+#include <type_traits>
 
 #include "kda_layer.cuh"
 #include "kda_tc.cuh"
@@ -136,7 +136,6 @@ __device__ __forceinline__ void ssm_clear_unowned(const SsmCall& a, int tid, int
     for (int64_t i = hi * width + tid; i < a.T * width; i += threads) out[i] = from_f32<TOut>(0.f);
 }
 
-constexpr int kSsmTile = 16;        // tokens staged at once
 
 // Packed prompts.  blockIdx.x: (request, head, slab of STEPS * ROWS rows); one CTA more gives zeros to rows of
 // no request.
@@ -146,6 +145,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
     using Sh = SsmShape<N>;
     constexpr int NV4 = Sh::NV4, LPR = Sh::LPR, R = Sh::ROWS * STEPS, E = 16 / (int)sizeof(TIn);
     constexpr int XR = R < 16 ? 16 : R;
+    constexpr int kSsmTile = N * sizeof(TIn) > 512 ? 8 : 16;       // tokens staged at once: at most 39 KB
     __shared__ __align__(16) TIn sB[2][kSsmTile][N], sC[2][kSsmTile][N], sx[2][kSsmTile][XR];
     __shared__ float sdt[2][kSsmTile], sa[2][kSsmTile];
     __shared__ __align__(16) TOut sy[kSsmTile][XR];
@@ -214,31 +214,54 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();                                 // this tile is in, the last one's outputs are out
         if (t0 + kSsmTile < last) stage(buf ^ 1, t0 + kSsmTile);
-#pragma unroll 2
-        for (int k = 0; k < count; ++k) {
-            const float decay = sa[buf][k], dt = sdt[buf][k];
-            float Bv[4 * NV4], Cv[4 * NV4];
+        // K tokens at a time: their row sums are independent and go through the shuffles together
+        constexpr int K = 4;
+        const auto tokens = [&](auto many, int k0) {
+            constexpr int M = decltype(many)::value;
+            float y[STEPS][M];
 #pragma unroll
-            for (int j = 0; j < NV4; ++j) {
-                load_floats<TIn, 4>(&sB[buf][k][4 * (li + LPR * j)], Bv + 4 * j);
-                load_floats<TIn, 4>(&sC[buf][k][4 * (li + LPR * j)], Cv + 4 * j);
-            }
+            for (int kk = 0; kk < M; ++kk) {
+                const int k = k0 + kk;
+                const float decay = sa[buf][k], dt = sdt[buf][k];
+                float Bv[4 * NV4], Cv[4 * NV4];
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int r = r0 + s * Sh::ROWS;
-                const float x = to_f32(sx[buf][k][r]);
-                const float u = dt * x;
-                float y = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4 * NV4; ++i) {
-                    st[s][i] = fmaf(u, Bv[i], decay * st[s][i]);
-                    y = fmaf(st[s][i], Cv[i], y);
+                for (int j = 0; j < NV4; ++j) {
+                    load_floats<TIn, 4>(&sB[buf][k][4 * (li + LPR * j)], Bv + 4 * j);
+                    load_floats<TIn, 4>(&sC[buf][k][4 * (li + LPR * j)], Cv + 4 * j);
                 }
 #pragma unroll
-                for (int off = LPR / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-                if (li == 0) sy[k][r] = from_f32<TOut>(fmaf(D, x, y));
+                for (int s = 0; s < STEPS; ++s) {
+                    const float u = dt * to_f32(sx[buf][k][r0 + s * Sh::ROWS]);
+                    float sum[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 4 * NV4; ++i) {
+                        st[s][i] = fmaf(u, Bv[i], decay * st[s][i]);
+                        sum[i & 1] = fmaf(st[s][i], Cv[i], sum[i & 1]);
+                    }
+                    y[s][kk] = sum[0] + sum[1];
+                }
             }
-        }
+#pragma unroll
+            for (int off = LPR / 2; off > 0; off >>= 1)
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                    for (int kk = 0; kk < M; ++kk) y[s][kk] += __shfl_xor_sync(0xffffffffu, y[s][kk], off);
+            if (li == 0) {
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                    for (int kk = 0; kk < M; ++kk) {
+                        const int r = r0 + s * Sh::ROWS;
+                        sy[k0 + kk][r] = from_f32<TOut>(fmaf(D, to_f32(sx[buf][k0 + kk][r]), y[s][kk]));
+                    }
+            }
+        };
+        int k = 0;
+#pragma unroll 1
+        for (; k + K <= count; k += K) tokens(std::integral_constant<int, K>(), k);
+#pragma unroll 1
+        for (; k < count; ++k) tokens(std::integral_constant<int, 1>(), k);
         __syncthreads();
         constexpr int O = 16 / (int)sizeof(TOut);
         for (int i = tid; i < count * (rows / O); i += kSsmThreads) {

@@ -69,10 +69,12 @@ struct Segment {
 // The call's segments, the states between them and how the slices are paired.
 struct Plan {
     Segment* segments;
-    int32_t* found;                              // number of segments
+    int32_t* found;                              // numbers of segments, of segments that another follows, of requests in several
+    int32_t* followed;                           // places of segments that another follows
+    int32_t* chains;                             // places of the first segments of requests in several
     float* states;                               // [..][H][P][N]: state before segment k of a request at base + k
     float* decays;                               // [..][H]: log2 of a segment's whole decay, at base + k + 1
-    int32_t max_segments;
+    int32_t max_segments, max_cuts;              // max_cuts bounds both lists
     int32_t pairs_per_group, pairs;              // slice pairs
     int32_t want;                                // tokens of a segment that fill the SMs
 };
@@ -80,57 +82,81 @@ struct Plan {
 // Lists the segments, the longest first (by 64 classes of length), so that no long one starts last.
 __global__ void __launch_bounds__(1024) ssm_plan_kernel(const SsmCall a, const Plan plan)
 {
-    __shared__ int32_t bucket[65], longest, states;
+    __shared__ int32_t bucket[65], longest, states, cuts[2];
     const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid < 65) bucket[tid] = 0;
-    if (tid == 0) longest = 1, states = 0;
-    __syncthreads();
-    // request b: its rows, slot, and the number of its segments, `size` tokens each but the last
-    auto cut = [&](int32_t b, int64_t& first, int64_t& len, int32_t& slot, int64_t& size) -> int32_t {
-        int64_t last;
-        if (!layer_rows(a.cu, b, a.T, first, last)) record_layer_error(kDevErrSeqlens);
-        len = last - first;
-        slot = a.idx[b];
-        if (slot >= a.num_slots) {
-            record_layer_error(kDevErrStateIndex);
-            slot = -1;
-        }
-        size = len;
-        if (len == 0) return 0;
-        const int64_t n = slot < 0 ? 1 : len / plan.want;
-        if (n <= 1) return 1;
-        size = ((len + n - 1) / n + kChunk - 1) / kChunk * kChunk;
-        return (int32_t)((len + size - 1) / size);                           // whole chunks may need fewer
+    if (tid == 0) longest = 1, states = 0, cuts[0] = 0, cuts[1] = 0;
+    struct Cut {
+        int64_t first, len, size;                // rows; `size` tokens a segment but the last
+        int32_t slot, n;                         // segments
     };
-    int64_t first, len, size;
-    int32_t slot;
-    for (int32_t b = tid; b < a.n; b += 1024)
-        if (cut(b, first, len, slot, size) > 0) atomicMax(&longest, (int32_t)size);
+    auto cut = [&](int32_t b) -> Cut {
+        Cut c;
+        int64_t last;
+        c.slot = a.idx[b];
+        if (!layer_rows(a.cu, b, a.T, c.first, last)) record_layer_error(kDevErrSeqlens);
+        c.len = last - c.first;
+        if (c.slot >= a.num_slots) {
+            record_layer_error(kDevErrStateIndex);
+            c.slot = -1;
+        }
+        c.size = c.len;
+        c.n = c.len > 0;
+        const int64_t n = c.slot < 0 || c.len < 2 * (int64_t)plan.want ? 1 : c.len / plan.want;
+        if (n > 1) {
+            c.size = ((c.len + n - 1) / n + kChunk - 1) / kChunk * kChunk;
+            c.n = (int32_t)((c.len + c.size - 1) / c.size);                  // whole chunks may need fewer
+        }
+        return c;
+    };
+    Cut mine = {};
+    if (tid < a.n) mine = cut(tid);
+    auto of = [&](int32_t b) { return b == tid ? mine : cut(b); };           // looked up once for up to 1,024 requests
     __syncthreads();
-    const int64_t top = longest;
+    for (int32_t b = tid; b < a.n; b += 1024) {
+        const Cut c = of(b);
+        if (c.n > 0) atomicMax(&longest, (int32_t)c.size);
+    }
+    __syncthreads();
+    const float scale = 63.f / (float)longest;
     for (int pass = 0; pass < 2; ++pass) {
         for (int32_t b = tid; b < a.n; b += 1024) {
-            const int32_t n = cut(b, first, len, slot, size);
-            const int32_t base = pass == 1 && n > 1 ? atomicAdd(&states, n) : 0;
-            for (int32_t k = 0; k < n; ++k) {
-                const int64_t at = k * size, part = len - at < size ? len - at : size;
-                const int key = 63 - (int)(part * 63 / top);
+            const Cut c = of(b);
+            const int32_t base = pass == 1 && c.n > 1 ? atomicAdd(&states, c.n) : 0;
+            for (int32_t k = 0; k < c.n; ++k) {
+                const int64_t at = k * c.size, part = c.len - at < c.size ? c.len - at : c.size;
+                const int key = max(0, 63 - (int)((float)part * scale));
                 const int32_t place = atomicAdd(&bucket[pass == 0 ? key + 1 : key], 1);
-                if (pass == 1 && place < plan.max_segments) {
-                    Segment s;
-                    s.b = b; s.slot = slot; s.first = (int32_t)(first + at); s.len = (int32_t)part;
-                    s.k = k; s.count = n; s.base = base; s.pad = 0;
-                    plan.segments[place] = s;
+                if (pass == 0 || place >= plan.max_segments) continue;
+                Segment s;
+                s.b = b; s.slot = c.slot; s.first = (int32_t)(c.first + at); s.len = (int32_t)part;
+                s.k = k; s.count = c.n; s.base = base; s.pad = 0;
+                plan.segments[place] = s;
+                if (k + 1 < c.n) {
+                    const int32_t i = atomicAdd(&cuts[0], 1);
+                    if (i < plan.max_cuts) plan.followed[i] = place;
+                }
+                if (k == 0 && c.n > 1) {
+                    const int32_t i = atomicAdd(&cuts[1], 1);
+                    if (i < plan.max_cuts) plan.chains[i] = place;
                 }
             }
         }
         __syncthreads();
-        if (pass == 0 && tid == 0) {
-            for (int i = 1; i < 65; ++i) bucket[i] += bucket[i - 1];         // first place of each class
-            *plan.found = bucket[64] < plan.max_segments ? bucket[64] : plan.max_segments;
+        if (pass == 0 && tid < 32) {                                         // first place of each class
+            int32_t v0 = bucket[2 * tid + 1], v1 = bucket[2 * tid + 2], sum = v0 + v1;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int32_t u = __shfl_up_sync(~0u, sum, off);
+                if (tid >= off) sum += u;
+            }
+            bucket[2 * tid + 1] = sum - v1;
+            bucket[2 * tid + 2] = sum;
+            if (tid == 31) plan.found[0] = sum < plan.max_segments ? sum : plan.max_segments;
         }
         __syncthreads();
     }
+    if (tid < 2) plan.found[1 + tid] = cuts[tid] < plan.max_cuts ? cuts[tid] : plan.max_cuts;
 }
 
 // ---- the chunk kernel ------------------------------------------------------------------------------
@@ -714,16 +740,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     TcBars* bars = reinterpret_cast<TcBars*>(smem + K::kEnd);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int32_t place = blockIdx.x / plan.pairs, pair = blockIdx.x % plan.pairs;
+    int32_t place = blockIdx.x / plan.pairs;
+    const int32_t pair = blockIdx.x % plan.pairs;
     TOut* out = reinterpret_cast<TOut*>(a.out);
+    // launched while the kernel before it runs; all wait for it, so that who waits for this one waits for that one too
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (ENDS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!ENDS && blockIdx.x == gridDim.x - 1) {
         ssm_clear_unowned<TOut>(a, tid, kTcThreads);
         return;
     }
-    if (place >= *plan.found) return;
+    if (place >= plan.found[ENDS ? 1 : 0]) return;
+    if (ENDS) place = plan.followed[place];
     TcWork w;
     w.seg = plan.segments[place];
-    if (ENDS && w.seg.k + 1 >= w.seg.count) return;              // nothing starts from a last segment's state
     const int per_head = a.P / kSlice, hpg = a.H / a.G;
     w.g = pair / plan.pairs_per_group;
     w.first = (pair % plan.pairs_per_group) * 2;
@@ -798,15 +828,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // The state before each segment: of the first the pool's, then S = decay S + (the segment's own).
-// blockIdx.x: (segment, head, 1024 states); only a request's first segment has work.
+// blockIdx.x: (request in several segments, head, 1024 states).
 __global__ void __launch_bounds__(256) ssm_chain_kernel(const SsmCall a, const Plan plan)
 {
     const int per = a.P * a.N / 1024;
     const int64_t bh = blockIdx.x / per;
-    const int32_t place = (int32_t)(bh / a.H), h = (int32_t)(bh - (int64_t)place * a.H);
-    if (place >= *plan.found) return;
-    const Segment seg = plan.segments[place];
-    if (seg.k != 0 || seg.count < 2) return;
+    const int32_t i = (int32_t)(bh / a.H), h = (int32_t)(bh - (int64_t)i * a.H);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (i >= plan.found[2]) return;
+    const Segment seg = plan.segments[plan.chains[i]];
     const int64_t all = (int64_t)a.H * a.P * a.N, at = (int64_t)h * a.P * a.N + (blockIdx.x % per) * 1024 + threadIdx.x * 4;
     float4 v = *reinterpret_cast<const float4*>(a.pool + seg.slot * all + at);
     float* to = plan.states + seg.base * all + at;
@@ -832,7 +863,7 @@ bool ssm_on_tensor_cores(const kda_ssm_params& p)
 struct SsmLayout {
     ssm::Plan plan;
     bool cut;                        // some request may have several segments
-    size_t segments, states, decays, total;
+    size_t segments, followed, chains, states, decays, total;
 };
 
 SsmLayout ssm_layout(const kda_ssm_params& p, int32_t n, int64_t T)
@@ -850,7 +881,10 @@ SsmLayout ssm_layout(const kda_ssm_params& p, int32_t n, int64_t T)
     w.plan.max_segments = (int32_t)(n + more);
     auto round = [](size_t x) { return (x + 255) / 256 * 256; };
     w.segments = 256;
-    w.states = w.segments + round(sizeof(ssm::Segment) * (size_t)w.plan.max_segments);
+    w.plan.max_cuts = w.cut ? (int32_t)more : 0;
+    w.followed = w.segments + round(sizeof(ssm::Segment) * (size_t)w.plan.max_segments);
+    w.chains = w.followed + round(4 * (size_t)w.plan.max_cuts);
+    w.states = w.chains + round(4 * (size_t)w.plan.max_cuts);
     const size_t held = w.cut ? (size_t)more : 0;
     w.decays = w.states + round(held * 4 * p.num_heads * p.head_dim * p.state_dim);
     w.total = w.decays + round(held * 4 * p.num_heads);
@@ -886,6 +920,23 @@ cudaError_t ssm_chunk_ready()
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ssm::TcCfg<N>::kSmem);
 }
 
+// Launched while the kernel before it in the stream runs; it waits for that one itself (griddepcontrol).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int64_t blocks, int threads, int smem, cudaStream_t stream, const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int N, typename TOut>
 cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* workspace, cudaStream_t s)
 {
@@ -893,6 +944,8 @@ cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* works
     uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
     w.plan.found = reinterpret_cast<int32_t*>(base);
     w.plan.segments = reinterpret_cast<ssm::Segment*>(base + w.segments);
+    w.plan.followed = reinterpret_cast<int32_t*>(base + w.followed);
+    w.plan.chains = reinterpret_cast<int32_t*>(base + w.chains);
     w.plan.states = reinterpret_cast<float*>(base + w.states);
     w.plan.decays = reinterpret_cast<float*>(base + w.decays);
     CUtensorMap xm, bm, cm, om = {};
@@ -903,17 +956,16 @@ cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* works
     if (e != cudaSuccess) return e;
     constexpr int smem = ssm::TcCfg<N>::kSmem;
     ssm::ssm_plan_kernel<<<1, 1024, 0, s>>>(a, w.plan);
-    const unsigned blocks = (unsigned)((int64_t)w.plan.max_segments * w.plan.pairs);
+    e = cudaGetLastError();
     if (w.cut) {
         e = ssm_chunk_ready<N, true, TOut>();
-        if (e != cudaSuccess) return e;
-        ssm::ssm_chunk_kernel<N, true, TOut><<<blocks, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm, om);
-        ssm::ssm_chain_kernel<<<(unsigned)((int64_t)w.plan.max_segments * a.H * (a.P * a.N / 1024)), 256, 0, s>>>(a, w.plan);
+        if (e == cudaSuccess) e = launch_after(ssm::ssm_chunk_kernel<N, true, TOut>, (int64_t)w.plan.max_cuts * w.plan.pairs, ssm::kTcThreads, smem, s, a, w.plan, xm, bm, cm, om);
+        // a request in several segments has two at least
+        if (e == cudaSuccess) e = launch_after(ssm::ssm_chain_kernel, (int64_t)(w.plan.max_cuts / 2 + 1) * a.H * (a.P * a.N / 1024), 256, 0, s, a, w.plan);
     }
-    e = ssm_chunk_ready<N, false, TOut>();
+    if (e == cudaSuccess) e = ssm_chunk_ready<N, false, TOut>();
     if (e != cudaSuccess) return e;
-    ssm::ssm_chunk_kernel<N, false, TOut><<<blocks + 1, ssm::kTcThreads, smem, s>>>(a, w.plan, xm, bm, cm, om);
-    return cudaGetLastError();
+    return launch_after(ssm::ssm_chunk_kernel<N, false, TOut>, (int64_t)w.plan.max_segments * w.plan.pairs + 1, ssm::kTcThreads, smem, s, a, w.plan, xm, bm, cm, om);
 }
 
 }  // namespace

@@ -154,7 +154,7 @@ SSM_LENS = [[1], [50], [130, 1, 0, 64, 3], [16, 17, 15, 128, 129], [0, 5], [300]
 @pytest.mark.parametrize("lens", SSM_LENS, ids=str)
 @pytest.mark.parametrize("H,P,N,G,dtype,out", [(4, 64, 128, 2, BF16, BF16), (3, 64, 128, 1, BF16, F32), (2, 128, 128, 1, BF16, BF16), (4, 64, 64, 4, BF16, F32),
                                                (2, 32, 16, 1, BF16, BF16), (3, 64, 128, 3, F32, F32), (2, 16, 32, 2, F32, F32), (2, 128, 64, 1, F32, BF16),
-                                               (1, 64, 256, 1, BF16, F32), (5, 64, 64, 1, BF16, BF16)])
+                                               (1, 64, 256, 1, BF16, F32), (5, 64, 64, 1, BF16, BF16), (2, 64, 256, 2, F32, F32)])
 def test_ssm_rows(lens, H, P, N, G, dtype, out):
     x, dt, B, C, A_log, dt_bias, D = ssm_inputs(5, lens, H, P, N, G, dtype, strided=len(lens) > 1)
     slots = [2 * len(lens) - i for i in range(len(lens))]
