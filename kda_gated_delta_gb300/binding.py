@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import threading
 from typing import NamedTuple
@@ -701,10 +702,7 @@ def _tokens(t, name, shape, dtype, dev):
     if t.shape[1:] != shape:
         raise ValueError(f"{name} must be [tokens, {', '.join(map(str, shape))}], got {tuple(t.shape)}")
     if t.is_contiguous():
-        n = 1
-        for d in shape:
-            n *= d
-        return t.data_ptr(), n
+        return t.data_ptr(), math.prod(shape)
     s, n = t.stride(), 1
     for i in range(len(shape), 0, -1):
         if shape[i - 1] > 1 and s[i] != n:
@@ -715,13 +713,13 @@ def _tokens(t, name, shape, dtype, dev):
     return t.data_ptr(), max(s[0], n)
 
 
-def _need_with_x(t, name, dtype, dev, shape=None):
-    if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
-        _dev(t, name, dtype)
+def _need_with_x(t, name, dtype, dev, shape):
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr()
+    _dev(t, name, dtype)
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, with x")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _here(t, name):
@@ -740,7 +738,10 @@ def _conv_params(C, W, code, act):
 
 
 @functools.lru_cache(maxsize=256)
-def _conv_split(parts):
+def _conv_split(parts, C):
+    """(channel counts as the library takes them, type of its array of pointers)."""
+    if not 1 <= len(parts) <= 4 or min(parts) < 1 or sum(parts) != C:
+        raise ValueError(f"split must be one to four channel counts with the sum {C}, got {parts}")
     return (ctypes.c_int32 * len(parts))(*(_clip(n) for n in parts)), ctypes.c_void_p * len(parts)
 
 
@@ -754,21 +755,27 @@ def causal_conv(x, weight, state_pool, state_idx, cu_seqlens=None, *, bias=None,
         with torch.cuda.stream(stream):
             return causal_conv(x, weight, state_pool, state_idx, cu_seqlens, bias=bias, activation=activation, split=split, out=out)
     dev = _here(x, "x")
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [tokens, channels]")
-    T, C = x.shape
+    T, C = shape
     dtype = x.dtype
     code = _code(dtype, "x")
-    xp, x_stride = _tokens(x, "x", x.shape[1:], dtype, dev)
-    wp = _need_with_x(weight, "weight", _F32, dev)
-    if weight.dim() != 2 or weight.shape[0] != C:
+    if x.is_contiguous():
+        xp, x_stride = x.data_ptr(), C
+    else:
+        xp, x_stride = _tokens(x, "x", shape[1:], dtype, dev)
+    if weight.dim() != 2:
         raise ValueError(f"weight must be [{C}, width]")
     W = weight.shape[1]
+    wp = _need_with_x(weight, "weight", _F32, dev, (C, W))
     bp = None if bias is None else _need_with_x(bias, "bias", _F32, dev, (C,))
-    pool = _need_with_x(state_pool, "state_pool", dtype, dev)
-    if state_pool.dim() != 3 or state_pool.shape[1:] != (W - 1, C):
+    if state_pool.dim() != 3:
         raise ValueError(f"state_pool must be [slots, {W - 1}, {C}]")
-    idx, n = _need_with_x(state_idx, "state_idx", _I32, dev), state_idx.numel()
+    slots = state_pool.shape[0]
+    pool = _need_with_x(state_pool, "state_pool", dtype, dev, (slots, W - 1, C))
+    n = state_idx.numel()
+    idx = _need_with_x(state_idx, "state_idx", _I32, dev, (n,))
     cu = None
     if cu_seqlens is not None:
         cu = _need_with_x(cu_seqlens, "cu_seqlens", _I32, dev, (n + 1,))
@@ -780,18 +787,17 @@ def causal_conv(x, weight, state_pool, state_idx, cu_seqlens=None, *, bias=None,
     if act < 0 or act > 1:
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
     parts = (C,) if split is None else tuple(split)
-    if sum(parts) != C or not 1 <= len(parts) <= 4 or min(parts) < 1:
-        raise ValueError(f"split must be one to four channel counts with the sum {C}, got {split}")
+    counts, pointers = _conv_split(parts, C)
     if out is None:
-        outs = [torch.empty((T, m), dtype=dtype, device=x.device) for m in parts]
+        device = x.device
+        outs = [torch.empty((T, m), dtype=dtype, device=device) for m in parts]
     else:
         outs = [out] if split is None else list(out)
         if len(outs) != len(parts):
             raise ValueError("out must have one tensor per part")
         for i, (o, m) in enumerate(zip(outs, parts)):
             _need_with_x(o, f"out[{i}]", dtype, dev, (T, m))
-    counts, pointers = _conv_split(parts)
-    rc = _fn("kda_causal_conv")(_conv_params(C, W, code, act), xp, x_stride, wp, bp, cu, n, T, pool, state_pool.shape[0], idx,
+    rc = _fn("kda_causal_conv")(_conv_params(C, W, code, act), xp, x_stride, wp, bp, cu, n, T, pool, slots, idx,
                                 pointers(*[o.data_ptr() for o in outs]), counts, len(parts), torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         _check(rc, "kda_causal_conv")
@@ -820,26 +826,30 @@ def ssm_prefill_workspace_size(num_heads, head_dim, state_dim, num_groups, num_s
 def _ssm_args(x, dt, B, C, A_log, state_pool, state_idx, dt_bias, D, out, out_dtype, threshold):
     """(device, params, the entry points' shared pointers, requests, pool, slots, indices, out)."""
     dev = _here(x, "x")
-    if x.dim() != 3 or B.dim() != 3:
+    shape, b_shape = x.shape, B.shape
+    if len(shape) != 3 or len(b_shape) != 3:
         raise ValueError("x must be [tokens, heads, head_dim], B and C [tokens, groups, states]")
-    T, H, P = x.shape
-    G, N = B.shape[1:]
+    T, H, P = shape
+    _, G, N = b_shape
     dtype = x.dtype
     code = _code(dtype, "x")
-    xp, xs = _tokens(x, "x", x.shape[1:], dtype, dev)
-    bp, bs = _tokens(B, "B", B.shape[1:], dtype, dev)
-    cp, cs = _tokens(C, "C", B.shape[1:], dtype, dev)
+    xp, xs = _tokens(x, "x", shape[1:], dtype, dev)
+    bp, bs = _tokens(B, "B", b_shape[1:], dtype, dev)
+    cp, cs = _tokens(C, "C", b_shape[1:], dtype, dev)
     dt_code = _code(dt.dtype, "dt")
     dp, ds = _tokens(dt, "dt", (H,), dt.dtype, dev)
-    if not T == B.shape[0] == C.shape[0] == dt.shape[0]:
+    if not T == b_shape[0] == C.shape[0] == dt.shape[0]:
         raise ValueError("x, dt, B and C must have the same number of tokens")
-    al = _need_with_x(A_log, "A_log", _F32, dev, (H,))
-    db = None if dt_bias is None else _need_with_x(dt_bias, "dt_bias", _F32, dev, (H,))
-    dd = None if D is None else _need_with_x(D, "D", _F32, dev, (H,))
-    pool = _need_with_x(state_pool, "state_pool", _F32, dev)
-    if state_pool.dim() != 4 or state_pool.shape[1:] != (H, P, N):
+    heads = (H,)
+    al = _need_with_x(A_log, "A_log", _F32, dev, heads)
+    db = None if dt_bias is None else _need_with_x(dt_bias, "dt_bias", _F32, dev, heads)
+    dd = None if D is None else _need_with_x(D, "D", _F32, dev, heads)
+    if state_pool.dim() != 4:
         raise ValueError(f"state_pool must be [slots, {H}, {P}, {N}]")
-    idx = _need_with_x(state_idx, "state_idx", _I32, dev)
+    slots = state_pool.shape[0]
+    pool = _need_with_x(state_pool, "state_pool", _F32, dev, (slots, H, P, N))
+    n = state_idx.numel()
+    idx = _need_with_x(state_idx, "state_idx", _I32, dev, (n,))
     if out is None:
         out_dtype = dtype if out_dtype is None else out_dtype
         out_code = _code(out_dtype, "out_dtype")
@@ -848,7 +858,7 @@ def _ssm_args(x, dt, B, C, A_log, state_pool, state_idx, dt_bias, D, out, out_dt
         out_code = _code(out.dtype, "out")
         _need_with_x(out, "out", out.dtype, dev, (T, H, P))
     p = _ssm_params(H, P, N, G, code, dt_code, out_code, threshold)
-    return dev, T, p, (p, xp, xs, dp, ds, bp, bs, cp, cs, al, db, dd), state_idx.numel(), (pool, state_pool.shape[0], idx, out.data_ptr()), out
+    return dev, T, p, (p, xp, xs, dp, ds, bp, bs, cp, cs, al, db, dd), n, (pool, slots, idx, out.data_ptr()), out
 
 
 def ssm_prefill(x, dt, B, C, A_log, cu_seqlens, state_pool, state_idx, *, dt_bias=None, D=None, out=None, out_dtype=None,
@@ -866,7 +876,8 @@ def ssm_prefill(x, dt, B, C, A_log, cu_seqlens, state_pool, state_idx, *, dt_bia
         raise ValueError("tokens without a request")
     need, ws = _ssm_workspace(p, n, T), None
     if workspace is not None:
-        ws, need = _need_with_x(workspace, "workspace", _U8, dev), workspace.numel()
+        need = workspace.numel()
+        ws = _need_with_x(workspace, "workspace", _U8, dev, (need,))
     elif need:
         workspace = torch.empty(need, dtype=_U8, device=x.device)
         ws = workspace.data_ptr()

@@ -21,6 +21,35 @@ namespace kda {
 
 constexpr int kSsmThreads = 128;
 
+namespace ssm {
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1, by the series of log(1 + e) = 2 artanh(e / (2 + e)), whose argument is at
+// most 1 / 3: the first term left out is below 2^-25 of the sum.
+__device__ __forceinline__ float softplus_series(float x, float threshold)
+{
+    const float e = exp2_fast(-fabsf(x) * kLog2e);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(2.0f + e));
+    const float u = e * r, q = u * u;
+    float p = fmaf(q, 1.f / 15, 1.f / 13);
+    p = fmaf(q, p, 1.f / 11);
+    p = fmaf(q, p, 1.f / 9);
+    p = fmaf(q, p, 1.f / 7);
+    p = fmaf(q, p, 1.f / 5);
+    p = fmaf(q, p, 1.f / 3);
+    p = fmaf(q, p, 1.f);
+    return x > threshold ? x : fmaf(2.f * u, p, fmaxf(x, 0.f));
+}
+}  // namespace ssm
+
 template <int N>
 struct SsmShape {
     static constexpr int CPL = N <= 32 ? 4 : N == 64 ? 8 : 16;   // states of a lane
@@ -30,13 +59,11 @@ struct SsmShape {
     static constexpr int NV4 = CPL / 4;
 };
 
-// dt_t and a_t of one head and token.
-__device__ __forceinline__ void ssm_step_size(const SsmCall& a, int64_t t, int h, float rate, float bias, float& dt, float& decay)
+// dt of one head and token before softplus.
+__device__ __forceinline__ float ssm_raw_step(const SsmCall& a, int64_t t, int h)
 {
     const int64_t i = t * a.dt_stride + h;
-    const float raw = a.dt_bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.dt)[i]) : reinterpret_cast<const float*>(a.dt)[i];
-    dt = softplus_f32(raw + bias, a.threshold);
-    decay = expf(-dt * rate);
+    return a.dt_bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.dt)[i]) : reinterpret_cast<const float*>(a.dt)[i];
 }
 
 // One token per request.  A CTA has STEPS * ROWS rows of one (request, head).
@@ -90,8 +117,8 @@ __global__ void __launch_bounds__(kSsmThreads, STEPS >= 4 ? 4 : 8) ssm_token_ker
     }
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) xv[s] = r0 + s * Sh::ROWS < a.P ? to_f32(xp[r0 + s * Sh::ROWS]) : 0.f;
-    float dt, decay;
-    ssm_step_size(a, b, h, expf(a.A_log[h]), a.dt_bias ? a.dt_bias[h] : 0.f, dt, decay);
+    const float dt = ssm::softplus_series(ssm_raw_step(a, b, h) + (a.dt_bias ? a.dt_bias[h] : 0.f), a.threshold);
+    const float decay = expf(-dt * expf(a.A_log[h]));
     const float D = a.D ? a.D[h] : 0.f;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -181,6 +208,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
     const TIn* xp = reinterpret_cast<const TIn*>(a.x) + (int64_t)h * a.P + row0;
     const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
 
+    float raw = tid < kSsmTile && first + tid < last ? ssm_raw_step(a, first + tid, h) : 0.f;
     auto stage = [&](int buf, int64_t t0) {
         const int count = last - t0 < kSsmTile ? (int)(last - t0) : kSsmTile;
         for (int i = tid; i < count * (N / E); i += kSsmThreads) {
@@ -193,7 +221,13 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
             ssm_cp_async16(&sx[buf][k][c], xp + (t0 + k) * a.x_stride + c);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        if (tid < count) ssm_step_size(a, t0 + tid, h, rate, bias, sdt[buf][tid], sa[buf][tid]);
+        if (tid < count) {
+            const float dt = ssm::softplus_series(raw + bias, a.threshold);
+            sdt[buf][tid] = dt;
+            sa[buf][tid] = expf(-dt * rate);
+        }
+        // the next tile's, so that nobody waits for it there
+        if (tid < kSsmTile && t0 + kSsmTile + tid < last) raw = ssm_raw_step(a, t0 + kSsmTile + tid, h);
     };
 
     const int li = tid % LPR, r0 = tid / LPR;

@@ -54,7 +54,6 @@ static_assert(256 * kStateRegs + 256 * kResultRegs + 128 * kOtherRegs <= kTcThre
 template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 constexpr uint32_t kPolls = 1u << 24;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFarStep = -128.f;               // log2 of a step's decay, bounded: 2^-128 leaves nothing either way
 
 // One segment of a request.
@@ -185,12 +184,6 @@ struct __align__(16) TcBars {
 };
 static_assert(sizeof(TcBars) <= 3072 && offsetof(TcBars, col) % 16 == 0 && offsetof(TcBars, diag) % 16 == 0, "barrier block; columns are read by 16 bytes");
 
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ uint64_t pack2(float x, float y)
 {
     uint64_t r;
@@ -382,24 +375,6 @@ struct TcThread {
         return a.dt_bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(a.dt)[i]) : reinterpret_cast<const float*>(a.dt)[i];
     }
 };
-
-// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1, by the series of log(1 + e) = 2 artanh(e / (2 + e)), whose argument is at
-// most 1 / 3: the first term left out is below 2^-25 of the sum.
-__device__ __forceinline__ float softplus_series(float x, float threshold)
-{
-    const float e = exp2_fast(-fabsf(x) * kLog2e);
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(2.0f + e));
-    const float u = e * r, q = u * u;
-    float p = fmaf(q, 1.f / 15, 1.f / 13);
-    p = fmaf(q, p, 1.f / 11);
-    p = fmaf(q, p, 1.f / 9);
-    p = fmaf(q, p, 1.f / 7);
-    p = fmaf(q, p, 1.f / 5);
-    p = fmaf(q, p, 1.f / 3);
-    p = fmaf(q, p, 1.f);
-    return x > threshold ? x : fmaf(2.f * u, p, fmaxf(x, 0.f));
-}
 
 // The warpgroup of a slice's state: X' and S.  A wait that gave up leaves the loop at the next barrier of the group, for
 // all its threads at once.
