@@ -171,8 +171,8 @@ struct TcCfg {
 };
 
 struct __align__(16) TcBars {
-    uint64_t full_c, full_b, full_x[2];
-    uint64_t gram, y_first, ds, y_full[2];                      // products done
+    uint64_t full_c, full_b[2], full_x[2];
+    uint64_t gram, y_first, ds[2], y_full[2];                   // products done
     uint64_t drain;
     // what each warp of the group concerned (M and Y: of both groups) arrives at, for all slices:
     uint64_t next_s, next_y, xs, ready;                         // S written, Y read, X' written, M and Y written
@@ -252,7 +252,8 @@ __device__ bool tc_issue(const int chunks_, uint32_t smem_, TcBars* bars, uint32
     const int chunks = (int)__reduce_max_sync(~0u, (unsigned)chunks_);
     const uint32_t tmem = __reduce_max_sync(~0u, tmem_), smem = __reduce_max_sync(~0u, smem_);
     const uint64_t c_k = tc::desc_sw128(smem + K::kC, 16, 1024), b_k = tc::desc_sw128(smem + K::kB, 16, 1024);
-    const uint64_t b_mn = tc::desc_sw128(smem + K::kB, K::kPanel, 1024), s_mn = tc::desc_sw128(smem + K::kS, K::kPanel, 1024);
+    const uint64_t b_mn = tc::desc_sw128(smem + K::kB, K::kPanel, 1024), other_mn = tc::desc_sw128(smem + K::kC, K::kPanel, 1024);
+    const uint64_t s_mn = tc::desc_sw128(smem + K::kS, K::kPanel, 1024);
     const uint64_t xs_mn = tc::desc_sw128(smem + K::kXs, K::kPanel, 1024), x_mn = tc::desc_sw128(smem + K::kX, K::kPanel, 1024);
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
@@ -260,7 +261,7 @@ __device__ bool tc_issue(const int chunks_, uint32_t smem_, TcBars* bars, uint32
         if constexpr (!ENDS) {
             if (!tc::mbar_wait(&bars->full_c, par, kPolls)) return false;
         }
-        if (!tc::mbar_wait(&bars->full_b, par, kPolls)) return false;
+        if (!tc::mbar_wait(&bars->full_b[par], (c >> 1) & 1, kPolls)) return false;
         tc::tc_fence_after();
         if constexpr (!ENDS) {
             if (leader) {
@@ -286,8 +287,8 @@ __device__ bool tc_issue(const int chunks_, uint32_t smem_, TcBars* bars, uint32
         if (leader) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)                              // eight steps with the high parts, eight with the low
-                tc::mma_f16_ss(tmem + kDsCol, b_mn + (k % 8) * 128, xs_mn + (k / 8) * 2 * kTile + (k % 8) * 128, id_ds, k > 0);
-            tc::mma_commit(&bars->ds);
+                tc::mma_f16_ss(tmem + kDsCol, (ENDS && par ? other_mn : b_mn) + (k % 8) * 128, xs_mn + (k / 8) * 2 * kTile + (k % 8) * 128, id_ds, k > 0);
+            tc::mma_commit(&bars->ds[par]);
         }
         if constexpr (!ENDS) {
             if (!tc::mbar_wait(&bars->ready, par, kPolls)) return false;
@@ -326,17 +327,17 @@ __device__ bool tc_load(const SsmCall& a, const TcWork& w, uint8_t* smem, TcBars
 #pragma unroll
             for (int p = 0; p < N / 64; ++p) tc::tma_load_2d(smem + at + p * K::kPanel, m, w.g * N + 64 * p, t, bar);
         };
-        if constexpr (ENDS) {
-            if (c > 0 && !tc::mbar_wait(&bars->ds, par ^ 1, kPolls)) return false;
-            load_x();                                             // X' of the chunk before the last one is done, too
-            load_tile(&bars->full_b, K::kB, bm);
+        if constexpr (ENDS) {                                     // B in two buffers, one of them C's
+            if (c > 1 && !tc::mbar_wait(&bars->ds[par], ((c >> 1) - 1) & 1, kPolls)) return false;
+            load_x();
+            load_tile(&bars->full_b[par], par ? K::kC : K::kB, bm);
         } else {
             if (c > 1 && !tc::mbar_wait(&bars->x_free[par], ((c >> 1) - 1) & 1, kPolls)) return false;
             load_x();
             if (c > 0 && !tc::mbar_wait(&bars->y_first, par ^ 1, kPolls)) return false;
             load_tile(&bars->full_c, K::kC, cm);
-            if (c > 0 && !tc::mbar_wait(&bars->ds, par ^ 1, kPolls)) return false;
-            load_tile(&bars->full_b, K::kB, bm);
+            if (c > 0 && !tc::mbar_wait(&bars->ds[par ^ 1], ((c - 1) >> 1) & 1, kPolls)) return false;
+            load_tile(&bars->full_b[par], K::kB, bm);
         }
     }
     return true;
@@ -452,7 +453,7 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         // ---- X' = weight x, in two parts
         t.wait(&bars->full_x[par], (c >> 1) & 1);
         uint8_t* x_row = smem + K::kX + (2 * s + par) * K::kPanel + r * 128;
-        if (len < kChunk) t.wait(&bars->full_b, par);
+        if (len < kChunk) t.wait(&bars->full_b[par], (c >> 1) & 1);
         if (live) {
             const uint64_t ww = pack2(weight, weight), minus = pack2(-1.f, -1.f);
 #pragma unroll 4
@@ -524,7 +525,7 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         // ---- S = gamma S + dS
         const uint64_t gg = pack2(gamma, gamma);
         if (c + 1 < w.chunks && !steps(c + 1, raw)) return false;      // while the product runs
-        t.wait(&bars->ds, par);
+        t.wait(&bars->ds[par], (c >> 1) & 1);
         tc::tc_fence_after();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -757,7 +758,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc::tmem_relinquish();
     }
     if constexpr (N < 128) {                                      // the states that are not there: zero rows of dS
-        for (int i = tid; i < K::kPanel / 16; i += kTcThreads) reinterpret_cast<uint4*>(smem + K::kB + K::kPanel)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < K::kPanel / 16; i += kTcThreads) {
+            reinterpret_cast<uint4*>(smem + K::kB + K::kPanel)[i] = make_uint4(0, 0, 0, 0);
+            if (ENDS) reinterpret_cast<uint4*>(smem + K::kC + K::kPanel)[i] = make_uint4(0, 0, 0, 0);
+        }
         tc::fence_proxy_async();
     }
     tc::tc_fence_before();
@@ -787,7 +791,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) {                                             // and the copies in flight land
                 for (uint32_t p = 0; p < 2; ++p) {
                     tc::mbar_wait(&bars->full_c, p, 1u << 16);
-                    tc::mbar_wait(&bars->full_b, p, 1u << 16);
+                    tc::mbar_wait(&bars->full_b[0], p, 1u << 16);
+                    tc::mbar_wait(&bars->full_b[1], p, 1u << 16);
                     tc::mbar_wait(&bars->full_x[0], p, 1u << 16);
                     tc::mbar_wait(&bars->full_x[1], p, 1u << 16);
                 }
