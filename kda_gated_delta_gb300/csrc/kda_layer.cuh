@@ -53,6 +53,7 @@ struct SsmCall {
     int32_t H, P, N, G;
     int32_t dt_bf16;
     float threshold;
+    int32_t short_len;        // requests of up to this many tokens go token by token; 0: all in the form that is called
 };
 
 struct NormCall {

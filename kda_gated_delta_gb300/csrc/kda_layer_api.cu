@@ -63,6 +63,7 @@ int32_t check_ssm(const kda_ssm_params* p, const void* x, int64_t x_stride, cons
     a->H = p->num_heads; a->P = p->head_dim; a->N = p->state_dim; a->G = p->num_groups;
     a->dt_bf16 = p->dt_dtype == KDA_BF16;
     a->threshold = p->softplus_threshold;
+    a->short_len = 0;
     return KDA_OK;
 }
 

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
     const int rows = a.P - row0 < R ? a.P - row0 : R;    // a multiple of 16
     int64_t first, last;
     if (!layer_rows(a.cu, (int32_t)b, a.T, first, last) && tid == 0) record_layer_error(kDevErrSeqlens);
-    if (first == last) return;
+    if (first == last || (a.short_len > 0 && last - first > a.short_len)) return;
     int64_t slot = a.idx[b];
     if (slot >= a.num_slots) {
         if (tid == 0) record_layer_error(kDevErrStateIndex);

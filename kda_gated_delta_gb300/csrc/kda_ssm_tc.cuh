@@ -101,9 +101,9 @@ __global__ void __launch_bounds__(1024) ssm_plan_kernel(const SsmCall a, const P
             c.slot = -1;
         }
         c.size = c.len;
-        c.n = c.len > 0;
+        c.n = c.len > a.short_len;
         const int64_t n = c.slot < 0 || c.len < 2 * (int64_t)plan.want ? 1 : c.len / plan.want;
-        if (n > 1) {
+        if (c.n > 0 && n > 1) {
             c.size = ((c.len + n - 1) / n + kChunk - 1) / kChunk * kChunk;
             c.n = (int32_t)((c.len + c.size - 1) / c.size);                  // whole chunks may need fewer
         }
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (ENDS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!ENDS && blockIdx.x == gridDim.x - 1) {
-        ssm_clear_unowned<TOut>(a, tid, kTcThreads);
+        if (a.short_len == 0) ssm_clear_unowned<TOut>(a, tid, kTcThreads);
         return;
     }
     if (place >= plan.found[ENDS ? 1 : 0]) return;
@@ -843,6 +843,7 @@ bool ssm_on_tensor_cores(const kda_ssm_params& p)
 struct SsmLayout {
     ssm::Plan plan;
     bool cut;                        // some request may have several segments
+    int32_t short_len;               // as in SsmCall
     size_t segments, followed, chains, states, decays, total;
 };
 
@@ -858,7 +859,12 @@ SsmLayout ssm_layout(const kda_ssm_params& p, int32_t n, int64_t T)
     w.cut = T >= 2 * want;
     w.plan.want = (int32_t)(want < (int64_t)1 << 30 ? want : (int64_t)1 << 30);
     const int64_t more = T / w.plan.want;                          // a request of k > 1 segments has k * want tokens or more
-    w.plan.max_segments = (int32_t)(n + more);
+    // A chunk costs the same for 1 token as for 128: up to some 32 tokens a request is done sooner token by token (64
+    // requests of 64 heads: 4 tokens 58 us against 193, 32 tokens 196 against 184).  Where the mean says that there
+    // may be such requests, they are taken out; which they are, the kernels see.
+    w.short_len = T < 64 * (int64_t)n ? 32 : 0;
+    const int64_t requests = w.short_len && T / (w.short_len + 1) < n ? T / (w.short_len + 1) : n;
+    w.plan.max_segments = (int32_t)(requests + more);
     auto round = [](size_t x) { return (x + 255) / 256 * 256; };
     w.segments = 256;
     w.plan.max_cuts = w.cut ? (int32_t)more : 0;
@@ -867,7 +873,7 @@ SsmLayout ssm_layout(const kda_ssm_params& p, int32_t n, int64_t T)
     w.states = w.chains + round(4 * (size_t)w.plan.max_cuts);
     const size_t held = w.cut ? (size_t)more : 0;
     w.decays = w.states + round(held * 4 * p.num_heads * p.head_dim * p.state_dim);
-    w.total = w.decays + round(held * 4 * p.num_heads);
+    w.total = w.plan.max_segments ? w.decays + round(held * 4 * p.num_heads) : 0;
     return w;
 }
 
@@ -918,9 +924,10 @@ cudaError_t launch_after(void (*kernel)(P...), int64_t blocks, int threads, int 
 }
 
 template <int N, typename TOut>
-cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* workspace, cudaStream_t s)
+cudaError_t ssm_tc_launch(const kda_ssm_params& p, SsmCall a, void* workspace, cudaStream_t s)
 {
     SsmLayout w = ssm_layout(p, a.n, a.T);
+    a.short_len = w.short_len;
     uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
     w.plan.found = reinterpret_cast<int32_t*>(base);
     w.plan.segments = reinterpret_cast<ssm::Segment*>(base + w.segments);
@@ -928,8 +935,11 @@ cudaError_t ssm_tc_launch(const kda_ssm_params& p, const SsmCall& a, void* works
     w.plan.chains = reinterpret_cast<int32_t*>(base + w.chains);
     w.plan.states = reinterpret_cast<float*>(base + w.states);
     w.plan.decays = reinterpret_cast<float*>(base + w.decays);
+    cudaError_t e = cudaSuccess;
+    if (w.short_len) e = ssm_dispatch<false>(p, a, s);
+    if (e != cudaSuccess || w.plan.max_segments == 0) return e;
     CUtensorMap xm, bm, cm, om = {};
-    cudaError_t e = ssm_map(&xm, a.x, a.T, (int64_t)a.H * a.P, a.x_stride, ssm::kChunk);
+    e = ssm_map(&xm, a.x, a.T, (int64_t)a.H * a.P, a.x_stride, ssm::kChunk);
     if (e == cudaSuccess) e = ssm_map(&bm, a.B, a.T, (int64_t)a.G * a.N, a.b_stride, ssm::kChunk);
     if (e == cudaSuccess) e = ssm_map(&cm, a.C, a.T, (int64_t)a.G * a.N, a.c_stride, ssm::kChunk);
     if (e == cudaSuccess && sizeof(TOut) == 2) e = ssm_map(&om, a.out, a.T, (int64_t)a.H * a.P, (int64_t)a.H * a.P, 32);

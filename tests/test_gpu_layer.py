@@ -396,6 +396,75 @@ def test_captured_layer_and_other_stream():
         assert torch.equal(got, want) and all(torch.equal(u, v) for u, v in zip(a, c))
 
 
+def test_places_past_32_bits():
+    """States, rows and outputs whose offsets pass 2^31 elements."""
+    g = gen(22)
+    H, P, N, G = 16, 64, 128, 1
+    slots = 16500                                            # 2^31.01 states
+    pool = torch.empty(slots, H, P, N, device=DEV)
+    x, dt, B, C, A_log, dt_bias, D = ssm_inputs(23, [140, 3], H, P, N, G, BF16)
+    for s in (0, slots - 1):
+        pool[s] = normal(gen(s), H, P, N)
+    small = torch.stack([pool[0], pool[-1]])
+    cu = ref.lengths_to_cu([140, 3], DEV)
+    want = kda.ssm_prefill(x, dt, B, C, A_log, cu, small, idx([0, 1]), dt_bias=dt_bias, D=D)
+    got = kda.ssm_prefill(x, dt, B, C, A_log, cu, pool, idx([0, slots - 1]), dt_bias=dt_bias, D=D)
+    assert torch.equal(got, want) and torch.equal(pool[0], small[0]) and torch.equal(pool[-1], small[1])
+    want = kda.ssm_decode(x[:2], dt[:2], B[:2], C[:2], A_log, small, idx([1, 0]), dt_bias=dt_bias, D=D)
+    got = kda.ssm_decode(x[:2], dt[:2], B[:2], C[:2], A_log, pool, idx([slots - 1, 0]), dt_bias=dt_bias, D=D)
+    assert torch.equal(got, want) and torch.equal(pool[0], small[0]) and torch.equal(pool[-1], small[1])
+    del pool
+    T, C_, wide = 70000, 64, 32768                           # 2^31.1 elements of rows
+    rows = torch.empty(T, wide, dtype=BF16, device=DEV)
+    rows[:, :C_] = normal(g, T, C_, dtype=BF16)
+    w, state = normal(g, C_, 4), torch.zeros(2, 3, C_, dtype=BF16, device=DEV)
+    cu = ref.lengths_to_cu([69000, 1000], DEV)
+    want = kda.causal_conv(rows[:, :C_].contiguous(), w, state.clone(), idx([0, 1]), cu)
+    assert torch.equal(kda.causal_conv(rows[:, :C_], w, state, idx([0, 1]), cu), want)
+    x = rows[:, :C_].unflatten(1, (2, 32))
+    assert torch.equal(kda.group_norm(x), kda.group_norm(x.contiguous()))
+    y = kda.group_norm(rows.view(T, 64, 512)[-3:])
+    assert torch.equal(kda.group_norm(rows.view(T, 64, 512), out=rows.view(T, 64, 512).clone())[-3:], y)
+
+
+@pytest.mark.parametrize("lens", [[5, 400, 0, 32, 33, 1, 2, 3, 4, 5, 6, 7], [1] * 30 + [300], [32] * 6], ids=str)
+def test_ssm_short_requests_beside_long_ones(lens):
+    """Requests of few tokens go token by token, the others of the same call in chunks; rows of no request get zeros."""
+    H, P, N, G = 2, 64, 128, 1
+    x, dt, B, C, A_log, dt_bias, D = ssm_inputs(24, lens + [9], H, P, N, G, BF16)
+    slots = list(range(len(lens)))
+    slots[1], slots[3] = -1, -1
+    pool = normal(gen(25), len(lens), H, P, N)
+    want, state, y_mag, mags = ref.ssm(x, dt, B, C, A_log, pool, slots + [-1], lens + [9], dt_bias, D)
+    got = kda.ssm_prefill(x, dt, B, C, A_log, ref.lengths_to_cu(lens, DEV), pool, idx(slots), dt_bias=dt_bias, D=D)
+    assert kda.check_device_errors() == 2                      # nine rows behind the last request
+    yb, sb = ssm_bounds(want, y_mag, mags, max(lens), N, BF16, True)
+    ref.within(got, want, yb)
+    ref.within(pool, state, sb)
+
+
+def test_calls_on_two_streams_at_once():
+    """Two layers' prompts side by side, each with its own workspace and states."""
+    lens, H, P, N, G = [700, 90], 4, 64, 128, 1
+    ins = [ssm_inputs(26 + i, lens, H, P, N, G, BF16) for i in range(2)]
+    cu = ref.lengths_to_cu(lens, DEV)
+    pools = [normal(gen(28 + i), 2, H, P, N) for i in range(2)]
+    alone = []
+    for v, p in zip(ins, pools):
+        q = p.clone()
+        alone.append((kda.ssm_prefill(*v[:5], cu, q, idx([0, 1]), dt_bias=v[5], D=v[6]), q))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for v, p, s in zip(ins, pools, streams):
+            with torch.cuda.stream(s):
+                q = p.clone()
+                got.append((kda.ssm_prefill(*v[:5], cu, q, idx([0, 1]), dt_bias=v[5], D=v[6]), q))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(got, alone) for a, b in zip(x, y))
+
+
 def test_bad_tables_are_recorded():
     """Slots past the pool, rows of no request and lengths past the tokens: zeros and a code, no access out of range."""
     g = gen(18)
