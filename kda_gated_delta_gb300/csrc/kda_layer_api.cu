@@ -22,7 +22,7 @@ constexpr int64_t kMaxStride = (int64_t)1 << 31;        // a row's offset then s
 int32_t check_ssm_params(const kda_ssm_params* p)
 {
     if (!p || p->num_heads <= 0 || p->num_groups <= 0 || p->num_heads % p->num_groups != 0 ||
-        !(p->softplus_threshold == p->softplus_threshold))
+        !(p->softplus_threshold >= 0.f))
         return KDA_ERR_INVALID_ARG;
     const int32_t P = p->head_dim, N = p->state_dim;
     if ((P != 16 && P != 32 && P != 64 && P != 128) || (N != 16 && N != 32 && N != 64 && N != 128 && N != 256) ||

@@ -81,11 +81,12 @@ struct Plan {
 // Lists the segments, the longest first (by 64 classes of length), so that no long one starts last.
 __global__ void __launch_bounds__(1024) ssm_plan_kernel(const SsmCall a, const Plan plan)
 {
-    __shared__ int32_t bucket[65], longest, states, cuts[2];
+    __shared__ int32_t bucket[65], longest, all, states[2], cuts[2];
     const int tid = threadIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid < 65) bucket[tid] = 0;
-    if (tid == 0) longest = 1, states = 0, cuts[0] = 0, cuts[1] = 0;
+    if (tid < 2) states[tid] = 0, cuts[tid] = 0;
+    if (tid == 0) longest = 1;
     struct Cut {
         int64_t first, len, size;                // rows; `size` tokens a segment but the last
         int32_t slot, n;                         // segments
@@ -122,40 +123,44 @@ __global__ void __launch_bounds__(1024) ssm_plan_kernel(const SsmCall a, const P
     for (int pass = 0; pass < 2; ++pass) {
         for (int32_t b = tid; b < a.n; b += 1024) {
             const Cut c = of(b);
-            const int32_t base = pass == 1 && c.n > 1 ? atomicAdd(&states, c.n) : 0;
+            const int32_t base = c.n > 1 ? atomicAdd(&states[pass], c.n) : 0;
             for (int32_t k = 0; k < c.n; ++k) {
                 const int64_t at = k * c.size, part = c.len - at < c.size ? c.len - at : c.size;
                 const int key = max(0, 63 - (int)((float)part * scale));
                 const int32_t place = atomicAdd(&bucket[pass == 0 ? key + 1 : key], 1);
-                if (pass == 0 || place >= plan.max_segments) continue;
+                if (pass == 0) continue;
                 Segment s;
                 s.b = b; s.slot = c.slot; s.first = (int32_t)(c.first + at); s.len = (int32_t)part;
                 s.k = k; s.count = c.n; s.base = base; s.pad = 0;
                 plan.segments[place] = s;
-                if (k + 1 < c.n) {
-                    const int32_t i = atomicAdd(&cuts[0], 1);
-                    if (i < plan.max_cuts) plan.followed[i] = place;
-                }
-                if (k == 0 && c.n > 1) {
-                    const int32_t i = atomicAdd(&cuts[1], 1);
-                    if (i < plan.max_cuts) plan.chains[i] = place;
-                }
+                if (k + 1 < c.n) plan.followed[atomicAdd(&cuts[0], 1)] = place;
+                if (k == 0 && c.n > 1) plan.chains[atomicAdd(&cuts[1], 1)] = place;
             }
         }
         __syncthreads();
         if (pass == 0 && tid < 32) {                                         // first place of each class
-            int32_t v0 = bucket[2 * tid + 1], v1 = bucket[2 * tid + 2], sum = v0 + v1;
+            const int32_t v0 = bucket[2 * tid + 1], v1 = bucket[2 * tid + 2];
+            int32_t sum = v0 + v1;
+#pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int32_t u = __shfl_up_sync(~0u, sum, off);
                 if (tid >= off) sum += u;
             }
             bucket[2 * tid + 1] = sum - v1;
             bucket[2 * tid + 2] = sum;
-            if (tid == 31) plan.found[0] = sum < plan.max_segments ? sum : plan.max_segments;
+            if (tid == 31) all = sum;
         }
         __syncthreads();
+        // Requests of a sound table share no rows, and then the workspace holds their segments and states.  If it does
+        // not, nothing is done: the bounds are those of every write here and in the kernels behind.
+        if (pass == 0 && (all > plan.max_segments || states[0] > plan.max_cuts)) {
+            if (tid < 3) plan.found[tid] = 0;
+            if (tid == 0) record_layer_error(kDevErrSeqlens);
+            return;
+        }
     }
-    if (tid < 2) plan.found[1 + tid] = cuts[tid] < plan.max_cuts ? cuts[tid] : plan.max_cuts;
+    if (tid == 0) plan.found[0] = all;
+    if (tid < 2) plan.found[1 + tid] = cuts[tid];
 }
 
 // ---- the chunk kernel ------------------------------------------------------------------------------

@@ -423,6 +423,7 @@ def test_places_past_32_bits():
     assert torch.equal(kda.causal_conv(rows[:, :C_], w, state, idx([0, 1]), cu), want)
     x = rows[:, :C_].unflatten(1, (2, 32))
     assert torch.equal(kda.group_norm(x), kda.group_norm(x.contiguous()))
+    rows[-3:] = normal(g, 3, wide, dtype=BF16)
     y = kda.group_norm(rows.view(T, 64, 512)[-3:])
     assert torch.equal(kda.group_norm(rows.view(T, 64, 512), out=rows.view(T, 64, 512).clone())[-3:], y)
 
@@ -441,6 +442,48 @@ def test_ssm_short_requests_beside_long_ones(lens):
     yb, sb = ssm_bounds(want, y_mag, mags, max(lens), N, BF16, True)
     ref.within(got, want, yb)
     ref.within(pool, state, sb)
+
+
+def test_ssm_many_requests():
+    """More requests than the planning CTA has threads, in no order of length."""
+    H, P, N, G = 1, 64, 64, 1
+    lens = [50 + (37 * i) % 61 for i in range(1100)]            # 80 on average: all in chunks
+    x, dt, B, C, A_log, dt_bias, D = ssm_inputs(30, lens, H, P, N, G, BF16)
+    slots = [(7 * i + 3) % 1103 for i in range(1100)]
+    pool = normal(gen(31), 1103, H, P, N)
+    want, state, y_mag, mags = ref.ssm(x, dt, B, C, A_log, pool, slots, lens, dt_bias, D)
+    got = kda.ssm_prefill(x, dt, B, C, A_log, ref.lengths_to_cu(lens, DEV), pool, idx(slots), dt_bias=dt_bias, D=D)
+    yb, sb = ssm_bounds(want, y_mag, mags, max(lens), N, BF16, True)
+    ref.within(got, want, yb)
+    ref.within(pool, state, sb)
+
+
+@pytest.mark.parametrize("lens", [[5000, 40, 3000], [9, 31, 140, 2]], ids=str)
+def test_ssm_same_call_same_bits(lens):
+    x, dt, B, C, A_log, dt_bias, D = ssm_inputs(32, lens, 2, 64, 128, 1, BF16)
+    pool = normal(gen(33), len(lens), 2, 64, 128)
+    first = None
+    for _ in range(10):
+        p = pool.clone()
+        y = kda.ssm_prefill(x, dt, B, C, A_log, ref.lengths_to_cu(lens, DEV), p, idx(list(range(len(lens)))), dt_bias=dt_bias, D=D)
+        first = first or (y, p)
+        assert torch.equal(y, first[0]) and torch.equal(p, first[1])
+
+
+def test_overlapping_requests_are_recorded():
+    """A table whose requests share rows has more segments and states than the workspace holds: recorded, nothing written
+    outside the outputs and slots."""
+    g = gen(34)
+    T, n, H, P, N = 6000, 20, 1, 64, 128
+    x, dt, B, C, A_log, dt_bias, D = ssm_inputs(35, [T], H, P, N, 1, BF16)
+    cu = torch.tensor([0, T] * (n // 2) + [T], dtype=torch.int32, device=DEV)
+    need = kda.ssm_prefill_workspace_size(H, P, N, 1, n, T)
+    ws = torch.full((need + 4096,), 77, dtype=torch.uint8, device=DEV)
+    pool = normal(g, n + 1, H, P, N)
+    before = pool.clone()
+    kda.ssm_prefill(x, dt, B, C, A_log, cu, pool, idx(list(range(n))), dt_bias=dt_bias, D=D, workspace=ws[:need])
+    assert kda.check_device_errors() == 2
+    assert bool((ws[need:] == 77).all()) and torch.equal(pool[n], before[n])
 
 
 def test_calls_on_two_streams_at_once():

@@ -67,7 +67,7 @@ def test_ssm_defaults(L):
 
 @pytest.mark.parametrize("call", [_prefill, _decode])
 def test_ssm_checks(L, call):
-    for kw in (dict(H=0), dict(G=0), dict(H=3), dict(softplus_threshold=float("nan"))):
+    for kw in (dict(H=0), dict(G=0), dict(H=3), dict(softplus_threshold=float("nan")), dict(softplus_threshold=-1.0)):
         assert call(L, p=_p(**kw)) == -1, kw
     for kw in (dict(P=48), dict(P=256), dict(P=8), dict(N=8), dict(N=96), dict(N=512), dict(io_dtype=2), dict(dt_dtype=-1), dict(out_dtype=3)):
         assert call(L, p=_p(**kw)) == -2, kw
