@@ -60,7 +60,7 @@ __device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + ex
 
 // ---- error words --------------------------------------------------------------------------------
 // Read a translation unit's device error word, and clear it if it holds a code.  A word without one is not written:
-// a copy takes some 10 us, and there are six words (a check takes 61 us; with all of them cleared always it took 83).
+// a copy takes some 10 us, and there are seven words (with six a check took 61 us; with all of them cleared always 83).
 inline cudaError_t read_and_clear(int32_t& word, int32_t* code)
 {
     const int32_t zero = 0;

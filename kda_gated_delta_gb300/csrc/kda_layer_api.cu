@@ -53,7 +53,7 @@ int32_t check_ssm(const kda_ssm_params* p, const void* x, int64_t x_stride, cons
     if (x_stride >= kMaxStride || b_stride >= kMaxStride || c_stride >= kMaxStride || dt_stride >= kMaxStride) return KDA_ERR_UNSUPPORTED;
     if (misaligned(x) || misaligned(B) || misaligned(C) || misaligned(pool) || misaligned(out) || odd(dt, size_of(p->dt_dtype)))
         return KDA_ERR_MISALIGNED;
-    if (T >= kMaxTokens || (int64_t)num_seqs * p->num_heads >= ((int64_t)1 << 30) / (p->head_dim >= 32 ? p->head_dim / 16 : 1))
+    if (T >= kMaxTokens || (int64_t)num_seqs * p->num_heads >= ((int64_t)1 << 29) / (p->head_dim / 16))
         return KDA_ERR_UNSUPPORTED;
     a->x = x; a->dt = dt; a->B = B; a->C = C;
     a->x_stride = x_stride; a->dt_stride = dt_stride; a->b_stride = b_stride; a->c_stride = c_stride;

@@ -7,9 +7,13 @@
 // across the tokens; y_t takes log2(LPR) shuffles a row.
 //
 //   ssm_token_kernel   one token per request: bound by the state's bytes, read and written once.
+//                      256 requests of 64 heads x 64 x 128 states: 155 us, the 157 us of the measured copy rate.
 //   ssm_rows_kernel    packed prompts, tokens staged through shared memory: 3 fp32 operations a state and
-//                      token, bound by the fp32 pipes; the path of fp32 inputs and of the shapes that the
-//                      tensor-core form (kda_ssm_tc.cuh) does not take.
+//                      token; the path of fp32 inputs, of the shapes that the tensor-core form
+//                      (kda_ssm_tc.cuh) does not take and of requests of few tokens.  Bound by the fp32 pipes when
+//                      it fills the SMs, by the chain loads - sums - shuffles of a token (some 260 cycles with one warp a
+//                      scheduler: 76 us for 5 requests of up to 583 tokens of 8 heads) when it does not; long
+//                      requests are then cut into segments.
 #pragma once
 
 #include <type_traits>
@@ -47,6 +51,139 @@ __device__ __forceinline__ float softplus_series(float x, float threshold)
     p = fmaf(q, p, 1.f / 3);
     p = fmaf(q, p, 1.f);
     return x > threshold ? x : fmaf(2.f * u, p, fmaxf(x, 0.f));
+}
+
+constexpr int kChunk = 128;                      // segments are whole chunks of the tensor-core form, but a request's last
+
+// One segment of a request.
+struct Segment {
+    int32_t b, slot;                             // slot < 0: padding, zeros
+    int32_t first, len;
+    int32_t k, count;                            // segment k of count
+    int32_t base;                                // count > 1: the request's first state in the workspace
+    int32_t pad;
+};
+
+// The call's segments, the states between them and how the slices are paired.
+struct Plan {
+    Segment* segments;
+    int32_t* found;                              // numbers of segments, of segments that another follows, of requests in several
+    int32_t* followed;                           // places of segments that another follows
+    int32_t* chains;                             // places of the first segments of requests in several
+    float* states;                               // [..][H][P][N]: state before segment k of a request at base + k
+    float* decays;                               // [..][H]: log2 of a segment's whole decay, at base + k + 1
+    int32_t max_segments, max_cuts;              // max_cuts bounds both lists
+    int32_t pairs_per_group, pairs;              // slice pairs
+    int32_t want;                                // tokens of a segment that fill the SMs
+};
+
+// Lists the segments, the longest first (by 64 classes of length), so that no long one starts last.
+__global__ void __launch_bounds__(1024) ssm_plan_kernel(const SsmCall a, const Plan plan)
+{
+    __shared__ int32_t bucket[65], longest, all, states[2], cuts[2];
+    const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid < 65) bucket[tid] = 0;
+    if (tid < 2) states[tid] = 0, cuts[tid] = 0;
+    if (tid == 0) longest = 1;
+    struct Cut {
+        int64_t first, len, size;                // rows; `size` tokens a segment but the last
+        int32_t slot, n;                         // segments
+    };
+    auto cut = [&](int32_t b) -> Cut {
+        Cut c;
+        int64_t last;
+        c.slot = a.idx[b];
+        if (!layer_rows(a.cu, b, a.T, c.first, last)) record_layer_error(kDevErrSeqlens);
+        c.len = last - c.first;
+        if (c.slot >= a.num_slots) {
+            record_layer_error(kDevErrStateIndex);
+            c.slot = -1;
+        }
+        c.size = c.len;
+        c.n = c.len > a.short_len;
+        const int64_t n = c.slot < 0 || c.len < 2 * (int64_t)plan.want ? 1 : c.len / plan.want;
+        if (c.n > 0 && n > 1) {
+            c.size = ((c.len + n - 1) / n + kChunk - 1) / kChunk * kChunk;
+            c.n = (int32_t)((c.len + c.size - 1) / c.size);                  // whole chunks may need fewer
+        }
+        return c;
+    };
+    Cut mine = {};
+    if (tid < a.n) mine = cut(tid);
+    auto of = [&](int32_t b) { return b == tid ? mine : cut(b); };           // looked up once for up to 1,024 requests
+    __syncthreads();
+    for (int32_t b = tid; b < a.n; b += 1024) {
+        const Cut c = of(b);
+        if (c.n > 0) atomicMax(&longest, (int32_t)c.size);
+    }
+    __syncthreads();
+    const float scale = 63.f / (float)longest;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int32_t b = tid; b < a.n; b += 1024) {
+            const Cut c = of(b);
+            const int32_t base = c.n > 1 ? atomicAdd(&states[pass], c.n) : 0;
+            for (int32_t k = 0; k < c.n; ++k) {
+                const int64_t at = k * c.size, part = c.len - at < c.size ? c.len - at : c.size;
+                const int key = max(0, 63 - (int)((float)part * scale));
+                const int32_t place = atomicAdd(&bucket[pass == 0 ? key + 1 : key], 1);
+                if (pass == 0) continue;
+                Segment s;
+                s.b = b; s.slot = c.slot; s.first = (int32_t)(c.first + at); s.len = (int32_t)part;
+                s.k = k; s.count = c.n; s.base = base; s.pad = 0;
+                plan.segments[place] = s;
+                if (k + 1 < c.n) plan.followed[atomicAdd(&cuts[0], 1)] = place;
+                if (k == 0 && c.n > 1) plan.chains[atomicAdd(&cuts[1], 1)] = place;
+            }
+        }
+        __syncthreads();
+        if (pass == 0 && tid < 32) {                                         // first place of each class
+            const int32_t v0 = bucket[2 * tid + 1], v1 = bucket[2 * tid + 2];
+            int32_t sum = v0 + v1;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int32_t u = __shfl_up_sync(~0u, sum, off);
+                if (tid >= off) sum += u;
+            }
+            bucket[2 * tid + 1] = sum - v1;
+            bucket[2 * tid + 2] = sum;
+            if (tid == 31) all = sum;
+        }
+        __syncthreads();
+        // Requests of a sound table share no rows, and then the workspace holds their segments and states.  If it does
+        // not, nothing is done: the bounds are those of every write here and in the kernels behind.
+        if (pass == 0 && (all > plan.max_segments || states[0] > plan.max_cuts)) {
+            if (tid < 3) plan.found[tid] = 0;
+            if (tid == 0) record_layer_error(kDevErrSeqlens);
+            return;
+        }
+    }
+    if (tid == 0) plan.found[0] = all;
+    if (tid < 2) plan.found[1 + tid] = cuts[tid];
+}
+
+// The state before each segment: of the first the pool's, then S = decay S + (the segment's own).
+// blockIdx.x: (request in several segments, head, 1024 states).
+__global__ void __launch_bounds__(256) ssm_chain_kernel(const SsmCall a, const Plan plan)
+{
+    const int per = (a.P * a.N + 1023) / 1024, place = (int)(blockIdx.x % per) * 1024 + threadIdx.x * 4;
+    const int64_t bh = blockIdx.x / per;
+    const int32_t i = (int32_t)(bh / a.H), h = (int32_t)(bh - (int64_t)i * a.H);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (i >= plan.found[2] || place >= a.P * a.N) return;
+    const Segment seg = plan.segments[plan.chains[i]];
+    const int64_t all = (int64_t)a.H * a.P * a.N, at = (int64_t)h * a.P * a.N + place;
+    float4 v = *reinterpret_cast<const float4*>(a.pool + seg.slot * all + at);
+    float* to = plan.states + seg.base * all + at;
+    *reinterpret_cast<float4*>(to) = v;
+    for (int k = 1; k < seg.count; ++k) {
+        to += all;
+        const float decay = exp2_fast(plan.decays[(int64_t)(seg.base + k) * a.H + h]);
+        const float4 e = *reinterpret_cast<const float4*>(to);
+        v = make_float4(fmaf(decay, v.x, e.x), fmaf(decay, v.y, e.y), fmaf(decay, v.z, e.z), fmaf(decay, v.w, e.w));
+        *reinterpret_cast<float4*>(to) = v;
+    }
 }
 }  // namespace ssm
 
@@ -164,10 +301,10 @@ __device__ __forceinline__ void ssm_clear_unowned(const SsmCall& a, int tid, int
 }
 
 
-// Packed prompts.  blockIdx.x: (request, head, slab of STEPS * ROWS rows); one CTA more gives zeros to rows of
-// no request.
-template <int N, int STEPS, typename TIn, typename TOut>
-__global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, int splits)
+// Packed prompts.  blockIdx.x: (request, or segment of the plan; head; slab of STEPS * ROWS rows); one CTA more gives
+// zeros to rows of no request.  ENDS: only the state that a segment leaves when it starts from zero.
+template <int N, int STEPS, bool ENDS, typename TIn, typename TOut>
+__global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, const ssm::Plan plan, int splits)
 {
     using Sh = SsmShape<N>;
     constexpr int NV4 = Sh::NV4, LPR = Sh::LPR, R = Sh::ROWS * STEPS, E = 16 / (int)sizeof(TIn);
@@ -178,23 +315,36 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
     __shared__ __align__(16) TOut sy[kSsmTile][XR];
     const int tid = threadIdx.x;
     const int64_t bh = blockIdx.x / splits;
-    const int64_t b = bh / a.H;
+    int64_t b = bh / a.H;
     TOut* out = reinterpret_cast<TOut*>(a.out);
     const int64_t width = (int64_t)a.H * a.P;
-    if (b >= a.n) {
+    if (plan.segments) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (ENDS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
+    if (!ENDS && blockIdx.x == gridDim.x - 1) {
         ssm_clear_unowned<TOut>(a, tid, kSsmThreads);
         return;
     }
     const int h = (int)(bh - b * a.H);
     const int row0 = (int)(blockIdx.x - bh * splits) * R;
     const int rows = a.P - row0 < R ? a.P - row0 : R;    // a multiple of 16
-    int64_t first, last;
-    if (!layer_rows(a.cu, (int32_t)b, a.T, first, last) && tid == 0) record_layer_error(kDevErrSeqlens);
-    if (first == last || (a.short_len > 0 && last - first > a.short_len)) return;
-    int64_t slot = a.idx[b];
-    if (slot >= a.num_slots) {
-        if (tid == 0) record_layer_error(kDevErrStateIndex);
-        slot = -1;
+    int64_t first, last, slot;
+    ssm::Segment seg = {};
+    if (plan.segments) {
+        if (b >= plan.found[ENDS ? 1 : 0]) return;
+        seg = plan.segments[ENDS ? plan.followed[b] : b];
+        first = seg.first;
+        last = first + seg.len;
+        slot = seg.slot;
+    } else {
+        if (!layer_rows(a.cu, (int32_t)b, a.T, first, last) && tid == 0) record_layer_error(kDevErrSeqlens);
+        if (first == last || (a.short_len > 0 && last - first > a.short_len)) return;
+        slot = a.idx[b];
+        if (slot >= a.num_slots) {
+            if (tid == 0) record_layer_error(kDevErrStateIndex);
+            slot = -1;
+        }
     }
     out += (int64_t)h * a.P + row0;
     if (slot < 0) {
@@ -214,7 +364,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
         for (int i = tid; i < count * (N / E); i += kSsmThreads) {
             const int k = i / (N / E), c = i % (N / E) * E;
             ssm_cp_async16(&sB[buf][k][c], Bp + (t0 + k) * a.b_stride + c);
-            ssm_cp_async16(&sC[buf][k][c], Cp + (t0 + k) * a.c_stride + c);
+            if (!ENDS) ssm_cp_async16(&sC[buf][k][c], Cp + (t0 + k) * a.c_stride + c);
         }
         for (int i = tid; i < count * (rows / E); i += kSsmThreads) {
             const int k = i / (rows / E), c = i % (rows / E) * E;
@@ -231,14 +381,17 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
     };
 
     const int li = tid % LPR, r0 = tid / LPR;
-    float* state = a.pool + ((slot * a.H + h) * a.P + row0 + r0) * N + 4 * li;
+    // where the state comes from and goes to: the pool, or the states between segments
+    const int64_t all = (int64_t)a.H * a.P * N, mine = ((int64_t)h * a.P + row0 + r0) * N + 4 * li;
+    const float* state = (seg.count > 1 ? plan.states + (seg.base + seg.k) * all : a.pool + slot * all) + mine;
+    float spent = 0.f;                                   // log2 of the decays so far
     float st[STEPS][4 * NV4];
     stage(0, first);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
         for (int j = 0; j < NV4; ++j) {
-            const float4 v = r0 + s * Sh::ROWS < rows ? *reinterpret_cast<const float4*>(state + (int64_t)s * Sh::ROWS * N + 4 * LPR * j)
+            const float4 v = !ENDS && r0 + s * Sh::ROWS < rows ? *reinterpret_cast<const float4*>(state + (int64_t)s * Sh::ROWS * N + 4 * LPR * j)
                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             st[s][4 * j] = v.x; st[s][4 * j + 1] = v.y; st[s][4 * j + 2] = v.z; st[s][4 * j + 3] = v.w;
         }
@@ -248,6 +401,8 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();                                 // this tile is in, the last one's outputs are out
         if (t0 + kSsmTile < last) stage(buf ^ 1, t0 + kSsmTile);
+        if (ENDS && tid == 0)
+            for (int k = 0; k < count; ++k) spent -= sdt[buf][k] * rate * ssm::kLog2e;
         // K tokens at a time: their row sums are independent and go through the shuffles together
         constexpr int K = 4;
         const auto tokens = [&](auto many, int k0) {
@@ -261,7 +416,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
 #pragma unroll
                 for (int j = 0; j < NV4; ++j) {
                     load_floats<TIn, 4>(&sB[buf][k][4 * (li + LPR * j)], Bv + 4 * j);
-                    load_floats<TIn, 4>(&sC[buf][k][4 * (li + LPR * j)], Cv + 4 * j);
+                    if (!ENDS) load_floats<TIn, 4>(&sC[buf][k][4 * (li + LPR * j)], Cv + 4 * j);
                 }
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) {
@@ -270,11 +425,12 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
 #pragma unroll
                     for (int i = 0; i < 4 * NV4; ++i) {
                         st[s][i] = fmaf(u, Bv[i], decay * st[s][i]);
-                        sum[i & 1] = fmaf(st[s][i], Cv[i], sum[i & 1]);
+                        if (!ENDS) sum[i & 1] = fmaf(st[s][i], Cv[i], sum[i & 1]);
                     }
                     y[s][kk] = sum[0] + sum[1];
                 }
             }
+            if (ENDS) return;
 #pragma unroll
             for (int off = LPR / 2; off > 0; off >>= 1)
 #pragma unroll
@@ -297,19 +453,23 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
 #pragma unroll 1
         for (; k < count; ++k) tokens(std::integral_constant<int, 1>(), k);
         __syncthreads();
+        if (ENDS) continue;
         constexpr int O = 16 / (int)sizeof(TOut);
         for (int i = tid; i < count * (rows / O); i += kSsmThreads) {
             const int k = i / (rows / O), c = i % (rows / O) * O;
             *reinterpret_cast<uint4*>(out + (t0 + k) * width + c) = *reinterpret_cast<const uint4*>(&sy[k][c]);
         }
     }
+    if (!ENDS && seg.k + 1 < seg.count) return;              // only a request's last segment has its final state
+    float* to = (ENDS ? plan.states + (seg.base + seg.k + 1) * all : a.pool + slot * all) + mine;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
         for (int j = 0; j < NV4; ++j)
             if (r0 + s * Sh::ROWS < rows)
-                *reinterpret_cast<float4*>(state + (int64_t)s * Sh::ROWS * N + 4 * LPR * j) =
+                *reinterpret_cast<float4*>(to + (int64_t)s * Sh::ROWS * N + 4 * LPR * j) =
                     make_float4(st[s][4 * j], st[s][4 * j + 1], st[s][4 * j + 2], st[s][4 * j + 3]);
+    if (ENDS && tid == 0 && row0 == 0) plan.decays[(int64_t)(seg.base + seg.k + 1) * a.H + h] = spent;
 }
 
 namespace {
@@ -337,28 +497,116 @@ cudaError_t ssm_token_steps(const SsmCall& a, cudaStream_t s)
     return ssm_token_launch<N, 1, TIn, TOut>(a, s);
 }
 
+// Launched while the kernel before it in the stream runs; it waits for that one itself (griddepcontrol).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int64_t blocks, int threads, int smem, cudaStream_t stream, const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+bool ssm_on_tensor_cores(const kda_ssm_params& p)
+{
+    return p.io_dtype == KDA_BF16 && (p.head_dim == 64 || p.head_dim == 128) && p.state_dim <= 128;
+}
+
+struct SsmLayout {
+    ssm::Plan plan;
+    bool cut;                        // some request may have several segments
+    int32_t short_len;               // as in SsmCall
+    size_t segments, followed, chains, states, decays, total;
+
+    void place(void* workspace)
+    {
+        uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
+        plan.found = reinterpret_cast<int32_t*>(base);
+        plan.segments = reinterpret_cast<ssm::Segment*>(base + segments);
+        plan.followed = reinterpret_cast<int32_t*>(base + followed);
+        plan.chains = reinterpret_cast<int32_t*>(base + chains);
+        plan.states = reinterpret_cast<float*>(base + states);
+        plan.decays = reinterpret_cast<float*>(base + decays);
+    }
+};
+
+// Rows of S that a CTA has at once in the token-by-token form.
+int ssm_rows_at_once(int N)
+{
+    return N <= 16 ? SsmShape<16>::ROWS : N <= 32 ? SsmShape<32>::ROWS : N <= 64 ? SsmShape<64>::ROWS : N <= 128 ? SsmShape<128>::ROWS : SsmShape<256>::ROWS;
+}
+
+SsmLayout ssm_layout(const kda_ssm_params& p, int32_t n, int64_t T)
+{
+    SsmLayout w = {};
+    const bool tensor = ssm_on_tensor_cores(p);
+    // segments so long that all of them, times the CTAs of each, just fill the SMs: one CTA an SM on the tensor cores, four
+    // token by token; at least eight chunks (shorter ones cost more in launches: 5 requests of up to 583 tokens 76 -> 88 us)
+    int64_t ctas = (int64_t)p.num_heads * ((p.head_dim + ssm_rows_at_once(p.state_dim) - 1) / ssm_rows_at_once(p.state_dim)), room = 4 * (int64_t)sm_count();
+    if (tensor) {
+        w.plan.pairs_per_group = (p.num_heads / p.num_groups * (p.head_dim / 64) + 1) / 2;
+        ctas = w.plan.pairs = w.plan.pairs_per_group * p.num_groups;
+        room = sm_count();
+    }
+    int64_t want = (T * ctas + room - 1) / room;
+    if (want < 8 * ssm::kChunk) want = 8 * ssm::kChunk;
+    w.cut = T >= 2 * want;
+    w.plan.want = (int32_t)(want < (int64_t)1 << 30 ? want : (int64_t)1 << 30);
+    const int64_t more = T / w.plan.want;                          // a request of k > 1 segments has k * want tokens or more
+    // A chunk costs the same for 1 token as for 128: up to some 32 tokens a request is done sooner token by token (64
+    // requests of 64 heads: 4 tokens 58 us against 193, 32 tokens 196 against 184).  Where the mean says that there
+    // may be such requests, they are taken out; which they are, the kernels see.
+    w.short_len = tensor && T < 64 * (int64_t)n ? 32 : 0;
+    int64_t requests = w.short_len && T / (w.short_len + 1) < n ? T / (w.short_len + 1) : n;
+    if (!tensor && !w.cut) requests = 0;                            // each request whole, without a plan
+    w.plan.max_segments = requests ? (int32_t)(requests + more) : 0;
+    w.plan.max_cuts = w.cut ? (int32_t)more : 0;
+    auto round = [](size_t x) { return (x + 255) / 256 * 256; };
+    w.segments = 256;
+    w.followed = w.segments + round(sizeof(ssm::Segment) * (size_t)w.plan.max_segments);
+    w.chains = w.followed + round(4 * (size_t)w.plan.max_cuts);
+    w.states = w.chains + round(4 * (size_t)w.plan.max_cuts);
+    w.decays = w.states + round((size_t)w.plan.max_cuts * 4 * p.num_heads * p.head_dim * p.state_dim);
+    w.total = w.plan.max_segments ? w.decays + round((size_t)w.plan.max_cuts * 4 * p.num_heads) : 0;
+    return w;
+}
+
 template <int N, int STEPS, typename TIn, typename TOut>
-cudaError_t ssm_rows_launch(const SsmCall& a, cudaStream_t s)
+cudaError_t ssm_rows_launch(const SsmCall& a, const ssm::Plan* plan, cudaStream_t s)
 {
     constexpr int R = SsmShape<N>::ROWS * STEPS;
     const int splits = (a.P + R - 1) / R;
-    const int64_t blocks = (int64_t)a.n * a.H * splits + 1;
-    ssm_rows_kernel<N, STEPS, TIn, TOut><<<(unsigned)blocks, kSsmThreads, 0, s>>>(a, splits);
+    if constexpr (STEPS == 1) {                  // calls in segments: as many CTAs as the plan counts on
+        if (plan) {
+            cudaError_t e = launch_after(ssm_rows_kernel<N, 1, true, TIn, TOut>, (int64_t)plan->max_cuts * a.H * splits, kSsmThreads, 0, s, a, *plan, splits);
+            if (e == cudaSuccess) e = launch_after(ssm::ssm_chain_kernel, (int64_t)(plan->max_cuts / 2 + 1) * a.H * ((a.P * N + 1023) / 1024), 256, 0, s, a, *plan);
+            if (e != cudaSuccess) return e;
+            return launch_after(ssm_rows_kernel<N, 1, false, TIn, TOut>, (int64_t)plan->max_segments * a.H * splits + 1, kSsmThreads, 0, s, a, *plan, splits);
+        }
+    }
+    ssm_rows_kernel<N, STEPS, false, TIn, TOut><<<(unsigned)((int64_t)a.n * a.H * splits + 1), kSsmThreads, 0, s>>>(a, ssm::Plan{}, splits);
     return cudaGetLastError();
 }
 
 template <int N, typename TIn, typename TOut>
-cudaError_t ssm_rows_steps(const SsmCall& a, cudaStream_t s)
+cudaError_t ssm_rows_steps(const SsmCall& a, const ssm::Plan* plan, cudaStream_t s)
 {
     constexpr int R = SsmShape<N>::ROWS;
-    if (a.P >= 2 * R && (int64_t)a.n * a.H * a.P >= (int64_t)sm_count() * 4 * R) return ssm_rows_launch<N, 2, TIn, TOut>(a, s);
-    return ssm_rows_launch<N, 1, TIn, TOut>(a, s);
+    if (!plan && a.P >= 2 * R && (int64_t)a.n * a.H * a.P >= (int64_t)sm_count() * 4 * R) return ssm_rows_launch<N, 2, TIn, TOut>(a, plan, s);
+    return ssm_rows_launch<N, 1, TIn, TOut>(a, plan, s);
 }
 
 template <bool TOKEN, typename TIn, typename TOut>
-cudaError_t ssm_states(const SsmCall& a, cudaStream_t s)
+cudaError_t ssm_states(const SsmCall& a, const ssm::Plan* plan, cudaStream_t s)
 {
-#define KDA_SSM_N(n) case n: return TOKEN ? ssm_token_steps<n, TIn, TOut>(a, s) : ssm_rows_steps<n, TIn, TOut>(a, s)
+#define KDA_SSM_N(n) case n: return TOKEN ? ssm_token_steps<n, TIn, TOut>(a, s) : ssm_rows_steps<n, TIn, TOut>(a, plan, s)
     switch (a.N) {
         KDA_SSM_N(16);
         KDA_SSM_N(32);
@@ -371,15 +619,15 @@ cudaError_t ssm_states(const SsmCall& a, cudaStream_t s)
 }
 
 template <bool TOKEN>
-cudaError_t ssm_dispatch(const kda_ssm_params& p, const SsmCall& a, cudaStream_t s)
+cudaError_t ssm_dispatch(const kda_ssm_params& p, const SsmCall& a, const ssm::Plan* plan, cudaStream_t s)
 {
     if (p.io_dtype == KDA_BF16)
-        return p.out_dtype == KDA_BF16 ? ssm_states<TOKEN, __nv_bfloat16, __nv_bfloat16>(a, s) : ssm_states<TOKEN, __nv_bfloat16, float>(a, s);
-    return p.out_dtype == KDA_BF16 ? ssm_states<TOKEN, float, __nv_bfloat16>(a, s) : ssm_states<TOKEN, float, float>(a, s);
+        return p.out_dtype == KDA_BF16 ? ssm_states<TOKEN, __nv_bfloat16, __nv_bfloat16>(a, plan, s) : ssm_states<TOKEN, __nv_bfloat16, float>(a, plan, s);
+    return p.out_dtype == KDA_BF16 ? ssm_states<TOKEN, float, __nv_bfloat16>(a, plan, s) : ssm_states<TOKEN, float, float>(a, plan, s);
 }
 
 }  // namespace
 
-cudaError_t launch_ssm_decode(const kda_ssm_params& p, const SsmCall& a, cudaStream_t s) { return ssm_dispatch<true>(p, a, s); }
+cudaError_t launch_ssm_decode(const kda_ssm_params& p, const SsmCall& a, cudaStream_t s) { return ssm_dispatch<true>(p, a, nullptr, s); }
 
 }  // namespace kda

@@ -1,5 +1,5 @@
 // kda_ssm_tc.cuh -- the selective state space recurrence over packed prompts on the tensor cores (bf16
-// inputs, head_dim 64 or 128, 64 or 128 states).
+// inputs, head_dim 64 or 128, up to 128 states; fewer than 64 are filled up with zeros by the copies).
 //
 // Unrolled over a chunk of 128 tokens that a state S [N][P] enters, with l_t = log2 a_t and G_r = sum_{i<=r} l_i:
 //
@@ -29,6 +29,11 @@
 // Long requests are cut into segments when there are fewer (request, slice pair) than SMs: a first pass
 // computes each segment's own state from zero (dS only), a small kernel chains them, and every segment then
 // starts from its true state.
+//
+// Measured (64 heads x 64 x 128 states, 8 groups, 8 prompts of 18,646 tokens): 152 us, 41% of the measured copy rate;
+// one prompt of 16,411 tokens (32 heads x 128 x 128, one group) 200 us.  Bound by shared memory: a chunk of a pair moves
+// 628 KB through it (products' operands 288, copies in 96, X' 96, S, X again and Y 128, the rest), 4,900 of some 6,600
+// cycles, of which the products take 2,400.  A third pair of warpgroups only contended for it (180 us).
 #pragma once
 
 #include <atomic>
@@ -41,7 +46,6 @@
 namespace kda {
 namespace ssm {
 
-constexpr int kChunk = 128;
 constexpr int kSlice = 64;                       // channels of a slice
 // tensor-memory columns; Y and dS of the two slices side by side, so that one product makes both
 constexpr uint32_t kGramCol = 0, kMCol = 128, kYCol = 256, kDsCol = 384;
@@ -55,113 +59,6 @@ template <int R> __device__ __forceinline__ void more_registers() { asm volatile
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 constexpr uint32_t kPolls = 1u << 24;
 constexpr float kFarStep = -128.f;               // log2 of a step's decay, bounded: 2^-128 leaves nothing either way
-
-// One segment of a request.
-struct Segment {
-    int32_t b, slot;                             // slot < 0: padding, zeros
-    int32_t first, len;
-    int32_t k, count;                            // segment k of count
-    int32_t base;                                // count > 1: the request's first state in the workspace
-    int32_t pad;
-};
-
-// The call's segments, the states between them and how the slices are paired.
-struct Plan {
-    Segment* segments;
-    int32_t* found;                              // numbers of segments, of segments that another follows, of requests in several
-    int32_t* followed;                           // places of segments that another follows
-    int32_t* chains;                             // places of the first segments of requests in several
-    float* states;                               // [..][H][P][N]: state before segment k of a request at base + k
-    float* decays;                               // [..][H]: log2 of a segment's whole decay, at base + k + 1
-    int32_t max_segments, max_cuts;              // max_cuts bounds both lists
-    int32_t pairs_per_group, pairs;              // slice pairs
-    int32_t want;                                // tokens of a segment that fill the SMs
-};
-
-// Lists the segments, the longest first (by 64 classes of length), so that no long one starts last.
-__global__ void __launch_bounds__(1024) ssm_plan_kernel(const SsmCall a, const Plan plan)
-{
-    __shared__ int32_t bucket[65], longest, all, states[2], cuts[2];
-    const int tid = threadIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid < 65) bucket[tid] = 0;
-    if (tid < 2) states[tid] = 0, cuts[tid] = 0;
-    if (tid == 0) longest = 1;
-    struct Cut {
-        int64_t first, len, size;                // rows; `size` tokens a segment but the last
-        int32_t slot, n;                         // segments
-    };
-    auto cut = [&](int32_t b) -> Cut {
-        Cut c;
-        int64_t last;
-        c.slot = a.idx[b];
-        if (!layer_rows(a.cu, b, a.T, c.first, last)) record_layer_error(kDevErrSeqlens);
-        c.len = last - c.first;
-        if (c.slot >= a.num_slots) {
-            record_layer_error(kDevErrStateIndex);
-            c.slot = -1;
-        }
-        c.size = c.len;
-        c.n = c.len > a.short_len;
-        const int64_t n = c.slot < 0 || c.len < 2 * (int64_t)plan.want ? 1 : c.len / plan.want;
-        if (c.n > 0 && n > 1) {
-            c.size = ((c.len + n - 1) / n + kChunk - 1) / kChunk * kChunk;
-            c.n = (int32_t)((c.len + c.size - 1) / c.size);                  // whole chunks may need fewer
-        }
-        return c;
-    };
-    Cut mine = {};
-    if (tid < a.n) mine = cut(tid);
-    auto of = [&](int32_t b) { return b == tid ? mine : cut(b); };           // looked up once for up to 1,024 requests
-    __syncthreads();
-    for (int32_t b = tid; b < a.n; b += 1024) {
-        const Cut c = of(b);
-        if (c.n > 0) atomicMax(&longest, (int32_t)c.size);
-    }
-    __syncthreads();
-    const float scale = 63.f / (float)longest;
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int32_t b = tid; b < a.n; b += 1024) {
-            const Cut c = of(b);
-            const int32_t base = c.n > 1 ? atomicAdd(&states[pass], c.n) : 0;
-            for (int32_t k = 0; k < c.n; ++k) {
-                const int64_t at = k * c.size, part = c.len - at < c.size ? c.len - at : c.size;
-                const int key = max(0, 63 - (int)((float)part * scale));
-                const int32_t place = atomicAdd(&bucket[pass == 0 ? key + 1 : key], 1);
-                if (pass == 0) continue;
-                Segment s;
-                s.b = b; s.slot = c.slot; s.first = (int32_t)(c.first + at); s.len = (int32_t)part;
-                s.k = k; s.count = c.n; s.base = base; s.pad = 0;
-                plan.segments[place] = s;
-                if (k + 1 < c.n) plan.followed[atomicAdd(&cuts[0], 1)] = place;
-                if (k == 0 && c.n > 1) plan.chains[atomicAdd(&cuts[1], 1)] = place;
-            }
-        }
-        __syncthreads();
-        if (pass == 0 && tid < 32) {                                         // first place of each class
-            const int32_t v0 = bucket[2 * tid + 1], v1 = bucket[2 * tid + 2];
-            int32_t sum = v0 + v1;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int32_t u = __shfl_up_sync(~0u, sum, off);
-                if (tid >= off) sum += u;
-            }
-            bucket[2 * tid + 1] = sum - v1;
-            bucket[2 * tid + 2] = sum;
-            if (tid == 31) all = sum;
-        }
-        __syncthreads();
-        // Requests of a sound table share no rows, and then the workspace holds their segments and states.  If it does
-        // not, nothing is done: the bounds are those of every write here and in the kernels behind.
-        if (pass == 0 && (all > plan.max_segments || states[0] > plan.max_cuts)) {
-            if (tid < 3) plan.found[tid] = 0;
-            if (tid == 0) record_layer_error(kDevErrSeqlens);
-            return;
-        }
-    }
-    if (tid == 0) plan.found[0] = all;
-    if (tid < 2) plan.found[1 + tid] = cuts[tid];
-}
 
 // ---- the chunk kernel ------------------------------------------------------------------------------
 template <int N>
@@ -330,7 +227,7 @@ __device__ bool tc_load(const SsmCall& a, const TcWork& w, uint8_t* smem, TcBars
         auto load_tile = [&](uint64_t* bar, int at, const CUtensorMap* m) {
             tc::mbar_arrive_expect_tx(bar, K::kPanel * (N / 64));
 #pragma unroll
-            for (int p = 0; p < N / 64; ++p) tc::tma_load_2d(smem + at + p * K::kPanel, m, w.g * N + 64 * p, t, bar);
+            for (int p = 0; p < N / 64; ++p) tc::tma_load_3d(smem + at + p * K::kPanel, m, 64 * p, w.g, t, bar);
         };
         if constexpr (ENDS) {                                     // B in two buffers, one of them C's
             if (c > 1 && !tc::mbar_wait(&bars->ds[par], ((c >> 1) - 1) & 1, kPolls)) return false;
@@ -397,15 +294,15 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
 
     // this thread has S[r][0 .. 63] of the slice
     float S[kSlice];
-    const int64_t tile = ((int64_t)t.h * a.P + t.channel) * N + r, all = (int64_t)a.H * a.P * N;
-    const bool own = r < N;
+    const int64_t tile = ((int64_t)t.h * a.P + t.channel) * a.N + r, all = (int64_t)a.H * a.P * a.N;
+    const bool own = r < a.N;
     if (ENDS) {
 #pragma unroll
         for (int i = 0; i < kSlice; ++i) S[i] = 0.f;
     } else {
         const float* from = (w.seg.count > 1 ? plan.states + (w.seg.base + w.seg.k) * all : a.pool + w.seg.slot * all) + tile;
 #pragma unroll
-        for (int i = 0; i < kSlice; ++i) S[i] = own ? from[(int64_t)i * N] : 0.f;
+        for (int i = 0; i < kSlice; ++i) S[i] = own ? from[(int64_t)i * a.N] : 0.f;
     }
     auto store_s = [&]() {                                        // S in bf16, as the product with C takes it
 #pragma unroll
@@ -555,13 +452,13 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         if (own) {
             float* to = plan.states + (w.seg.base + w.seg.k + 1) * all + tile;
 #pragma unroll
-            for (int i = 0; i < kSlice; ++i) to[(int64_t)i * N] = S[i];
+            for (int i = 0; i < kSlice; ++i) to[(int64_t)i * a.N] = S[i];
         }
         if (r == 0 && t.channel == 0) plan.decays[(int64_t)(w.seg.base + w.seg.k + 1) * a.H + t.h] = all_steps;
     } else if (w.seg.k == w.seg.count - 1 && own) {
         float* to = a.pool + w.seg.slot * all + tile;
 #pragma unroll
-        for (int i = 0; i < kSlice; ++i) to[(int64_t)i * N] = S[i];
+        for (int i = 0; i < kSlice; ++i) to[(int64_t)i * a.N] = S[i];
     }
     return !t.bad;
 }
@@ -812,75 +709,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == 16) tc::tmem_dealloc(tmem, 512);
 }
 
-// The state before each segment: of the first the pool's, then S = decay S + (the segment's own).
-// blockIdx.x: (request in several segments, head, 1024 states).
-__global__ void __launch_bounds__(256) ssm_chain_kernel(const SsmCall a, const Plan plan)
-{
-    const int per = a.P * a.N / 1024;
-    const int64_t bh = blockIdx.x / per;
-    const int32_t i = (int32_t)(bh / a.H), h = (int32_t)(bh - (int64_t)i * a.H);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (i >= plan.found[2]) return;
-    const Segment seg = plan.segments[plan.chains[i]];
-    const int64_t all = (int64_t)a.H * a.P * a.N, at = (int64_t)h * a.P * a.N + (blockIdx.x % per) * 1024 + threadIdx.x * 4;
-    float4 v = *reinterpret_cast<const float4*>(a.pool + seg.slot * all + at);
-    float* to = plan.states + seg.base * all + at;
-    *reinterpret_cast<float4*>(to) = v;
-    for (int k = 1; k < seg.count; ++k) {
-        to += all;
-        const float decay = exp2_fast(plan.decays[(int64_t)(seg.base + k) * a.H + h]);
-        const float4 e = *reinterpret_cast<const float4*>(to);
-        v = make_float4(fmaf(decay, v.x, e.x), fmaf(decay, v.y, e.y), fmaf(decay, v.z, e.z), fmaf(decay, v.w, e.w));
-        *reinterpret_cast<float4*>(to) = v;
-    }
-}
-
 }  // namespace ssm
 
 namespace {
-
-bool ssm_on_tensor_cores(const kda_ssm_params& p)
-{
-    return p.io_dtype == KDA_BF16 && (p.head_dim == 64 || p.head_dim == 128) && (p.state_dim == 64 || p.state_dim == 128);
-}
-
-struct SsmLayout {
-    ssm::Plan plan;
-    bool cut;                        // some request may have several segments
-    int32_t short_len;               // as in SsmCall
-    size_t segments, followed, chains, states, decays, total;
-};
-
-SsmLayout ssm_layout(const kda_ssm_params& p, int32_t n, int64_t T)
-{
-    SsmLayout w = {};
-    const int sms = sm_count(), per_head = p.head_dim / ssm::kSlice;
-    w.plan.pairs_per_group = (p.num_heads / p.num_groups * per_head + 1) / 2;
-    w.plan.pairs = w.plan.pairs_per_group * p.num_groups;
-    // segments so long that all of them, times the pairs, just fill the SMs; at least eight chunks
-    int64_t want = (T * w.plan.pairs + sms - 1) / sms;
-    if (want < 8 * ssm::kChunk) want = 8 * ssm::kChunk;
-    w.cut = T >= 2 * want;
-    w.plan.want = (int32_t)(want < (int64_t)1 << 30 ? want : (int64_t)1 << 30);
-    const int64_t more = T / w.plan.want;                          // a request of k > 1 segments has k * want tokens or more
-    // A chunk costs the same for 1 token as for 128: up to some 32 tokens a request is done sooner token by token (64
-    // requests of 64 heads: 4 tokens 58 us against 193, 32 tokens 196 against 184).  Where the mean says that there
-    // may be such requests, they are taken out; which they are, the kernels see.
-    w.short_len = T < 64 * (int64_t)n ? 32 : 0;
-    const int64_t requests = w.short_len && T / (w.short_len + 1) < n ? T / (w.short_len + 1) : n;
-    w.plan.max_segments = (int32_t)(requests + more);
-    auto round = [](size_t x) { return (x + 255) / 256 * 256; };
-    w.segments = 256;
-    w.plan.max_cuts = w.cut ? (int32_t)more : 0;
-    w.followed = w.segments + round(sizeof(ssm::Segment) * (size_t)w.plan.max_segments);
-    w.chains = w.followed + round(4 * (size_t)w.plan.max_cuts);
-    w.states = w.chains + round(4 * (size_t)w.plan.max_cuts);
-    const size_t held = w.cut ? (size_t)more : 0;
-    w.decays = w.states + round(held * 4 * p.num_heads * p.head_dim * p.state_dim);
-    w.total = w.plan.max_segments ? w.decays + round(held * 4 * p.num_heads) : 0;
-    return w;
-}
 
 cudaError_t ssm_map(CUtensorMap* m, const void* base, int64_t rows, int64_t width, int64_t stride, int box_rows)
 {
@@ -891,6 +722,20 @@ cudaError_t ssm_map(CUtensorMap* m, const void* base, int64_t rows, int64_t widt
     const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// B or C as [tokens][groups][states], in boxes of 64 states of a group; states that are not there read as zeros.
+cudaError_t ssm_group_map(CUtensorMap* m, const void* base, int64_t rows, int64_t groups, int64_t states, int64_t stride)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tc::tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)states, (cuuint64_t)groups, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)states * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)ssm::kChunk};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -911,42 +756,19 @@ cudaError_t ssm_chunk_ready()
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ssm::TcCfg<N>::kSmem);
 }
 
-// Launched while the kernel before it in the stream runs; it waits for that one itself (griddepcontrol).
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), int64_t blocks, int threads, int smem, cudaStream_t stream, const A&... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int N, typename TOut>
 cudaError_t ssm_tc_launch(const kda_ssm_params& p, SsmCall a, void* workspace, cudaStream_t s)
 {
     SsmLayout w = ssm_layout(p, a.n, a.T);
     a.short_len = w.short_len;
-    uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
-    w.plan.found = reinterpret_cast<int32_t*>(base);
-    w.plan.segments = reinterpret_cast<ssm::Segment*>(base + w.segments);
-    w.plan.followed = reinterpret_cast<int32_t*>(base + w.followed);
-    w.plan.chains = reinterpret_cast<int32_t*>(base + w.chains);
-    w.plan.states = reinterpret_cast<float*>(base + w.states);
-    w.plan.decays = reinterpret_cast<float*>(base + w.decays);
+    w.place(workspace);
     cudaError_t e = cudaSuccess;
-    if (w.short_len) e = ssm_dispatch<false>(p, a, s);
+    if (w.short_len) e = ssm_dispatch<false>(p, a, nullptr, s);
     if (e != cudaSuccess || w.plan.max_segments == 0) return e;
     CUtensorMap xm, bm, cm, om = {};
     e = ssm_map(&xm, a.x, a.T, (int64_t)a.H * a.P, a.x_stride, ssm::kChunk);
-    if (e == cudaSuccess) e = ssm_map(&bm, a.B, a.T, (int64_t)a.G * a.N, a.b_stride, ssm::kChunk);
-    if (e == cudaSuccess) e = ssm_map(&cm, a.C, a.T, (int64_t)a.G * a.N, a.c_stride, ssm::kChunk);
+    if (e == cudaSuccess) e = ssm_group_map(&bm, a.B, a.T, a.G, a.N, a.b_stride);
+    if (e == cudaSuccess) e = ssm_group_map(&cm, a.C, a.T, a.G, a.N, a.c_stride);
     if (e == cudaSuccess && sizeof(TOut) == 2) e = ssm_map(&om, a.out, a.T, (int64_t)a.H * a.P, (int64_t)a.H * a.P, 32);
     if (e != cudaSuccess) return e;
     constexpr int smem = ssm::TcCfg<N>::kSmem;
@@ -956,7 +778,7 @@ cudaError_t ssm_tc_launch(const kda_ssm_params& p, SsmCall a, void* workspace, c
         e = ssm_chunk_ready<N, true, TOut>();
         if (e == cudaSuccess) e = launch_after(ssm::ssm_chunk_kernel<N, true, TOut>, (int64_t)w.plan.max_cuts * w.plan.pairs, ssm::kTcThreads, smem, s, a, w.plan, xm, bm, cm, om);
         // a request in several segments has two at least
-        if (e == cudaSuccess) e = launch_after(ssm::ssm_chain_kernel, (int64_t)(w.plan.max_cuts / 2 + 1) * a.H * (a.P * a.N / 1024), 256, 0, s, a, w.plan);
+        if (e == cudaSuccess) e = launch_after(ssm::ssm_chain_kernel, (int64_t)(w.plan.max_cuts / 2 + 1) * a.H * ((a.P * a.N + 1023) / 1024), 256, 0, s, a, w.plan);
     }
     if (e == cudaSuccess) e = ssm_chunk_ready<N, false, TOut>();
     if (e != cudaSuccess) return e;
@@ -965,15 +787,19 @@ cudaError_t ssm_tc_launch(const kda_ssm_params& p, SsmCall a, void* workspace, c
 
 }  // namespace
 
-size_t ssm_workspace_bytes(const kda_ssm_params& p, int32_t num_seqs, int64_t total_tokens)
-{
-    return ssm_on_tensor_cores(p) ? ssm_layout(p, num_seqs, total_tokens).total : 0;
-}
+size_t ssm_workspace_bytes(const kda_ssm_params& p, int32_t num_seqs, int64_t total_tokens) { return ssm_layout(p, num_seqs, total_tokens).total; }
 
 cudaError_t launch_ssm_prefill(const kda_ssm_params& p, const SsmCall& a, void* workspace, cudaStream_t s)
 {
-    if (!ssm_on_tensor_cores(p)) return ssm_dispatch<false>(p, a, s);
-    if (p.state_dim == 64)
+    if (!ssm_on_tensor_cores(p)) {
+        SsmLayout w = ssm_layout(p, a.n, a.T);
+        if (!w.cut) return ssm_dispatch<false>(p, a, nullptr, s);
+        w.place(workspace);
+        ssm::ssm_plan_kernel<<<1, 1024, 0, s>>>(a, w.plan);
+        const cudaError_t e = cudaGetLastError();
+        return e != cudaSuccess ? e : ssm_dispatch<false>(p, a, &w.plan, s);
+    }
+    if (p.state_dim <= 64)
         return p.out_dtype == KDA_BF16 ? ssm_tc_launch<64, __nv_bfloat16>(p, a, workspace, s) : ssm_tc_launch<64, float>(p, a, workspace, s);
     return p.out_dtype == KDA_BF16 ? ssm_tc_launch<128, __nv_bfloat16>(p, a, workspace, s) : ssm_tc_launch<128, float>(p, a, workspace, s);
 }

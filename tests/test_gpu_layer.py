@@ -133,13 +133,13 @@ def ssm_inputs(seed, lens, H, P, N, G, dtype, dt_dtype=F32, strided=False, big_s
 
 # Bounds of the recurrence in fp32: a step adds at most 6 half steps to a state (decay's own error 3, the product,
 # the sum, dt's share), a result's sum N + 2 half steps and dt x B's own error some 8, all of the sums of magnitudes.
-# On the tensor-core form (bf16 inputs, dims of 64 or 128, states of 64 or 128) a state's increments are products of
+# On the tensor-core form (bf16 inputs, dims of 64 or 128, up to 128 states) a state's increments are products of
 # halves of 16 bits together, 2^-16, and the factors of a result are rounded to bf16 once, 2^-8, of the magnitudes; an
 # exponent inside 32 tokens is the difference of two sums of up to 32 steps of at most 128 each: six additions of half
 # a step of 4096, 6 * 2^-13, twice, 1.5e-3 or 1.0e-3 of a factor (times ln 2).
 
 def on_tensor_cores(dtype, P, N):
-    return dtype is BF16 and P in (64, 128) and N in (64, 128)
+    return dtype is BF16 and P in (64, 128) and N <= 128
 
 
 def ssm_bounds(want, y_mag, mags, longest, N, out, tc):
@@ -154,7 +154,8 @@ SSM_LENS = [[1], [50], [130, 1, 0, 64, 3], [16, 17, 15, 128, 129], [0, 5], [300]
 @pytest.mark.parametrize("lens", SSM_LENS, ids=str)
 @pytest.mark.parametrize("H,P,N,G,dtype,out", [(4, 64, 128, 2, BF16, BF16), (3, 64, 128, 1, BF16, F32), (2, 128, 128, 1, BF16, BF16), (4, 64, 64, 4, BF16, F32),
                                                (2, 32, 16, 1, BF16, BF16), (3, 64, 128, 3, F32, F32), (2, 16, 32, 2, F32, F32), (2, 128, 64, 1, F32, BF16),
-                                               (1, 64, 256, 1, BF16, F32), (5, 64, 64, 1, BF16, BF16), (2, 64, 256, 2, F32, F32)])
+                                               (1, 64, 256, 1, BF16, F32), (5, 64, 64, 1, BF16, BF16), (2, 64, 256, 2, F32, F32),
+                                                   (4, 64, 16, 2, BF16, BF16), (2, 128, 32, 2, BF16, F32)])
 def test_ssm_rows(lens, H, P, N, G, dtype, out):
     x, dt, B, C, A_log, dt_bias, D = ssm_inputs(5, lens, H, P, N, G, dtype, strided=len(lens) > 1)
     slots = [2 * len(lens) - i for i in range(len(lens))]
@@ -186,17 +187,17 @@ def test_ssm_decode(H, P, N, G, dtype, out, batch):
 
 
 @pytest.mark.parametrize("lens", [[2300], [700, 3333, 0, 1, 2048, 4100]], ids=str)
-@pytest.mark.parametrize("H,P,N,G", [(3, 64, 128, 1), (1, 128, 64, 1)])
-def test_ssm_requests_in_segments(lens, H, P, N, G):
+@pytest.mark.parametrize("H,P,N,G,dtype", [(3, 64, 128, 1, BF16), (1, 128, 64, 1, BF16), (4, 64, 16, 2, BF16), (2, 64, 64, 1, F32), (3, 16, 16, 3, F32), (2, 32, 128, 1, BF16)])
+def test_ssm_requests_in_segments(lens, H, P, N, G, dtype):
     """Long requests of few heads are cut into segments that start from chained states; the pool is updated in place."""
-    x, dt, B, C, A_log, dt_bias, D = ssm_inputs(20, lens, H, P, N, G, BF16)
+    x, dt, B, C, A_log, dt_bias, D = ssm_inputs(20, lens, H, P, N, G, dtype)
     A_log = A_log - 3                                       # states that last over thousands of tokens
     slots = [len(lens) - i for i in range(len(lens))]
     pool = normal(gen(21), len(lens) + 2, H, P, N)
     want, state, y_mag, mags = ref.ssm(x, dt, B, C, A_log, pool, slots, lens, dt_bias, D)
     kda.ssm_prefill(x, dt, B, C, A_log, ref.lengths_to_cu(lens, DEV), pool.clone(), idx(slots), dt_bias=dt_bias, D=D)
     got = kda.ssm_prefill(x, dt, B, C, A_log, ref.lengths_to_cu(lens, DEV), pool, idx(slots), dt_bias=dt_bias, D=D)
-    yb, sb = ssm_bounds(want, y_mag, mags, max(lens), N, BF16, True)
+    yb, sb = ssm_bounds(want, y_mag, mags, max(lens), N, dtype, on_tensor_cores(dtype, P, N))
     ref.within(got, want, yb)
     ref.within(pool, state, sb)
 
