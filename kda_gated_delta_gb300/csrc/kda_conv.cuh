@@ -19,6 +19,19 @@ namespace kda {
 
 constexpr int kConvThreads = 128;
 
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // The V channels from `c` on, their output and the parameters of their taps.
 template <typename T, int V, int W>
 struct ConvLane {
@@ -61,13 +74,27 @@ struct ConvLane {
     __device__ __forceinline__ void step(float (&window)[W - 1][V], int at, const float* x, int64_t t)
     {
         float y[V];
+        if constexpr (V > 1) {                        // two channels an instruction: the kernel is near its issue rate
+#pragma unroll
+            for (int v = 0; v < V; v += 2) {
+                uint64_t s = pair(bias[v], bias[v + 1]);
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i) {
+                    const float* x0 = &window[(at + i) % (W - 1)][v];
+                    s = fma_pair(pair(x0[0], x0[1]), pair(w[i][v], w[i][v + 1]), s);
+                }
+                s = fma_pair(pair(x[v], x[v + 1]), pair(w[W - 1][v], w[W - 1][v + 1]), s);
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(y[v]), "=f"(y[v + 1]) : "l"(s));
+            }
+        } else {
+            y[0] = bias[0];
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) y[0] = fmaf(window[(at + i) % (W - 1)][0], w[i][0], y[0]);
+            y[0] = fmaf(x[0], w[W - 1][0], y[0]);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float s = bias[v];
-#pragma unroll
-            for (int i = 0; i < W - 1; ++i) s = fmaf(window[(at + i) % (W - 1)][v], w[i][v], s);
-            s = fmaf(x[v], w[W - 1][v], s);
-            y[v] = SILU ? s * fast_sigmoid(s) : s;
+            if (SILU) y[v] *= fast_sigmoid(y[v]);
             window[at][v] = x[v];
         }
         store_raw<T, V>(out + t * out_stride, from_floats<T, V>(y));
