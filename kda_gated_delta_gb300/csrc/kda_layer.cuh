@@ -168,10 +168,13 @@ __device__ __forceinline__ void store_floats(T* p, const float* f)
 // sigmoid with the special-function unit's exponential and reciprocal: relative error of some 2^-21, far
 // below a bf16 result's 2^-9 and of the order of the fp32 sums before it.  e^{-x} past the largest float
 // gives 1 / inf = 0.
+// (With flushing of subnormals: the plain forms take three further instructions an element for them, and 1 + e is
+// the same.)
 __device__ __forceinline__ float fast_sigmoid(float x)
 {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
 }
 

@@ -430,21 +430,22 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
                     y[s][kk] = sum[0] + sum[1];
                 }
             }
-            if (ENDS) return;
+            if constexpr (!ENDS) {
 #pragma unroll
-            for (int off = LPR / 2; off > 0; off >>= 1)
+                for (int off = LPR / 2; off > 0; off >>= 1)
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s)
+                    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                    for (int kk = 0; kk < M; ++kk) y[s][kk] += __shfl_xor_sync(0xffffffffu, y[s][kk], off);
-            if (li == 0) {
+                        for (int kk = 0; kk < M; ++kk) y[s][kk] += __shfl_xor_sync(0xffffffffu, y[s][kk], off);
+                if (li == 0) {
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s)
+                    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                    for (int kk = 0; kk < M; ++kk) {
-                        const int r = r0 + s * Sh::ROWS;
-                        sy[k0 + kk][r] = from_f32<TOut>(fmaf(D, to_f32(sx[buf][k0 + kk][r]), y[s][kk]));
-                    }
+                        for (int kk = 0; kk < M; ++kk) {
+                            const int r = r0 + s * Sh::ROWS;
+                            sy[k0 + kk][r] = from_f32<TOut>(fmaf(D, to_f32(sx[buf][k0 + kk][r]), y[s][kk]));
+                        }
+                }
             }
         };
         int k = 0;
@@ -453,11 +454,12 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
 #pragma unroll 1
         for (; k < count; ++k) tokens(std::integral_constant<int, 1>(), k);
         __syncthreads();
-        if (ENDS) continue;
-        constexpr int O = 16 / (int)sizeof(TOut);
-        for (int i = tid; i < count * (rows / O); i += kSsmThreads) {
-            const int k = i / (rows / O), c = i % (rows / O) * O;
-            *reinterpret_cast<uint4*>(out + (t0 + k) * width + c) = *reinterpret_cast<const uint4*>(&sy[k][c]);
+        if constexpr (!ENDS) {
+            constexpr int O = 16 / (int)sizeof(TOut);
+            for (int i = tid; i < count * (rows / O); i += kSsmThreads) {
+                const int k = i / (rows / O), c = i % (rows / O) * O;
+                *reinterpret_cast<uint4*>(out + (t0 + k) * width + c) = *reinterpret_cast<const uint4*>(&sy[k][c]);
+            }
         }
     }
     if (!ENDS && seg.k + 1 < seg.count) return;              // only a request's last segment has its final state

@@ -185,6 +185,7 @@ __device__ bool tc_issue(const int chunks_, uint32_t smem_, TcBars* bars, uint32
             }
         }
         if (!tc::mbar_wait(&bars->xs, par, kPolls)) return false;
+        if (ENDS && c > 0 && !tc::mbar_wait(&bars->next_y, par ^ 1, kPolls)) return false;
         tc::tc_fence_after();
         if (leader) {
 #pragma unroll
@@ -279,9 +280,13 @@ struct TcThread {
     }
 };
 
+// Who makes X' and who S: one warpgroup both; or, where no results are wanted, one each, so that the next chunk's X' is
+// made while this one's S is updated (one prompt of 16,411 tokens: the first pass 75 us with one).
+enum { kBoth = 0, kIncrements = 1, kStates = 2 };
+
 // The warpgroup of a slice's state: X' and S.  A wait that gave up leaves the loop at the next barrier of the group, for
 // all its threads at once.
-template <int N, bool ENDS>
+template <int N, bool ENDS, int PART>
 __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, uint8_t* smem, TcThread t)
 {
     using K = TcCfg<N>;
@@ -329,14 +334,15 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
             if (lane >= off) head += u;
             if (lane + off < 32) tail += v;
         }
-        if (lane == 0) bars->tail[c & 1][s][warp] = tail;
+        float (&sums)[4] = PART == kIncrements ? bars->total[c & 1][s] : bars->tail[c & 1][s];
+        if (lane == 0) sums[warp] = tail;
         tail = __shfl_down_sync(~0u, tail, 1);
         if (lane == 31) tail = 0.f;
         if (slice_any(t.id, t.bad)) return false;
         float whole = 0.f;
 #pragma unroll
         for (int i = 3; i >= 0; --i) {
-            const float f = bars->tail[c & 1][s][i];
+            const float f = sums[i];
             if (i > warp) tail += f;
             if (i < warp) head += f;
             whole += f;
@@ -352,47 +358,49 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         const uint32_t par = c & 1;
         const int len = w.seg.len - c * kChunk < kChunk ? w.seg.len - c * kChunk : kChunk;
         const bool live = r < len;
-        // ---- X' = weight x, in two parts
-        t.wait(&bars->full_x[par], (c >> 1) & 1);
         uint8_t* x_row = smem + K::kX + (2 * s + par) * K::kPanel + r * 128;
-        if (len < kChunk) t.wait(&bars->full_b[par], (c >> 1) & 1);
-        if (live) {
-            const uint64_t ww = pack2(weight, weight), minus = pack2(-1.f, -1.f);
+        if constexpr (PART != kStates) {
+            // ---- X' = weight x, in two parts
+            if (PART == kIncrements && c > 0) t.wait(&bars->ds[par ^ 1], ((c - 1) >> 1) & 1);      // the last X' has been read
+            t.wait(&bars->full_x[par], (c >> 1) & 1);
+            if (len < kChunk) t.wait(&bars->full_b[par], (c >> 1) & 1);
+            if (live) {
+                const uint64_t ww = pack2(weight, weight), minus = pack2(-1.f, -1.f);
 #pragma unroll 4
-            for (int q = 0; q < 8; ++q) {
-                const int at = (q ^ (r & 7)) << 4;
-                const uint4 raw_x = *reinterpret_cast<const uint4*>(x_row + at);
-                const uint32_t xw[4] = {raw_x.x, raw_x.y, raw_x.z, raw_x.w};
-                uint32_t hi[4], lo[4];
+                for (int q = 0; q < 8; ++q) {
+                    const int at = (q ^ (r & 7)) << 4;
+                    const uint4 raw_x = *reinterpret_cast<const uint4*>(x_row + at);
+                    const uint32_t xw[4] = {raw_x.x, raw_x.y, raw_x.z, raw_x.w};
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    float f[2];
-                    unpack_bf16(xw[z], f);
-                    const uint64_t v = mul2(pack2(f[0], f[1]), ww);
-                    const float2 vf = unpack2(v);
-                    hi[z] = pack_bf16(vf.x, vf.y);
-                    unpack_bf16(hi[z], f);
-                    const float2 rest = unpack2(fma2(pack2(f[0], f[1]), minus, v));
-                    lo[z] = pack_bf16(rest.x, rest.y);
+                    for (int z = 0; z < 4; ++z) {
+                        float f[2];
+                        unpack_bf16(xw[z], f);
+                        const uint64_t v = mul2(pack2(f[0], f[1]), ww);
+                        const float2 vf = unpack2(v);
+                        hi[z] = pack_bf16(vf.x, vf.y);
+                        unpack_bf16(hi[z], f);
+                        const float2 rest = unpack2(fma2(pack2(f[0], f[1]), minus, v));
+                        lo[z] = pack_bf16(rest.x, rest.y);
+                    }
+                    *reinterpret_cast<uint4*>(xs_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(xs_row + 2 * K::kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                *reinterpret_cast<uint4*>(xs_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(xs_row + 2 * K::kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-        } else {
-            // rows behind the request's last: another's, or nobody's; zeros, for a weight of zero does not stop a NaN
-            const uint4 none = make_uint4(0, 0, 0, 0);
+            } else {
+                // rows behind the request's last: another's, or nobody's; zeros, for a weight of zero does not stop a NaN
+                const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-            for (int q = 0; q < 128; q += 16) {
-                *reinterpret_cast<uint4*>(x_row + q) = none;
-                *reinterpret_cast<uint4*>(xs_row + q) = none;
-                *reinterpret_cast<uint4*>(xs_row + 2 * K::kPanel + q) = none;
+                for (int q = 0; q < 128; q += 16) {
+                    *reinterpret_cast<uint4*>(x_row + q) = none;
+                    *reinterpret_cast<uint4*>(xs_row + q) = none;
+                    *reinterpret_cast<uint4*>(xs_row + 2 * K::kPanel + q) = none;
 #pragma unroll
-                for (int p = 0; p < N / 64; ++p) *reinterpret_cast<uint4*>(smem + K::kB + p * K::kPanel + r * 128 + q) = none;
+                    for (int p = 0; p < N / 64; ++p) *reinterpret_cast<uint4*>(smem + K::kB + p * K::kPanel + r * 128 + q) = none;
+                }
             }
+            tc::fence_proxy_async();
+            t.arrive(&bars->xs);
         }
-        tc::fence_proxy_async();
-        t.arrive(&bars->xs);
-
         const float raw = t.raw_step(a, w, c + 1);                 // wanted further down
         // ---- Y = 2^G C S + D x; the product M X is added to it
         if constexpr (!ENDS) {
@@ -427,6 +435,7 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
         // ---- S = gamma S + dS
         const uint64_t gg = pack2(gamma, gamma);
         if (c + 1 < w.chunks && !steps(c + 1, raw)) return false;      // while the product runs
+        if (PART == kIncrements) continue;
         t.wait(&bars->ds[par], (c >> 1) & 1);
         tc::tc_fence_after();
 #pragma unroll
@@ -443,19 +452,20 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
                 e[1] = v.y;
             }
         }
+        if (PART == kStates) t.arrive(&bars->next_y);              // dS has been read
         if constexpr (!ENDS) {
             store_s();                                             // (the product with the last S is done)
             t.arrive(&bars->next_s);
         }
     }
-    if (ENDS) {
+    if (ENDS && PART != kIncrements) {
         if (own) {
             float* to = plan.states + (w.seg.base + w.seg.k + 1) * all + tile;
 #pragma unroll
             for (int i = 0; i < kSlice; ++i) to[(int64_t)i * a.N] = S[i];
         }
         if (r == 0 && t.channel == 0) plan.decays[(int64_t)(w.seg.base + w.seg.k + 1) * a.H + t.h] = all_steps;
-    } else if (w.seg.k == w.seg.count - 1 && own) {
+    } else if (!ENDS && w.seg.k == w.seg.count - 1 && own) {
         float* to = a.pool + w.seg.slot * all + tile;
 #pragma unroll
         for (int i = 0; i < kSlice; ++i) to[(int64_t)i * a.N] = S[i];
@@ -674,11 +684,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp < 8) {
         fewer_registers<kResultRegs>();
         const int s = warp / 4;
-        if (!ENDS && s < w.slices) ok = tc_results<N, TOut>(a, w, smem, TcThread(a, w, bars, tmem, s, tid & 127, 1 + s), &om);
+        if (s < w.slices) {
+            const TcThread t(a, w, bars, tmem, s, tid & 127, 1 + s);
+            if constexpr (ENDS) ok = tc_state<N, true, kIncrements>(a, plan, w, smem, t);
+            else ok = tc_results<N, TOut>(a, w, smem, t, &om);
+        }
     } else if (warp < 16) {
         more_registers<kStateRegs>();
         const int s = warp / 4 - 2;
-        if (s < w.slices) ok = tc_state<N, ENDS>(a, plan, w, smem, TcThread(a, w, bars, tmem, s, tid & 127, 3 + s));
+        if (s < w.slices) ok = tc_state<N, ENDS, ENDS ? kStates : kBoth>(a, plan, w, smem, TcThread(a, w, bars, tmem, s, tid & 127, 3 + s));
     } else {
         fewer_registers<kOtherRegs>();
         if (warp == 16) {
