@@ -19,7 +19,9 @@
 // it is a difference of sums over at most 32 steps.
 // Roundings: M and S (for C S) to bf16 once, 2^-8 of a factor at most, for one operand type with x, B and C, which
 // are exact.  X' is kept as the sum of two bf16 numbers, 2^-16, because its errors stay in the state: with one
-// the states would be off by 2e-3.  S itself stays in fp32 registers from a segment's first chunk to its last.
+// the states would be off by 2e-3 of their size, with two they are by 0.7e-6 to 1.8e-6, with three by 0.2e-6 (the third
+// in S's tile, once C S has read it), but then the packed prompts below take 198 us; the fp32 recurrences of this
+// library are held to 1e-5.  S itself stays in fp32 registers from a segment's first chunk to its last.
 //
 // A CTA takes the tokens of one request (or a segment of them) for two slices of 64 channels of x that share B
 // and C: two heads of 64 channels or the halves of one of 128.  A slice has two warpgroups, one for its results (M, Y)
@@ -31,7 +33,7 @@
 // starts from its true state.
 //
 // Measured (64 heads x 64 x 128 states, 8 groups, 8 prompts of 18,646 tokens): 152 us, 41% of the measured copy rate;
-// one prompt of 16,411 tokens (32 heads x 128 x 128, one group) 200 us.  Bound by shared memory: a chunk of a pair moves
+// one prompt of 16,411 tokens (32 heads x 128 x 128, one group) 192 us.  Bound by shared memory: a chunk of a pair moves
 // 628 KB through it (products' operands 288, copies in 96, X' 96, S, X again and Y 128, the rest), 4,900 of some 6,600
 // cycles, of which the products take 2,400.  A third pair of warpgroups only contended for it (180 us).
 #pragma once
