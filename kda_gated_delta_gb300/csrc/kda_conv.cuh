@@ -158,27 +158,14 @@ __device__ __forceinline__ void copy_async16(void* dst, const void* src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
-// Where the tile that would end before row e ends: a request's first W - 1 tokens, whose outputs depend on
-// its old state, stay with the CTA that has its first token and replaces that state.
-template <int W>
-__device__ __forceinline__ int64_t conv_tile_edge(const ConvCall& a, int64_t e)
-{
-    if (e >= a.T) return a.T;
-    int64_t first, last;
-    const int32_t b = layer_owner(a.cu, a.n, e);
-    if (b < 0 || b >= a.n || !layer_rows(a.cu, b, a.T, first, last)) return e;
-    if (first >= e || e - first >= W - 1) return e;
-    return first + (W - 1) < last ? first + (W - 1) : last;
-}
-
 // Packed prompts: blockIdx.x the tile of `tile` tokens, blockIdx.y the channels.
 template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(kConvThreads, 4) conv_rows_kernel(const ConvCall a, int tile)
 {
     const int c = (blockIdx.y * kConvThreads + threadIdx.x) * V;
     if (c >= a.C) return;
-    const int64_t t0 = conv_tile_edge<W>(a, (int64_t)blockIdx.x * tile);
-    const int64_t t1 = conv_tile_edge<W>(a, ((int64_t)blockIdx.x + 1) * tile);
+    const int64_t t0 = conv_tile_edge<W>(a.cu, a.n, a.T, (int64_t)blockIdx.x * tile);
+    const int64_t t1 = conv_tile_edge<W>(a.cu, a.n, a.T, ((int64_t)blockIdx.x + 1) * tile);
     if (t0 >= t1) return;
     const T* x = reinterpret_cast<const T*>(a.x) + c;
     ConvLane<T, V, W> lane(a, c);
@@ -211,21 +198,19 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_rows_kernel(const ConvCa
 #pragma unroll 1
     for (int64_t t = t0; t < t1;) {
         if (t >= last) {                             // a stretch begins, or the tile begins inside one
-            while (b < a.n && a.cu[b + 1] <= t) ++b;
-            int64_t first = t;
+            const Stretch s = conv_stretch<W>(a.cu, a.n, a.T, t, b);
+            const int64_t first = s.first;
+            last = s.last;
             slot = -1;
-            const bool ok = b >= 0 && b < a.n && layer_rows(a.cu, b, a.T, first, last);
-            if (ok) {
+            if (s.own) {
                 slot = a.idx[b];
                 if (slot >= a.num_slots) {
                     if (threadIdx.x == 0) record_layer_error(kDevErrStateIndex);
                     slot = -1;
                 }
-            } else {                                 // rows of no request
-                if (threadIdx.x == 0) record_layer_error(kDevErrSeqlens);
-                last = b < 0 ? a.cu[0] : b < a.n ? t + 1 : a.T;
+            } else if (threadIdx.x == 0) {           // rows of no request
+                record_layer_error(kDevErrSeqlens);
             }
-            if (last <= t) last = t + 1;
             if (slot >= 0) {
                 T* state = reinterpret_cast<T*>(a.pool) + slot * (W - 1) * a.C + c;
                 typename Vec<T, V>::Raw old[W - 1];

@@ -10,6 +10,7 @@
 
 #include "kda.h"
 #include "kda_internal.cuh"
+#include "kda_walk.cuh"
 
 namespace kda {
 
@@ -176,36 +177,6 @@ __device__ __forceinline__ float fast_sigmoid(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
-}
-
-// Rows [first, last) of request b, clamped to the packed tensor; a bad pair is reported by the return.
-__device__ __forceinline__ bool layer_rows(const int32_t* cu, int32_t b, int64_t T, int64_t& first, int64_t& last)
-{
-    if (cu == nullptr) {
-        first = b;
-        last = b + 1;
-        return true;
-    }
-    first = cu[b];
-    last = cu[b + 1];
-    if (first < 0 || last < first || last > T) {
-        first = last = 0;
-        return false;
-    }
-    return true;
-}
-
-// The request that owns row t: the last b with cu[b] <= t, or -1 (row before the first entry).  May be n
-// (row from the last entry on).
-__device__ __forceinline__ int32_t layer_owner(const int32_t* cu, int32_t n, int64_t t)
-{
-    int32_t lo = 0, hi = n + 1;                 // first entry > t lies in [lo, hi]
-    while (lo < hi) {
-        const int32_t mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo - 1;
 }
 
 // SMs of the current device, looked up once each.
