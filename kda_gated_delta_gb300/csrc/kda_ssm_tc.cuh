@@ -790,6 +790,7 @@ cudaError_t ssm_tc_launch(const kda_ssm_params& p, SsmCall a, void* workspace, c
     constexpr int smem = ssm::TcCfg<N>::kSmem;
     ssm::ssm_plan_kernel<<<1, 1024, 0, s>>>(a, w.plan);
     e = cudaGetLastError();
+    if (e != cudaSuccess) return e;                                // without its plan a workspace holds anything
     if (w.cut) {
         e = ssm_chunk_ready<N, true, TOut>();
         if (e == cudaSuccess) e = launch_after(ssm::ssm_chunk_kernel<N, true, TOut>, (int64_t)w.plan.max_cuts * w.plan.pairs, ssm::kTcThreads, smem, s, a, w.plan, xm, bm, cm, om);
