@@ -436,8 +436,8 @@ int32_t kda_paged_attention(const kda_kv_params* p,
  * cu_seqlens[i+1]-1, state_idx[i] is its slot, a negative slot marks padding (zero outputs, no state read
  * or written), slots of distinct requests are distinct, a slot >= num_slots is padding and recorded
  * (code 1), a malformed cu_seqlens is recorded (code 2) and never causes an access out of range: rows that
- * belong to no request get zeros, a table that decreases has unspecified outputs.  A request without
- * tokens leaves its state as it is.
+ * belong to no request get zeros, a table that decreases has unspecified outputs and states.  A request
+ * without tokens leaves its state as it is.
  * The rows of x, dt, B, C and gate may be strided: *_stride is the distance between tokens in elements
  * (what belongs to one token is contiguous).  Parameters (weight, bias, A_log, dt_bias, D) are fp32.
  * Outputs may not overlap inputs.  Results do not depend on timing: the same call gives the same bits.

@@ -162,6 +162,13 @@ __device__ __forceinline__ void copy_async16(void* dst, const void* src)
 template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(kConvThreads, 4) conv_rows_kernel(const ConvCall a, int tile)
 {
+    // each request of the table is looked up once: the walk over the rows steps over those that own none
+    if (blockIdx.y == 0) {
+        for (int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x; i < a.n; i += (int64_t)gridDim.x * kConvThreads) {
+            int64_t first, last;
+            if (!layer_rows(a.cu, (int32_t)i, a.T, first, last)) record_layer_error(kDevErrSeqlens);
+        }
+    }
     const int c = (blockIdx.y * kConvThreads + threadIdx.x) * V;
     if (c >= a.C) return;
     const int64_t t0 = conv_tile_edge<W>(a.cu, a.n, a.T, (int64_t)blockIdx.x * tile);

@@ -30,3 +30,67 @@ def test_conv_reads_no_row_before_a_request(W, cu, dtype, C):
     y = kda.causal_conv(x, w, pool, idx(list(range(n))), table(cu))
     assert kda.check_device_errors() == 2
     assert bool(y.isfinite().all()) and bool(pool.isfinite().all())
+
+
+# tables that decrease, in front, in the middle and behind, by steps that the walk over the rows goes over; with requests
+# before the first row and behind the last
+UNSOUND = [[0, 20, 10, 30], [0, 2, 1, 30], [0, 30, 0, 30], [0, 10, 10, 9, 30], [0, 5, 3, 3, 30], [0, 29, 30, 29, 30], [0, 30, 77], [0, 30, 30, 31],
+           [-5, 0, 30], [-5, -7, 0, 30], [0, 17, -3, 17, 30], [30, 0], [12, 30, 0]]
+
+
+@pytest.mark.parametrize("cu", UNSOUND, ids=str)
+@pytest.mark.parametrize("W,dtype,C", [(4, BF16, 64), (4, BF16, 9), (2, F32, 64)])
+def test_conv_records_tables(cu, W, dtype, C):
+    """Recorded, and nothing outside is touched: NaN around x, slots of no request, and values around the outputs."""
+    g = gen(41)
+    T, n = 30, len(cu) - 1
+    rows = torch.full((T + 2000, C), float("nan"), dtype=dtype, device=DEV)
+    x = rows[1000:1000 + T]
+    x.copy_(normal(g, T, C, dtype=dtype))
+    pool, w = normal(g, n + 1, W - 1, C, dtype=dtype), normal(g, C, W)
+    before = pool[n].clone()
+    out = torch.full((T + 2000, C), 7.0, dtype=dtype, device=DEV)
+    y = kda.causal_conv(x, w, pool, idx(list(range(n))), table(cu), out=out[1000:1000 + T])
+    assert kda.check_device_errors() == 2
+    assert bool(y.isfinite().all()) and bool(pool.isfinite().all()) and torch.equal(pool[n], before)
+    assert bool((out[:1000] == 7).all()) and bool((out[1000 + T:] == 7).all())
+    assert kda.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("many", [1, 700])
+@pytest.mark.parametrize("bad", [None, 0, 1, 300, 698])
+def test_conv_tables_of_many_requests(many, bad):
+    """One pair out of order among 700 requests without tokens, before or behind the rows; the sound table records nothing."""
+    g = gen(42)
+    T, C = 40, 2056
+    for front in (True, False):
+        cu = [0] * many + [T] if front else [0] + [T] * many
+        if bad is not None and bad + 1 < len(cu):
+            cu[bad] += 1 if front else -1
+        sound = all(a <= b for a, b in zip(cu, cu[1:])) and cu[0] == 0 and cu[-1] == T
+        x, w, pool = normal(g, T, C, dtype=BF16), normal(g, C, 4), normal(g, many, 3, C, dtype=BF16)
+        y = kda.causal_conv(x, w, pool, idx(list(range(many))), table(cu))
+        assert kda.check_device_errors() == (0 if sound else 2)
+        assert bool(y.isfinite().all())
+
+
+@pytest.mark.parametrize("cu", UNSOUND, ids=str)
+@pytest.mark.parametrize("scale,dtype,P,N", [(10, BF16, 64, 128), (1, BF16, 64, 128), (1, F32, 32, 16)])
+def test_ssm_records_tables(cu, scale, dtype, P, N):
+    """The same of the recurrence, in chunks (300 rows), and token by token."""
+    cu = [c * scale for c in cu]
+    H, G, T, n = 2, 1, 30 * scale, len(cu) - 1
+    g = gen(43)
+    rows = torch.full((T + 400, H * P + 2 * G * N), float("nan"), dtype=dtype, device=DEV)
+    mine = rows[200:200 + T]
+    mine.copy_(normal(g, *mine.shape, dtype=dtype))
+    x, B, C = (t.unflatten(1, s) for t, s in zip(mine.split([H * P, G * N, G * N], 1), ((H, P), (G, N), (G, N))))
+    dt, A_log, pool = normal(g, T, H), torch.rand(H, generator=g, device=DEV), normal(g, n + 1, H, P, N)
+    before = pool[n].clone()
+    out = torch.zeros((T + 400, H, P), dtype=dtype, device=DEV)
+    out[:200] = out[200 + T:] = 7
+    kda.ssm_prefill(x, dt, B, C, A_log, table(cu), pool, idx(list(range(n))), out=out[200:200 + T])
+    assert kda.check_device_errors() == 2
+    assert bool(out.isfinite().all()) and bool(pool.isfinite().all()) and torch.equal(pool[n], before)
+    assert bool((out[:200] == 7).all()) and bool((out[200 + T:] == 7).all())
+    assert kda.check_device_errors() == 0
