@@ -286,20 +286,19 @@ __device__ __forceinline__ void ssm_cp_async16(void* dst, const void* src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
 }
 
-// Zeros for the rows before the first request and behind the last, by one CTA.
+// Zeros for the rows of no request, by one CTA.
 template <typename TOut>
 __device__ __forceinline__ void ssm_clear_unowned(const SsmCall& a, int tid, int threads)
 {
+    if (a.cu[0] == 0 && a.cu[a.n] == a.T) return;
+    if (tid == 0) record_layer_error(kDevErrSeqlens);
+    int64_t lo, hi;
+    unowned_rows(a.cu, a.n, a.T, lo, hi);
     TOut* out = reinterpret_cast<TOut*>(a.out);
     const int64_t width = (int64_t)a.H * a.P;
-    int64_t lo = a.cu[0], hi = a.cu[a.n];
-    lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
-    hi = hi < 0 ? 0 : hi > a.T ? a.T : hi;
-    if ((lo > 0 || hi < a.T) && tid == 0) record_layer_error(kDevErrSeqlens);
     for (int64_t i = tid; i < lo * width; i += threads) out[i] = from_f32<TOut>(0.f);
     for (int64_t i = hi * width + tid; i < a.T * width; i += threads) out[i] = from_f32<TOut>(0.f);
 }
-
 
 // Packed prompts.  blockIdx.x: (request, or segment of the plan; head; slab of STEPS * ROWS rows); one CTA more gives
 // zeros to rows of no request.  ENDS: only the state that a segment leaves when it starts from zero.

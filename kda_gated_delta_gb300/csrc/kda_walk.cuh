@@ -37,6 +37,15 @@ __host__ __device__ __forceinline__ int32_t layer_owner(const int32_t* cu, int32
     return lo - 1;
 }
 
+// Rows of no request in a table that does not decrease: [0, lo) and [hi, T), lo <= hi.  They lie before the first entry that is
+// not negative and behind the last that is not above T: a request that reaches past either is taken by nobody.
+__host__ __device__ __forceinline__ void unowned_rows(const int32_t* cu, int32_t n, int64_t T, int64_t& lo, int64_t& hi)
+{
+    const int32_t from = layer_owner(cu, n, -1) + 1, to = layer_owner(cu, n, T);
+    lo = from <= n && cu[from] < T ? cu[from] : T;
+    hi = to >= 0 && cu[to] > lo ? cu[to] : lo;
+}
+
 // Where the convolution's tile that would end before row e ends: a request's first W - 1 tokens, whose outputs depend on
 // its old state, stay with the CTA that has its first token and replaces that state.
 template <int W>

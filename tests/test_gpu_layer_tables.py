@@ -94,3 +94,37 @@ def test_ssm_records_tables(cu, scale, dtype, P, N):
     assert bool(out.isfinite().all()) and bool(pool.isfinite().all()) and torch.equal(pool[n], before)
     assert bool((out[:200] == 7).all()) and bool((out[200 + T:] == 7).all())
     assert kda.check_device_errors() == 0
+
+
+def ssm_call(g, T, dtype, H, P, N, tail=0):
+    """Inputs of a recurrence over T rows, and an output that holds sevens."""
+    ins = (normal(g, T, H, P, dtype=dtype), normal(g, T, H), normal(g, T, 1, N, dtype=dtype), normal(g, T, 1, N, dtype=dtype), torch.rand(H, generator=g, device=DEV))
+    return ins, torch.full((T, H, P), 7.0, dtype=dtype, device=DEV)
+
+
+# scale 10: in chunks
+FORMS = [(10, BF16, 64, 128), (1, BF16, 64, 128), (1, F32, 32, 16), (1, BF16, 64, 256)]
+
+
+@pytest.mark.parametrize("scale,dtype,P,N", FORMS)
+@pytest.mark.parametrize("cu,taken", [([0, 10, 77], [0]), ([-5, 10, 30], [1]), ([-5, 10, 20, 77], [1]), ([-9, -5, 4, 30], [2]), ([0, 12, 40, 77], [0]),
+                                      ([4, 10, 25], [0, 1]), ([-5, 77], []), ([-5, -5], []), ([77, 77], []), ([0, 0, 0], [0, 1]), ([30, 30], [0])], ids=str)
+def test_ssm_rows_of_no_request_get_zeros(cu, taken, scale, dtype, P, N):
+    """Requests that reach past either end are taken by nobody: zeros in their rows, their states as they were, and the other
+    requests' outputs and states are those of a sound call."""
+    H, T, n = 2, 30 * scale, len(cu) - 1
+    cu = [c * scale for c in cu]
+    g = gen(44)
+    ins, out = ssm_call(g, T, dtype, H, P, N)
+    pool = normal(g, n, H, P, N)
+    before = pool.clone()
+    kda.ssm_prefill(*ins, table(cu), pool, idx(list(range(n))), out=out)
+    assert kda.check_device_errors() == 2
+    want, state = torch.zeros_like(out), before.clone()
+    for b in taken:
+        lo, hi = cu[b], cu[b + 1]
+        if lo < hi:
+            one = before[b:b + 1].clone()
+            want[lo:hi] = kda.ssm_prefill(*[t[lo:hi] for t in ins[:4]], ins[4], table([0, hi - lo]), one, idx([0]))
+            state[b] = one[0]
+    assert torch.equal(out, want) and torch.equal(pool, state)

@@ -1,6 +1,6 @@
-"""The convolution's walk over packed requests, taken on the host over every small table of lengths: whatever the
+"""The walk over packed requests, taken on the host over every small table of lengths.  The convolution's: whatever the
 table holds, no row outside the packed tensor or before the request's own is read, every row of a tile is gone over
-once, and sound tables give each row to its request."""
+once, and sound tables give each row to its request.  The recurrence's: rows of no request get zeros."""
 import os
 import subprocess
 
@@ -74,6 +74,23 @@ static void walk(int T, int tile)
     }
 }
 
+// The rows that the recurrence gives zeros to: in a table that does not decrease, all that no request owns, and no others.
+static void unowned(int T)
+{
+    const int n = (int)cu.size() - 1;
+    int64_t lo, hi, first, last;
+    kda::unowned_rows(cu.data(), n, T, lo, hi);
+    if (lo < 0 || hi < lo || hi > T) fail("zeros outside the rows", T, 0, 0);
+    std::vector<char> owned(T, 0);
+    for (int b = 0; b < n; ++b) {
+        if (cu[b] > cu[b + 1]) return;
+        if (kda::layer_rows(cu.data(), b, T, first, last))
+            for (int64_t t = first; t < last; ++t) owned[t] = 1;
+    }
+    for (int t = 0; t < T; ++t)
+        if (owned[t] == (t < lo || t >= hi)) fail("zeros in a request's rows, or none in nobody's", T, 0, 0);
+}
+
 static void all(size_t at, int lo, int hi, int T)
 {
     if (at < cu.size()) {
@@ -84,6 +101,7 @@ static void all(size_t at, int lo, int hi, int T)
         return;
     }
     ++tables;
+    unowned(T);
     for (int tile : {4, 12}) {
         walk<2>(T, tile);
         walk<3>(T, tile);
