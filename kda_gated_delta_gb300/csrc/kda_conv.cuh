@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_rows_kernel(const ConvCa
         for (int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x; i < a.n; i += (int64_t)gridDim.x * kConvThreads) {
             int64_t first, last;
             if (!layer_rows(a.cu, (int32_t)i, a.T, first, last)) record_layer_error(kDevErrSeqlens);
+            if (a.idx[i] >= a.num_slots) record_layer_error(kDevErrStateIndex);
         }
     }
     const int c = (blockIdx.y * kConvThreads + threadIdx.x) * V;
@@ -211,10 +212,7 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_rows_kernel(const ConvCa
             slot = -1;
             if (s.own) {
                 slot = a.idx[b];
-                if (slot >= a.num_slots) {
-                    if (threadIdx.x == 0) record_layer_error(kDevErrStateIndex);
-                    slot = -1;
-                }
+                if (slot >= a.num_slots) slot = -1;
             } else if (threadIdx.x == 0) {           // rows of no request
                 record_layer_error(kDevErrSeqlens);
             }

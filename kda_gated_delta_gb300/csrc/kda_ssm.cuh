@@ -337,13 +337,12 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
         last = first + seg.len;
         slot = seg.slot;
     } else {
-        if (!layer_rows(a.cu, (int32_t)b, a.T, first, last) && tid == 0) record_layer_error(kDevErrSeqlens);
-        if (first == last || (a.short_len > 0 && last - first > a.short_len)) return;
+        const bool ok = layer_rows(a.cu, (int32_t)b, a.T, first, last);
         slot = a.idx[b];
-        if (slot >= a.num_slots) {
-            if (tid == 0) record_layer_error(kDevErrStateIndex);
-            slot = -1;
-        }
+        if (tid == 0 && !ok) record_layer_error(kDevErrSeqlens);
+        if (tid == 0 && slot >= a.num_slots) record_layer_error(kDevErrStateIndex);
+        if (first == last || (a.short_len > 0 && last - first > a.short_len)) return;
+        if (slot >= a.num_slots) slot = -1;
     }
     out += (int64_t)h * a.P + row0;
     if (slot < 0) {

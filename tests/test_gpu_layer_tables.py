@@ -128,3 +128,21 @@ def test_ssm_rows_of_no_request_get_zeros(cu, taken, scale, dtype, P, N):
             want[lo:hi] = kda.ssm_prefill(*[t[lo:hi] for t in ins[:4]], ins[4], table([0, hi - lo]), one, idx([0]))
             state[b] = one[0]
     assert torch.equal(out, want) and torch.equal(pool, state)
+
+
+@pytest.mark.parametrize("at", [0, 1, 2, 3])
+def test_slots_of_requests_without_tokens(at):
+    """A slot past the pool is recorded whether its request has tokens or not, in every form."""
+    g = gen(45)
+    cu, slots = [0, 0, 200, 200, 200], [0, 1, 2, 3]
+    slots[at] = 4
+    x, w, pool = normal(g, 200, 64), normal(g, 64, 4), normal(g, 4, 3, 64)
+    kda.causal_conv(x, w, pool, idx(slots), table(cu))
+    assert kda.check_device_errors() == 1
+    for dtype, P, N in ((BF16, 64, 128), (F32, 32, 16)):
+        for n in (4, 3):                                 # 50 tokens a request: with short ones apart; 66: without
+            if n == 3 and at == 3:
+                continue
+            ins, out = ssm_call(g, 200, dtype, 2, P, N)
+            kda.ssm_prefill(*ins, table(cu[:n + 1]), normal(g, 4, 2, P, N), idx(slots[:n]), out=out)
+            assert kda.check_device_errors() == 1
