@@ -61,6 +61,7 @@ template <int R> __device__ __forceinline__ void more_registers() { asm volatile
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 constexpr uint32_t kPolls = 1u << 24;
 constexpr float kFarStep = -128.f;               // log2 of a step's decay, bounded: 2^-128 leaves nothing either way
+__device__ __forceinline__ float bounded_step(float step) { return step < kFarStep ? kFarStep : step; }   // a NaN stays one
 
 // ---- the chunk kernel ------------------------------------------------------------------------------
 template <int N>
@@ -329,7 +330,7 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
     auto steps = [&](int c, float raw) -> bool {
         const bool live = c * kChunk + r < w.seg.len;
         const float dt = live ? softplus_series(raw + t.bias, a.threshold) : 0.f;
-        float head = live ? fmaxf(-dt * t.rate, kFarStep) : 0.f, tail = head;
+        float head = live ? bounded_step(-dt * t.rate) : 0.f, tail = head;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const float u = ENDS ? 0.f : __shfl_up_sync(~0u, head, off), v = __shfl_down_sync(~0u, tail, off);
@@ -493,7 +494,7 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
     auto steps = [&](int c, float raw) -> bool {
         const bool live = c * kChunk + r < w.seg.len;
         const float dt = live ? softplus_series(raw + t.bias, a.threshold) : 0.f;
-        float tail = head = live ? fmaxf(-dt * t.rate, kFarStep) : 0.f;
+        float tail = head = live ? bounded_step(-dt * t.rate) : 0.f;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const float u = __shfl_up_sync(~0u, head, off), v = __shfl_down_sync(~0u, tail, off);
