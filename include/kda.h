@@ -504,7 +504,8 @@ void kda_ssm_params_init(kda_ssm_params* p, int32_t num_heads, int32_t head_dim,
  *   out          [T][H][P] out_dtype
  *   workspace    kda_ssm_prefill_workspace_size(...) bytes, 256-byte aligned, contents garbage before and
  *                after; it must not be shared with a call that overlaps in time.
- * x, B, C, the pool and out are 16-byte aligned; x_stride, b_stride and c_stride are multiples of 8.
+ * x, B, C, the pool and out are 16-byte aligned, all other tensors as their elements are; x_stride, b_stride
+ * and c_stride are multiples of 8.
  * States are held and updated in fp32.  Prompts in bf16 with a head_dim of 64 or 128 and up to 128 states go through the
  * tensor cores in chunks of 128 tokens: the factors C . B dt decay and the states enter the products with x and C
  * rounded to bf16 once, a token's increment dt decay x as two bf16 numbers (2^-16 of it); a non-finite x can make

@@ -51,7 +51,8 @@ int32_t check_ssm(const kda_ssm_params* p, const void* x, int64_t x_stride, cons
         c_stride % 8 != 0)
         return KDA_ERR_INVALID_ARG;
     if (x_stride >= kMaxStride || b_stride >= kMaxStride || c_stride >= kMaxStride || dt_stride >= kMaxStride) return KDA_ERR_UNSUPPORTED;
-    if (misaligned(x) || misaligned(B) || misaligned(C) || misaligned(pool) || misaligned(out) || odd(dt, size_of(p->dt_dtype)))
+    if (misaligned(x) || misaligned(B) || misaligned(C) || misaligned(pool) || misaligned(out) || odd(dt, size_of(p->dt_dtype)) ||
+        odd(A_log, 4) || odd(dt_bias, 4) || odd(D, 4) || odd(idx, 4))
         return KDA_ERR_MISALIGNED;
     if (T >= kMaxTokens || (int64_t)num_seqs * p->num_heads >= ((int64_t)1 << 29) / (p->head_dim / 16))
         return KDA_ERR_UNSUPPORTED;
@@ -96,7 +97,8 @@ int32_t kda_causal_conv(const kda_conv_params* p, const void* x, int64_t x_strid
     if (total_tokens == 0 || num_seqs == 0) return KDA_OK;
     if (!x || !weight || !state_pool || !state_idx || x_stride < p->num_channels) return KDA_ERR_INVALID_ARG;
     const uintptr_t size = size_of(p->io_dtype);
-    if (odd(x, size) || odd(state_pool, size) || odd(weight, 4) || odd(bias, 4)) return KDA_ERR_MISALIGNED;
+    if (odd(x, size) || odd(state_pool, size) || odd(weight, 4) || odd(bias, 4) || odd(cu_seqlens, 4) || odd(state_idx, 4))
+        return KDA_ERR_MISALIGNED;
     for (int j = 0; j < num_outs; ++j) {
         if (!outs[j]) return KDA_ERR_INVALID_ARG;
         if (odd(outs[j], size)) return KDA_ERR_MISALIGNED;
@@ -139,6 +141,7 @@ int32_t kda_ssm_prefill(const kda_ssm_params* p, const void* x, int64_t x_stride
                                  state_pool, num_slots, state_idx, out, &a, &noop);
     if (rc != KDA_OK || noop) return rc;
     if (!cu_seqlens) return KDA_ERR_INVALID_ARG;
+    if (odd(cu_seqlens, 4)) return KDA_ERR_MISALIGNED;
     const size_t need = kda::ssm_workspace_bytes(*p, num_seqs, total_tokens);
     if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return KDA_ERR_WORKSPACE;
     a.cu = cu_seqlens;

@@ -196,3 +196,20 @@ def test_refusals_of_their_own(reached):  # noqa: F811
     conv(split=(48, 16), out=(t["o1"], t["o2"]), activation="silu")
     kda.causal_conv(on(0, 4, 80, dtype=BF)[:, 16:], t["w"], t["pc"], t["idx"], t["cu"], out=on(0, 4, 64, dtype=BF))
     assert reached == ["kda_causal_conv"] * 2
+
+
+def test_element_alignment(L):
+    """fp32 parameters and the int32 tables need their elements' alignment: a kernel that read them elsewhere would fault."""
+    for at in (1, 2, 3):
+        off = FAKE + at
+        for kw in (dict(cu=off), dict(idx=off)):
+            assert _conv(L, **kw) == -3, kw
+        assert _conv(L, cu=None, T=2, idx=off) == -3
+        for call in (_prefill, _decode):
+            assert call(L, A=off) == -3 and call(L, idx=off) == -3
+        assert _prefill(L, cu=off) == -3
+        p = ctypes.byref(_p())
+        head = (p, FAKE, 256, FAKE, 4, FAKE, 256, FAKE, 256, FAKE)
+        for bias, D in ((off, None), (None, off)):
+            assert L.kda_ssm_prefill(*head, bias, D, FAKE, 2, 5, FAKE, 4, FAKE, FAKE, FAKE, 1 << 40, None) == -3
+            assert L.kda_ssm_decode(*head, bias, D, 2, FAKE, 4, FAKE, FAKE, None) == -3
