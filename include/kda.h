@@ -502,8 +502,9 @@ void kda_ssm_params_init(kda_ssm_params* p, int32_t num_heads, int32_t head_dim,
  *   x    [T][H][P], dt [T][H], B, C [T][G][N], A_log [H], dt_bias [H] or NULL, D [H] or NULL
  *   state_pool   fp32 [num_slots][H][P][N], as the delta-rule pool (value row, key channel contiguous)
  *   out          [T][H][P] out_dtype
- *   workspace    kda_ssm_prefill_workspace_size(...) bytes, 256-byte aligned, contents garbage before and
- *                after; it must not be shared with a call that overlaps in time.
+ *   workspace    kda_ssm_prefill_workspace_size(...) bytes as the call's device gives them (the current
+ *                one: the size depends on its number of SMs), 256-byte aligned, contents garbage before
+ *                and after; it must not be shared with a call that overlaps in time.
  * x, B, C, the pool and out are 16-byte aligned, all other tensors as their elements are; x_stride, b_stride
  * and c_stride are multiples of 8.
  * States are held and updated in fp32.  Prompts in bf16 with a head_dim of 64 or 128 and up to 128 states go through the

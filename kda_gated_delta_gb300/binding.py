@@ -810,17 +810,18 @@ def _ssm_params(H, P, N, G, io, dt, out, threshold):
 
 
 @functools.lru_cache(maxsize=4096)
-def _ssm_workspace(p, n, T):
+def _ssm_workspace(p, n, T, dev):
+    """For device `dev`, which is the current one: requests are cut by its number of SMs."""
     return int(lib().kda_ssm_prefill_workspace_size(p, _clip(n), T))
 
 
 def ssm_prefill_workspace_size(num_heads, head_dim, state_dim, num_groups, num_seqs, num_tokens, *, dtype=torch.bfloat16,
                                out_dtype=None) -> int:
-    """Bytes of ``workspace`` that :func:`ssm_prefill` needs for these sizes (it allocates them itself when none is
-    given)."""
+    """Bytes of ``workspace`` that :func:`ssm_prefill` needs for these sizes on the current device (it allocates them itself
+    when none is given)."""
     io = _code(dtype, "dtype")
     p = _ssm_params(num_heads, head_dim, state_dim, num_groups, io, KDA_F32, io if out_dtype is None else _code(out_dtype, "out_dtype"), 20.0)
-    return _ssm_workspace(p, num_seqs, num_tokens)
+    return _ssm_workspace(p, num_seqs, num_tokens, _device() if torch.cuda.is_available() else -1)
 
 
 def _ssm_args(x, dt, B, C, A_log, state_pool, state_idx, dt_bias, D, out, out_dtype, threshold):
@@ -874,7 +875,7 @@ def ssm_prefill(x, dt, B, C, A_log, cu_seqlens, state_pool, state_idx, *, dt_bia
     cu = _need_with_x(cu_seqlens, "cu_seqlens", _I32, dev, (n + 1,))
     if n == 0 and T > 0:
         raise ValueError("tokens without a request")
-    need, ws = _ssm_workspace(p, n, T), None
+    need, ws = _ssm_workspace(p, n, T, dev), None
     if workspace is not None:
         need = workspace.numel()
         ws = _need_with_x(workspace, "workspace", _U8, dev, (need,))

@@ -213,3 +213,21 @@ def test_element_alignment(L):
         for bias, D in ((off, None), (None, off)):
             assert L.kda_ssm_prefill(*head, bias, D, FAKE, 2, 5, FAKE, 4, FAKE, FAKE, FAKE, 1 << 40, None) == -3
             assert L.kda_ssm_decode(*head, bias, D, 2, FAKE, 4, FAKE, FAKE, None) == -3
+
+
+def test_workspace_by_device(reached, monkeypatch):  # noqa: F811
+    """A call's workspace is that of its device: another device's size, looked up earlier, is not taken for it."""
+    at, given = [0], []
+
+    class Lib:
+        def kda_ssm_prefill_workspace_size(self, p, n, T):
+            return 1000 + at[0]
+
+    monkeypatch.setattr(binding, "lib", lambda: Lib())
+    monkeypatch.setattr(binding, "_device", lambda: at[0])
+    monkeypatch.setattr(binding, "_fn", lambda name: lambda *args: given.append(args[-2]) or 0)
+    for dev in (0, 1, 0):
+        at[0] = dev
+        t, _ = calls(dev)
+        kda.ssm_prefill(t["x"], t["dt"], t["B"], t["C"], t["A"], t["cu"], t["pool"], t["idx"], out=t["out"], softplus_threshold=7.0)
+    assert given == [1000, 1001, 1000]
