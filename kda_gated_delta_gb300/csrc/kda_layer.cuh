@@ -179,7 +179,7 @@ __device__ __forceinline__ float fast_sigmoid(float x)
     return r;
 }
 
-// SMs of the current device, looked up once each.
+// SMs of the current device, looked up once each; where that fails, a number that is not kept.
 inline int sm_count()
 {
     static std::atomic<int> known[64];
@@ -187,7 +187,7 @@ inline int sm_count()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
         known[dev].store(n, std::memory_order_relaxed);
     }
     return n;

@@ -1,4 +1,5 @@
-"""Launches of the operators around a recurrence over a runtime of our own: a launch that fails ends the call."""
+"""Launches of the operators around a recurrence over a runtime of our own: a launch that fails ends the call, and
+device properties are those of the device."""
 import ctypes
 
 import pytest
@@ -35,3 +36,20 @@ def test_a_failed_launch_ends_the_call(L, p, n, T, launches):
     assert prefill(L, p, n, T) == (0, launches)
     for k in range(launches):
         assert prefill(L, p, n, T, fail=k) == (-5, k + 1)
+
+
+def test_number_of_sms(L):
+    """A query that fails leaves no number behind, and each device has its own."""
+    size = L.kda_ssm_prefill_workspace_size
+    size.restype = ctypes.c_size_t
+    p, n, T = params(H=1), 1, ctypes.c_int64(1 << 20)
+
+    def need(dev, sms, silent=0):
+        L.fake_device(dev, sms)
+        L.fake_silent(silent)
+        return size(ctypes.byref(p), n, T)
+
+    other = need(3, 40)
+    assert need(1, 152, silent=100) == need(2, 148) != need(4, 152)
+    assert need(1, 152) == need(4, 152)
+    assert need(3, 40) == other != need(1, 152)
