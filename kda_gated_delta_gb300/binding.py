@@ -654,7 +654,7 @@ def paged_attention(q, cache, block_table, kv_lens, cu_seqlens=None, *, window=0
             raise ValueError("lse must be [tokens, q heads]")
     elif return_lse:
         lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
-    p = _kv_params(Hq, Hkv, D, page, fp4, 0, False, window, sinks, scale)
+    p = _kv_params(Hq, Hkv, D, page, fp4, 0, False, window, sinks, None if scale is None else float(scale))
     need = _attention_workspace(p, batch[3], T, max_new, max_len)
     ws = None
     if workspace is not None:
@@ -858,7 +858,7 @@ def _ssm_args(x, dt, B, C, A_log, state_pool, state_idx, dt_bias, D, out, out_dt
     else:
         out_code = _code(out.dtype, "out")
         _need_with_x(out, "out", out.dtype, dev, (T, H, P))
-    p = _ssm_params(H, P, N, G, code, dt_code, out_code, threshold)
+    p = _ssm_params(H, P, N, G, code, dt_code, out_code, float(threshold))
     return dev, T, p, (p, xp, xs, dp, ds, bp, bs, cp, cs, al, db, dd), n, (pool, slots, idx, out.data_ptr()), out
 
 
@@ -946,7 +946,7 @@ def group_norm(x, weight=None, bias=None, *, gate=None, activation=None, gate_fi
     act = _ACTIVATIONS.get(activation, -1)
     if act < 0:
         raise ValueError(f"activation must be None, 'silu' or 'sigmoid', got {activation!r}")
-    rc = _fn("kda_group_norm")(_norm_params(G, n, code, out_code, act, 1 if gate_first else 0, 1 if center else 0, eps), xp, xs, gp, gs, wp, bp,
+    rc = _fn("kda_group_norm")(_norm_params(G, n, code, out_code, act, 1 if gate_first else 0, 1 if center else 0, float(eps)), xp, xs, gp, gs, wp, bp,
                                T, out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         _check(rc, "kda_group_norm")

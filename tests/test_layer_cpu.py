@@ -215,6 +215,32 @@ def test_element_alignment(L):
             assert L.kda_ssm_decode(*head, bias, D, 2, FAKE, 4, FAKE, FAKE, None) == -3
 
 
+def test_numbers_given_as_tensors(reached, monkeypatch):  # noqa: F811
+    """A scalar that changes in place between two calls is not answered with its old value."""
+    t, table = calls(0)
+    seen = []
+
+    def fn(name):
+        def call(p, *args):
+            p = p._obj
+            seen.append(p.eps if name == "kda_group_norm" else p.softmax_scale if name == "kda_paged_attention" else p.softplus_threshold)
+            return 0
+        return call
+
+    monkeypatch.setattr(binding, "_fn", fn)
+    number = torch.tensor(0.5)
+    cache = on(0, 8, 2, 16, 64, dtype=BF), on(0, 8, 2, 16, 64, dtype=BF)
+    q, pages, lens = on(0, 2, 4, 64, dtype=BF), on(0, 2, 4, dtype=I32), on(0, 2, dtype=I32)
+    for value in (0.5, 0.25):
+        number.fill_(value)
+        kda.group_norm(t["x"], eps=number)
+        kda.ssm_prefill(t["x"], t["dt"], t["B"], t["C"], t["A"], t["cu"], t["pool"], t["idx"], softplus_threshold=number, workspace=t["ws"])
+        kda.ssm_decode(t["x"], t["dt"], t["B"], t["C"], t["A"], t["pool"], t["i4"], softplus_threshold=number)
+        kda.paged_attention(q, (*cache, None, None), pages, lens, scale=number)
+        assert seen == [value] * 4
+        seen.clear()
+
+
 def test_workspace_by_device(reached, monkeypatch):  # noqa: F811
     """A call's workspace is that of its device: another device's size, looked up earlier, is not taken for it."""
     at, given = [0], []
