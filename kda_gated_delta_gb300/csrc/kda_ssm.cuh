@@ -286,9 +286,9 @@ __device__ __forceinline__ void ssm_cp_async16(void* dst, const void* src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
 }
 
-// Zeros for the rows of no request, by one CTA.
+// Zeros for the rows of no request, by one CTA.  (A call, so that it takes no part in the registers of the kernels around it.)
 template <typename TOut>
-__device__ __forceinline__ void ssm_clear_unowned(const SsmCall& a, int tid, int threads)
+__device__ __noinline__ void ssm_clear_unowned(const SsmCall& a, int tid, int threads)
 {
     if (a.cu[0] == 0 && a.cu[a.n] == a.T) return;
     if (tid == 0) record_layer_error(kDevErrSeqlens);

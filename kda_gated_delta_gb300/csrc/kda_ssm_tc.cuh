@@ -61,7 +61,12 @@ template <int R> __device__ __forceinline__ void more_registers() { asm volatile
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 constexpr uint32_t kPolls = 1u << 24;
 constexpr float kFarStep = -128.f;               // log2 of a step's decay, bounded: 2^-128 leaves nothing either way
-__device__ __forceinline__ float bounded_step(float step) { return step < kFarStep ? kFarStep : step; }   // a NaN stays one
+__device__ __forceinline__ float bounded_step(float step)                                            // a NaN stays one
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(step), "f"(kFarStep));
+    return r;
+}
 
 // ---- the chunk kernel ------------------------------------------------------------------------------
 template <int N>
