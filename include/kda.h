@@ -509,9 +509,9 @@ void kda_ssm_params_init(kda_ssm_params* p, int32_t num_heads, int32_t head_dim,
  * and c_stride are multiples of 8.
  * States are held and updated in fp32.  Prompts in bf16 with a head_dim of 64 or 128 and up to 128 states go through the
  * tensor cores in chunks of 128 tokens: the factors C . B dt decay and the states enter the products with x and C
- * rounded to bf16 once, a token's increment dt decay x as two bf16 numbers (2^-16 of it); a non-finite x can make
- * the outputs of earlier tokens of its chunk non-finite.  All other shapes and types, requests of few tokens and
- * single tokens go token by token in fp32.
+ * rounded to bf16 once, a token's increment dt decay x as two bf16 numbers (2^-16 of it).  All other shapes and types,
+ * requests of few tokens and single tokens go token by token in fp32.  In either, a non-finite input reaches what the
+ * recurrence makes of it and nothing else.
  * Limits (KDA_ERR_UNSUPPORTED beyond them): total_tokens < 2^31 - 64,
  * H <= 4096, num_seqs * H * P / 16 < 2^29, strides < 2^31.
  * total_tokens = 0 or num_seqs = 0 is a no-op.

@@ -91,6 +91,8 @@ struct __align__(16) TcBars {
     float total[2][2][4], tail[2][2][4];                        // [parity][slice][warp]: sums of the blocks' steps
     __align__(16) float col[2][kChunk];                         // [slice]: dt_j times the decay from j to its block's end
     __align__(16) float diag[2][kChunk];                        // [slice]: dt_j against the steps of its block up to j, or their log2
+    int32_t odd_from[2][kSlice];                                // [slice][channel]: the segment's first token whose x is not finite
+    int32_t odd[2];                                             // whether there is one
 };
 static_assert(sizeof(TcBars) <= 3072 && offsetof(TcBars, col) % 16 == 0 && offsetof(TcBars, diag) % 16 == 0, "barrier block; columns are read by 16 bytes");
 
@@ -288,6 +290,21 @@ struct TcThread {
     }
 };
 
+// Zeros in M do not keep an x that is not finite from the rows before its token.  It is set to zero in the tile, and the
+// rows from its token on get a NaN in its channel as they leave; the states have it from X'.  Looking for one costs an
+// instruction a pair of channels (eight prompts 152.0 -> 153.6 us).
+__device__ __noinline__ void tc_set_aside(TcBars* bars, int s, uint8_t* x_row, int r, int token)
+{
+    for (int i = 0; i < kSlice; ++i) {
+        uint16_t* x = reinterpret_cast<uint16_t*>(x_row + (((i / 8) ^ (r & 7)) << 4)) + i % 8;
+        if ((*x & 0x7f80u) == 0x7f80u) {
+            atomicMin(&bars->odd_from[s][i], token);
+            *x = 0;
+            bars->odd[s] = 1;
+        }
+    }
+}
+
 // Who makes X' and who S: one warpgroup both; or, where no results are wanted, one each, so that the next chunk's X' is
 // made while this one's S is updated (one prompt of 16,411 tokens: the first pass 75 us with one).
 enum { kBoth = 0, kIncrements = 1, kStates = 2 };
@@ -374,6 +391,7 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
             if (len < kChunk) t.wait(&bars->full_b[par], (c >> 1) & 1);
             if (live) {
                 const uint64_t ww = pack2(weight, weight), minus = pack2(-1.f, -1.f);
+                uint64_t nothing = 0;                              // two zeros, until a part of X' is not finite
 #pragma unroll 4
                 for (int q = 0; q < 8; ++q) {
                     const int at = (q ^ (r & 7)) << 4;
@@ -388,12 +406,16 @@ __device__ bool tc_state(const SsmCall& a, const Plan& plan, const TcWork& w, ui
                         const float2 vf = unpack2(v);
                         hi[z] = pack_bf16(vf.x, vf.y);
                         unpack_bf16(hi[z], f);
-                        const float2 rest = unpack2(fma2(pack2(f[0], f[1]), minus, v));
+                        const uint64_t small = fma2(pack2(f[0], f[1]), minus, v);
+                        const float2 rest = unpack2(small);
                         lo[z] = pack_bf16(rest.x, rest.y);
+                        if (!ENDS) nothing = fma2(small, 0, nothing);
                     }
                     *reinterpret_cast<uint4*>(xs_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(xs_row + 2 * K::kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
+                const float2 flag = unpack2(nothing);
+                if (!ENDS && !(flag.x + flag.y == 0.f)) tc_set_aside(bars, s, x_row, r, c * kChunk + r);
             } else {
                 // rows behind the request's last: another's, or nobody's; zeros, for a weight of zero does not stop a NaN
                 const uint4 none = make_uint4(0, 0, 0, 0);
@@ -585,6 +607,7 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
         const uint8_t* warp_rows = x_row - lane * 128;
         const int left = len - (r & 96);                           // rows of this warp that are the request's
         const bool whole = sizeof(TOut) == 2 && left >= 32;        // all rows of the warp: one tensor-map copy
+        const bool odd = *(volatile int32_t*)&bars->odd[s] != 0;
 #pragma unroll 1
         for (int part = 0; part < kSlice; part += 8 * E) {
             if (part) __syncwarp();
@@ -594,6 +617,11 @@ __device__ bool tc_results(const SsmCall& a, const TcWork& w, uint8_t* smem, TcT
                 tc::tmem_ld32(t_y + part + x, y);
                 tc::tmem_wait_ld();
                 tc::pin32(y);
+                if (odd) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (*(volatile int32_t*)&bars->odd_from[s][part + x + i] <= c * kChunk + r) y[i] = 0x7fc00000u;
+                }
 #pragma unroll
                 for (int q = 0; q < 32 / E; ++q) {
                     float f[E];
@@ -673,6 +701,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (uint64_t* bar = &bars->next_s; bar <= &bars->x_free[1]; ++bar) tc::mbar_init(bar, (bar == &bars->ready ? 8 : 4) * w.slices);
             tc::fence_mbar_init();
         }
+    } else if (warp == 1) {
+        for (int i = lane; i < 2 * kSlice; i += 32) bars->odd_from[0][i] = 0x7fffffff;
+        if (lane < 2) bars->odd[lane] = 0;
     } else if (warp == 16) {
         tc::tmem_alloc(&bars->tmem, 512);
         tc::tmem_relinquish();

@@ -83,3 +83,41 @@ def test_b_and_c_of_a_token(at, value, dtype, H, P, N, G, T):
     keep = torch.arange(T, device=DEV) != at
     assert torch.equal(s, state) and torch.equal(y[keep], want[keep]) and torch.equal(y[at, :mine], want[at, :mine])
     assert not bool(y[at, mine:].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype,H,P,N,G,T", FORMS)
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("at", [(0,), (77,), (128,), (299,), (40, 33, 127, 255)], ids=str)
+def test_x_of_a_token(at, value, dtype, H, P, N, G, T):
+    """A non-finite x reaches its own channel from its token on, and its channel's states; all else keeps its bits."""
+    i = inputs(56, dtype, H, P, N, G, T)
+    pool = normal(gen(57), 1, H, P, N)
+    want, state = prefill(i, pool, T)
+    i["x"] = i["x"].clone()
+    touched, spoilt = torch.zeros(T, H, P, dtype=torch.bool, device=DEV), torch.zeros(H, P, dtype=torch.bool, device=DEV)
+    for k, t in enumerate(at):
+        h, c = (H - 1 - k) % H, (P - 7 + 5 * k) % P
+        i["x"][t, h, c] = value
+        touched[t:, h, c] = True
+        spoilt[h, c] = True
+    y, s = prefill(i, pool, T)
+    assert torch.equal(y[~touched], want[~touched]) and torch.equal(s[~spoilt], state[~spoilt])
+    assert not bool(y[touched].isfinite().any()) and not bool(s[spoilt].isfinite().any())
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_x_not_finite_behind_a_request(out):
+    """Rows of x that are not finite behind a request's last, inside its last chunk, and a request that is nothing but NaN."""
+    H, P, N, G, lens = 2, 64, 128, 1, [300, 60, 100]
+    x, dt, B, C, A_log, dt_bias, D = ssm_inputs(58, lens, H, P, N, G, BF16)
+    pool = normal(gen(59), 3, H, P, N)
+    calls = []
+    for bad in (False, True):
+        p = pool.clone()
+        if bad:
+            x = x.clone()
+            x[300:360] = NAN
+        calls.append((kda.ssm_prefill(x, dt, B, C, A_log, ref.lengths_to_cu(lens, DEV), p, idx([0, 1, 2]), dt_bias=dt_bias, D=D, out_dtype=out), p))
+    (want, state), (y, s) = calls
+    assert torch.equal(y[:300], want[:300]) and torch.equal(y[360:], want[360:]) and torch.equal(s[[0, 2]], state[[0, 2]])
+    assert bool(y[300:360].isnan().all()) and bool(s[1].isnan().all())
