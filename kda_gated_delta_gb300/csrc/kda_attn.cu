@@ -729,13 +729,6 @@ cudaError_t launch_attention(const kda_kv_params& p, const AttnCall& a, void* wo
     return fp4 ? launch_typed<64, true>(p, a, workspace, stream) : launch_typed<64, false>(p, a, workspace, stream);
 }
 
-cudaError_t attn_read_and_clear_error(int32_t* code)
-{
-    int32_t many = 0;
-    cudaError_t e = read_and_clear(g_attn_error, code);
-    if (e == cudaSuccess) e = attn_tc_read_and_clear_error(&many);
-    if (*code == 0) *code = many;
-    return e;
-}
+cudaError_t attn_error_word(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_attn_error); }
 
 }  // namespace kda

@@ -205,6 +205,5 @@ __device__ __forceinline__ void join_row(const AttnCall& a, const Parts& parts, 
 attn::Cut cut_many(const kda_kv_params& p, int32_t n, int64_t T, int32_t max_new, int32_t max_len);
 template <int D, bool FP4>
 cudaError_t launch_many(const kda_kv_params& p, const AttnCall& a, const attn::Parts& parts, cudaStream_t stream);
-cudaError_t attn_tc_read_and_clear_error(int32_t* code);
 
 }  // namespace kda

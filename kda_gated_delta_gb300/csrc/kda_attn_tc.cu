@@ -888,6 +888,6 @@ template cudaError_t launch_many<64, true>(const kda_kv_params&, const AttnCall&
 template cudaError_t launch_many<128, false>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
 template cudaError_t launch_many<128, true>(const kda_kv_params&, const AttnCall&, const Parts&, cudaStream_t);
 
-cudaError_t attn_tc_read_and_clear_error(int32_t* code) { return read_and_clear(g_attn_tc_error, code); }
+cudaError_t attn_tc_error_word(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_attn_tc_error); }
 
 }  // namespace kda

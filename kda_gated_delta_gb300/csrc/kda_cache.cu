@@ -309,6 +309,6 @@ cudaError_t launch_kv_read(const kda_kv_params& p, kv::Paged c, void* k_out, voi
     });
 }
 
-cudaError_t cache_read_and_clear_error(int32_t* code) { return read_and_clear(g_cache_error, code); }
+cudaError_t cache_error_word(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_cache_error); }
 
 }  // namespace kda

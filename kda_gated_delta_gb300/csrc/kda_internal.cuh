@@ -58,16 +58,6 @@ __device__ __forceinline__ float gate_log_decay(float x, float rate, const GateP
 
 __device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// ---- error words --------------------------------------------------------------------------------
-// Read a translation unit's device error word, and clear it if it holds a code.  A word without one is not written:
-// a copy takes some 10 us, and there are seven words (with six a check took 61 us; with all of them cleared always 83).
-inline cudaError_t read_and_clear(int32_t& word, int32_t* code)
-{
-    const int32_t zero = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(code, word, sizeof(int32_t));
-    return e != cudaSuccess || *code == 0 ? e : cudaMemcpyToSymbol(word, &zero, sizeof(int32_t));
-}
-
 // ---- host-side argument handling (kda_api.cu) ----------------------------------------------------
 GateParams gate_params(const kda_params& p);
 // The host-side checks of a chunk-prefill call, in one place for every prefill entry point (the
@@ -88,7 +78,7 @@ cudaError_t launch_recurrent(const kda_params& p, const GateParams& gp, const vo
                              float* pool_out, float* inter, int64_t num_slots,
                              const int32_t* state_idx, void* out, cudaStream_t stream);
 bool recurrent_supported(const kda_params& p);
-cudaError_t recurrent_read_and_clear_error(int32_t* code);
+cudaError_t recurrent_error_word(int32_t** word);   // the translation unit's device error word
 cudaError_t launch_replay(const kda_params& p, const GateParams& gp, const void* q, const void* k,
                           const void* v, const float* g_raw, const float* b_raw, const float* A_log,
                           const float* dt_bias, int32_t batch, float* pool, int64_t num_slots,
@@ -109,8 +99,8 @@ cudaError_t launch_prefill(const kda_params& p, const GateParams& gp, const void
                            const cudaEvent_t* events = nullptr,
                            float* chunk_states = nullptr, int64_t chunk_states_capacity = 0);
 bool prefill_supported(const kda_params& p);
-cudaError_t prefill_read_and_clear_error(int32_t* code);
+cudaError_t prefill_error_word(int32_t** word);   // the translation unit's device error word
 cudaError_t launch_wait_selftest(uint32_t polls, int32_t* result, cudaStream_t stream);
-cudaError_t selftest_read_and_clear_error(int32_t* code);
+cudaError_t selftest_error_word(int32_t** word);   // the translation unit's device error word
 
 }  // namespace kda

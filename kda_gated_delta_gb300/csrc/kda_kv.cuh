@@ -181,7 +181,7 @@ cudaError_t launch_kv_append(const kda_kv_params& p, kv::Paged c, const void* q,
                              int64_t k_stride, const void* v, int64_t v_stride, const float* rope, int64_t rope_rows,
                              const int32_t* positions, void* q_out, cudaStream_t stream);
 cudaError_t launch_kv_read(const kda_kv_params& p, kv::Paged c, void* k_out, void* v_out, cudaStream_t stream);
-cudaError_t cache_read_and_clear_error(int32_t* code);
+cudaError_t cache_error_word(int32_t** word);
 
 struct AttnCall {
     kv::Paged c;
@@ -200,6 +200,7 @@ struct AttnCall {
 size_t attention_workspace_bytes(const kda_kv_params& p, int32_t num_seqs, int64_t total_tokens, int32_t max_new,
                                  int32_t max_len);
 cudaError_t launch_attention(const kda_kv_params& p, const AttnCall& a, void* workspace, cudaStream_t stream);
-cudaError_t attn_read_and_clear_error(int32_t* code);
+cudaError_t attn_error_word(int32_t** word);
+cudaError_t attn_tc_error_word(int32_t** word);
 
 }  // namespace kda

@@ -7,7 +7,7 @@ namespace {
 __device__ int32_t g_layer_error = 0;
 }
 __device__ __forceinline__ void record_layer_error(int32_t code) { atomicCAS(&g_layer_error, 0, code); }
-cudaError_t layer_read_and_clear_error(int32_t* code) { return read_and_clear(g_layer_error, code); }
+cudaError_t layer_error_word(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_layer_error); }
 }  // namespace kda
 
 #include "kda_conv.cuh"

@@ -76,9 +76,9 @@ cudaError_t launch_norm(const kda_norm_params& p, const NormCall& a, cudaStream_
 cudaError_t launch_ssm_decode(const kda_ssm_params& p, const SsmCall& a, cudaStream_t stream);
 size_t ssm_workspace_bytes(const kda_ssm_params& p, int32_t num_seqs, int64_t total_tokens);
 cudaError_t launch_ssm_prefill(const kda_ssm_params& p, const SsmCall& a, void* workspace, cudaStream_t stream);
-cudaError_t layer_read_and_clear_error(int32_t* code);
+cudaError_t layer_error_word(int32_t** word);
 
-// The device error word of these operators (one translation unit: a check of the words takes 10 us each).
+// The device error word of these operators is one translation unit's.
 __device__ __forceinline__ void record_layer_error(int32_t code);
 
 // ---- vectors of V elements as fp32 -----------------------------------------------------------------

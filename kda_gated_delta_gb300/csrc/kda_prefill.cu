@@ -1995,6 +1995,6 @@ cudaError_t launch_prefill(const kda_params& p, const GateParams& gp, const void
     return cudaErrorInvalidValue;
 }
 
-cudaError_t prefill_read_and_clear_error(int32_t* code) { return read_and_clear(g_prefill_error, code); }
+cudaError_t prefill_error_word(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_prefill_error); }
 
 }  // namespace kda

@@ -654,6 +654,6 @@ cudaError_t launch_commit(int H, int D, const float* inter, int32_t batch, int32
     return cudaGetLastError();
 }
 
-cudaError_t recurrent_read_and_clear_error(int32_t* code) { return read_and_clear(g_recurrent_error, code); }
+cudaError_t recurrent_error_word(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_recurrent_error); }
 
 }  // namespace kda

@@ -60,6 +60,6 @@ cudaError_t launch_wait_selftest(uint32_t polls, int32_t* result, cudaStream_t s
     return cudaGetLastError();
 }
 
-cudaError_t selftest_read_and_clear_error(int32_t* code) { return read_and_clear(g_selftest_error, code); }
+cudaError_t selftest_error_word(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_selftest_error); }
 
 }  // namespace kda

@@ -1,5 +1,5 @@
-"""The operators around a recurrence over a CUDA runtime of our own, for host-side tests without a GPU: their object files
-linked with a library that counts launches, lets one fail, and says what device there is.  No kernel runs."""
+"""The library over a CUDA runtime of our own, for host-side tests without a GPU: its object files linked with one that counts
+launches and copies, lets a launch fail, and says what device there is.  No kernel runs."""
 import ctypes
 import os
 import subprocess
@@ -10,7 +10,7 @@ SOURCE = r"""
 #include <cuda_runtime_api.h>
 #include <cstring>
 
-static int launches = 0, fail_at = -1, sms = 152, device = 0, silent = 0;
+static int launches = 0, copies = 0, fail_at = -1, sms = 152, device = 0, silent = 0;
 static cudaError_t last = cudaSuccess;
 
 static cudaError_t launch()
@@ -22,7 +22,8 @@ static int encode(...) { return 0; }
 
 extern "C" {
 // the test's side
-void fake_reset(int fail) { launches = 0; fail_at = fail; last = cudaSuccess; }
+void fake_reset(int fail) { launches = copies = 0; fail_at = fail; last = cudaSuccess; }
+int fake_copies() { return copies; }
 int fake_launches() { return launches; }
 void fake_device(int dev, int count) { device = dev; sms = count; }
 void fake_silent(int queries) { silent = queries; }        // so many attribute queries fail
@@ -62,11 +63,20 @@ cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** f, unsigned, un
     *r = cudaDriverEntryPointSuccess;
     return cudaSuccess;
 }
-cudaError_t cudaMemcpyFromSymbol(void* to, const void*, size_t n, size_t, enum cudaMemcpyKind) { memset(to, 0, n); return cudaSuccess; }
-cudaError_t cudaMemcpyToSymbol(const void*, const void*, size_t, size_t, enum cudaMemcpyKind) { return cudaSuccess; }
+cudaError_t cudaMemcpyFromSymbol(void* to, const void*, size_t n, size_t, enum cudaMemcpyKind) { ++copies; memset(to, 0, n); return cudaSuccess; }
+cudaError_t cudaMemcpyToSymbol(const void*, const void*, size_t, size_t, enum cudaMemcpyKind) { ++copies; return cudaSuccess; }
+cudaError_t cudaMemcpyFromSymbolAsync(void* to, const void*, size_t n, size_t, enum cudaMemcpyKind, cudaStream_t)
+{
+    ++copies;
+    memset(to, 0, n);
+    return cudaSuccess;
+}
+cudaError_t cudaGetSymbolAddress(void** p, const void*) { *p = (void*)(size_t)(1 << 20); return cudaSuccess; }
+cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
+cudaError_t cudaEventRecord(cudaEvent_t, cudaStream_t) { return cudaSuccess; }
 }
 """
-OBJECTS = ("kda_layer_api.o", "kda_layer.o", "kda_norm.o")
+OBJECTS = [os.path.splitext(f)[0] + ".o" for f in build.SOURCES]
 
 
 def load(folder) -> ctypes.CDLL:

@@ -146,3 +146,12 @@ def test_slots_of_requests_without_tokens(at):
             ins, out = ssm_call(g, 200, dtype, 2, P, N)
             kda.ssm_prefill(*ins, table(cu[:n + 1]), normal(g, 4, 2, P, N), idx(slots[:n]), out=out)
             assert kda.check_device_errors() == 1
+
+
+def test_codes_of_two_units_at_once():
+    """A check gives one code and clears them all."""
+    g = gen(46)
+    for _ in range(3):
+        kda.causal_conv(normal(g, 30, 8), normal(g, 8, 4), normal(g, 2, 3, 8), idx([0, 1]), table([0, 20, 31]))
+        kda.selftest_wait_timeout(100)
+        assert kda.check_device_errors() == 3 and kda.check_device_errors() == 0

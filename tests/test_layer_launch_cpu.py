@@ -1,4 +1,4 @@
-"""Launches of the operators around a recurrence over a runtime of our own: a launch that fails ends the call, and
+"""The library's host side over a runtime of our own: a launch that fails ends the call, and
 device properties are those of the device."""
 import ctypes
 
@@ -53,3 +53,13 @@ def test_number_of_sms(L):
     assert need(1, 152, silent=100) == need(2, 148) != need(4, 152)
     assert need(1, 152) == need(4, 152)
     assert need(3, 40) == other != need(1, 152)
+
+
+def test_a_check_makes_one_copy(L):
+    """However many translation units have an error word."""
+    L.fake_reset(-1)
+    code = ctypes.c_int32(7)
+    assert L.kda_check_device_errors(None, ctypes.byref(code)) == 0 and code.value == 0
+    assert L.fake_copies() == 1
+    L.fake_reset(0)
+    assert L.kda_check_device_errors(None, ctypes.byref(code)) == -5 and code.value == 0 and L.fake_copies() == 0
