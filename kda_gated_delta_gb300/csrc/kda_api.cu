@@ -37,8 +37,8 @@ int32_t check_common(const kda_params* p, const void* q, const void* k, const vo
 int32_t from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
 // ---- the device error words of the translation units ------------------------------------------------
-// A warp takes and clears them all, so that a check makes one copy whatever their number: a copy takes some 10 us (with one
-// for each of the seven words a check took 71 us, so it takes 23).
+// A warp takes and clears them all, so that a check makes one copy whatever their number: a copy takes some 10 us, and a check
+// with one for each of the seven words took 71 us where this takes 23.
 constexpr int kErrorWords = 7;
 constexpr uint32_t kChecks = 64;                    // checks at the same time, each with a place of its own
 struct ErrorWords {

@@ -560,10 +560,12 @@ SsmLayout ssm_layout(const kda_ssm_params& p, int32_t n, int64_t T)
     w.cut = T >= 2 * want;
     w.plan.want = (int32_t)(want < (int64_t)1 << 30 ? want : (int64_t)1 << 30);
     const int64_t more = T / w.plan.want;                          // a request of k > 1 segments has k * want tokens or more
-    // A chunk costs the same for 1 token as for 128: up to some 32 tokens a request is done sooner token by token (64
-    // requests of 64 heads: 4 tokens 58 us against 193, 32 tokens 196 against 184).  Where the mean says that there
-    // may be such requests, they are taken out; which they are, the kernels see.
-    w.short_len = tensor && T < 64 * (int64_t)n ? 32 : 0;
+    // A chunk costs the same for 1 token as for 128, so requests of few tokens are done sooner token by token.  16 and 64
+    // requests, us token by token and in chunks: 64 heads, 4 tokens 23 and 64 against 60 and 199, 24 tokens 50 and 168 against
+    // 58 and 192, 32 tokens 61 and 214 against 55 and 186; 8 heads, 4 tokens 8 and 15 against 16 and 32, 24 tokens 15 and 30
+    // against 16 and 31, 32 tokens 17 and 37 against 15 and 32.  Where the mean says that there may be such requests, they are
+    // taken out; which they are, the kernels see.
+    w.short_len = tensor && T < 64 * (int64_t)n ? 24 : 0;
     int64_t requests = w.short_len && T / (w.short_len + 1) < n ? T / (w.short_len + 1) : n;
     if (!tensor && !w.cut) requests = 0;                            // each request whole, without a plan
     w.plan.max_segments = requests ? (int32_t)(requests + more) : 0;
