@@ -467,8 +467,8 @@ typedef struct kda_conv_params {
  *   outs        host array of num_outs (1 to 4) device pointers; output j is contiguous
  *               [total_tokens][out_channels[j]] and receives the next out_channels[j] channels (host
  *               int32 array of sum C): the parts of a fused projection come out ready for what follows
- * Rows of 16-byte aligned x, pool and outputs whose stride and channel counts are multiples of 16 bytes go
- * by vectors; all others by single elements.  total_tokens < 2^31 - 64, C <= 2^20, num_seqs < 2^30.
+ * Rows of 16-byte aligned x, weight, pool and outputs whose stride and channel counts are multiples of 16 bytes
+ * go by vectors; all others by single elements.  total_tokens < 2^31 - 64, C <= 2^20, num_seqs < 2^30.
  * total_tokens = 0 or num_seqs = 0 is a no-op.
  */
 int32_t kda_causal_conv(const kda_conv_params* p, const void* x, int64_t x_stride,

@@ -9,8 +9,8 @@
 // writes the request's new state: it has read the old one by then, and nobody else touches these
 // channels of the slot, so the update in place needs neither a second launch nor an order among CTAs.
 //
-// Measured (12,288 channels in bf16, 4 taps, SiLU): 8 prompts of 18,646 tokens in 155 us, 88% of the measured copy
-// rate; 256 single tokens in 16 us on the GPU (50 MB: 7.4 us at that rate, the rest start and end of one wave).
+// Measured (12,288 channels in bf16, 4 taps, SiLU): 8 prompts of 18,646 tokens in 152 us, 90% of the measured copy
+// rate; 256 single tokens in 10.8 us on the GPU (50 MB: 7.4 us at that rate, the rest start and end of one wave).
 #pragma once
 
 #include "kda_layer.cuh"

@@ -166,9 +166,10 @@ __device__ __forceinline__ void store_floats(T* p, const float* f)
     }
 }
 
-// sigmoid with the special-function unit's exponential and reciprocal: relative error of some 2^-21, far
-// below a bf16 result's 2^-9 and of the order of the fp32 sums before it.  e^{-x} past the largest float
-// gives 1 / inf = 0.
+// sigmoid with the special-function unit's exponential and reciprocal, each off by some 2^-22.  The exponent x log2 e is
+// off by up to 2^-23.7 of itself before, so a negative x adds |x| 2^-23.7 of the result: 2^-19.7 at 16, 2^-17.3 at 85.  Both are
+// below a bf16 result's 2^-9; in fp32 they are the larger part of the error.  e^{-x} past the largest float gives
+// 1 / inf = 0, and so do results below the smallest normal float (x < -87).
 // (With flushing of subnormals: the plain forms take three further instructions an element for them, and 1 + e is
 // the same.)
 __device__ __forceinline__ float fast_sigmoid(float x)

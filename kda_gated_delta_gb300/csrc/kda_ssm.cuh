@@ -11,8 +11,8 @@
 //   ssm_rows_kernel    packed prompts, tokens staged through shared memory: 3 fp32 operations a state and
 //                      token; the path of fp32 inputs, of the shapes that the tensor-core form
 //                      (kda_ssm_tc.cuh) does not take and of requests of few tokens.  Bound by the fp32 pipes when
-//                      it fills the SMs, by the chain loads - sums - shuffles of a token (some 260 cycles with one warp a
-//                      scheduler: 76 us for 5 requests of up to 583 tokens of 8 heads) when it does not; long
+//                      it fills the SMs, by the chain loads - sums - shuffles of a token (some 240 cycles with one warp a
+//                      scheduler: 72 us for 5 requests of up to 583 tokens of 8 heads) when it does not; long
 //                      requests are then cut into segments.
 #pragma once
 
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_rows_kernel(const SsmCall a, 
     }
     const int h = (int)(bh - b * a.H);
     const int row0 = (int)(blockIdx.x - bh * splits) * R;
-    const int rows = a.P - row0 < R ? a.P - row0 : R;    // a multiple of 16
+    const int rows = a.P - row0 < R ? a.P - row0 : R;    // a multiple of 8
     int64_t first, last, slot;
     ssm::Segment seg = {};
     if (plan.segments) {

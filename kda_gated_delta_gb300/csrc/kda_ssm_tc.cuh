@@ -32,8 +32,8 @@
 // computes each segment's own state from zero (dS only), a small kernel chains them, and every segment then
 // starts from its true state.
 //
-// Measured (64 heads x 64 x 128 states, 8 groups, 8 prompts of 18,646 tokens): 152 us, 41% of the measured copy rate;
-// one prompt of 16,411 tokens (32 heads x 128 x 128, one group) 192 us.  Bound by shared memory: a chunk of a pair moves
+// Measured (64 heads x 64 x 128 states, 8 groups, 8 prompts of 18,646 tokens): 153 us, 41% of the measured copy rate;
+// one prompt of 16,411 tokens (32 heads x 128 x 128, one group) 191 us.  Bound by shared memory: a chunk of a pair moves
 // 628 KB through it (products' operands 288, copies in 96, X' 96, S, X again and Y 128, the rest), 4,900 of some 6,600
 // cycles, of which the products take 2,400.  A third pair of warpgroups only contended for it (180 us).
 #pragma once
